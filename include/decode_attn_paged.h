@@ -1,0 +1,161 @@
+/*
+ * decode_attn_paged.h -- a KV cache kept in pages, for NVIDIA GB300 (sm_103a): decode
+ * attention over it and the append that fills it, with pages of 16-bit or of 8-bit
+ * elements. It stands beside decode_attn_splitkv.h (caches packed through
+ * cu_seqlens_k, or one slab per sequence) and shares its status codes, its layouts,
+ * its conventions and its device error word.
+ *
+ * The cache. Keys and values live in `num_pages` pages of `page_size` tokens; a
+ * sequence's tokens 0 .. L_b - 1 are spread over the pages that its row of the block
+ * table names, token p in page block_table[b][p / page_size] at slot p % page_size.
+ * Pages may be shared for reading (common prefixes) and lie in any order.
+ *
+ * One decode step is an append, then an attention:
+ *
+ *     kv_lens += new tokens                       (the caller's own kernel)
+ *     decode_attn_paged_append(q, k, v, ...)      rotates, writes the new keys and values
+ *     decode_attn_paged(q_out, ...)               attends to everything up to each token
+ *
+ * Conventions are those of decode_attn_splitkv.h: device pointers of the current
+ * device, asynchronous work on `stream`, host checks first (a call that returns
+ * anything but DA_OK has enqueued nothing), nothing allocated and nothing kept.
+ */
+#ifndef DECODE_ATTN_PAGED_H
+#define DECODE_ATTN_PAGED_H
+
+#include "decode_attn_splitkv.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Element type of a page besides DA_F16 and DA_BF16: 8 bits (1 sign, 4 exponent and 3
+   mantissa bits, largest value 448, no infinity), times one float32 scale per page and
+   KV head. */
+#define DA_E4M3 2
+
+/* More bits of the device error word (decode_attn_splitkv_get_error). */
+#define DA_DEVERR_PAGE 0x4u     /* a block-table entry outside [0, num_pages): its keys and values read as
+                                   zeros, and nothing is written through it */
+#define DA_DEVERR_POSITION 0x8u /* an appended token's position has no row in cos_sin: the token is left out */
+
+/* Largest batch, and largest page, accepted by the calls below. */
+#define DA_MAX_PAGED_BATCH 1024
+#define DA_MAX_PAGE_SIZE 1024
+
+typedef struct {
+    void* k;          /* device, 16-byte aligned: [num_pages, page_size, Hkv, D] (DA_LAYOUT_VARLEN)      */
+    void* v;          /*   or [num_pages, Hkv, page_size, D] (DA_LAYOUT_BHSD), contiguous                */
+    float* k_scale;   /* device, float32 [num_pages, Hkv], 4-byte aligned, finite and not negative: */
+    float* v_scale;   /*   DA_E4M3 only (else ignored, may be NULL)                                      */
+    int num_pages;    /* >= 1 */
+    int page_size;    /* a multiple of 16 in [16, DA_MAX_PAGE_SIZE] */
+    int Hkv;          /* KV heads, >= 1 */
+    int D;            /* head size: 64 or 128 */
+    int kv_dtype;     /* DA_F16, DA_BF16 or DA_E4M3 */
+    int layout;       /* DA_LAYOUT_VARLEN or DA_LAYOUT_BHSD: the order of tokens and heads in a page */
+} da_paged_cache;
+
+/*
+ * Workspace of the calls below: bytes for any batch and any lengths with these heads
+ * (the split step cuts the whole batch's keys into a bounded number of equal ranges,
+ * so the size does not grow with the batch). 0 if an argument is out of range.
+ * Its base is 256-byte aligned; its first 256 bytes are the header of
+ * decode_attn_splitkv.h (error word first), then come counters that are zero between
+ * calls, then partial results. Calls that may overlap on the GPU (other streams, two
+ * graphs replayed at once) need a workspace each; calls in stream order share one.
+ */
+size_t decode_attn_paged_workspace_size(int T_q, int Hq, int Hkv, int D);
+
+/*
+ * Zero a workspace's header and counters: once on fresh memory, and again after a
+ * DA_DEVERR_TIMEOUT. Enqueued on `stream`. Errors: DA_ERR_INVALID_ARG (NULL or too
+ * small for any call), DA_ERR_ALIGNMENT, DA_ERR_CUDA.
+ */
+da_status decode_attn_paged_workspace_init(void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Decode attention over the paged cache. For query token t of T_q (the last T_q tokens
+ * of the sequence, at positions L_b - T_q + t), head h and KV head h / (Hq / Hkv):
+ *
+ *     x_j = scale * k_scale * (q . k_j)              j <= L_b - T_q + t
+ *     out = sum_j softmax(x)_j * v_scale * v_j,      lse = ln sum_j exp(x_j)
+ *
+ * with the scales of key j's page and head (1 in 16-bit pages). A token that sees no key
+ * gets out = 0 and lse = -inf.
+ *   q            device, [B, T_q, Hq, D] elements of `dtype`, 16-byte aligned
+ *   cache        host pointer, read during the call; 16-bit pages hold elements of `dtype`
+ *   kv_lens      device, int32 [B]: keys of each sequence, the query tokens' own included. A
+ *                length below 0 or above max_pages * page_size counts as 0 and sets
+ *                DA_DEVERR_SEQLENS
+ *   block_table  device, int32 [B][table_stride], the first max_pages entries of a row
+ *                readable; only the entries of a sequence's own tokens are read
+ *   B            in [1, DA_MAX_PAGED_BATCH]; T_q in [1, DA_MAX_QUERY_TOKENS]; Hq % Hkv == 0
+ *   dtype        DA_F16 or DA_BF16
+ *   scale        finite
+ *   out          device, [B, T_q, Hq, D] elements of `dtype`, 16-byte aligned
+ *   lse          device, float32 [B, T_q, Hq], or NULL
+ *   workspace    >= decode_attn_paged_workspace_size(T_q, Hq, Hkv, D) bytes, initialised once
+ * Memory in a page behind a sequence's last token may hold anything. The results do not
+ * depend on timing: the same inputs on the same device give the same bits.
+ * Errors (nothing enqueued): DA_ERR_INVALID_ARG, DA_ERR_UNSUPPORTED (D, or a batch
+ * above the limit), DA_ERR_ALIGNMENT, DA_ERR_WORKSPACE_TOO_SMALL; DA_ERR_CUDA.
+ */
+da_status decode_attn_paged(const void* q, const da_paged_cache* cache, const int32_t* kv_lens,
+                            const int32_t* block_table, int max_pages, int table_stride, int B, int T_q,
+                            int Hq, da_dtype dtype, float scale, void* out, float* lse, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* How decode_attn_paged_append rotates the first rot_dim dims of queries and keys. */
+typedef enum {
+    DA_ROPE_NONE = 0,        /* not at all (cos_sin may be NULL) */
+    DA_ROPE_HALF = 1,        /* dim i with dim i + rot_dim / 2 */
+    DA_ROPE_INTERLEAVED = 2  /* dim 2i with dim 2i + 1 */
+} da_rope;
+
+/*
+ * Append new tokens to the paged cache, and rotate their queries. Sequence b's new
+ * tokens are rows cu_new[b] .. cu_new[b+1] - 1 of q, k and v; row i of them sits at
+ * position p = kv_lens[b] - (cu_new[b+1] - cu_new[b]) + i (kv_lens counts them already).
+ * With (c, s) = (cos_sin[p][j], cos_sin[p][rot_dim / 2 + j]) a pair (x, y) of a query or
+ * key turns into (x c - y s, y c + x s), in float32; the other dims and the values pass
+ * as they are. The queries go to q_out, the keys and values to their pages, rounded to
+ * nearest-even once.
+ *
+ * 8-bit pages. An element is stored as x / s rounded to e4m3, s the scale of its page
+ * and head in the cache. The call sets s: with `need` the least power of two 2^e (e >= -126)
+ * for which every finite new element of the page and head is at most 448 * 2^e,
+ *     s = need             if the new tokens start at the page's first slot
+ *     s = max(s, need)     otherwise; where s grew, the page's earlier elements are rounded
+ *                          again to the new scale
+ * A power of two costs no precision (e4m3 is a floating format, so only the smallest
+ * values of a page notice its scale) and makes growing a page's scale exact for all
+ * elements but those. +-Inf is stored as +-448 s, NaN as NaN; neither moves the scale.
+ *
+ *   q, k, v      device, T_new rows of `dtype` elements: Hq (Hkv) heads of D contiguous
+ *                elements each, rows q_stride (k_stride, v_stride) elements apart, 16-byte
+ *                aligned, strides multiples of 8. q may be NULL (nothing to rotate)
+ *   q_out        device, rows like q's, q_out_stride elements apart; may be q itself with the
+ *                same stride, else it must not overlap q, k or v
+ *   cos_sin      device, float32 [max_pos][rot_dim], 16-byte aligned: cosines, then sines
+ *   rot_dim      a multiple of 16 in [16, D] (ignored without rotation)
+ *   cu_new       device, int32 [B+1], non-decreasing; rows from cu_new[B] on are left alone
+ *   T_new        rows that q, k and v hold, >= 0; a sequence whose rows lie outside them, or
+ *                whose kv_lens is smaller than its new tokens or larger than max_pages *
+ *                page_size, is left out and sets DA_DEVERR_SEQLENS
+ *   workspace    its header alone is used (the error word): initialised, 256-byte aligned
+ * The pages that one call writes must be distinct (no two sequences append to the same
+ * page). Other arguments and errors as decode_attn_paged.
+ */
+da_status decode_attn_paged_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                   const void* v, int64_t v_stride, const float* cos_sin, int max_pos,
+                                   int rot_dim, da_rope rope, const int32_t* cu_new, const int32_t* kv_lens,
+                                   const int32_t* block_table, int max_pages, int table_stride, int B,
+                                   int T_new, int Hq, da_dtype dtype, const da_paged_cache* cache, void* q_out,
+                                   int64_t q_out_stride, void* workspace, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* DECODE_ATTN_PAGED_H */

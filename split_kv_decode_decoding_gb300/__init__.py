@@ -1,4 +1,5 @@
-"""Python binding of the split-KV decode attention C ABI (include/decode_attn_splitkv.h).
+"""Python binding of the split-KV decode attention C ABI (include/decode_attn_splitkv.h; the
+paged-cache part, include/decode_attn_paged.h, is bound in paged.py and offered here too).
 
 Argument marshalling only: every step of the computation runs in the CUDA
 library ``_build/libdecode_attn_splitkv.so``. Tensors are PyTorch CUDA tensors
@@ -12,7 +13,11 @@ import ctypes
 import math
 import os
 
+from . import paged as _paged
 from .build import LIB, build
+from .paged import (DA_DEVERR_PAGE, DA_DEVERR_POSITION, DA_E4M3, DA_MAX_PAGE_SIZE, DA_MAX_PAGED_BATCH, DA_ROPE_HALF,
+                    DA_ROPE_INTERLEAVED, DA_ROPE_NONE, EXPORTED_PAGED, PagedCache, alloc_paged_workspace,
+                    decode_attn_paged, decode_attn_paged_append, paged_workspace_size)
 
 DA_OK, DA_ERR_INVALID_ARG, DA_ERR_UNSUPPORTED, DA_ERR_ALIGNMENT = 0, 1, 2, 3
 DA_ERR_WORKSPACE_TOO_SMALL, DA_ERR_CUDA, DA_ERR_SCRATCH_LIMIT, DA_ERR_DEVICE_TIMEOUT = 4, 5, 6, 7
@@ -110,6 +115,7 @@ def load(path: str = LIB):
     lib.decode_attn_splitkv_model_best_splits.restype = I
     lib.decode_attn_splitkv_status_string.argtypes = [I]
     lib.decode_attn_splitkv_status_string.restype = ctypes.c_char_p
+    _paged.declare(lib)
     _lib = lib
     return lib
 

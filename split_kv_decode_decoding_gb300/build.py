@@ -1,4 +1,4 @@
-"""Compile the CUDA library for sm_103a, in tree (no cmake): four translation units
+"""Compile the CUDA library for sm_103a, in tree (no cmake): six translation units
 compiled in parallel, then linked into one shared library."""
 from __future__ import annotations
 
@@ -12,8 +12,10 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 SOURCES = [os.path.join(CSRC, n) for n in
-           ("decode_attn_splitkv.cu", "comparison_arms.cu", "picker.cpp", "time_model.cpp")]
+           ("decode_attn_splitkv.cu", "comparison_arms.cu", "paged_attn.cu", "paged_append.cu", "picker.cpp",
+            "time_model.cpp")]
 HEADER = os.path.join(ROOT, "include", "decode_attn_splitkv.h")
+PAGED_HEADER = os.path.join(ROOT, "include", "decode_attn_paged.h")
 LIB = os.path.join(PKG, "_build", "libdecode_attn_splitkv.so")
 # the read-ceiling probe the benchmark times beside the decode call (not part of the library)
 PROBE_SRC = os.path.join(CSRC, "read_probe.cu")
@@ -36,7 +38,7 @@ def nvcc() -> str:
 
 def inputs() -> list:
     """Every file the library is built from (sources and headers)."""
-    return SOURCES + [HEADER] + sorted(glob.glob(os.path.join(CSRC, "*.h")) +
+    return SOURCES + [HEADER, PAGED_HEADER] + sorted(glob.glob(os.path.join(CSRC, "*.h")) +
                                        glob.glob(os.path.join(CSRC, "*.cuh")))
 
 
