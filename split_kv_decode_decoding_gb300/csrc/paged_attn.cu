@@ -1,90 +1,1026 @@
-// Decode attention over a paged KV cache (decode_attn_paged.h): a warp per query row.
+// Decode attention over a paged KV cache (decode_attn_paged.h) for GB300 / sm_103a, with
+// pages of 16-bit or of e4m3 elements.
 //
-// Each lane owns D / 32 dims of the row; per key one dot product by shuffles and one step of
-// the online softmax in the exp2 domain, float32 throughout.
+// Per (sequence b, KV head, chunk of up to 8 or 16 packed (token, head) columns):
+//     x_j = scale * ks * (q . k_j),   out = sum_j 2^(x_j log2e - m) vs v_j / sum_j 2^(x_j log2e - m)
+// in one pass over the keys with a running maximum m (ks, vs: the scales of key j's page and
+// head, 1 in 16-bit pages).
+//
+// What bounds it: the K/V bytes. A key costs 4 D (16-bit) or 2 D (e4m3) bytes for 4 D
+// operations per column, far below what the tensor cores deliver, so everything here serves
+// the stream.
+//
+// How the work is cut. The unit is a stage of 64 (e4m3: 128) keys of one sequence and KV
+// head. All units of the batch, in order (sequence, KV head, keys), are cut into about as many
+// equal ranges as there are persistent CTAs, whatever the lengths are: the host knows none of
+// them, and no split count has to be chosen. A range may hold the end of one (sequence, head),
+// several whole ones and the beginning of another; a (sequence, head) that lies in one
+// range is written by it directly, otherwise each of its ranges leaves a partial result (at
+// most two per range, so the workspace does not grow with the batch) and the warp that
+// finishes a column last merges that column's partials, in range order whoever it is: the
+// result does not depend on timing.
+//
+// A CTA is one producer warp and four consumer warps around a three-stage ring, as in the
+// split kernel for contiguous caches. The producer's lanes read the block table (and the scales) of the
+// next 32 boxes at once, one batch ahead of the copies, and each lane issues its own box: 64-key
+// TMA boxes (pages smaller than that: their size), 16-key boxes at a sequence's ragged end, so that
+// a box never crosses a page.
+//
+// e4m3 pages. The products run as fp16 tensor-core products: every e4m3 value is an fp16
+// value, and a conversion instruction takes two elements, 2.5 issue slots per key and SM out
+// of the 11 cycles that a key takes to stream (measured: 0.5 cycles per conversion and SM). Queries in bf16
+// are scaled by a power of two per column into the top of the fp16 range (an element below 2^-28 of its
+// column's largest loses bits, by at most 2^-39 of that largest). The order of the dims inside a 16-dim step is free, so
+// one ldmatrix of 16-bit pairs feeds two steps. The scales never touch the elements: ks multiplies the score, and
+// vs goes into the exponent of the weight, 2^(x + log2 vs - mv), with a running maximum mv of
+// its own, so that the fp16 weights keep their precision however unequal the pages' scales are.
 
 #include "paged_common.cuh"
 
 namespace da_impl {
 
-constexpr int kPagedShares = 2048;   // bound of the workspace's partial results
+constexpr int kPagedShares = 2048;   // bound of (range, chunk) pairs, each with two partial results
+constexpr size_t kPagedCounterBytes = static_cast<size_t>(kPagedShares) * kConsumerWarps * 4;
+constexpr int kMinUnits = 4;         // units per range at least
+constexpr float kNoKey = -1e30f;     // running maximum of a column that has seen no key (finite: no NaN arises)
+
+template <int D, bool KV8, int NT>
+struct PagedShape {
+    static constexpr int kKeys = KV8 ? 128 : 64;                    // keys per stage
+    static constexpr int kBoxes = kKeys / kConsumerWarps / 16;      // 16-key boxes per consumer warp
+    static constexpr int kRowBytes = KV8 ? D : 2 * D;
+    static constexpr int kSliceRow = kRowBytes < 128 ? kRowBytes : 128;   // bytes per row of a TMA box
+    static constexpr int kSlices = kRowBytes / kSliceRow;
+    static constexpr int kSliceBytes = kKeys * kSliceRow;
+    static constexpr int kTileBytes = kSlices * kSliceBytes;
+    static constexpr int kStageBytes = 2 * kTileBytes;
+    static constexpr int kRingBytes = kStages * kStageBytes;
+    static constexpr int kCols = 8 * NT;
+    // the merge of the four warps, in a ring stage: [warp][8][D + 4] accumulators, then [warp][8]
+    // maxima, maxima of the weights, and sums
+    static constexpr int kMergeRow = D + 4;
+    static constexpr int kMergeFloats = kConsumerWarps * 8 * kMergeRow;
+    static_assert((kMergeFloats + 3 * kConsumerWarps * 8) * 4 <= kStageBytes, "item merge must fit in one ring stage");
+    static constexpr int kQBytes = kCols * D * 2;
+    static constexpr int kQOff = kRingBytes;
+    static constexpr int kSlotOff = kQOff + kItemSlots * kQBytes;
+    static constexpr int kSlotBytes = 64;
+    static constexpr int kScaleOff = kSlotOff + kItemSlots * kSlotBytes;   // [stage][box] {ks, log2 vs}
+    static constexpr int kScaleBytes = KV8 ? kStages * (kKeys / 16) * 8 : 0;
+    static constexpr int kBarOff = kScaleOff + kScaleBytes;
+    static constexpr int kNumBars = 2 * kStages + 2 * kItemSlots + 2;
+    static constexpr int kSeqOff = kBarOff + kNumBars * 8;                 // prefix[B + 1], then pad[B]
+    static constexpr int smem_bytes(int B) { return 1024 + kSeqOff + (4 * (B + 1) + B + 15) / 16 * 16; }
+};
 
 struct PagedParams {
     const uint16_t* q;
-    const uint8_t* k;
-    const uint8_t* v;
     const float* ks;
     const float* vs;
     const int32_t* lens;
     const int32_t* table;
     uint16_t* out;
-    float* lse;
+    float* lse;              // or nullptr
     uint32_t* err;
-    int B, tq, Hq, Hkv, P, max_pages, table_stride, num_pages, layout;
+    uint32_t* work;          // work-queue head
+    uint32_t* arrived;       // [share][consumer warp] partials written, at the share that begins a (sequence, head)
+    float* part_lse;         // [2 * share][columns], log2
+    float* part;             // [2 * share][columns][D]
+    int B, tq, Hq, Hkv, G, P, max_pages, table_stride, num_pages, layout, chunks;
+    int box_keys;            // keys of a full TMA box: gcd(page size, stage keys)
     float scale_log2;
+    unsigned long long wait_limit_ns;
 };
 
-template <int DT, bool KV8>
-__device__ __forceinline__ float element(const uint8_t* base, int64_t i) {
-    if constexpr (KV8) {
-        uint32_t h2;
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(base[i])));
-        return bits_to_f32<DA_F16>(h2 & 0xffffu);
+struct PagedItem {           // one piece of a (sequence, KV head): what a range holds of it
+    int32_t valid, b, kvh, c0, nh;
+    int32_t key0, nkeys, ntiles;
+    int32_t vis0;            // keys of the piece that query token 0 may see (may be <= 0)
+    int32_t part;            // partial result to write, or -1: the piece is the whole
+    int32_t first_share;     // share that holds the (sequence, head)'s first key
+    int32_t nparts;
+};
+static_assert(sizeof(PagedItem) <= 64, "PagedItem fits its slot");
+
+// The cut of `units` into ranges (see above).
+struct Ranges {
+    int64_t units;
+    int n;
+    __device__ __forceinline__ Ranges(int64_t u, int slots) : units(u) {
+        const int64_t most = (u + kMinUnits - 1) / kMinUnits;
+        n = static_cast<int>(most < slots ? most : slots);
+    }
+    __device__ __forceinline__ int64_t begin(int r) const { return units * r / n; }
+    // the range that holds unit x: the last r with units * r / n <= x
+    __device__ __forceinline__ int of(int64_t x) const { return static_cast<int>(((x + 1) * n - 1) / units); }
+};
+
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+// Two e4m3 values to two fp16 values (exact).
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t x, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(x));
+}
+
+template <int D, int DT, bool KV8, int NT>
+struct PagedKernel {
+    using Sh = PagedShape<D, KV8, NT>;
+
+    struct Layout {
+        uint8_t* smem;
+        PagedItem* slots;
+        float2* scales;
+        int32_t* prefix;
+        uint8_t* pad;
+        uint32_t ring, qbuf, full0, empty0, ifull0, iempty0, mfull, mdone;
+    };
+
+    static __device__ __forceinline__ Layout layout(uint8_t* raw, const PagedParams& p) {
+        Layout s;
+        s.smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+        s.slots = reinterpret_cast<PagedItem*>(s.smem + Sh::kSlotOff);
+        s.scales = reinterpret_cast<float2*>(s.smem + Sh::kScaleOff);
+        s.prefix = reinterpret_cast<int32_t*>(s.smem + Sh::kSeqOff);
+        s.pad = reinterpret_cast<uint8_t*>(s.prefix + p.B + 1);
+        s.ring = smem_addr(s.smem);
+        s.qbuf = s.ring + Sh::kQOff;
+        s.full0 = s.ring + Sh::kBarOff;
+        s.empty0 = s.full0 + 8 * kStages;
+        s.ifull0 = s.empty0 + 8 * kStages;
+        s.iempty0 = s.ifull0 + 8 * kItemSlots;
+        s.mfull = s.iempty0 + 8 * kItemSlots;
+        s.mdone = s.mfull + 8;
+        return s;
+    }
+
+    static __device__ __forceinline__ PagedItem* slot_of(const Layout& s, int i) {
+        return reinterpret_cast<PagedItem*>(reinterpret_cast<uint8_t*>(s.slots) + i * Sh::kSlotBytes);
+    }
+
+    // Stages per sequence and their running sum, by the whole CTA.
+    static __device__ __forceinline__ void count_units(const Layout& s, const PagedParams& p) {
+        __shared__ int32_t warp_sum[kThreads / 32];
+        const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+        const int per = (p.B + kThreads - 1) / kThreads;
+        const int64_t most = static_cast<int64_t>(p.max_pages) * p.P;
+        int mine = 0;
+        for (int i = 0; i < per; ++i) {
+            const int b = tid * per + i;
+            if (b >= p.B) break;
+            int L = ld_cg_s32(p.lens + b);
+            if (L < 0 || L > most) {
+                if (blockIdx.x == 0) flag_error(p.err, DA_DEVERR_SEQLENS);
+                L = 0;
+            }
+            const int n = L == 0 ? 1 : (L + Sh::kKeys - 1) / Sh::kKeys;   // an empty sequence: one empty stage
+            s.pad[b] = static_cast<uint8_t>(n * Sh::kKeys - L);
+            s.prefix[b + 1] = n;
+            mine += n;
+        }
+        int run = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, run, off);
+            if (lane >= off) run += y;
+        }
+        if (lane == 31) warp_sum[warp] = run;
+        __syncthreads();
+        int sum = run - mine;
+        for (int w = 0; w < warp; ++w) sum += warp_sum[w];
+        for (int i = 0; i < per; ++i) {
+            const int b = tid * per + i;
+            if (b >= p.B) break;
+            sum += s.prefix[b + 1];
+            s.prefix[b + 1] = sum;
+        }
+        if (tid == 0) s.prefix[0] = 0;
+        __syncthreads();
+    }
+
+    // ------------------------------------------------------------ producer
+    struct Box {        // what a lane knows of its box: one page and head
+        int page;
+        float ks, lvs;
+    };
+
+    static __device__ __forceinline__ Box load_box(const PagedParams& p, const PagedItem& it, int box) {
+        Box x;
+        x.page = 0;
+        x.ks = 0.f;
+        x.lvs = -INFINITY;
+        const int key = box * p.box_keys;
+        if (static_cast<uint32_t>(key) < static_cast<uint32_t>(it.nkeys)) {   // (a product past 2^31 is none)
+            const int page = ld_cg_s32(p.table + static_cast<int64_t>(it.b) * p.table_stride + (it.key0 + key) / p.P);
+            const bool good = page >= 0 && page < p.num_pages;
+            // a bad page: a coordinate past the cache, which the copy fills with zeros
+            x.page = good ? page : p.num_pages;
+            if (!good) flag_error(p.err, DA_DEVERR_PAGE);
+            if constexpr (KV8) {
+                if (good) {
+                    const int64_t at = static_cast<int64_t>(page) * p.Hkv + it.kvh;
+                    x.ks = __ldcg(p.ks + at);
+                    x.lvs = fast_log2(__ldcg(p.vs + at));
+                }
+            }
+        }
+        return x;
+    }
+
+    static __device__ __forceinline__ void copy_box(const PagedParams& p, uint32_t dst, const CUtensorMap* map, int page,
+                                                    int slot, int kvh, uint32_t bar) {
+        constexpr int kInner = Sh::kSliceRow / (KV8 ? 1 : 2);
+#pragma unroll
+        for (int hf = 0; hf < Sh::kSlices; ++hf) {
+            if (p.layout == DA_LAYOUT_VARLEN)
+                tma_load_3d(dst + hf * Sh::kSliceBytes, map, hf * kInner, kvh, page * p.P + slot, bar);
+            else
+                tma_load_3d(dst + hf * Sh::kSliceBytes, map, hf * kInner, slot, page * p.Hkv + kvh, bar);
+        }
+    }
+
+    static __device__ void producer(const Layout& s, const PagedParams& p, const CUtensorMap* tmK, const CUtensorMap* tmV,
+                                    const CUtensorMap* tmK16, const CUtensorMap* tmV16) {
+        const int lane = threadIdx.x & 31;
+        const int64_t units = static_cast<int64_t>(s.prefix[p.B]) * p.Hkv;
+        const Ranges ranges(units, max(1, min(static_cast<int>(gridDim.x), kPagedShares) / p.chunks));
+        const int shares = ranges.n * p.chunks;
+        const bool queued = shares > static_cast<int>(gridDim.x);
+
+        // cursor: the units left of this CTA's share, and where the first of them lies
+        int share = static_cast<int>(blockIdx.x), range = 0, chunk = 0;
+        int64_t u = 0, end = 0;
+        int b = 0, kvh = 0, stage = 0;
+        auto open_share = [&]() -> bool {
+            if (share >= shares) return false;
+            range = share / p.chunks;
+            chunk = share - range * p.chunks;
+            u = ranges.begin(range);
+            end = ranges.begin(range + 1);
+            int lo = 0, hi = p.B - 1;   // last b with Hkv * prefix[b] <= u
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (static_cast<int64_t>(s.prefix[mid]) * p.Hkv <= u) lo = mid;
+                else hi = mid - 1;
+            }
+            b = lo;
+            const int n = s.prefix[b + 1] - s.prefix[b];
+            const int r = static_cast<int>(u - static_cast<int64_t>(s.prefix[b]) * p.Hkv);
+            kvh = r / n;
+            stage = r - kvh * n;
+            return true;
+        };
+        // the next piece: valid 0 when this CTA has none left
+        auto next_piece = [&](PagedItem& it, int taken) {
+            it.valid = 0;
+            if (u == end) {
+                share = taken;
+                if (!open_share()) return;
+            }
+            const int n = s.prefix[b + 1] - s.prefix[b];
+            const int L = n * Sh::kKeys - s.pad[b];
+            const int last = static_cast<int>(min(static_cast<int64_t>(n), stage + (end - u)));
+            it.valid = 1;
+            it.b = b;
+            it.kvh = kvh;
+            it.c0 = chunk * Sh::kCols;
+            it.nh = min(Sh::kCols, p.G * p.tq - it.c0);
+            it.key0 = stage * Sh::kKeys;
+            it.nkeys = min(L, last * Sh::kKeys) - it.key0;
+            it.ntiles = (it.nkeys + Sh::kKeys - 1) / Sh::kKeys;
+            it.vis0 = L - p.tq + 1 - it.key0;
+            it.part = -1;
+            it.first_share = it.nparts = 0;
+            if (stage > 0 || last < n) {
+                const int64_t u0 = static_cast<int64_t>(s.prefix[b]) * p.Hkv + static_cast<int64_t>(kvh) * n;
+                const int ra = ranges.of(u0);
+                it.first_share = ra * p.chunks + chunk;
+                it.nparts = ranges.of(u0 + n - 1) - ra + 1;
+                it.part = 2 * share + (stage == 0 ? 1 : 0);
+            }
+            u += last - stage;
+            stage = last;
+            if (stage == n) {
+                stage = 0;
+                if (++kvh == p.Hkv) {
+                    kvh = 0;
+                    ++b;
+                }
+            }
+        };
+        auto publish = [&](uint32_t i, const PagedItem& it) -> bool {
+            const int slot = i % kItemSlots;
+            if (!mbar_wait_warp(s.iempty0 + 8 * slot, ((i / kItemSlots) & 1) ^ 1, p.wait_limit_ns)) {
+                if (lane == 0) flag_error(p.err, DA_DEVERR_TIMEOUT);
+                return false;
+            }
+            const uint32_t bar = s.ifull0 + 8 * slot;
+            if (lane == 0) {
+                *slot_of(s, slot) = it;
+                if (it.valid) mbar_arrive_expect_tx(bar, it.nh * D * 2);
+                else mbar_arrive(bar);
+            }
+            __syncwarp();
+            if (it.valid) {
+                const uint32_t dst = s.qbuf + slot * Sh::kQBytes;
+                const int64_t row = static_cast<int64_t>(it.b) * p.tq * p.Hq + it.kvh * p.G;
+                if (p.tq == 1) {
+                    if (lane == 0) bulk_load(dst, p.q + (row + it.c0) * D, it.nh * D * 2, bar);
+                } else if (lane < it.nh) {
+                    const int c = it.c0 + lane;
+                    bulk_load(dst + lane * D * 2, p.q + (row + static_cast<int64_t>(c / p.G) * p.Hq + c % p.G) * D, D * 2, bar);
+                }
+            }
+            return true;
+        };
+
+        PagedItem item;
+        int st = 0;
+        uint32_t ph = 0;
+        next_piece(item, share);       // u == end == 0: opens the first share
+        if (!publish(0, item) || !item.valid) return;
+        Box cur = load_box(p, item, lane), nxt;
+        const int per_stage = Sh::kKeys / p.box_keys;
+        for (uint32_t i = 0; item.valid; ++i) {
+            int taken = shares;
+            const int fetch_at = max(0, item.ntiles - kStages);
+            nxt = load_box(p, item, 32 + lane);
+            bool ok = true;
+            for (int t = 0; t <= item.ntiles; ++t) {
+                // take the next share from the queue a few stages before this one's end. A call
+                // takes exactly `shares` numbers (one per share), and the last take resets the
+                // counter for the next call on this workspace.
+                if (t == fetch_at && queued && u == end) {
+                    uint32_t raw = 0;
+                    if (lane == 0) {
+                        raw = atomicAdd(p.work, 1u);
+                        if (raw + 1u == static_cast<uint32_t>(shares)) atomicExch(p.work, 0u);
+                    }
+                    taken = static_cast<int>(gridDim.x + __shfl_sync(0xffffffffu, raw, 0));
+                }
+                if (t == item.ntiles) break;
+                const int box0 = t * per_stage;
+                if (t > 0 && box0 % 32 == 0) {
+                    cur = nxt;
+                    nxt = load_box(p, item, box0 + 32 + lane);
+                }
+                if (!mbar_wait_warp(s.empty0 + 8 * st, ph ^ 1, p.wait_limit_ns)) {
+                    if (lane == 0) flag_error(p.err, DA_DEVERR_TIMEOUT);
+                    ok = false;
+                    break;
+                }
+                const int keys = min(Sh::kKeys, item.nkeys - t * Sh::kKeys);
+                const uint32_t fb = s.full0 + 8 * st;
+                const uint32_t kdst = s.ring + st * Sh::kStageBytes;
+                const uint32_t vdst = kdst + Sh::kTileBytes;
+                const int key = item.key0 + t * Sh::kKeys;
+                const int nbox16 = (keys + 15) / 16;
+                if (lane == 0)
+                    mbar_expect_tx(fb, 2 * (keys == Sh::kKeys ? Sh::kTileBytes : nbox16 * 16 * Sh::kRowBytes));
+                __syncwarp();
+                const int in32 = box0 % 32;
+                if (keys == Sh::kKeys) {
+                    // a full stage: the lanes that hold its boxes copy them
+                    const int i0 = lane - in32;
+                    if (i0 >= 0 && i0 < per_stage) {
+                        const int off = i0 * p.box_keys;
+                        const int slot = (key + off) % p.P;
+                        copy_box(p, kdst + off * Sh::kSliceRow, tmK, cur.page, slot, item.kvh, fb);
+                        copy_box(p, vdst + off * Sh::kSliceRow, tmV, cur.page, slot, item.kvh, fb);
+                    }
+                } else {
+                    // the ragged end of a sequence: 16-key boxes up to it
+                    const int page = __shfl_sync(0xffffffffu, cur.page, (in32 + lane * 16 / p.box_keys) & 31);
+                    if (lane < nbox16) {
+                        const int slot = (key + lane * 16) % p.P;
+                        copy_box(p, kdst + lane * 16 * Sh::kSliceRow, tmK16, page, slot, item.kvh, fb);
+                        copy_box(p, vdst + lane * 16 * Sh::kSliceRow, tmV16, page, slot, item.kvh, fb);
+                    }
+                }
+                if constexpr (KV8) {
+                    // the scales of the stage's 16-key boxes
+                    const int from = (in32 + lane * 16 / p.box_keys) & 31;
+                    const float ks = __shfl_sync(0xffffffffu, cur.ks, from);
+                    const float lvs = __shfl_sync(0xffffffffu, cur.lvs, from);
+                    if (lane < Sh::kKeys / 16) s.scales[st * (Sh::kKeys / 16) + lane] = make_float2(ks, lvs);
+                    __syncwarp();
+                }
+                if (lane == 0) mbar_arrive(fb);
+                if (++st == kStages) {
+                    st = 0;
+                    ph ^= 1;
+                }
+            }
+            if (!ok) return;
+            // the next piece's descriptor, queries and table entries go out before this one's merge
+            PagedItem next;
+            next_piece(next, taken);
+            if (!publish(i + 1, next)) return;
+            if (next.valid) cur = load_box(p, next, lane);
+            // hand the consumers the next stage, empty, for this piece's merge
+            if (!mbar_wait_warp(s.empty0 + 8 * st, ph ^ 1, p.wait_limit_ns)) {
+                if (lane == 0) flag_error(p.err, DA_DEVERR_TIMEOUT);
+                return;
+            }
+            if (lane == 0) mbar_arrive(s.full0 + 8 * st);
+            if (++st == kStages) {
+                st = 0;
+                ph ^= 1;
+            }
+            item = next;
+        }
+    }
+
+    // ------------------------------------------------------------ consumers
+    static __device__ __forceinline__ uint32_t chunk_addr(uint32_t tile, int row, int chunk) {
+        constexpr int kChunks = Sh::kSliceRow / 16;
+        const int x = kChunks == 8 ? row & 7 : (row >> 1) & 3;   // the copy's 128- or 64-byte swizzle
+        return tile + (chunk / kChunks) * Sh::kSliceBytes + row * Sh::kSliceRow + (((chunk % kChunks) ^ x) << 4);
+    }
+
+    // Query fragments (B operand, k16 x n8) of n-tile n, and the factor that takes a product to
+    // the exp2 domain for this thread's two columns.
+    static __device__ __forceinline__ void load_queries(const PagedParams& p, uint32_t qrows, int nh,
+                                                        uint32_t (&qf)[D / 16][NT][2], float (&qs)[NT][2]) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const bool live = 8 * n + g < nh;
+            const uint32_t row = qrows + (live ? 8 * n + g : 0) * D * 2;
+            qs[n][0] = qs[n][1] = p.scale_log2;
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+                uint32_t a0, a1;
+                if constexpr (KV8) {
+                    // dims 16 ks + 4 t4 .. + 3: where an e4m3 row's ldmatrix puts a lane's four bytes
+                    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(a0), "=r"(a1) : "r"(row + (ks * 16 + 4 * t4) * 2));
+                } else {
+                    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(a0) : "r"(row + (ks * 16 + 2 * t4) * 2));
+                    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(a1) : "r"(row + (ks * 16 + 8 + 2 * t4) * 2));
+                }
+                qf[ks][n][0] = live ? a0 : 0u;
+                qf[ks][n][1] = live ? a1 : 0u;
+            }
+            if constexpr (KV8 && DT == DA_BF16) {
+                uint32_t top = 0;   // largest exponent field of the column
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        top = max(top, max((qf[ks][n][j] >> 7) & 0xffu, (qf[ks][n][j] >> 23) & 0xffu));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                // 2^e takes the largest element to [2^14, 2^15); an infinity or a NaN stays one
+                const int field = top == 255 ? 127 : min(max(268 - static_cast<int>(top), 14), 240);
+                const float up = __uint_as_float(static_cast<uint32_t>(field) << 23);
+                const float down = __uint_as_float(static_cast<uint32_t>(254 - field) << 23);
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        qf[ks][n][j] = pack2<DA_F16>(__uint_as_float(qf[ks][n][j] << 16) * up,
+                                                     __uint_as_float(qf[ks][n][j] & 0xffff0000u) * up);
+                qs[n][0] *= __shfl_sync(0xffffffffu, down, 8 * t4);       // column 2 t4 is row g = 2 t4 of the operand
+                qs[n][1] *= __shfl_sync(0xffffffffu, down, 8 * t4 + 4);
+            }
+        }
+    }
+
+    // S^T[16 keys, 8 columns per n-tile] of box `row0`.
+    static __device__ __forceinline__ void scores(uint32_t tile, int row0, const uint32_t (&qf)[D / 16][NT][2],
+                                                  float (&x)[NT][4]) {
+        const int lane = threadIdx.x & 31, mi = lane >> 3, r8 = lane & 7;
+        const int row = row0 + (mi & 1) * 8 + r8;
+        if constexpr (KV8) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) x[n][0] = x[n][1] = x[n][2] = x[n][3] = 0.f;
+#pragma unroll
+            for (int kk = 0; kk < D / 32; ++kk) {
+                uint32_t w[4];   // rows lo / hi of 16 dims, then of the next 16
+                ldsm_x4(chunk_addr(tile, row, 2 * kk + (mi >> 1)), w);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t a[4];
+                    e4m3x4_to_f16(w[2 * h], a[0], a[2]);
+                    e4m3x4_to_f16(w[2 * h + 1], a[1], a[3]);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) mma_16816<DA_F16>(x[n], a, qf[2 * kk + h][n][0], qf[2 * kk + h][n][1]);
+                }
+            }
+        } else {
+            float y[NT][4];   // two independent chains
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[n][j] = y[n][j] = 0.f;
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+                uint32_t a[4];
+                ldsm_x4(chunk_addr(tile, row, 2 * ks + (mi >> 1)), a);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    if (ks & 1) mma_16816<DT>(y[n], a, qf[ks][n][0], qf[ks][n][1]);
+                    else mma_16816<DT>(x[n], a, qf[ks][n][0], qf[ks][n][1]);
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[n][j] += y[n][j];
+        }
+    }
+
+    // O^T[D, 8 columns per n-tile] += V^T P^T of box `row0`; in 8-bit tiles rows g and g + 8 of
+    // step i are dims 16 i + 2 g and 16 i + 2 g + 1, in 16-bit tiles 16 i + g and 16 i + g + 8.
+    static __device__ __forceinline__ void weigh(uint32_t tile, int row0, const uint32_t (&pb)[NT][2],
+                                                 float (&acc)[D / 16][NT][4]) {
+        const int lane = threadIdx.x & 31, mi = lane >> 3, r8 = lane & 7;
+        if constexpr (KV8) {
+            const int row = row0 + (mi & 1) * 8 + r8;
+#pragma unroll
+            for (int ii = 0; ii < D / 32; ++ii) {
+                uint32_t w[4];   // keys lo / hi of 16 dims, then of the next 16: two keys x two dims each
+                ldsm_x4_trans(chunk_addr(tile, row, 2 * ii + (mi >> 1)), w);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t a[4];
+                    e4m3x4_to_f16(__byte_perm(w[2 * h], 0, 0x3120), a[0], a[1]);
+                    e4m3x4_to_f16(__byte_perm(w[2 * h + 1], 0, 0x3120), a[2], a[3]);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) mma_16816<DA_F16>(acc[2 * ii + h][n], a, pb[n][0], pb[n][1]);
+                }
+            }
+        } else {
+            const int row = row0 + (mi >> 1) * 8 + r8;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                uint32_t a[4];
+                ldsm_x4_trans(chunk_addr(tile, row, 2 * i + (mi & 1)), a);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma_16816<DT>(acc[i][n], a, pb[n][0], pb[n][1]);
+            }
+        }
+    }
+
+    static __device__ __forceinline__ int64_t output_row(const PagedParams& p, const PagedItem& it, int col) {
+        const int c = it.c0 + col;
+        return (static_cast<int64_t>(it.b) * p.tq + c / p.G) * p.Hq + it.kvh * p.G + c % p.G;
+    }
+
+    // One finished column: four dims of its output, and its lse (log2).
+    static __device__ __forceinline__ void store_output(const PagedParams& p, int64_t row, int d0, const float4& o,
+                                                        float lse2) {
+        *reinterpret_cast<uint2*>(p.out + row * D + d0) = make_uint2(pack2<DT>(o.x, o.y), pack2<DT>(o.z, o.w));
+        if (p.lse != nullptr && d0 == 0) p.lse[row] = lse2 * kLn2;
+    }
+
+    // Columns 8n .. 8n + 7 of a piece from the four warps' states: warp w writes columns w and w + 4.
+    static __device__ __forceinline__ void write_piece(const PagedParams& p, const PagedItem& it, const float* red_acc, int n) {
+        const float* red_m = red_acc + Sh::kMergeFloats;
+        const float* red_mv = red_m + kConsumerWarps * 8;
+        const float* red_l = red_mv + kConsumerWarps * 8;
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        constexpr int kLanes = D / 4, kHeads = 32 / kLanes;
+        const int d0 = (lane % kLanes) * 4;
+#pragma unroll
+        for (int pass = 0; pass < 2 / kHeads; ++pass) {
+            const int hh = warp + kConsumerWarps * (pass * kHeads + lane / kLanes);
+            float M = kNoKey, Mv = kNoKey;
+#pragma unroll
+            for (int w = 0; w < kConsumerWarps; ++w) {
+                M = fmaxf(M, red_m[w * 8 + hh]);
+                Mv = fmaxf(Mv, red_mv[w * 8 + hh]);
+            }
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            float l = 0.f;
+#pragma unroll
+            for (int w = 0; w < kConsumerWarps; ++w) {
+                l = fmaf(fast_exp2(red_m[w * 8 + hh] - M), red_l[w * 8 + hh], l);
+                const float wt = fast_exp2(red_mv[w * 8 + hh] - Mv);
+                const float4 a = *reinterpret_cast<const float4*>(red_acc + (w * 8 + hh) * Sh::kMergeRow + d0);
+                o.x = fmaf(wt, a.x, o.x);
+                o.y = fmaf(wt, a.y, o.y);
+                o.z = fmaf(wt, a.z, o.z);
+                o.w = fmaf(wt, a.w, o.w);
+            }
+            const bool none = M == kNoKey;   // the column saw no key: output 0, lse -inf
+            // l >= 1 otherwise (the key that set M weighs 1). In 8-bit pages o is relative to Mv, l to M.
+            float inv = none ? 0.f : 1.f / l;
+            if constexpr (KV8) inv *= Mv == kNoKey ? 0.f : fast_exp2(Mv - M);
+            o.x *= inv;
+            o.y *= inv;
+            o.z *= inv;
+            o.w *= inv;
+            const float lse2 = none ? -INFINITY : M + log2f(l);
+            const int col = 8 * n + hh;
+            if (col < it.nh) {
+                if (it.part < 0) {
+                    store_output(p, output_row(p, it, col), d0, o, lse2);
+                } else {
+                    const int64_t at = static_cast<int64_t>(it.part) * Sh::kCols + col;
+                    *reinterpret_cast<float4*>(p.part + at * D + d0) = o;
+                    if (d0 == 0) p.part_lse[at] = lse2;
+                }
+            }
+        }
+    }
+
+    // Merge this warp's columns of a (sequence, head) whose partials are all written.
+    static __device__ __forceinline__ void merge_parts(const PagedParams& p, const PagedItem& it) {
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        constexpr int kLanes = D / 4, kHeads = 32 / kLanes;
+        const int d0 = (lane % kLanes) * 4;
+        for (int c = warp + kConsumerWarps * (lane / kLanes); c < Sh::kCols; c += kConsumerWarps * kHeads) {
+            if (c >= it.nh) break;
+            float m = -INFINITY, z = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            constexpr int kAhead = 8;
+            for (int j0 = 0; j0 < it.nparts; j0 += kAhead) {
+                float lv[kAhead];
+                float4 ov[kAhead];
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    const int j = j0 + i;
+                    lv[i] = -INFINITY;
+                    ov[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (j < it.nparts) {
+                        const int64_t part = j == 0 ? 2 * it.first_share + 1 : 2 * (it.first_share + j * p.chunks);
+                        lv[i] = __ldcg(p.part_lse + part * Sh::kCols + c);
+                        ov[i] = __ldcg(reinterpret_cast<const float4*>(p.part + (part * Sh::kCols + c) * D + d0));
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    if (lv[i] == -INFINITY) continue;
+                    const float mn = fmaxf(m, lv[i]);
+                    const float a = fast_exp2(m - mn), w = fast_exp2(lv[i] - mn);
+                    m = mn;
+                    z = fmaf(z, a, w);
+                    acc.x = fmaf(acc.x, a, w * ov[i].x);
+                    acc.y = fmaf(acc.y, a, w * ov[i].y);
+                    acc.z = fmaf(acc.z, a, w * ov[i].z);
+                    acc.w = fmaf(acc.w, a, w * ov[i].w);
+                }
+            }
+            const float inv = m == -INFINITY ? 0.f : 1.f / z;
+            store_output(p, output_row(p, it, c), d0, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv),
+                         m == -INFINITY ? -INFINITY : m + log2f(z));
+        }
+    }
+
+    static __device__ void consumer(const Layout& s, const PagedParams& p) {
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+        constexpr int kRows = 16 * Sh::kBoxes;   // keys of a stage that are this warp's
+        bool ok = true;
+        uint32_t bad_bar = 0, bad_ph = 0;
+        int st = 0;
+        uint32_t ph = 0, mz = 0, md = 0;
+        for (uint32_t i = 0;; ++i) {
+            const int slot = i % kItemSlots;
+            if (!mbar_wait_warp(s.ifull0 + 8 * slot, (i / kItemSlots) & 1, p.wait_limit_ns)) {
+                if (lane == 0) flag_error(p.err, DA_DEVERR_TIMEOUT);
+                ok = false;
+                break;
+            }
+            const PagedItem item = *slot_of(s, slot);
+            uint32_t qf[D / 16][NT][2];
+            float qs[NT][2];
+            if (item.valid) load_queries(p, s.qbuf + slot * Sh::kQBytes, item.nh, qf, qs);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(s.iempty0 + 8 * slot);
+            if (!item.valid) break;
+
+            int vis[NT][2];   // keys of the piece that this thread's columns may see
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    vis[n][c] = item.nkeys;
+                    if (p.tq > 1) vis[n][c] = min(item.nkeys, item.vis0 + (item.c0 + 8 * n + 2 * t4 + c) / p.G);
+                }
+            float acc[D / 16][NT][4];
+#pragma unroll
+            for (int a = 0; a < D / 16; ++a)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) acc[a][n][0] = acc[a][n][1] = acc[a][n][2] = acc[a][n][3] = 0.f;
+            // running maximum of the scores and (8-bit) of the weights, this thread's share of the sum
+            float m[NT][2], mv[NT][2], l[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    m[n][c] = mv[n][c] = kNoKey;
+                    l[n][c] = 0.f;
+                }
+
+            for (int t = 0; t < item.ntiles; ++t) {
+                const uint32_t fb = s.full0 + 8 * st;
+                if (ok && !mbar_wait_warp(fb, ph, p.wait_limit_ns)) {
+                    ok = false;
+                    bad_bar = fb;
+                    bad_ph = ph;
+                    if (lane == 0) flag_error(p.err, DA_DEVERR_TIMEOUT);
+                }
+                const int keys = min(Sh::kKeys, item.nkeys - t * Sh::kKeys);
+                const int valid = keys - warp * kRows;
+                bool zeroed = false;
+                if (ok && valid > 0) {
+                    const uint32_t ktile = s.ring + st * Sh::kStageBytes;
+                    const uint32_t vtile = ktile + Sh::kTileBytes;
+                    if (valid < kRows) {
+                        // rows past the end hold anything: their weight is 0, but 0 * NaN is not
+                        constexpr int kPerRow = Sh::kRowBytes / 16;
+                        for (int c = lane; c < (kRows - valid) * kPerRow; c += 32)
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                             chunk_addr(vtile, warp * kRows + valid + c / kPerRow, c % kPerRow)),
+                                         "r"(0u)
+                                         : "memory");
+                        zeroed = true;
+                        __syncwarp();
+                    }
+                    float x[Sh::kBoxes][NT][4], lv[Sh::kBoxes];
+                    bool move = false;
+#pragma unroll
+                    for (int bx = 0; bx < Sh::kBoxes; ++bx) {
+                        scores(ktile, warp * kRows + bx * 16, qf, x[bx]);
+                        float ks = 1.f;
+                        lv[bx] = 0.f;
+                        if constexpr (KV8) {
+                            const float2 f = s.scales[st * (Sh::kKeys / 16) + warp * Sh::kBoxes + bx];
+                            ks = f.x;
+                            lv[bx] = f.y;
+                        }
+                        const int key = t * Sh::kKeys + warp * kRows + bx * 16 + g;
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const float f = KV8 ? qs[n][j & 1] * ks : qs[n][j & 1];
+                                const bool seen = key + 8 * (j >> 1) < vis[n][j & 1];
+                                x[bx][n][j] = seen ? x[bx][n][j] * f : -INFINITY;
+                                move = move || x[bx][n][j] > m[n][j & 1] + kLazyRescale;
+                                if constexpr (KV8) move = move || x[bx][n][j] + lv[bx] > mv[n][j & 1] + kLazyRescale;
+                            }
+                    }
+                    // The reference of a column moves only when a score passes it by more than
+                    // kLazyRescale, so the shuffles and the rescale run on a few stages per piece; the
+                    // weights stay below 2^8.
+                    if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                float top = m[n][c], topv = mv[n][c];
+#pragma unroll
+                                for (int bx = 0; bx < Sh::kBoxes; ++bx) {
+                                    const float y = fmaxf(x[bx][n][c], x[bx][n][c + 2]);
+                                    top = fmaxf(top, y);
+                                    topv = fmaxf(topv, y + lv[bx]);
+                                }
+#pragma unroll
+                                for (int off = 4; off < 32; off <<= 1) {
+                                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+                                    if constexpr (KV8) topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, off));
+                                }
+                                const float al = fast_exp2(m[n][c] - top);
+                                const float av = KV8 ? fast_exp2(mv[n][c] - topv) : al;
+                                m[n][c] = top;
+                                mv[n][c] = KV8 ? topv : top;
+                                l[n][c] *= al;
+#pragma unroll
+                                for (int a = 0; a < D / 16; ++a) {
+                                    acc[a][n][c] *= av;
+                                    acc[a][n][c + 2] *= av;
+                                }
+                            }
+                    }
+#pragma unroll
+                    for (int bx = 0; bx < Sh::kBoxes; ++bx) {
+                        uint32_t pb[NT][2];
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            float w[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                w[j] = fast_exp2(x[bx][n][j] - m[n][j & 1]);
+                                l[n][j & 1] += w[j];
+                                if constexpr (KV8) w[j] = fast_exp2(x[bx][n][j] + (lv[bx] - mv[n][j & 1]));
+                            }
+                            // the weights are rounded to the 16-bit type of the product's other operand
+                            pb[n][0] = movmatrix_trans(pack2<KV8 ? DA_F16 : DT>(w[0], w[1]));
+                            pb[n][1] = movmatrix_trans(pack2<KV8 ? DA_F16 : DT>(w[2], w[3]));
+                        }
+                        weigh(vtile, warp * kRows + bx * 16, pb, acc);
+                    }
+                }
+                // order the generic-proxy stores above before the copy that refills the stage
+                if (zeroed) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(s.empty0 + 8 * st);
+                if (++st == kStages) {
+                    st = 0;
+                    ph ^= 1;
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int off = 4; off < 32; off <<= 1) l[n][c] += __shfl_xor_sync(0xffffffffu, l[n][c], off);
+
+            // ---- merge the four warps in the stage that the producer handed over, 8 columns a round
+            if (ok && !mbar_wait_warp(s.full0 + 8 * st, ph, p.wait_limit_ns)) {
+                ok = false;
+                if (lane == 0) flag_error(p.err, DA_DEVERR_TIMEOUT);
+            }
+            float* red = reinterpret_cast<float*>(s.smem + st * Sh::kStageBytes);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                if (n > 0) {
+                    // every warp has read the previous round's rows
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(s.mdone);
+                    if (ok && !mbar_wait_warp(s.mdone, md & 1, p.wait_limit_ns)) {
+                        ok = false;
+                        if (lane == 0) flag_error(p.err, DA_DEVERR_TIMEOUT);
+                    }
+                    ++md;
+                }
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int col = warp * 8 + 2 * t4 + c;
+                    if (g == 0) {
+                        red[Sh::kMergeFloats + col] = m[n][c];
+                        red[Sh::kMergeFloats + kConsumerWarps * 8 + col] = mv[n][c];
+                        red[Sh::kMergeFloats + 2 * kConsumerWarps * 8 + col] = l[n][c];
+                    }
+                    float* row = red + col * Sh::kMergeRow;
+#pragma unroll
+                    for (int a = 0; a < D / 16; ++a) {
+                        if constexpr (KV8) {
+                            *reinterpret_cast<float2*>(row + a * 16 + 2 * g) = make_float2(acc[a][n][c], acc[a][n][c + 2]);
+                        } else {
+                            row[a * 16 + g] = acc[a][n][c];
+                            row[a * 16 + g + 8] = acc[a][n][c + 2];
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(s.mfull);
+                if (ok && !mbar_wait_warp(s.mfull, mz & 1, p.wait_limit_ns)) {
+                    ok = false;
+                    if (lane == 0) flag_error(p.err, DA_DEVERR_TIMEOUT);
+                }
+                ++mz;
+                if (ok) write_piece(p, item, red, n);
+            }
+            // release the stage: order these generic-proxy stores before the copy that refills it
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(s.empty0 + 8 * st);
+            if (++st == kStages) {
+                st = 0;
+                ph ^= 1;
+            }
+            if (!ok) break;
+            if (item.part >= 0) {
+                // Warp w wrote the same columns of every partial, so the four warps count apart: the
+                // one whose arrival completes the count merges its columns, and sets the count back.
+                uint32_t n = 0;
+                __syncwarp();
+                if (lane == 0) {
+                    uint32_t* count = p.arrived + item.first_share * kConsumerWarps + warp;
+                    __threadfence();
+                    n = atomicAdd(count, 1u) + 1;
+                    if (n == static_cast<uint32_t>(item.nparts)) {
+                        atomicExch(count, 0u);
+                        __threadfence();
+                    }
+                }
+                n = __shfl_sync(0xffffffffu, n, 0);
+                __syncwarp();
+                if (n == static_cast<uint32_t>(item.nparts)) merge_parts(p, item);
+            }
+        }
+        // after a timed-out wait, a copy still in flight into this CTA's shared memory gets one more
+        // bounded wait before the CTA exits
+        if (!ok && bad_bar != 0) mbar_wait(bad_bar, bad_ph, p.wait_limit_ns);
+    }
+};
+
+template <int D, int DT, bool KV8, int NT>
+__global__ void __launch_bounds__(kThreads, kMinBlocksPerSm)
+paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+             const __grid_constant__ CUtensorMap tmK16, const __grid_constant__ CUtensorMap tmV16, const PagedParams p) {
+    using K = PagedKernel<D, DT, KV8, NT>;
+    extern __shared__ uint8_t smem_raw[];
+    const auto s = K::layout(smem_raw, p);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(s.full0 + 8 * i, 1);
+            mbar_init(s.empty0 + 8 * i, kConsumerWarps);
+        }
+        for (int i = 0; i < kItemSlots; ++i) {
+            mbar_init(s.ifull0 + 8 * i, 1);
+            mbar_init(s.iempty0 + 8 * i, kConsumerWarps);
+        }
+        mbar_init(s.mfull, kConsumerWarps);
+        mbar_init(s.mdone, kConsumerWarps);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        prefetch_tensormap(&tmK);
+        prefetch_tensormap(&tmV);
+        prefetch_tensormap(&tmK16);
+        prefetch_tensormap(&tmV16);
+    }
+    // From here on this grid touches global memory: wait for the previous kernel.
+    grid_dependency_wait();
+    if (threadIdx.x == 0) grid_dependents_launch();
+    K::count_units(s, p);   // its barriers also publish the initialised mbarriers
+    if ((threadIdx.x >> 5) == kConsumerWarps) K::producer(s, p, &tmK, &tmV, &tmK16, &tmV16);
+    else K::consumer(s, p);
+}
+
+// ------------------------------------------------------------ host side
+inline int gcd_of(int a, int b) {
+    while (b) {
+        const int r = a % b;
+        a = b;
+        b = r;
+    }
+    return a;
+}
+
+// Tensor map of a cache's keys or values: boxes of `rows` tokens of one head, slices of `inner` elements.
+inline bool make_page_map(CUtensorMap* map, const void* base, const da_paged_cache& c, int inner, int rows) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t size = c.kv_dtype == DA_E4M3 ? 1 : 2;
+    cuuint64_t dims[3], strides[2];
+    cuuint32_t box[3], step[3] = {1, 1, 1};
+    dims[0] = c.D;
+    strides[0] = c.D * size;
+    box[0] = inner;
+    if (c.layout == DA_LAYOUT_VARLEN) {
+        dims[1] = c.Hkv;
+        dims[2] = static_cast<cuuint64_t>(c.num_pages) * c.page_size;
+        strides[1] = static_cast<cuuint64_t>(c.Hkv) * c.D * size;
+        box[1] = 1;
+        box[2] = rows;
     } else {
-        return bits_to_f32<DT>(reinterpret_cast<const uint16_t*>(base)[i]);
+        dims[1] = c.page_size;
+        dims[2] = static_cast<cuuint64_t>(c.num_pages) * c.Hkv;
+        strides[1] = static_cast<cuuint64_t>(c.page_size) * c.D * size;
+        box[1] = rows;
+        box[2] = 1;
     }
+    const CUtensorMapDataType type = c.kv_dtype == DA_E4M3   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                     : c.kv_dtype == DA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                             : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    return fn(map, type, 3, const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              inner * size == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int DT, bool KV8>
-__global__ void __launch_bounds__(128) paged_kernel(const PagedParams p) {
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (row >= static_cast<int64_t>(p.B) * p.tq * p.Hq) return;
-    const int h = static_cast<int>(row % p.Hq), t = static_cast<int>(row / p.Hq % p.tq);
-    const int b = static_cast<int>(row / p.Hq / p.tq), kvh = h / (p.Hq / p.Hkv);
-    int L = p.lens[b];
-    if (L < 0 || L > static_cast<int64_t>(p.max_pages) * p.P) {
-        if (lane == 0) flag_error(p.err, DA_DEVERR_SEQLENS);
-        L = 0;
-    }
-    const int seen = min(L, L - p.tq + t + 1);
-    constexpr int kDims = D / 32;
-    float q[kDims], acc[kDims], m = -INFINITY, l = 0.f;
-    for (int i = 0; i < kDims; ++i) {
-        q[i] = bits_to_f32<DT>(p.q[row * D + i * 32 + lane]);
-        acc[i] = 0.f;
-    }
-    for (int j = 0; j < seen; ++j) {
-        const int page = p.table[static_cast<int64_t>(b) * p.table_stride + j / p.P];
-        const bool good = page >= 0 && page < p.num_pages;
-        if (!good && lane == 0) flag_error(p.err, DA_DEVERR_PAGE);
-        const int64_t at = page_row(p.layout, good ? page : 0, j % p.P, kvh, p.P, p.Hkv) * D;
-        const int64_t sc = static_cast<int64_t>(good ? page : 0) * p.Hkv + kvh;
-        float dot = 0.f;
-        for (int i = 0; i < kDims; ++i) dot += good ? q[i] * element<DT, KV8>(p.k, at + i * 32 + lane) : 0.f;
-        for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
-        const float x = dot * p.scale_log2 * (KV8 ? p.ks[sc] : 1.f);
-        const float mn = fmaxf(m, x);
-        const float w = fast_exp2(x - mn), al = fast_exp2(m - mn);
-        m = mn;
-        l = l * al + w;
-        for (int i = 0; i < kDims; ++i)
-            acc[i] = acc[i] * al + (good ? w * element<DT, KV8>(p.v, at + i * 32 + lane) * (KV8 ? p.vs[sc] : 1.f) : 0.f);
-    }
-    for (int i = 0; i < kDims; ++i) p.out[row * D + i * 32 + lane] = to_bits<DT>(seen > 0 ? acc[i] / l : 0.f);
-    if (p.lse && lane == 0) p.lse[row] = seen > 0 ? (m + log2f(l)) * kLn2 : -INFINITY;
-}
-
-template <int D, int DT, bool KV8>
-da_status launch_paged(const PagedParams& p, cudaStream_t s) {
-    const int64_t rows = static_cast<int64_t>(p.B) * p.tq * p.Hq;
-    paged_kernel<D, DT, KV8><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, s>>>(p);
-    return cudaGetLastError() == cudaSuccess ? DA_OK : DA_ERR_CUDA;
+template <int D, int DT, bool KV8, int NT>
+da_status launch_paged(const da_paged_cache& c, PagedParams& p, cudaStream_t stream) {
+    using Sh = PagedShape<D, KV8, NT>;
+    constexpr int kInner = Sh::kSliceRow / (KV8 ? 1 : 2);
+    p.chunks = (p.G * p.tq + Sh::kCols - 1) / Sh::kCols;
+    p.box_keys = gcd_of(c.page_size, Sh::kKeys);
+    CUtensorMap mk, mv, mk16, mv16;
+    if (!make_page_map(&mk, c.k, c, kInner, p.box_keys) || !make_page_map(&mv, c.v, c, kInner, p.box_keys) ||
+        !make_page_map(&mk16, c.k, c, kInner, 16) || !make_page_map(&mv16, c.v, c, kInner, 16))
+        return DA_ERR_CUDA;
+    // units of the largest batch that the table can describe
+    const int64_t stages = (static_cast<int64_t>(p.max_pages) * p.P + Sh::kKeys - 1) / Sh::kKeys;
+    const int64_t units = static_cast<int64_t>(p.B) * p.Hkv * stages;
+    if (units > 0x7fffffffll || p.chunks > kPagedShares) return DA_ERR_INVALID_ARG;
+    auto kern = paged_kernel<D, DT, KV8, NT>;
+    static DeviceCache cache;
+    int grid = 0;
+    if (persistent_grid(kern, kThreads, Sh::smem_bytes(DA_MAX_PAGED_BATCH), cache, &grid) != cudaSuccess) return DA_ERR_CUDA;
+    grid = static_cast<int>(std::min<int64_t>(std::max(grid, p.chunks), ((units + kMinUnits - 1) / kMinUnits) * p.chunks));
+    cudaLaunchAttribute attrs[1] = {pdl_attr()};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Sh::smem_bytes(p.B);
+    cfg.stream = stream;
+    cfg.attrs = attrs;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, mk, mv, mk16, mv16, p) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
 }
 
 template <int D, int DT>
-da_status launch_paged_kv(const PagedParams& p, bool e4m3, cudaStream_t s) {
-    return e4m3 ? launch_paged<D, DT, true>(p, s) : launch_paged<D, DT, false>(p, s);
+da_status launch_paged_any(const da_paged_cache& c, PagedParams& p, cudaStream_t s) {
+    const bool wide = item_cols(static_cast<int64_t>(p.G) * p.tq) > kHeadsPerCta;
+    if (c.kv_dtype == DA_E4M3) return wide ? launch_paged<D, DT, true, 2>(c, p, s) : launch_paged<D, DT, true, 1>(c, p, s);
+    return wide ? launch_paged<D, DT, false, 2>(c, p, s) : launch_paged<D, DT, false, 1>(c, p, s);
 }
 
 }  // namespace da_impl
@@ -96,11 +1032,11 @@ extern "C" {
 size_t decode_attn_paged_workspace_size(int T_q, int Hq, int Hkv, int D) {
     if (T_q < 1 || T_q > DA_MAX_QUERY_TOKENS || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || (D != 64 && D != 128)) return 0;
     const int cols = item_cols(static_cast<int64_t>(Hq / Hkv) * T_q);
-    return kPagedHeaderBytes + kPagedShares * 16 + static_cast<size_t>(2 * kPagedShares) * cols * (D + 1) * 4;
+    return kPagedHeaderBytes + kPagedCounterBytes + static_cast<size_t>(2 * kPagedShares) * cols * (D + 1) * 4;
 }
 
 da_status decode_attn_paged_workspace_init(void* workspace, size_t workspace_bytes, void* stream) {
-    const size_t head = kPagedHeaderBytes + kPagedShares * 16;
+    const size_t head = kPagedHeaderBytes + kPagedCounterBytes;
     if (!workspace || workspace_bytes < head) return DA_ERR_INVALID_ARG;
     if (!aligned(workspace, 256)) return DA_ERR_ALIGNMENT;
     return cudaMemsetAsync(workspace, 0, head, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
@@ -119,16 +1055,21 @@ da_status decode_attn_paged(const void* q, const da_paged_cache* cache, const in
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 256)) return DA_ERR_ALIGNMENT;
     if (workspace_bytes < decode_attn_paged_workspace_size(T_q, Hq, c.Hkv, c.D)) return DA_ERR_WORKSPACE_TOO_SMALL;
     PagedParams p;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
     p.q = static_cast<const uint16_t*>(q);
-    p.k = static_cast<const uint8_t*>(c.k);
-    p.v = static_cast<const uint8_t*>(c.v);
     p.ks = c.k_scale;
     p.vs = c.v_scale;
     p.lens = kv_lens;
     p.table = block_table;
     p.out = static_cast<uint16_t*>(out);
     p.lse = lse;
-    p.err = static_cast<uint32_t*>(workspace);
+    p.err = reinterpret_cast<uint32_t*>(ws);
+    p.work = reinterpret_cast<uint32_t*>(ws + kWorkCounterOff);
+    p.arrived = reinterpret_cast<uint32_t*>(ws + kPagedHeaderBytes);
+    p.G = Hq / c.Hkv;
+    const int cols = item_cols(static_cast<int64_t>(p.G) * T_q);
+    p.part = reinterpret_cast<float*>(ws + kPagedHeaderBytes + kPagedCounterBytes);
+    p.part_lse = p.part + static_cast<size_t>(2 * kPagedShares) * cols * c.D;
     p.B = B;
     p.tq = T_q;
     p.Hq = Hq;
@@ -139,11 +1080,10 @@ da_status decode_attn_paged(const void* q, const da_paged_cache* cache, const in
     p.num_pages = c.num_pages;
     p.layout = c.layout;
     p.scale_log2 = scale * kLog2e;
+    p.wait_limit_ns = kWaitLimitNs;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const bool e4m3 = c.kv_dtype == DA_E4M3;
-    if (c.D == 128)
-        return dtype == DA_F16 ? launch_paged_kv<128, DA_F16>(p, e4m3, s) : launch_paged_kv<128, DA_BF16>(p, e4m3, s);
-    return dtype == DA_F16 ? launch_paged_kv<64, DA_F16>(p, e4m3, s) : launch_paged_kv<64, DA_BF16>(p, e4m3, s);
+    if (c.D == 128) return dtype == DA_F16 ? launch_paged_any<128, DA_F16>(c, p, s) : launch_paged_any<128, DA_BF16>(c, p, s);
+    return dtype == DA_F16 ? launch_paged_any<64, DA_F16>(c, p, s) : launch_paged_any<64, DA_BF16>(c, p, s);
 }
 
 }  // extern "C"
