@@ -82,29 +82,36 @@ da_status decode_attn_paged_workspace_init(void* workspace, size_t workspace_byt
  *     out = sum_j softmax(x)_j * v_scale * v_j,      lse = ln sum_j exp(x_j)
  *
  * with the scales of key j's page and head (1 in 16-bit pages). A token that sees no key
- * gets out = 0 and lse = -inf.
- *   q            device, [B, T_q, Hq, D] elements of `dtype`, 16-byte aligned
- *   cache        host pointer, read during the call; 16-bit pages hold elements of `dtype`
- *   kv_lens      device, int32 [B]: keys of each sequence, the query tokens' own included. A
- *                length below 0 or above max_pages * page_size counts as 0 and sets
- *                DA_DEVERR_SEQLENS
- *   block_table  device, int32 [B][table_stride], the first max_pages entries of a row
- *                readable; only the entries of a sequence's own tokens are read
- *   B            in [1, DA_MAX_PAGED_BATCH]; T_q in [1, DA_MAX_QUERY_TOKENS]; Hq % Hkv == 0
- *   dtype        DA_F16 or DA_BF16
- *   scale        finite
- *   out          device, [B, T_q, Hq, D] elements of `dtype`, 16-byte aligned
- *   lse          device, float32 [B, T_q, Hq], or NULL
- *   workspace    >= decode_attn_paged_workspace_size(T_q, Hq, Hkv, D) bytes, initialised once
- * Memory in a page behind a sequence's last token may hold anything. The results do not
- * depend on timing: the same inputs on the same device give the same bits.
+ * gets out = 0 and lse = -inf. Memory in a page behind a sequence's last token may hold
+ * anything. The results do not depend on timing: the same inputs on the same device give
+ * the same bits.
+ *
+ * The call's arguments are the fields of a struct (host memory, read during the call).
  * Errors (nothing enqueued): DA_ERR_INVALID_ARG, DA_ERR_UNSUPPORTED (D, or a batch
  * above the limit), DA_ERR_ALIGNMENT, DA_ERR_WORKSPACE_TOO_SMALL; DA_ERR_CUDA.
  */
-da_status decode_attn_paged(const void* q, const da_paged_cache* cache, const int32_t* kv_lens,
-                            const int32_t* block_table, int max_pages, int table_stride, int B, int T_q,
-                            int Hq, da_dtype dtype, float scale, void* out, float* lse, void* workspace,
-                            size_t workspace_bytes, void* stream);
+typedef struct {
+    const void* q;               /* device, [B, T_q, Hq, D] elements of `dtype`, 16-byte aligned */
+    const da_paged_cache* cache; /* host; 16-bit pages hold elements of `dtype` */
+    const int32_t* kv_lens;      /* device, int32 [B]: keys of each sequence, the query tokens' own included. A
+                                    length below 0 or above max_pages * page_size counts as 0 and sets
+                                    DA_DEVERR_SEQLENS */
+    const int32_t* block_table;  /* device, int32 [B][table_stride], the first max_pages entries of a row
+                                    readable; only the entries of a sequence's own tokens are read */
+    int max_pages;               /* >= 1 */
+    int table_stride;            /* >= max_pages */
+    int B;                       /* in [1, DA_MAX_PAGED_BATCH] */
+    int T_q;                     /* in [1, DA_MAX_QUERY_TOKENS] */
+    int Hq;                      /* a multiple of the cache's Hkv */
+    int dtype;                   /* DA_F16 or DA_BF16 */
+    float scale;                 /* finite */
+    void* out;                   /* device, [B, T_q, Hq, D] elements of `dtype`, 16-byte aligned */
+    float* lse;                  /* device, float32 [B, T_q, Hq], or NULL */
+    void* workspace;             /* decode_attn_paged_workspace_size(T_q, Hq, Hkv, D) bytes, initialised once */
+    size_t workspace_bytes;
+} da_paged_attn;
+
+da_status decode_attn_paged(const da_paged_attn* args, void* stream);
 
 /* How decode_attn_paged_append rotates the first rot_dim dims of queries and keys. */
 typedef enum {
@@ -132,27 +139,37 @@ typedef enum {
  * values of a page notice its scale) and makes growing a page's scale exact for all
  * elements but those. +-Inf is stored as +-448 s, NaN as NaN; neither moves the scale.
  *
- *   q, k, v      device, T_new rows of `dtype` elements: Hq (Hkv) heads of D contiguous
- *                elements each, rows q_stride (k_stride, v_stride) elements apart, 16-byte
- *                aligned, strides multiples of 8. q may be NULL (nothing to rotate)
- *   q_out        device, rows like q's, q_out_stride elements apart; may be q itself with the
- *                same stride, else it must not overlap q, k or v
- *   cos_sin      device, float32 [max_pos][rot_dim], 16-byte aligned: cosines, then sines
- *   rot_dim      a multiple of 16 in [16, D] (ignored without rotation)
- *   cu_new       device, int32 [B+1], non-decreasing; rows from cu_new[B] on are left alone
- *   T_new        rows that q, k and v hold, >= 0; a sequence whose rows lie outside them, or
- *                whose kv_lens is smaller than its new tokens or larger than max_pages *
- *                page_size, is left out and sets DA_DEVERR_SEQLENS
- *   workspace    its header alone is used (the error word): initialised, 256-byte aligned
  * The pages that one call writes must be distinct (no two sequences append to the same
- * page). Other arguments and errors as decode_attn_paged.
+ * page). Arguments and errors otherwise as decode_attn_paged.
  */
-da_status decode_attn_paged_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
-                                   const void* v, int64_t v_stride, const float* cos_sin, int max_pos,
-                                   int rot_dim, da_rope rope, const int32_t* cu_new, const int32_t* kv_lens,
-                                   const int32_t* block_table, int max_pages, int table_stride, int B,
-                                   int T_new, int Hq, da_dtype dtype, const da_paged_cache* cache, void* q_out,
-                                   int64_t q_out_stride, void* workspace, void* stream);
+typedef struct {
+    const void* q;               /* device, T_new rows of Hq heads of D contiguous elements of `dtype`, */
+    const void* k;               /*   16-byte aligned, rows q_stride elements apart (a multiple of 8), or */
+    const void* v;               /*   NULL: nothing to rotate; k and v alike, with Hkv heads */
+    int64_t q_stride, k_stride, v_stride;
+    const float* cos_sin;        /* device, float32 [max_pos][rot_dim], 16-byte aligned: cosines, then sines */
+    int max_pos;
+    int rot_dim;                 /* a multiple of 16 in [16, D] (ignored without rotation) */
+    int rope;                    /* da_rope */
+    const int32_t* cu_new;       /* device, int32 [B+1], non-decreasing; rows from cu_new[B] on are left alone */
+    const int32_t* kv_lens;      /* device, int32 [B], the new tokens counted */
+    const int32_t* block_table;  /* as above */
+    int max_pages;
+    int table_stride;
+    int B;
+    int T_new;                   /* rows that q, k and v hold, >= 0; a sequence whose rows lie outside them, or
+                                    whose kv_lens is smaller than its new tokens or larger than max_pages *
+                                    page_size, is left out and sets DA_DEVERR_SEQLENS */
+    int Hq;
+    int dtype;
+    const da_paged_cache* cache;
+    void* q_out;                 /* device, rows like q's, q_out_stride elements apart; may be q itself with the
+                                    same stride, else it must not overlap q, k or v */
+    int64_t q_out_stride;
+    void* workspace;             /* its header alone is used (the error word): initialised, 256-byte aligned */
+} da_paged_append;
+
+da_status decode_attn_paged_append(const da_paged_append* args, void* stream);
 
 #ifdef __cplusplus
 }

@@ -494,65 +494,63 @@ da_status run_append(AppendParams& p, bool e4m3, cudaStream_t stream) {
 
 using namespace da_impl;
 
-extern "C" da_status decode_attn_paged_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
-                                              const void* v, int64_t v_stride, const float* cos_sin, int max_pos,
-                                              int rot_dim, da_rope rope, const int32_t* cu_new, const int32_t* kv_lens,
-                                              const int32_t* block_table, int max_pages, int table_stride, int B,
-                                              int T_new, int Hq, da_dtype dtype, const da_paged_cache* cache,
-                                              void* q_out, int64_t q_out_stride, void* workspace, void* stream) {
-    da_status st = check_cache(cache, dtype, kv_lens, block_table, max_pages, table_stride, B, Hq);
+extern "C" da_status decode_attn_paged_append(const da_paged_append* args, void* stream) {
+    if (!args) return DA_ERR_INVALID_ARG;
+    const da_paged_append& a = *args;
+    da_status st = check_cache(a.cache, a.dtype, a.kv_lens, a.block_table, a.max_pages, a.table_stride, a.B, a.Hq);
     if (st != DA_OK) return st;
-    const da_paged_cache& c = *cache;
-    if (T_new < 0 || !cu_new || !workspace) return DA_ERR_INVALID_ARG;
-    if (rope != DA_ROPE_NONE && rope != DA_ROPE_HALF && rope != DA_ROPE_INTERLEAVED) return DA_ERR_INVALID_ARG;
-    if (rope != DA_ROPE_NONE && (!cos_sin || max_pos < 1 || rot_dim < 16 || rot_dim > c.D || rot_dim % 16))
-        return DA_ERR_INVALID_ARG;
-    if (!q) Hq = 0;
-    if (Hq > 0 && !q_out) return DA_ERR_INVALID_ARG;
-    if (T_new > 0 && (!k || !v)) return DA_ERR_INVALID_ARG;
+    const da_paged_cache& c = *a.cache;
+    if (a.T_new < 0 || !a.cu_new || !a.workspace) return DA_ERR_INVALID_ARG;
+    if (a.rope != DA_ROPE_NONE && a.rope != DA_ROPE_HALF && a.rope != DA_ROPE_INTERLEAVED) return DA_ERR_INVALID_ARG;
+    const bool turns = a.rope != DA_ROPE_NONE;
+    if (turns && (!a.cos_sin || a.max_pos < 1 || a.rot_dim < 16 || a.rot_dim > c.D || a.rot_dim % 16)) return DA_ERR_INVALID_ARG;
+    const int Hq = a.q ? a.Hq : 0;
+    if (Hq > 0 && !a.q_out) return DA_ERR_INVALID_ARG;
+    if (a.T_new > 0 && (!a.k || !a.v)) return DA_ERR_INVALID_ARG;
     const int64_t kv_row = static_cast<int64_t>(c.Hkv) * c.D, q_row = static_cast<int64_t>(Hq) * c.D;
-    if (k_stride < kv_row || v_stride < kv_row || (Hq > 0 && (q_stride < q_row || q_out_stride < q_row)))
+    if (a.k_stride < kv_row || a.v_stride < kv_row || (Hq > 0 && (a.q_stride < q_row || a.q_out_stride < q_row)))
         return DA_ERR_INVALID_ARG;
-    if (!aligned(workspace, 256) || !aligned(cu_new, 4) || !aligned(k, 16) || !aligned(v, 16) || k_stride % 8 || v_stride % 8)
+    if (!aligned(a.workspace, 256) || !aligned(a.cu_new, 4) || !aligned(a.k, 16) || !aligned(a.v, 16) || a.k_stride % 8 ||
+        a.v_stride % 8)
         return DA_ERR_ALIGNMENT;
-    if (Hq > 0 && (!aligned(q, 16) || !aligned(q_out, 16) || q_stride % 8 || q_out_stride % 8)) return DA_ERR_ALIGNMENT;
-    if (rope != DA_ROPE_NONE && !aligned(cos_sin, 16)) return DA_ERR_ALIGNMENT;
-    if (T_new == 0) return DA_OK;
+    if (Hq > 0 && (!aligned(a.q, 16) || !aligned(a.q_out, 16) || a.q_stride % 8 || a.q_out_stride % 8)) return DA_ERR_ALIGNMENT;
+    if (turns && !aligned(a.cos_sin, 16)) return DA_ERR_ALIGNMENT;
+    if (a.T_new == 0) return DA_OK;
     AppendParams p;
-    p.q = static_cast<const uint16_t*>(q);
-    p.k = static_cast<const uint16_t*>(k);
-    p.v = static_cast<const uint16_t*>(v);
-    p.q_stride = q_stride;
-    p.k_stride = k_stride;
-    p.v_stride = v_stride;
-    p.q_out_stride = q_out_stride;
-    p.cos_sin = cos_sin;
-    p.cu = cu_new;
-    p.lens = kv_lens;
-    p.table = block_table;
-    p.q_out = static_cast<uint16_t*>(q_out);
+    p.q = static_cast<const uint16_t*>(a.q);
+    p.k = static_cast<const uint16_t*>(a.k);
+    p.v = static_cast<const uint16_t*>(a.v);
+    p.q_stride = a.q_stride;
+    p.k_stride = a.k_stride;
+    p.v_stride = a.v_stride;
+    p.q_out_stride = a.q_out_stride;
+    p.cos_sin = a.cos_sin;
+    p.cu = a.cu_new;
+    p.lens = a.kv_lens;
+    p.table = a.block_table;
+    p.q_out = static_cast<uint16_t*>(a.q_out);
     p.kc = static_cast<uint8_t*>(c.k);
     p.vc = static_cast<uint8_t*>(c.v);
     p.ks = c.k_scale;
     p.vs = c.v_scale;
-    p.err = static_cast<uint32_t*>(workspace);
-    p.B = B;
-    p.T = T_new;
+    p.err = static_cast<uint32_t*>(a.workspace);
+    p.B = a.B;
+    p.T = a.T_new;
     p.Hq = Hq;
     p.Hkv = c.Hkv;
     p.P = c.page_size;
-    p.max_pages = max_pages;
-    p.table_stride = table_stride;
+    p.max_pages = a.max_pages;
+    p.table_stride = a.table_stride;
     p.num_pages = c.num_pages;
     p.layout = c.layout;
-    p.max_pos = rope == DA_ROPE_NONE ? 0x7fffffff : max_pos;
-    p.rot = rope == DA_ROPE_NONE ? 0 : rot_dim;
-    p.rope = rope;
+    p.max_pos = turns ? a.max_pos : 0x7fffffff;
+    p.rot = turns ? a.rot_dim : 0;
+    p.rope = a.rope;
     p.tokens_per_block = 1;
     p.row_blocks = 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool e4m3 = c.kv_dtype == DA_E4M3;
     if (c.D == 128)
-        return dtype == DA_F16 ? run_append<128, DA_F16>(p, e4m3, s) : run_append<128, DA_BF16>(p, e4m3, s);
-    return dtype == DA_F16 ? run_append<64, DA_F16>(p, e4m3, s) : run_append<64, DA_BF16>(p, e4m3, s);
+        return a.dtype == DA_F16 ? run_append<128, DA_F16>(p, e4m3, s) : run_append<128, DA_BF16>(p, e4m3, s);
+    return a.dtype == DA_F16 ? run_append<64, DA_F16>(p, e4m3, s) : run_append<64, DA_BF16>(p, e4m3, s);
 }

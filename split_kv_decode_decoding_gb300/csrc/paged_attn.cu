@@ -41,7 +41,9 @@ namespace da_impl {
 
 constexpr int kPagedShares = 2048;   // bound of (range, chunk) pairs, each with two partial results
 constexpr size_t kPagedCounterBytes = static_cast<size_t>(kPagedShares) * kConsumerWarps * 4;
-constexpr int kMinUnits = 4;         // units per range at least
+constexpr int kMinRange = 2;         // units per range at least
+constexpr int kAlignRange = 16;      // up to here ranges of an even batch follow its (sequence, head)s
+constexpr int kMaxSlack = 4;         // units that a cut may move to avoid a partial result
 constexpr float kNoKey = -1e30f;     // running maximum of a column that has seen no key (finite: no NaN arises)
 
 template <int D, bool KV8, int NT>
@@ -67,10 +69,11 @@ struct PagedShape {
     static constexpr int kSlotBytes = 64;
     static constexpr int kScaleOff = kSlotOff + kItemSlots * kSlotBytes;   // [stage][box] {ks, log2 vs}
     static constexpr int kScaleBytes = KV8 ? kStages * (kKeys / 16) * 8 : 0;
-    static constexpr int kBarOff = kScaleOff + kScaleBytes;
+    static constexpr int kLastOff = kScaleOff + kScaleBytes;               // [consumer warp][2] merges to do
+    static constexpr int kBarOff = kLastOff + kConsumerWarps * 2 * kSlotBytes;
     static constexpr int kNumBars = 2 * kStages + 2 * kItemSlots + 2;
-    static constexpr int kSeqOff = kBarOff + kNumBars * 8;                 // prefix[B + 1], then pad[B]
-    static constexpr int smem_bytes(int B) { return 1024 + kSeqOff + (4 * (B + 1) + B + 15) / 16 * 16; }
+    static constexpr int kSeqOff = kBarOff + kNumBars * 8;                 // prefix[B + 1], even, then pad[B]
+    static constexpr int smem_bytes(int B) { return 1024 + kSeqOff + (4 * (B + 2) + B + 15) / 16 * 16; }
 };
 
 struct PagedParams {
@@ -82,14 +85,21 @@ struct PagedParams {
     uint16_t* out;
     float* lse;              // or nullptr
     uint32_t* err;
-    uint32_t* work;          // work-queue head
     uint32_t* arrived;       // [share][consumer warp] partials written, at the share that begins a (sequence, head)
     float* part_lse;         // [2 * share][columns], log2
     float* part;             // [2 * share][columns][D]
     int B, tq, Hq, Hkv, G, P, max_pages, table_stride, num_pages, layout, chunks;
+    int lanes;               // CTAs per range: Hkv * chunks
+    int slots, one;          // ranges that run at once, and ranges that have an SM to themselves
     int box_keys;            // keys of a full TMA box: gcd(page size, stage keys)
+    uint32_t page_mul;       // position / P by multiplication (page())
+    int page_shift;
     float scale_log2;
     unsigned long long wait_limit_ns;
+
+    __device__ __forceinline__ int page(int pos) const {
+        return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(pos)) * page_mul) >> page_shift);
+    }
 };
 
 struct PagedItem {           // one piece of a (sequence, KV head): what a range holds of it
@@ -102,22 +112,67 @@ struct PagedItem {           // one piece of a (sequence, KV head): what a range
 };
 static_assert(sizeof(PagedItem) <= 64, "PagedItem fits its slot");
 
-// The cut of `units` into ranges (see above).
+// The cut of the batch's `units` into n ranges, for every KV head and chunk alike: k raw cuts at equal distances (q or q + 1 units) in every w units.
+// A batch of unequal lengths is one period of w = units. Where every sequence has the same t
+// units and ranges are short, a period is one of them (cut into k parts) or several whole ones (k = 1),
+// so that no range holds the end of one and the beginning of the next: that costs a second merge of the
+// warps and a partial result, 2 to 3 us against the 1 to 1.5 us that a unit takes to stream with every SM busy
+// (256 sequences of 256 keys, 2 KV heads: 24.0 us with plain equal cuts, 16.6 us with whole heads).
+// Otherwise a raw cut within `slack` units of a border moves there (4 slack <= q keeps the ranges in order).
+//
+// Every method is for a whole warp. A division by a number that is not known at compile time takes some 70 ns
+// and nothing streams before these are done, so independent ones run in different lanes at once.
 struct Ranges {
-    int64_t units;
-    int n;
-    __device__ __forceinline__ Ranges(int64_t u, int slots) : units(u) {
-        const int64_t most = (u + kMinUnits - 1) / kMinUnits;
-        n = static_cast<int>(most < slots ? most : slots);
+    int units, n, w, k, q, rem, split, slack;
+    // t: units of every sequence, or 0. slots: ranges that run at once; `one` of them take an
+    // SM each.
+    __device__ __forceinline__ Ranges(int u, int t, int slots, int one, int short_range) : units(u) {
+        const int lane = threadIdx.x & 31;
+        const int by = lane == 0 ? one : slots;
+        const int share = (u + by - 1) / by;
+        // one range per SM while it is short, then all slots
+        int size = max(kMinRange, __shfl_sync(0xffffffffu, share, 0));
+        if (size > (t >= size ? kAlignRange : short_range)) size = max(short_range, __shfl_sync(0xffffffffu, share, 1));
+        const int num = lane == 0 ? u + size - 1 : lane == 1 ? t : size + t - 1;
+        const int quot = num / (lane == 2 ? max(t, 1) : size);
+        w = units;
+        k = min(__shfl_sync(0xffffffffu, quot, 0), slots);
+        if (t > 0 && size <= kAlignRange) {
+            w = size < t ? t : __shfl_sync(0xffffffffu, quot, 2) * t;
+            k = size < t ? __shfl_sync(0xffffffffu, quot, 1) : 1;
+        }
+        const int last = (lane == 0 ? units + w - 1 : w) / (lane == 0 ? w : k);
+        n = __shfl_sync(0xffffffffu, last, 0) * k;
+        q = __shfl_sync(0xffffffffu, last, 1);
+        rem = w - q * k;
+        split = rem * (q + 1);
+        slack = min(q / 4, kMaxSlack);
     }
-    __device__ __forceinline__ int64_t begin(int r) const { return units * r / n; }
-    // the range that holds unit x: the last r with units * r / n <= x
-    __device__ __forceinline__ int of(int64_t x) const { return static_cast<int>(((x + 1) * n - 1) / units); }
+    // (per lane) cut r, and the first r with raw(r) >= x
+    __device__ __forceinline__ int raw(int r) const {
+        const int p = r / k, j = r - p * k;
+        return p * w + j * q + min(j, rem);
+    }
+    __device__ __forceinline__ int first_from(int x) const {
+        const int p = x / w, y = x - p * w;
+        const bool low = y <= split;
+        const int j = (low ? y + q : y - split + q - 1) / (low ? q + 1 : q);
+        return p * k + (low ? j : rem + j);
+    }
+    // Ranges that hold parts of the sequence of units [a, b): the first, and their number.
+    __device__ __forceinline__ void parts(int a, int b, int& first, int& count) const {
+        const int r = first_from((threadIdx.x & 31) == 0 ? a + slack + 1 : b - slack);
+        const int lo = __shfl_sync(0xffffffffu, r, 0), end = __shfl_sync(0xffffffffu, r, 1);   // cuts lo .. end - 1 lie inside
+        first = lo - 1;
+        count = max(end - lo, 0) + 1;
+    }
 };
 
 __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
+
+__device__ __forceinline__ void fence_acq_rel() { asm volatile("fence.acq_rel.gpu;" ::: "memory"); }
 
 // Two e4m3 values to two fp16 values (exact).
 __device__ __forceinline__ void e4m3x4_to_f16(uint32_t x, uint32_t& lo, uint32_t& hi) {
@@ -146,7 +201,7 @@ struct PagedKernel {
         s.slots = reinterpret_cast<PagedItem*>(s.smem + Sh::kSlotOff);
         s.scales = reinterpret_cast<float2*>(s.smem + Sh::kScaleOff);
         s.prefix = reinterpret_cast<int32_t*>(s.smem + Sh::kSeqOff);
-        s.pad = reinterpret_cast<uint8_t*>(s.prefix + p.B + 1);
+        s.pad = reinterpret_cast<uint8_t*>(s.prefix + p.B + 2);
         s.ring = smem_addr(s.smem);
         s.qbuf = s.ring + Sh::kQOff;
         s.full0 = s.ring + Sh::kBarOff;
@@ -162,24 +217,32 @@ struct PagedKernel {
         return reinterpret_cast<PagedItem*>(reinterpret_cast<uint8_t*>(s.slots) + i * Sh::kSlotBytes);
     }
 
-    // Stages per sequence and their running sum, by the whole CTA.
+    static __device__ __forceinline__ PagedItem* last_of(const Layout& s, int warp, int i) {
+        return reinterpret_cast<PagedItem*>(s.smem + Sh::kLastOff + (2 * warp + i) * Sh::kSlotBytes);
+    }
+
+    // Stages per sequence, their running sum, and the stages that all have (prefix[B + 1], 0 where they
+    // differ), by the whole CTA.
     static __device__ __forceinline__ void count_units(const Layout& s, const PagedParams& p) {
         __shared__ int32_t warp_sum[kThreads / 32];
         const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-        const int per = (p.B + kThreads - 1) / kThreads;
+        constexpr int kMost = (DA_MAX_PAGED_BATCH + kThreads - 1) / kThreads;
+        const int per = (p.B + kThreads - 1) / kThreads, b0 = tid * per;
         const int64_t most = static_cast<int64_t>(p.max_pages) * p.P;
-        int mine = 0;
-        for (int i = 0; i < per; ++i) {
-            const int b = tid * per + i;
-            if (b >= p.B) break;
-            int L = ld_cg_s32(p.lens + b);
+        int len[kMost], mine = 0;
+#pragma unroll
+        for (int i = 0; i < kMost; ++i) len[i] = i < per && b0 + i < p.B ? ld_cg_s32(p.lens + b0 + i) : 0;
+#pragma unroll
+        for (int i = 0; i < kMost; ++i) {
+            if (i >= per || b0 + i >= p.B) break;
+            int L = len[i];
             if (L < 0 || L > most) {
                 if (blockIdx.x == 0) flag_error(p.err, DA_DEVERR_SEQLENS);
                 L = 0;
             }
             const int n = L == 0 ? 1 : (L + Sh::kKeys - 1) / Sh::kKeys;   // an empty sequence: one empty stage
-            s.pad[b] = static_cast<uint8_t>(n * Sh::kKeys - L);
-            s.prefix[b + 1] = n;
+            s.pad[b0 + i] = static_cast<uint8_t>(n * Sh::kKeys - L);
+            len[i] = n;
             mine += n;
         }
         int run = mine;
@@ -192,14 +255,30 @@ struct PagedKernel {
         __syncthreads();
         int sum = run - mine;
         for (int w = 0; w < warp; ++w) sum += warp_sum[w];
-        for (int i = 0; i < per; ++i) {
-            const int b = tid * per + i;
-            if (b >= p.B) break;
-            sum += s.prefix[b + 1];
-            s.prefix[b + 1] = sum;
+#pragma unroll
+        for (int i = 0; i < kMost; ++i) {
+            if (i >= per || b0 + i >= p.B) break;
+            sum += len[i];
+            s.prefix[b0 + i + 1] = sum;
         }
         if (tid == 0) s.prefix[0] = 0;
+        // the stages of every sequence, or 0 where they differ
         __syncthreads();
+        const int first = s.prefix[1];
+        bool same = true;
+#pragma unroll
+        for (int i = 0; i < kMost; ++i) same = same && (i >= per || b0 + i >= p.B || len[i] == first);
+        same = __syncthreads_and(same);
+        if (tid == 0) s.prefix[p.B + 1] = same ? first : 0;
+        __syncthreads();
+    }
+
+    // Up to this many units a range has an SM to itself, from there on as many run as fit: a stage takes about
+    // as long at head size 64 as at 128, for half the bytes.
+    static constexpr int kShortRange = D == 128 ? 8 : 4;
+
+    static __device__ __forceinline__ Ranges cut(const Layout& s, const PagedParams& p) {
+        return Ranges(s.prefix[p.B], s.prefix[p.B + 1], p.slots, p.one, kShortRange);
     }
 
     // ------------------------------------------------------------ producer
@@ -215,7 +294,7 @@ struct PagedKernel {
         x.lvs = -INFINITY;
         const int key = box * p.box_keys;
         if (static_cast<uint32_t>(key) < static_cast<uint32_t>(it.nkeys)) {   // (a product past 2^31 is none)
-            const int page = ld_cg_s32(p.table + static_cast<int64_t>(it.b) * p.table_stride + (it.key0 + key) / p.P);
+            const int page = ld_cg_s32(p.table + static_cast<int64_t>(it.b) * p.table_stride + p.page(it.key0 + key));
             const bool good = page >= 0 && page < p.num_pages;
             // a bad page: a coordinate past the cache, which the copy fills with zeros
             x.page = good ? page : p.num_pages;
@@ -246,44 +325,46 @@ struct PagedKernel {
     static __device__ void producer(const Layout& s, const PagedParams& p, const CUtensorMap* tmK, const CUtensorMap* tmV,
                                     const CUtensorMap* tmK16, const CUtensorMap* tmV16) {
         const int lane = threadIdx.x & 31;
-        const int64_t units = static_cast<int64_t>(s.prefix[p.B]) * p.Hkv;
-        const Ranges ranges(units, max(1, min(static_cast<int>(gridDim.x), kPagedShares) / p.chunks));
-        const int shares = ranges.n * p.chunks;
-        const bool queued = shares > static_cast<int>(gridDim.x);
+        const Ranges ranges = cut(s, p);
+        const int shares = ranges.n * p.lanes;
 
-        // cursor: the units left of this CTA's share, and where the first of them lies
-        int share = static_cast<int>(blockIdx.x), range = 0, chunk = 0;
-        int64_t u = 0, end = 0;
-        int b = 0, kvh = 0, stage = 0;
-        auto open_share = [&]() -> bool {
-            if (share >= shares) return false;
-            range = share / p.chunks;
-            chunk = share - range * p.chunks;
-            u = ranges.begin(range);
-            end = ranges.begin(range + 1);
-            int lo = 0, hi = p.B - 1;   // last b with Hkv * prefix[b] <= u
+        // cursor: where this CTA's next unit lies, and the units left of its share. Lane 0 looks up the share's
+        // begin, lane 1 its end.
+        const int share = static_cast<int>(blockIdx.x);
+        const int range = share / p.lanes, sub = share - range * p.lanes;
+        const int kvh = p.chunks == 1 ? sub : sub / p.chunks, chunk = sub - kvh * p.chunks;
+        int b = 0, stage = 0, left = 0;
+        if (share < shares) {
+            const int r = range + (lane == 1 ? 1 : 0);
+            const int u = min(ranges.raw(r), ranges.units - 1);
+            int lo = 0, hi = p.B - 1;   // last b with prefix[b] <= u
             while (lo < hi) {
                 const int mid = (lo + hi + 1) >> 1;
-                if (static_cast<int64_t>(s.prefix[mid]) * p.Hkv <= u) lo = mid;
+                if (s.prefix[mid] <= u) lo = mid;
                 else hi = mid - 1;
             }
-            b = lo;
-            const int n = s.prefix[b + 1] - s.prefix[b];
-            const int r = static_cast<int>(u - static_cast<int64_t>(s.prefix[b]) * p.Hkv);
-            kvh = r / n;
-            stage = r - kvh * n;
-            return true;
-        };
-        // the next piece: valid 0 when this CTA has none left
-        auto next_piece = [&](PagedItem& it, int taken) {
-            it.valid = 0;
-            if (u == end) {
-                share = taken;
-                if (!open_share()) return;
+            int at = u, st = u - s.prefix[lo];
+            const int rest = s.prefix[lo + 1] - u;
+            if (st <= ranges.slack) {          // a cut near a border moves there
+                at -= st;
+                st = 0;
+            } else if (rest <= ranges.slack) {
+                at += rest;
+                st = 0;
+                ++lo;
             }
+            if (r >= ranges.n) at = ranges.units;
+            b = __shfl_sync(0xffffffffu, lo, 0);
+            stage = __shfl_sync(0xffffffffu, st, 0);
+            left = __shfl_sync(0xffffffffu, at, 1) - __shfl_sync(0xffffffffu, at, 0);
+        }
+        // the next piece: valid 0 when this CTA has none left
+        auto next_piece = [&](PagedItem& it) {
+            it.valid = 0;
+            if (left == 0) return;
             const int n = s.prefix[b + 1] - s.prefix[b];
             const int L = n * Sh::kKeys - s.pad[b];
-            const int last = static_cast<int>(min(static_cast<int64_t>(n), stage + (end - u)));
+            const int count = min(n - stage, left), last = stage + count;
             it.valid = 1;
             it.b = b;
             it.kvh = kvh;
@@ -294,22 +375,12 @@ struct PagedKernel {
             it.ntiles = (it.nkeys + Sh::kKeys - 1) / Sh::kKeys;
             it.vis0 = L - p.tq + 1 - it.key0;
             it.part = -1;
-            it.first_share = it.nparts = 0;
-            if (stage > 0 || last < n) {
-                const int64_t u0 = static_cast<int64_t>(s.prefix[b]) * p.Hkv + static_cast<int64_t>(kvh) * n;
-                const int ra = ranges.of(u0);
-                it.first_share = ra * p.chunks + chunk;
-                it.nparts = ranges.of(u0 + n - 1) - ra + 1;
-                it.part = 2 * share + (stage == 0 ? 1 : 0);
-            }
-            u += last - stage;
+            if (count < n) it.part = 2 * share + (stage == 0 ? 1 : 0);
+            left -= count;
             stage = last;
             if (stage == n) {
                 stage = 0;
-                if (++kvh == p.Hkv) {
-                    kvh = 0;
-                    ++b;
-                }
+                ++b;
             }
         };
         auto publish = [&](uint32_t i, const PagedItem& it) -> bool {
@@ -341,28 +412,14 @@ struct PagedKernel {
         PagedItem item;
         int st = 0;
         uint32_t ph = 0;
-        next_piece(item, share);       // u == end == 0: opens the first share
+        next_piece(item);
         if (!publish(0, item) || !item.valid) return;
         Box cur = load_box(p, item, lane), nxt;
         const int per_stage = Sh::kKeys / p.box_keys;
         for (uint32_t i = 0; item.valid; ++i) {
-            int taken = shares;
-            const int fetch_at = max(0, item.ntiles - kStages);
             nxt = load_box(p, item, 32 + lane);
             bool ok = true;
-            for (int t = 0; t <= item.ntiles; ++t) {
-                // take the next share from the queue a few stages before this one's end. A call
-                // takes exactly `shares` numbers (one per share), and the last take resets the
-                // counter for the next call on this workspace.
-                if (t == fetch_at && queued && u == end) {
-                    uint32_t raw = 0;
-                    if (lane == 0) {
-                        raw = atomicAdd(p.work, 1u);
-                        if (raw + 1u == static_cast<uint32_t>(shares)) atomicExch(p.work, 0u);
-                    }
-                    taken = static_cast<int>(gridDim.x + __shfl_sync(0xffffffffu, raw, 0));
-                }
-                if (t == item.ntiles) break;
+            for (int t = 0; t < item.ntiles; ++t) {
                 const int box0 = t * per_stage;
                 if (t > 0 && box0 % 32 == 0) {
                     cur = nxt;
@@ -388,7 +445,7 @@ struct PagedKernel {
                     const int i0 = lane - in32;
                     if (i0 >= 0 && i0 < per_stage) {
                         const int off = i0 * p.box_keys;
-                        const int slot = (key + off) % p.P;
+                        const int slot = key + off - p.page(key + off) * p.P;
                         copy_box(p, kdst + off * Sh::kSliceRow, tmK, cur.page, slot, item.kvh, fb);
                         copy_box(p, vdst + off * Sh::kSliceRow, tmV, cur.page, slot, item.kvh, fb);
                     }
@@ -396,7 +453,7 @@ struct PagedKernel {
                     // the ragged end of a sequence: 16-key boxes up to it
                     const int page = __shfl_sync(0xffffffffu, cur.page, (in32 + lane * 16 / p.box_keys) & 31);
                     if (lane < nbox16) {
-                        const int slot = (key + lane * 16) % p.P;
+                        const int slot = key + lane * 16 - p.page(key + lane * 16) * p.P;
                         copy_box(p, kdst + lane * 16 * Sh::kSliceRow, tmK16, page, slot, item.kvh, fb);
                         copy_box(p, vdst + lane * 16 * Sh::kSliceRow, tmV16, page, slot, item.kvh, fb);
                     }
@@ -416,9 +473,20 @@ struct PagedKernel {
                 }
             }
             if (!ok) return;
+            if (item.part >= 0) {
+                // which ranges hold the others, for the consumers' end of the piece (they read it after the
+                // hand-over below)
+                int first, count;
+                ranges.parts(s.prefix[item.b], s.prefix[item.b + 1], first, count);
+                if (lane == 0) {
+                    PagedItem* at = slot_of(s, i % kItemSlots);
+                    at->first_share = first * p.lanes + sub;
+                    at->nparts = count;
+                }
+            }
             // the next piece's descriptor, queries and table entries go out before this one's merge
             PagedItem next;
-            next_piece(next, taken);
+            next_piece(next);
             if (!publish(i + 1, next)) return;
             if (next.valid) cur = load_box(p, next, lane);
             // hand the consumers the next stage, empty, for this piece's merge
@@ -629,46 +697,92 @@ struct PagedKernel {
         }
     }
 
-    // Merge this warp's columns of a (sequence, head) whose partials are all written.
+    // Merge this warp's columns of a (sequence, head) whose partials are all written, two columns at a
+    // time. Lane j takes part j's lse and weight, so that every load is issued before any of them is
+    // needed; the order of the sums is that of the parts.
     static __device__ __forceinline__ void merge_parts(const PagedParams& p, const PagedItem& it) {
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-        constexpr int kLanes = D / 4, kHeads = 32 / kLanes;
-        const int d0 = (lane % kLanes) * 4;
-        for (int c = warp + kConsumerWarps * (lane / kLanes); c < Sh::kCols; c += kConsumerWarps * kHeads) {
-            if (c >= it.nh) break;
-            float m = -INFINITY, z = 0.f;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            constexpr int kAhead = 8;
-            for (int j0 = 0; j0 < it.nparts; j0 += kAhead) {
-                float lv[kAhead];
-                float4 ov[kAhead];
+        constexpr int kLanes = D / 4, kHalves = 32 / kLanes;   // head size 64: each half warp takes every other part
+        constexpr int kAhead = NT == 1 ? 8 : 4;                // loads in flight per lane and column
+        const int d0 = (lane % kLanes) * 4, half = lane / kLanes;
+        const int nparts = it.nparts, nh = it.nh;
+        for (int c0 = warp; c0 < nh; c0 += 2 * kConsumerWarps) {
+            const int cols = c0 + kConsumerWarps < nh ? 2 : 1;
+            float m[2] = {kNoKey, kNoKey}, z[2] = {0.f, 0.f};
+            float4 acc[2];
+            acc[0] = acc[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int j0 = 0; j0 < nparts; j0 += 32) {
+                const int count = min(32, nparts - j0);
+                auto row_of = [&](int j, int c) -> int64_t {
+                    const int part = j == 0 ? 2 * it.first_share + 1 : 2 * (it.first_share + j * p.lanes);
+                    return static_cast<int64_t>(part) * Sh::kCols + c0 + kConsumerWarps * c;
+                };
+                float lv[2], w[2];
+                float4 o[2][kAhead];
+                auto load = [&](int j) {
 #pragma unroll
-                for (int i = 0; i < kAhead; ++i) {
-                    const int j = j0 + i;
-                    lv[i] = -INFINITY;
-                    ov[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (j < it.nparts) {
-                        const int64_t part = j == 0 ? 2 * it.first_share + 1 : 2 * (it.first_share + j * p.chunks);
-                        lv[i] = __ldcg(p.part_lse + part * Sh::kCols + c);
-                        ov[i] = __ldcg(reinterpret_cast<const float4*>(p.part + (part * Sh::kCols + c) * D + d0));
-                    }
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int i = 0; i < kAhead; ++i) {
+                            const int kk = j + i * kHalves + half;
+                            if (kk < count && c < cols)
+                                o[c][i] = __ldcg(reinterpret_cast<const float4*>(p.part + row_of(j0 + kk, c) * D + d0));
+                        }
+                };
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    lv[c] = lane < count && c < cols ? __ldcg(p.part_lse + row_of(j0 + lane, c)) : -INFINITY;
+                load(0);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float top = lv[c];
+#pragma unroll
+                    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+                    const float mn = fmaxf(m[c], top);       // stays kNoKey while no part has seen a key
+                    w[c] = fast_exp2(lv[c] - mn);
+                    float sum = w[c];
+#pragma unroll
+                    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+                    const float al = fast_exp2(m[c] - mn);
+                    m[c] = mn;
+                    z[c] = fmaf(z[c], al, sum);
+                    acc[c].x *= al;
+                    acc[c].y *= al;
+                    acc[c].z *= al;
+                    acc[c].w *= al;
                 }
+                for (int j = 0; j < count; j += kAhead * kHalves) {
+                    if (j > 0) load(j);
 #pragma unroll
-                for (int i = 0; i < kAhead; ++i) {
-                    if (lv[i] == -INFINITY) continue;
-                    const float mn = fmaxf(m, lv[i]);
-                    const float a = fast_exp2(m - mn), w = fast_exp2(lv[i] - mn);
-                    m = mn;
-                    z = fmaf(z, a, w);
-                    acc.x = fmaf(acc.x, a, w * ov[i].x);
-                    acc.y = fmaf(acc.y, a, w * ov[i].y);
-                    acc.z = fmaf(acc.z, a, w * ov[i].z);
-                    acc.w = fmaf(acc.w, a, w * ov[i].w);
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int i = 0; i < kAhead; ++i) {
+                            const int kk = j + i * kHalves + half;
+                            const float wk = __shfl_sync(0xffffffffu, w[c], kk & 31);
+                            if (kk < count && c < cols) {
+                                acc[c].x = fmaf(wk, o[c][i].x, acc[c].x);
+                                acc[c].y = fmaf(wk, o[c][i].y, acc[c].y);
+                                acc[c].z = fmaf(wk, o[c][i].z, acc[c].z);
+                                acc[c].w = fmaf(wk, o[c][i].w, acc[c].w);
+                            }
+                        }
                 }
             }
-            const float inv = m == -INFINITY ? 0.f : 1.f / z;
-            store_output(p, output_row(p, it, c), d0, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv),
-                         m == -INFINITY ? -INFINITY : m + log2f(z));
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                if constexpr (kHalves == 2) {
+                    acc[c].x += __shfl_xor_sync(0xffffffffu, acc[c].x, 16);
+                    acc[c].y += __shfl_xor_sync(0xffffffffu, acc[c].y, 16);
+                    acc[c].z += __shfl_xor_sync(0xffffffffu, acc[c].z, 16);
+                    acc[c].w += __shfl_xor_sync(0xffffffffu, acc[c].w, 16);
+                }
+                const bool none = m[c] == kNoKey;
+                const float inv = none ? 0.f : 1.f / z[c];
+                if (half == 0 && c < cols)
+                    store_output(p, output_row(p, it, c0 + kConsumerWarps * c), d0,
+                                 make_float4(acc[c].x * inv, acc[c].y * inv, acc[c].z * inv, acc[c].w * inv),
+                                 none ? -INFINITY : m[c] + log2f(z[c]));
+            }
         }
     }
 
@@ -679,6 +793,7 @@ struct PagedKernel {
         uint32_t bad_bar = 0, bad_ph = 0;
         int st = 0;
         uint32_t ph = 0, mz = 0, md = 0;
+        int merges = 0;
         for (uint32_t i = 0;; ++i) {
             const int slot = i % kItemSlots;
             if (!mbar_wait_warp(s.ifull0 + 8 * slot, (i / kItemSlots) & 1, p.wait_limit_ns)) {
@@ -686,21 +801,22 @@ struct PagedKernel {
                 ok = false;
                 break;
             }
-            const PagedItem item = *slot_of(s, slot);
+            // stays in shared memory (the slot is handed back at the piece's end): the loop below needs
+            // every register
+            const PagedItem& item = *slot_of(s, slot);
+            if (!item.valid) break;
             uint32_t qf[D / 16][NT][2];
             float qs[NT][2];
-            if (item.valid) load_queries(p, s.qbuf + slot * Sh::kQBytes, item.nh, qf, qs);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(s.iempty0 + 8 * slot);
-            if (!item.valid) break;
+            load_queries(p, s.qbuf + slot * Sh::kQBytes, item.nh, qf, qs);
+            const int nkeys = item.nkeys, ntiles = item.ntiles;
 
             int vis[NT][2];   // keys of the piece that this thread's columns may see
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    vis[n][c] = item.nkeys;
-                    if (p.tq > 1) vis[n][c] = min(item.nkeys, item.vis0 + (item.c0 + 8 * n + 2 * t4 + c) / p.G);
+                    vis[n][c] = nkeys;
+                    if (p.tq > 1) vis[n][c] = min(nkeys, item.vis0 + (item.c0 + 8 * n + 2 * t4 + c) / p.G);
                 }
             float acc[D / 16][NT][4];
 #pragma unroll
@@ -717,7 +833,7 @@ struct PagedKernel {
                     l[n][c] = 0.f;
                 }
 
-            for (int t = 0; t < item.ntiles; ++t) {
+            for (int t = 0; t < ntiles; ++t) {
                 const uint32_t fb = s.full0 + 8 * st;
                 if (ok && !mbar_wait_warp(fb, ph, p.wait_limit_ns)) {
                     ok = false;
@@ -725,7 +841,7 @@ struct PagedKernel {
                     bad_ph = ph;
                     if (lane == 0) flag_error(p.err, DA_DEVERR_TIMEOUT);
                 }
-                const int keys = min(Sh::kKeys, item.nkeys - t * Sh::kKeys);
+                const int keys = min(Sh::kKeys, nkeys - t * Sh::kKeys);
                 const int valid = keys - warp * kRows;
                 bool zeroed = false;
                 if (ok && valid > 0) {
@@ -895,18 +1011,26 @@ struct PagedKernel {
                 __syncwarp();
                 if (lane == 0) {
                     uint32_t* count = p.arrived + item.first_share * kConsumerWarps + warp;
-                    __threadfence();
+                    fence_acq_rel();
                     n = atomicAdd(count, 1u) + 1;
                     if (n == static_cast<uint32_t>(item.nparts)) {
                         atomicExch(count, 0u);
-                        __threadfence();
+                        fence_acq_rel();
                     }
                 }
                 n = __shfl_sync(0xffffffffu, n, 0);
-                __syncwarp();
-                if (n == static_cast<uint32_t>(item.nparts)) merge_parts(p, item);
+                // The merge waits for the end of the range (at most its first and last piece need one): it
+                // then has the registers of the loop above to itself.
+                if (n == static_cast<uint32_t>(item.nparts)) {
+                    if (lane == 0) *last_of(s, warp, merges) = item;
+                    ++merges;
+                }
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(s.iempty0 + 8 * slot);
         }
+        __syncwarp();
+        for (int i = 0; i < merges; ++i) merge_parts(p, *last_of(s, warp, i));
         // after a timed-out wait, a copy still in flight into this CTA's shared memory gets one more
         // bounded wait before the CTA exits
         if (!ok && bad_bar != 0) mbar_wait(bad_bar, bad_ph, p.wait_limit_ns);
@@ -986,6 +1110,19 @@ inline bool make_page_map(CUtensorMap* map, const void* base, const da_paged_cac
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// SMs of the current device (152 if it cannot be queried).
+inline int device_sms() {
+    static std::atomic<int> known[64] = {};
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 152;
+    sms = known[dev].load(std::memory_order_relaxed);
+    if (sms == 0) {
+        if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) return 152;
+        known[dev].store(sms, std::memory_order_relaxed);
+    }
+    return sms;
+}
+
 template <int D, int DT, bool KV8, int NT>
 da_status launch_paged(const da_paged_cache& c, PagedParams& p, cudaStream_t stream) {
     using Sh = PagedShape<D, KV8, NT>;
@@ -998,13 +1135,19 @@ da_status launch_paged(const da_paged_cache& c, PagedParams& p, cudaStream_t str
         return DA_ERR_CUDA;
     // units of the largest batch that the table can describe
     const int64_t stages = (static_cast<int64_t>(p.max_pages) * p.P + Sh::kKeys - 1) / Sh::kKeys;
-    const int64_t units = static_cast<int64_t>(p.B) * p.Hkv * stages;
-    if (units > 0x7fffffffll || p.chunks > kPagedShares) return DA_ERR_INVALID_ARG;
+    const int64_t units = static_cast<int64_t>(p.B) * stages, lanes = static_cast<int64_t>(p.Hkv) * p.chunks;
+    if (units > 0x3fff0000ll || lanes > 0x1000000ll) return DA_ERR_INVALID_ARG;
     auto kern = paged_kernel<D, DT, KV8, NT>;
     static DeviceCache cache;
-    int grid = 0;
-    if (persistent_grid(kern, kThreads, Sh::smem_bytes(DA_MAX_PAGED_BATCH), cache, &grid) != cudaSuccess) return DA_ERR_CUDA;
-    grid = static_cast<int>(std::min<int64_t>(std::max(grid, p.chunks), ((units + kMinUnits - 1) / kMinUnits) * p.chunks));
+    int resident = 0;
+    if (persistent_grid(kern, kThreads, Sh::smem_bytes(DA_MAX_PAGED_BATCH), cache, &resident) != cudaSuccess)
+        return DA_ERR_CUDA;
+    p.lanes = static_cast<int>(lanes);
+    p.slots = std::max(1, std::min(resident, kPagedShares) / p.lanes);
+    p.one = std::max(1, device_sms() / p.lanes);
+    // CTAs for the most ranges that the kernel can make of these units (see Ranges)
+    const int64_t most = units <= static_cast<int64_t>(p.one) * PagedKernel<D, DT, KV8, NT>::kShortRange ? p.one : p.slots;
+    const int grid = static_cast<int>(std::min<int64_t>(most, (units + kMinRange - 1) / kMinRange)) * p.lanes;
     cudaLaunchAttribute attrs[1] = {pdl_attr()};
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
@@ -1042,48 +1185,51 @@ da_status decode_attn_paged_workspace_init(void* workspace, size_t workspace_byt
     return cudaMemsetAsync(workspace, 0, head, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
 }
 
-da_status decode_attn_paged(const void* q, const da_paged_cache* cache, const int32_t* kv_lens,
-                            const int32_t* block_table, int max_pages, int table_stride, int B, int T_q, int Hq,
-                            da_dtype dtype, float scale, void* out, float* lse, void* workspace,
-                            size_t workspace_bytes, void* stream) {
-    da_status st = check_cache(cache, dtype, kv_lens, block_table, max_pages, table_stride, B, Hq);
+da_status decode_attn_paged(const da_paged_attn* args, void* stream) {
+    if (!args) return DA_ERR_INVALID_ARG;
+    const da_paged_attn& a = *args;
+    da_status st = check_cache(a.cache, a.dtype, a.kv_lens, a.block_table, a.max_pages, a.table_stride, a.B, a.Hq);
     if (st != DA_OK) return st;
-    const da_paged_cache& c = *cache;
-    if (Hq < 1 || T_q < 1 || T_q > DA_MAX_QUERY_TOKENS || !std::isfinite(scale)) return DA_ERR_INVALID_ARG;
-    if (!q || !out || !workspace) return DA_ERR_INVALID_ARG;
-    if (static_cast<int64_t>(B) * T_q * Hq * c.D > 0x7fffffffll) return DA_ERR_INVALID_ARG;
-    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 256)) return DA_ERR_ALIGNMENT;
-    if (workspace_bytes < decode_attn_paged_workspace_size(T_q, Hq, c.Hkv, c.D)) return DA_ERR_WORKSPACE_TOO_SMALL;
+    const da_paged_cache& c = *a.cache;
+    if (a.Hq < 1 || a.T_q < 1 || a.T_q > DA_MAX_QUERY_TOKENS || !std::isfinite(a.scale)) return DA_ERR_INVALID_ARG;
+    if (!a.q || !a.out || !a.workspace) return DA_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(a.B) * a.T_q * a.Hq * c.D > 0x7fffffffll) return DA_ERR_INVALID_ARG;
+    if (!aligned(a.q, 16) || !aligned(a.out, 16) || !aligned(a.lse, 4) || !aligned(a.workspace, 256)) return DA_ERR_ALIGNMENT;
+    if (a.workspace_bytes < decode_attn_paged_workspace_size(a.T_q, a.Hq, c.Hkv, c.D)) return DA_ERR_WORKSPACE_TOO_SMALL;
     PagedParams p;
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
-    p.q = static_cast<const uint16_t*>(q);
+    uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+    p.q = static_cast<const uint16_t*>(a.q);
     p.ks = c.k_scale;
     p.vs = c.v_scale;
-    p.lens = kv_lens;
-    p.table = block_table;
-    p.out = static_cast<uint16_t*>(out);
-    p.lse = lse;
+    p.lens = a.kv_lens;
+    p.table = a.block_table;
+    p.out = static_cast<uint16_t*>(a.out);
+    p.lse = a.lse;
     p.err = reinterpret_cast<uint32_t*>(ws);
-    p.work = reinterpret_cast<uint32_t*>(ws + kWorkCounterOff);
     p.arrived = reinterpret_cast<uint32_t*>(ws + kPagedHeaderBytes);
-    p.G = Hq / c.Hkv;
-    const int cols = item_cols(static_cast<int64_t>(p.G) * T_q);
+    p.G = a.Hq / c.Hkv;
+    const int cols = item_cols(static_cast<int64_t>(p.G) * a.T_q);
     p.part = reinterpret_cast<float*>(ws + kPagedHeaderBytes + kPagedCounterBytes);
     p.part_lse = p.part + static_cast<size_t>(2 * kPagedShares) * cols * c.D;
-    p.B = B;
-    p.tq = T_q;
-    p.Hq = Hq;
+    p.B = a.B;
+    p.tq = a.T_q;
+    p.Hq = a.Hq;
     p.Hkv = c.Hkv;
     p.P = c.page_size;
-    p.max_pages = max_pages;
-    p.table_stride = table_stride;
+    // floor(pos / P) = pos * ceil(2^(31 + l) / P) >> (31 + l) for every pos < 2^31, with 2^l >= P > 2^(l - 1)
+    int l = 0;
+    while ((1 << l) < p.P) ++l;
+    p.page_shift = 31 + l;
+    p.page_mul = static_cast<uint32_t>(((1ull << p.page_shift) + p.P - 1) / p.P);
+    p.max_pages = a.max_pages;
+    p.table_stride = a.table_stride;
     p.num_pages = c.num_pages;
     p.layout = c.layout;
-    p.scale_log2 = scale * kLog2e;
+    p.scale_log2 = a.scale * kLog2e;
     p.wait_limit_ns = kWaitLimitNs;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (c.D == 128) return dtype == DA_F16 ? launch_paged_any<128, DA_F16>(c, p, s) : launch_paged_any<128, DA_BF16>(c, p, s);
-    return dtype == DA_F16 ? launch_paged_any<64, DA_F16>(c, p, s) : launch_paged_any<64, DA_BF16>(c, p, s);
+    if (c.D == 128) return a.dtype == DA_F16 ? launch_paged_any<128, DA_F16>(c, p, s) : launch_paged_any<128, DA_BF16>(c, p, s);
+    return a.dtype == DA_F16 ? launch_paged_any<64, DA_F16>(c, p, s) : launch_paged_any<64, DA_BF16>(c, p, s);
 }
 
 }  // extern "C"

@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 
 DA_E4M3 = 2
 DA_DEVERR_PAGE, DA_DEVERR_POSITION = 0x4, 0x8
@@ -27,23 +28,34 @@ class _CacheStruct(ctypes.Structure):
                 ("Hkv", ctypes.c_int), ("D", ctypes.c_int), ("kv_dtype", ctypes.c_int), ("layout", ctypes.c_int)]
 
 
+_handle = None
+
+
 def declare(lib) -> None:
     """Argument and result types of the paged entry points (called once, by load())."""
-    P, I, I64, SZ, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
+    global _handle
+    P, I, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
     lib.decode_attn_paged_workspace_size.argtypes = [I, I, I, I]
     lib.decode_attn_paged_workspace_size.restype = SZ
     lib.decode_attn_paged_workspace_init.argtypes = [P, SZ, P]
     lib.decode_attn_paged_workspace_init.restype = I
-    lib.decode_attn_paged.argtypes = [P, P, P, P, I, I, I, I, I, I, F, P, P, P, SZ, P]
-    lib.decode_attn_paged.restype = I
-    lib.decode_attn_paged_append.argtypes = [P, I64, P, I64, P, I64, P, I, I, I, P, P, P, I, I, I, I, I, I, P, P,
-                                             I64, P, P]
-    lib.decode_attn_paged_append.restype = I
+    for f in (lib.decode_attn_paged, lib.decode_attn_paged_append):
+        f.argtypes = [ctypes.c_char_p, P]
+        f.restype = I
+    _handle = lib
+
+
+# da_paged_attn and da_paged_append, field by field: packing a struct costs a third of what ctypes
+# takes to convert as many arguments
+_pack_attn = struct.Struct("@PPPPiiiiiifPPPN").pack
+_pack_append = struct.Struct("@PPPqqqPiiiPPPiiiiiiPPqP").pack
 
 
 def _lib():
-    from . import load
-    return load()
+    if _handle is None:
+        from . import load
+        load()
+    return _handle
 
 
 def _fail(status: int, where: str) -> None:
@@ -51,16 +63,29 @@ def _fail(status: int, where: str) -> None:
     raise DecodeAttnError(status, where)
 
 
-_dtypes = None
+_torch = None
+
+
+def _types():
+    """torch's types by name, looked up on first use (importing the binding does not import torch)."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = (torch.int32, torch.float32,
+                  {torch.float16: 0, torch.bfloat16: 1, torch.float8_e4m3fn: DA_E4M3})
+    return _torch
+
+
+def _int32():
+    return _types()[0]
+
+
+def _float32():
+    return _types()[1]
 
 
 def _codes():
-    """torch dtype -> element type code (torch is imported on first use)."""
-    global _dtypes
-    if _dtypes is None:
-        import torch
-        _dtypes = {torch.float16: 0, torch.bfloat16: 1, torch.float8_e4m3fn: DA_E4M3}
-    return _dtypes
+    return _types()[2]
 
 
 def _raw_stream(stream, device: int) -> int:
@@ -74,7 +99,7 @@ def _check_device(device: int) -> None:
     import torch
     if device < 0:
         raise ValueError("tensors must be CUDA tensors")
-    if device != torch.cuda.current_device():
+    if device != torch._C._cuda_getDevice():
         raise ValueError(f"tensors are on cuda:{device}, which is not the current device")
 
 
@@ -148,14 +173,13 @@ def alloc_paged_workspace(T_q: int, Hq: int, Hkv: int, D: int, device="cuda", st
 
 
 def _check_sequences(cache, kv_lens, block_table, dev):
-    import torch
-    i32 = torch.int32
+    """(B, max_pages, table_stride) of kv_lens [B] and block_table [B, max_pages]."""
+    i32 = _int32()
     if kv_lens.dtype is not i32 or block_table.dtype is not i32:
         raise TypeError("kv_lens and block_table must be int32")
-    shape = block_table.shape
-    if kv_lens.dim() != 1 or len(shape) != 2 or shape[0] != kv_lens.shape[0]:
+    shape, stride = block_table.shape, block_table.stride()
+    if len(shape) != 2 or kv_lens.shape != shape[:1]:
         raise ValueError("kv_lens must be [B] and block_table [B, max_pages]")
-    stride = block_table.stride()
     if not kv_lens.is_contiguous() or stride[1] != 1:
         raise ValueError("kv_lens and the rows of block_table must be contiguous")
     if kv_lens.get_device() != dev or block_table.get_device() != dev or cache.device != dev:
@@ -174,46 +198,50 @@ def decode_attn_paged(q, cache: PagedCache, kv_lens, block_table, out, workspace
     dev = q.get_device()
     _check_device(dev)
     B, max_pages, table_stride = _check_sequences(cache, kv_lens, block_table, dev)
-    shape = q.shape
-    T_q, Hq, D = (1, *shape[1:]) if len(shape) == 3 else shape[1:]
-    code = _codes().get(q.dtype, -1)
+    shape, dtype = q.shape, q.dtype
+    code = _codes().get(dtype, -1)
     if code not in (0, 1):
-        raise TypeError(f"q must be float16 or bfloat16, not {q.dtype}")
+        raise TypeError(f"q must be float16 or bfloat16, not {dtype}")
     if cache.kv_dtype != DA_E4M3 and cache.kv_dtype != code:
-        raise TypeError(f"q is {q.dtype}, the cache {cache.dtype}")
-    if shape[0] != B or D != cache.D:
+        raise TypeError(f"q is {dtype}, the cache {cache.dtype}")
+    if len(shape) == 4:
+        n, T_q, Hq, D = shape
+    elif len(shape) == 3:
+        (n, Hq, D), T_q = shape, 1
+    else:
+        raise ValueError(f"q must be [B, T_q, Hq, D] or [B, Hq, D], not {tuple(shape)}")
+    if n != B or D != cache.D:
         raise ValueError(f"q {tuple(shape)} does not fit {B} sequences of head size {cache.D}")
-    if out.shape != shape or out.dtype != q.dtype or out.get_device() != dev:
+    if out.shape != shape or out.dtype is not dtype or out.get_device() != dev:
         raise ValueError("out must have q's shape, type and device")
     if not (q.is_contiguous() and out.is_contiguous()):
         raise ValueError("q and out must be contiguous")
-    lse_ptr = None
+    lse_ptr = 0
     if lse is not None:
-        import torch
-        if lse.shape != shape[:-1] or lse.dtype is not torch.float32 or not lse.is_contiguous() or lse.get_device() != dev:
+        if lse.shape != shape[:-1] or lse.dtype is not _float32() or not lse.is_contiguous() or lse.get_device() != dev:
             raise ValueError("lse must be contiguous float32 of q's shape without its last dimension")
         lse_ptr = lse.data_ptr()
     if workspace.get_device() != dev:
         raise ValueError("the workspace must be on q's device")
     st = _lib().decode_attn_paged(
-        q.data_ptr(), cache._ref, kv_lens.data_ptr(), block_table.data_ptr(), max_pages, table_stride, B, T_q, Hq, code,
-        1.0 / math.sqrt(D) if scale is None else scale, out.data_ptr(), lse_ptr, workspace.data_ptr(), workspace.nbytes,
-        _raw_stream(stream, dev))
+        _pack_attn(q.data_ptr(), cache._ref, kv_lens.data_ptr(), block_table.data_ptr(), max_pages, table_stride, B, T_q, Hq,
+                   code, 1.0 / math.sqrt(D) if scale is None else scale, out.data_ptr(), lse_ptr, workspace.data_ptr(),
+                   workspace.numel() * workspace.itemsize), _raw_stream(stream, dev))
     if st:
         _fail(st, "decode_attn_paged")
     return out
 
 
-def _rows(x, name, T, heads, D, code, dev):
+def _rows(x, name, T, heads, D, dtype, dev):
     """Check [T, heads, D] rows with contiguous heads; their row stride."""
     stride = x.stride()
-    if x.dim() != 3 or x.shape[0] != T or x.shape[2] != D or (heads is not None and x.shape[1] != heads):
-        raise ValueError(f"{name} must be [T, heads, {D}] with {T} rows, not {tuple(x.shape)}")
-    if stride[2] != 1 or (stride[1] != D and x.shape[1] > 1):
+    if x.shape != (T, heads, D):
+        raise ValueError(f"{name} must be {(T, heads, D)}, not {tuple(x.shape)}")
+    if stride[2] != 1 or (stride[1] != D and heads > 1):
         raise ValueError(f"the heads of a row of {name} must be contiguous")
-    if _codes().get(x.dtype, -1) != code or x.get_device() != dev:
+    if x.dtype is not dtype or x.get_device() != dev:
         raise ValueError(f"{name} must have k's type and device")
-    return stride[0] if T > 1 else x.shape[1] * D   # the stride of a single row is any number
+    return stride[0] if T > 1 else heads * D   # the stride of a single row is any number
 
 
 def decode_attn_paged_append(q, k, v, cache: PagedCache, cu_new, kv_lens, block_table, workspace, *, cos_sin=None,
@@ -225,42 +253,42 @@ def decode_attn_paged_append(q, k, v, cache: PagedCache, cu_new, kv_lens, block_
     [max_pos, rot_dim], or None for no rotation. q_out: like q (q itself to rotate in place);
     returned.
     """
-    import torch
     dev = k.get_device()
     _check_device(dev)
     B, max_pages, table_stride = _check_sequences(cache, kv_lens, block_table, dev)
-    code = _codes().get(k.dtype, -1)
+    dtype = k.dtype
+    code = _codes().get(dtype, -1)
     if code not in (0, 1):
-        raise TypeError(f"k must be float16 or bfloat16, not {k.dtype}")
+        raise TypeError(f"k must be float16 or bfloat16, not {dtype}")
     if cache.kv_dtype != DA_E4M3 and cache.kv_dtype != code:
-        raise TypeError(f"k is {k.dtype}, the cache {cache.dtype}")
+        raise TypeError(f"k is {dtype}, the cache {cache.dtype}")
     T, D = k.shape[0], cache.D
-    k_stride = _rows(k, "k", T, cache.Hkv, D, code, dev)
-    v_stride = _rows(v, "v", T, cache.Hkv, D, code, dev)
-    q_ptr = out_ptr = None
-    q_stride = out_stride = Hq = 0
+    k_stride = _rows(k, "k", T, cache.Hkv, D, dtype, dev)
+    v_stride = _rows(v, "v", T, cache.Hkv, D, dtype, dev)
+    q_ptr = out_ptr = q_stride = out_stride = Hq = 0
     if q is not None:
         if q_out is None:
             raise ValueError("q needs q_out")
+        if q.dim() != 3:
+            raise ValueError(f"q must be [T, Hq, D], not {tuple(q.shape)}")
         Hq = q.shape[1]
-        q_stride, out_stride = _rows(q, "q", T, None, D, code, dev), _rows(q_out, "q_out", T, Hq, D, code, dev)
+        q_stride = _rows(q, "q", T, Hq, D, dtype, dev)
+        out_stride = q_stride if q_out is q else _rows(q_out, "q_out", T, Hq, D, dtype, dev)
         q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
-    if cu_new.dtype is not torch.int32 or cu_new.dim() != 1 or cu_new.shape[0] != B + 1 or not cu_new.is_contiguous() \
-            or cu_new.get_device() != dev:
+    if cu_new.dtype is not _int32() or cu_new.shape != (B + 1,) or not cu_new.is_contiguous() or cu_new.get_device() != dev:
         raise ValueError("cu_new must be contiguous int32 [B + 1]")
     if cos_sin is None:
-        rope, cs_ptr, max_pos, rot = DA_ROPE_NONE, None, 0, 0
+        rope, cs_ptr, max_pos, rot = DA_ROPE_NONE, 0, 0, 0
     else:
-        if cos_sin.dtype is not torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous() \
-                or cos_sin.get_device() != dev:
+        if cos_sin.dtype is not _float32() or cos_sin.dim() != 2 or not cos_sin.is_contiguous() or cos_sin.get_device() != dev:
             raise ValueError("cos_sin must be contiguous float32 [max_pos, rot_dim]")
         cs_ptr, (max_pos, rot) = cos_sin.data_ptr(), cos_sin.shape
-    if workspace.get_device() != dev or workspace.nbytes < 256:
+    if workspace.get_device() != dev or workspace.numel() * workspace.itemsize < 256:
         raise ValueError("the workspace must be on the tensors' device")
     st = _lib().decode_attn_paged_append(
-        q_ptr, q_stride, k.data_ptr(), k_stride, v.data_ptr(), v_stride, cs_ptr, max_pos, rot, rope, cu_new.data_ptr(),
-        kv_lens.data_ptr(), block_table.data_ptr(), max_pages, table_stride, B, T, Hq, code, cache._ref, out_ptr,
-        out_stride, workspace.data_ptr(), _raw_stream(stream, dev))
+        _pack_append(q_ptr, k.data_ptr(), v.data_ptr(), q_stride, k_stride, v_stride, cs_ptr, max_pos, rot, rope,
+                     cu_new.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), max_pages, table_stride, B, T, Hq, code,
+                     cache._ref, out_ptr, out_stride, workspace.data_ptr()), _raw_stream(stream, dev))
     if st:
         _fail(st, "decode_attn_paged_append")
     return q_out

@@ -70,20 +70,48 @@ def cache_struct(**change):
 
 
 def attend(lib, cache={}, **change):
+    from split_kv_decode_decoding_gb300.paged import _pack_attn
     a = {**ATTEND, **change}
     c = cache_struct(**cache) if cache is not None else None
-    return lib.decode_attn_paged(a["q"], None if c is None else ctypes.addressof(c), a["lens"], a["table"], a["max_pages"],
-                                 a["table_stride"], a["B"], a["T_q"], a["Hq"], a["dtype"], a["scale"], a["out"],
-                                 a["lse"], a["ws"], a["ws_bytes"], None)
+    return lib.decode_attn_paged(
+        _pack_attn(a["q"], 0 if c is None else ctypes.addressof(c), a["lens"], a["table"], a["max_pages"], a["table_stride"], a["B"],
+                   a["T_q"], a["Hq"], a["dtype"], a["scale"], a["out"], a["lse"], a["ws"], a["ws_bytes"]), None)
 
 
 def append(lib, cache={}, **change):
+    from split_kv_decode_decoding_gb300.paged import _pack_append
     a = {**APPEND, **change}
     c = cache_struct(**cache) if cache is not None else None
     return lib.decode_attn_paged_append(
-        a["q"], a["q_stride"], a["k"], a["k_stride"], a["v"], a["v_stride"], a["cos_sin"], a["max_pos"], a["rot"], a["rope"],
-        a["cu"], a["lens"], a["table"], a["max_pages"], a["table_stride"], a["B"], a["T"], a["Hq"], a["dtype"],
-        None if c is None else ctypes.addressof(c), a["q_out"], a["q_out_stride"], a["ws"], None)
+        _pack_append(a["q"], a["k"], a["v"], a["q_stride"], a["k_stride"], a["v_stride"], a["cos_sin"], a["max_pos"], a["rot"],
+                     a["rope"], a["cu"], a["lens"], a["table"], a["max_pages"], a["table_stride"], a["B"], a["T"], a["Hq"],
+                     a["dtype"], 0 if c is None else ctypes.addressof(c), a["q_out"], a["q_out_stride"], a["ws"]), None)
+
+
+def test_packed_structs_lie_as_the_header_declares(tmp_path):
+    """Offsets of every field of the two argument structs, from the C compiler, against the binding's formats."""
+    import struct as st
+    import subprocess
+    from split_kv_decode_decoding_gb300 import paged
+    text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+    for name, fmt in (("da_paged_attn", "@PPPPiiiiiifPPPN"), ("da_paged_append", "@PPPqqqPiiiPPPiiiiiiPPqP")):
+        body = re.search(r"typedef struct \{([^}]*)\} " + name + ";", text).group(1)
+        fields = [w.strip(" *") for d in body.split(";") if d.strip() for w in re.sub(r"^\s*(const\s+)?\w+", "", d.strip()).split(",")]
+        assert len(fields) == len(fmt) - 1
+        src = tmp_path / (name + ".c")
+        src.write_text('#include <stdio.h>\n#include "decode_attn_paged.h"\nint main(void) {\n' + "".join(
+            f'printf("%zu ", offsetof({name}, {f}));\n' for f in fields) + f'printf("%zu", sizeof({name}));\nreturn 0; }}\n')
+        exe = tmp_path / name
+        subprocess.run(["gcc", "-I", os.path.dirname(HEADER), "-o", str(exe), str(src)], check=True)
+        got = [int(x) for x in subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()]
+        want = [st.calcsize(fmt[:i + 1] + "0" + fmt[i + 1]) for i in range(len(fields))]
+        assert got[:-1] == want and got[-1] == st.calcsize(fmt + "0P")
+    assert paged._pack_attn(*([0] * 10), 0.0, 0, 0, 0, 0)[:8] == bytes(8)
+
+
+def test_null_arguments(lib):
+    assert lib.decode_attn_paged(None, None) == da.DA_ERR_INVALID_ARG
+    assert lib.decode_attn_paged_append(None, None) == da.DA_ERR_INVALID_ARG
 
 
 ARG, UNSUP, ALIGN, SMALL = da.DA_ERR_INVALID_ARG, da.DA_ERR_UNSUPPORTED, da.DA_ERR_ALIGNMENT, da.DA_ERR_WORKSPACE_TOO_SMALL
