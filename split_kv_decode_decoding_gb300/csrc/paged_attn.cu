@@ -168,11 +168,35 @@ struct Ranges {
     }
 };
 
+// mbar_wait and mbar_wait_warp with their loop kept a loop: unrolled at some twenty places it makes up a
+// third of the kernel's code, and a call on a short sequence spends a microsecond fetching code.
+__device__ __forceinline__ bool wait_lane(uint32_t bar, uint32_t parity, unsigned long long limit_ns) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const unsigned long long t0 = global_ns();
+#pragma unroll 1
+    do {
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
+    } while (global_ns() - t0 <= limit_ns);
+    return false;
+}
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, unsigned long long limit_ns) {
+    const bool ok = wait_lane(bar, parity, limit_ns);
+    return __all_sync(0xffffffffu, ok);
+}
+
 __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 
 __device__ __forceinline__ void fence_acq_rel() { asm volatile("fence.acq_rel.gpu;" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
+    uint32_t v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
 
 // Two e4m3 values to two fp16 values (exact).
 __device__ __forceinline__ void e4m3x4_to_f16(uint32_t x, uint32_t& lo, uint32_t& hi) {
@@ -230,20 +254,26 @@ struct PagedKernel {
         const int per = (p.B + kThreads - 1) / kThreads, b0 = tid * per;
         const int64_t most = static_cast<int64_t>(p.max_pages) * p.P;
         int len[kMost], mine = 0;
-#pragma unroll
-        for (int i = 0; i < kMost; ++i) len[i] = i < per && b0 + i < p.B ? ld_cg_s32(p.lens + b0 + i) : 0;
-#pragma unroll
-        for (int i = 0; i < kMost; ++i) {
-            if (i >= per || b0 + i >= p.B) break;
-            int L = len[i];
+        auto stages = [&](int b, int L) {
             if (L < 0 || L > most) {
                 if (blockIdx.x == 0) flag_error(p.err, DA_DEVERR_SEQLENS);
                 L = 0;
             }
             const int n = L == 0 ? 1 : (L + Sh::kKeys - 1) / Sh::kKeys;   // an empty sequence: one empty stage
-            s.pad[b0 + i] = static_cast<uint8_t>(n * Sh::kKeys - L);
-            len[i] = n;
-            mine += n;
+            s.pad[b] = static_cast<uint8_t>(n * Sh::kKeys - L);
+            return n;
+        };
+        if (per == 1) {
+            if (tid < p.B) mine = len[0] = stages(tid, ld_cg_s32(p.lens + tid));
+        } else {
+#pragma unroll
+            for (int i = 0; i < kMost; ++i) len[i] = i < per && b0 + i < p.B ? ld_cg_s32(p.lens + b0 + i) : 0;
+#pragma unroll
+            for (int i = 0; i < kMost; ++i) {
+                if (i >= per || b0 + i >= p.B) break;
+                len[i] = stages(b0 + i, len[i]);
+                mine += len[i];
+            }
         }
         int run = mine;
 #pragma unroll
@@ -255,19 +285,27 @@ struct PagedKernel {
         __syncthreads();
         int sum = run - mine;
         for (int w = 0; w < warp; ++w) sum += warp_sum[w];
+        if (per == 1) {
+            if (tid < p.B) s.prefix[tid + 1] = sum + len[0];
+        } else {
 #pragma unroll
-        for (int i = 0; i < kMost; ++i) {
-            if (i >= per || b0 + i >= p.B) break;
-            sum += len[i];
-            s.prefix[b0 + i + 1] = sum;
+            for (int i = 0; i < kMost; ++i) {
+                if (i >= per || b0 + i >= p.B) break;
+                sum += len[i];
+                s.prefix[b0 + i + 1] = sum;
+            }
         }
         if (tid == 0) s.prefix[0] = 0;
         // the stages of every sequence, or 0 where they differ
         __syncthreads();
         const int first = s.prefix[1];
         bool same = true;
+        if (per == 1) {
+            same = tid >= p.B || len[0] == first;
+        } else {
 #pragma unroll
-        for (int i = 0; i < kMost; ++i) same = same && (i >= per || b0 + i >= p.B || len[i] == first);
+            for (int i = 0; i < kMost; ++i) same = same && (i >= per || b0 + i >= p.B || len[i] == first);
+        }
         same = __syncthreads_and(same);
         if (tid == 0) s.prefix[p.B + 1] = same ? first : 0;
         __syncthreads();
@@ -310,16 +348,12 @@ struct PagedKernel {
         return x;
     }
 
-    static __device__ __forceinline__ void copy_box(const PagedParams& p, uint32_t dst, const CUtensorMap* map, int page,
-                                                    int slot, int kvh, uint32_t bar) {
+    // Copy one box of keys or values to `dst`.
+    static __device__ __forceinline__ void copy_box(const PagedParams& p, uint32_t dst, const CUtensorMap* map, int c1, int c2,
+                                                    uint32_t bar) {
         constexpr int kInner = Sh::kSliceRow / (KV8 ? 1 : 2);
 #pragma unroll
-        for (int hf = 0; hf < Sh::kSlices; ++hf) {
-            if (p.layout == DA_LAYOUT_VARLEN)
-                tma_load_3d(dst + hf * Sh::kSliceBytes, map, hf * kInner, kvh, page * p.P + slot, bar);
-            else
-                tma_load_3d(dst + hf * Sh::kSliceBytes, map, hf * kInner, slot, page * p.Hkv + kvh, bar);
-        }
+        for (int hf = 0; hf < Sh::kSlices; ++hf) tma_load_3d(dst + hf * Sh::kSliceBytes, map, hf * kInner, c1, c2, bar);
     }
 
     static __device__ void producer(const Layout& s, const PagedParams& p, const CUtensorMap* tmK, const CUtensorMap* tmV,
@@ -385,7 +419,7 @@ struct PagedKernel {
         };
         auto publish = [&](uint32_t i, const PagedItem& it) -> bool {
             const int slot = i % kItemSlots;
-            if (!mbar_wait_warp(s.iempty0 + 8 * slot, ((i / kItemSlots) & 1) ^ 1, p.wait_limit_ns)) {
+            if (!wait_warp(s.iempty0 + 8 * slot, ((i / kItemSlots) & 1) ^ 1, p.wait_limit_ns)) {
                 if (lane == 0) flag_error(p.err, DA_DEVERR_TIMEOUT);
                 return false;
             }
@@ -410,53 +444,60 @@ struct PagedKernel {
         };
 
         PagedItem item;
+        item.valid = 0;
         int st = 0;
         uint32_t ph = 0;
-        next_piece(item);
-        if (!publish(0, item) || !item.valid) return;
-        Box cur = load_box(p, item, lane), nxt;
         const int per_stage = Sh::kKeys / p.box_keys;
-        for (uint32_t i = 0; item.valid; ++i) {
-            nxt = load_box(p, item, 32 + lane);
-            bool ok = true;
-            for (int t = 0; t < item.ntiles; ++t) {
-                const int box0 = t * per_stage;
-                if (t > 0 && box0 % 32 == 0) {
-                    cur = nxt;
-                    nxt = load_box(p, item, box0 + 32 + lane);
-                }
-                if (!mbar_wait_warp(s.empty0 + 8 * st, ph ^ 1, p.wait_limit_ns)) {
+        for (uint32_t i = 0;; ++i) {
+            // the next piece's descriptor, queries and table entries go out before the last one's merge
+            PagedItem next;
+            next_piece(next);
+            if (!publish(i, next)) return;
+            Box cur = {};
+            if (next.valid) cur = load_box(p, next, lane);
+            if (item.valid) {
+                // hand the consumers the next stage, empty, for that merge
+                if (!wait_warp(s.empty0 + 8 * st, ph ^ 1, p.wait_limit_ns)) {
                     if (lane == 0) flag_error(p.err, DA_DEVERR_TIMEOUT);
-                    ok = false;
-                    break;
+                    return;
                 }
+                if (lane == 0) mbar_arrive(s.full0 + 8 * st);
+                if (++st == kStages) {
+                    st = 0;
+                    ph ^= 1;
+                }
+            }
+            if (!next.valid) return;
+            item = next;
+            Box ahead = load_box(p, item, 32 + lane);   // the next batch of boxes
+            for (int t = 0; t < item.ntiles; ++t) {
+                const int box0 = t * per_stage, in32 = box0 % 32;
+                if (t > 0 && in32 == 0) {
+                    cur = ahead;
+                    ahead = load_box(p, item, box0 + 32 + lane);
+                }
+                if (!wait_warp(s.empty0 + 8 * st, ph ^ 1, p.wait_limit_ns)) {
+                    if (lane == 0) flag_error(p.err, DA_DEVERR_TIMEOUT);
+                    return;
+                }
+                // A full stage in boxes of box_keys keys, the ragged end of a sequence in 16-key boxes up to it:
+                // lane l copies box l.
                 const int keys = min(Sh::kKeys, item.nkeys - t * Sh::kKeys);
+                const bool full = keys == Sh::kKeys;
+                const int box = full ? p.box_keys : 16, boxes = full ? per_stage : (keys + 15) / 16;
                 const uint32_t fb = s.full0 + 8 * st;
-                const uint32_t kdst = s.ring + st * Sh::kStageBytes;
-                const uint32_t vdst = kdst + Sh::kTileBytes;
-                const int key = item.key0 + t * Sh::kKeys;
-                const int nbox16 = (keys + 15) / 16;
-                if (lane == 0)
-                    mbar_expect_tx(fb, 2 * (keys == Sh::kKeys ? Sh::kTileBytes : nbox16 * 16 * Sh::kRowBytes));
+                if (lane == 0) mbar_expect_tx(fb, 2 * boxes * box * Sh::kRowBytes);
                 __syncwarp();
-                const int in32 = box0 % 32;
-                if (keys == Sh::kKeys) {
-                    // a full stage: the lanes that hold its boxes copy them
-                    const int i0 = lane - in32;
-                    if (i0 >= 0 && i0 < per_stage) {
-                        const int off = i0 * p.box_keys;
-                        const int slot = key + off - p.page(key + off) * p.P;
-                        copy_box(p, kdst + off * Sh::kSliceRow, tmK, cur.page, slot, item.kvh, fb);
-                        copy_box(p, vdst + off * Sh::kSliceRow, tmV, cur.page, slot, item.kvh, fb);
-                    }
-                } else {
-                    // the ragged end of a sequence: 16-key boxes up to it
-                    const int page = __shfl_sync(0xffffffffu, cur.page, (in32 + lane * 16 / p.box_keys) & 31);
-                    if (lane < nbox16) {
-                        const int slot = key + lane * 16 - p.page(key + lane * 16) * p.P;
-                        copy_box(p, kdst + lane * 16 * Sh::kSliceRow, tmK16, page, slot, item.kvh, fb);
-                        copy_box(p, vdst + lane * 16 * Sh::kSliceRow, tmV16, page, slot, item.kvh, fb);
-                    }
+                const int off = lane * box;
+                const int page = __shfl_sync(0xffffffffu, cur.page, (in32 + off / p.box_keys) & 31);
+                if (lane < boxes) {
+                    const int pos = item.key0 + t * Sh::kKeys + off;
+                    const int slot = pos - p.page(pos) * p.P;
+                    const bool thd = p.layout == DA_LAYOUT_VARLEN;
+                    const int c1 = thd ? item.kvh : slot, c2 = thd ? page * p.P + slot : page * p.Hkv + item.kvh;
+                    const uint32_t dst = s.ring + st * Sh::kStageBytes + off * Sh::kSliceRow;
+                    copy_box(p, dst, full ? tmK : tmK16, c1, c2, fb);
+                    copy_box(p, dst + Sh::kTileBytes, full ? tmV : tmV16, c1, c2, fb);
                 }
                 if constexpr (KV8) {
                     // the scales of the stage's 16-key boxes
@@ -472,10 +513,9 @@ struct PagedKernel {
                     ph ^= 1;
                 }
             }
-            if (!ok) return;
             if (item.part >= 0) {
-                // which ranges hold the others, for the consumers' end of the piece (they read it after the
-                // hand-over below)
+                // which ranges hold the other parts, for the consumers' end of the piece (they read it after the
+                // hand-over above)
                 int first, count;
                 ranges.parts(s.prefix[item.b], s.prefix[item.b + 1], first, count);
                 if (lane == 0) {
@@ -484,22 +524,6 @@ struct PagedKernel {
                     at->nparts = count;
                 }
             }
-            // the next piece's descriptor, queries and table entries go out before this one's merge
-            PagedItem next;
-            next_piece(next);
-            if (!publish(i + 1, next)) return;
-            if (next.valid) cur = load_box(p, next, lane);
-            // hand the consumers the next stage, empty, for this piece's merge
-            if (!mbar_wait_warp(s.empty0 + 8 * st, ph ^ 1, p.wait_limit_ns)) {
-                if (lane == 0) flag_error(p.err, DA_DEVERR_TIMEOUT);
-                return;
-            }
-            if (lane == 0) mbar_arrive(s.full0 + 8 * st);
-            if (++st == kStages) {
-                st = 0;
-                ph ^= 1;
-            }
-            item = next;
         }
     }
 
@@ -639,150 +663,163 @@ struct PagedKernel {
         return (static_cast<int64_t>(it.b) * p.tq + c / p.G) * p.Hq + it.kvh * p.G + c % p.G;
     }
 
-    // One finished column: four dims of its output, and its lse (log2).
-    static __device__ __forceinline__ void store_output(const PagedParams& p, int64_t row, int d0, const float4& o,
-                                                        float lse2) {
-        *reinterpret_cast<uint2*>(p.out + row * D + d0) = make_uint2(pack2<DT>(o.x, o.y), pack2<DT>(o.z, o.w));
-        if (p.lse != nullptr && d0 == 0) p.lse[row] = lse2 * kLn2;
+    // Outputs are written by half a warp per column: the halves of warp w have columns w and w + 4 of an
+    // n-tile. A lane has kVec times four dims, 64 v + 4 (lane % 16) on.
+    static constexpr int kVec = D / 64;
+
+    // One finished column: its output, and its lse (log2).
+    static __device__ __forceinline__ void store_output(const PagedParams& p, int64_t row, const float4 (&o)[kVec], float lse2) {
+        const int l16 = threadIdx.x & 15;
+#pragma unroll
+        for (int v = 0; v < kVec; ++v)
+            *reinterpret_cast<uint2*>(p.out + row * D + 64 * v + 4 * l16) =
+                make_uint2(pack2<DT>(o[v].x, o[v].y), pack2<DT>(o[v].z, o[v].w));
+        if (p.lse != nullptr && l16 == 0) p.lse[row] = lse2 * kLn2;
     }
 
-    // Columns 8n .. 8n + 7 of a piece from the four warps' states: warp w writes columns w and w + 4.
-    static __device__ __forceinline__ void write_piece(const PagedParams& p, const PagedItem& it, const float* red_acc, int n) {
+    // Where part j of a (sequence, head)'s column lies, in units of columns: j = 0 is the part with the first
+    // key, which its range left in its second place (a range's first place is for the end of a sequence).
+    static __device__ __forceinline__ int64_t part_row(const PagedParams& p, int first_share, int j, int col) {
+        return static_cast<int64_t>(j == 0 ? 2 * first_share + 1 : 2 * (first_share + j * p.lanes)) * Sh::kCols + col;
+    }
+
+    static __device__ __forceinline__ void scale4(float4& a, float by) {
+        a.x *= by;
+        a.y *= by;
+        a.z *= by;
+        a.w *= by;
+    }
+    static __device__ __forceinline__ void fma4(float4& a, float w, const float4& b) {
+        a.x = fmaf(w, b.x, a.x);
+        a.y = fmaf(w, b.y, a.y);
+        a.z = fmaf(w, b.z, a.z);
+        a.w = fmaf(w, b.w, a.w);
+    }
+
+    // Columns 8n .. 8n + 7 of a piece from the four warps' states. With `direct` the piece is the first of two
+    // parts and the second one is written: they are merged here, in the order and with the roundings of merge_parts.
+    static __device__ __forceinline__ void write_piece(const PagedParams& p, const PagedItem& it, const float* red_acc, int n,
+                                                       bool direct) {
         const float* red_m = red_acc + Sh::kMergeFloats;
         const float* red_mv = red_m + kConsumerWarps * 8;
         const float* red_l = red_mv + kConsumerWarps * 8;
-        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-        constexpr int kLanes = D / 4, kHeads = 32 / kLanes;
-        const int d0 = (lane % kLanes) * 4;
+        const int l16 = threadIdx.x & 15;
+        const int hh = (threadIdx.x >> 5) + kConsumerWarps * ((threadIdx.x >> 4) & 1), col = 8 * n + hh;
+        const bool live = col < it.nh;
+        float lse1 = -INFINITY;
+        float4 o1[kVec];
+        if (direct && live) {
+            const int64_t at = part_row(p, it.first_share, 1, col);
+            lse1 = __ldcg(p.part_lse + at);
 #pragma unroll
-        for (int pass = 0; pass < 2 / kHeads; ++pass) {
-            const int hh = warp + kConsumerWarps * (pass * kHeads + lane / kLanes);
-            float M = kNoKey, Mv = kNoKey;
+            for (int v = 0; v < kVec; ++v) o1[v] = __ldcg(reinterpret_cast<const float4*>(p.part + at * D + 64 * v + 4 * l16));
+        }
+        float M = kNoKey, Mv = kNoKey;
 #pragma unroll
-            for (int w = 0; w < kConsumerWarps; ++w) {
-                M = fmaxf(M, red_m[w * 8 + hh]);
-                Mv = fmaxf(Mv, red_mv[w * 8 + hh]);
-            }
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            float l = 0.f;
+        for (int w = 0; w < kConsumerWarps; ++w) {
+            M = fmaxf(M, red_m[w * 8 + hh]);
+            if constexpr (KV8) Mv = fmaxf(Mv, red_mv[w * 8 + hh]);
+        }
+        float4 o[kVec];
 #pragma unroll
-            for (int w = 0; w < kConsumerWarps; ++w) {
-                l = fmaf(fast_exp2(red_m[w * 8 + hh] - M), red_l[w * 8 + hh], l);
-                const float wt = fast_exp2(red_mv[w * 8 + hh] - Mv);
-                const float4 a = *reinterpret_cast<const float4*>(red_acc + (w * 8 + hh) * Sh::kMergeRow + d0);
-                o.x = fmaf(wt, a.x, o.x);
-                o.y = fmaf(wt, a.y, o.y);
-                o.z = fmaf(wt, a.z, o.z);
-                o.w = fmaf(wt, a.w, o.w);
+        for (int v = 0; v < kVec; ++v) o[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+        float l = 0.f;
+#pragma unroll
+        for (int w = 0; w < kConsumerWarps; ++w) {
+            const float wl = fast_exp2(red_m[w * 8 + hh] - M);
+            const float wt = KV8 ? fast_exp2(red_mv[w * 8 + hh] - Mv) : wl;
+            l = fmaf(wl, red_l[w * 8 + hh], l);
+            const float* row = red_acc + (w * 8 + hh) * Sh::kMergeRow + 4 * l16;
+#pragma unroll
+            for (int v = 0; v < kVec; ++v) fma4(o[v], wt, *reinterpret_cast<const float4*>(row + 64 * v));
+        }
+        const bool none = M == kNoKey;   // the column saw no key: output 0, lse -inf
+        // l >= 1 otherwise (the key that set M weighs 1). In 8-bit pages o is relative to Mv, l to M.
+        float inv = none ? 0.f : 1.f / l;
+        if constexpr (KV8) inv *= Mv == kNoKey ? 0.f : fast_exp2(Mv - M);
+#pragma unroll
+        for (int v = 0; v < kVec; ++v) scale4(o[v], inv);
+        float lse2 = none ? -INFINITY : M + fast_log2(l);
+        if (!live) return;
+        if (direct) {
+            const float m = fmaxf(kNoKey, fmaxf(lse2, lse1));
+            const float w0 = fast_exp2(lse2 - m), w1 = fast_exp2(lse1 - m), z = w0 + w1;
+            const float by = m == kNoKey ? 0.f : 1.f / z;
+#pragma unroll
+            for (int v = 0; v < kVec; ++v) {
+                scale4(o[v], w0);
+                fma4(o[v], w1, o1[v]);
+                scale4(o[v], by);
             }
-            const bool none = M == kNoKey;   // the column saw no key: output 0, lse -inf
-            // l >= 1 otherwise (the key that set M weighs 1). In 8-bit pages o is relative to Mv, l to M.
-            float inv = none ? 0.f : 1.f / l;
-            if constexpr (KV8) inv *= Mv == kNoKey ? 0.f : fast_exp2(Mv - M);
-            o.x *= inv;
-            o.y *= inv;
-            o.z *= inv;
-            o.w *= inv;
-            const float lse2 = none ? -INFINITY : M + log2f(l);
-            const int col = 8 * n + hh;
-            if (col < it.nh) {
-                if (it.part < 0) {
-                    store_output(p, output_row(p, it, col), d0, o, lse2);
-                } else {
-                    const int64_t at = static_cast<int64_t>(it.part) * Sh::kCols + col;
-                    *reinterpret_cast<float4*>(p.part + at * D + d0) = o;
-                    if (d0 == 0) p.part_lse[at] = lse2;
-                }
-            }
+            lse2 = m == kNoKey ? -INFINITY : m + fast_log2(z);
+        }
+        if (it.part < 0 || direct) {
+            store_output(p, output_row(p, it, col), o, lse2);
+        } else {
+            const int64_t at = static_cast<int64_t>(it.part) * Sh::kCols + col;
+#pragma unroll
+            for (int v = 0; v < kVec; ++v) *reinterpret_cast<float4*>(p.part + at * D + 64 * v + 4 * l16) = o[v];
+            if (l16 == 0) p.part_lse[at] = lse2;
         }
     }
 
-    // Merge this warp's columns of a (sequence, head) whose partials are all written, two columns at a
-    // time. Lane j takes part j's lse and weight, so that every load is issued before any of them is
-    // needed; the order of the sums is that of the parts.
+    // Merge this warp's columns of a (sequence, head) whose partials are all written. Lane j of a half warp
+    // takes part j's lse and weight, so that every load is issued before any of them is needed; the order
+    // of the sums is that of the parts.
     static __device__ __forceinline__ void merge_parts(const PagedParams& p, const PagedItem& it) {
-        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-        constexpr int kLanes = D / 4, kHalves = 32 / kLanes;   // head size 64: each half warp takes every other part
-        constexpr int kAhead = NT == 1 ? 8 : 4;                // loads in flight per lane and column
-        const int d0 = (lane % kLanes) * 4, half = lane / kLanes;
-        const int nparts = it.nparts, nh = it.nh;
-        for (int c0 = warp; c0 < nh; c0 += 2 * kConsumerWarps) {
-            const int cols = c0 + kConsumerWarps < nh ? 2 : 1;
-            float m[2] = {kNoKey, kNoKey}, z[2] = {0.f, 0.f};
-            float4 acc[2];
-            acc[0] = acc[1] = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int j0 = 0; j0 < nparts; j0 += 32) {
-                const int count = min(32, nparts - j0);
-                auto row_of = [&](int j, int c) -> int64_t {
-                    const int part = j == 0 ? 2 * it.first_share + 1 : 2 * (it.first_share + j * p.lanes);
-                    return static_cast<int64_t>(part) * Sh::kCols + c0 + kConsumerWarps * c;
-                };
-                float lv[2], w[2];
-                float4 o[2][kAhead];
-                auto load = [&](int j) {
+        constexpr int kAhead = NT == 1 ? 8 / kVec : 4 / kVec;   // parts in flight
+        const int l16 = threadIdx.x & 15, nparts = it.nparts, nh = it.nh, first_share = it.first_share;
+#pragma unroll 1
+        for (int c = (threadIdx.x >> 5) + kConsumerWarps * ((threadIdx.x >> 4) & 1); c - 4 * static_cast<int>((threadIdx.x >> 4) & 1) < nh;
+             c += 8) {
+            const bool live = c < nh;
+            float m = kNoKey, z = 0.f;
+            float4 acc[kVec];
 #pragma unroll
-                    for (int c = 0; c < 2; ++c)
+            for (int v = 0; v < kVec; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+            for (int j0 = 0; j0 < nparts; j0 += 16) {
+                const int count = live ? min(16, nparts - j0) : 0;
+                const float lv = l16 < count ? __ldcg(p.part_lse + part_row(p, first_share, j0 + l16, c)) : -INFINITY;
+                float w = 0.f;
+#pragma unroll 1
+                for (int j = 0; j < min(16, nparts - j0); j += kAhead) {
+                    float4 o[kAhead][kVec];
 #pragma unroll
-                        for (int i = 0; i < kAhead; ++i) {
-                            const int kk = j + i * kHalves + half;
-                            if (kk < count && c < cols)
-                                o[c][i] = __ldcg(reinterpret_cast<const float4*>(p.part + row_of(j0 + kk, c) * D + d0));
-                        }
-                };
+                    for (int i = 0; i < kAhead; ++i) {
+                        const float* at = p.part + part_row(p, first_share, j0 + j + i, c) * D + 4 * l16;
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
-                    lv[c] = lane < count && c < cols ? __ldcg(p.part_lse + row_of(j0 + lane, c)) : -INFINITY;
-                load(0);
+                        for (int v = 0; v < kVec; ++v)
+                            o[i][v] = j + i < count ? __ldcg(reinterpret_cast<const float4*>(at + 64 * v)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
+                    if (j == 0) {
+                        float top = lv;
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    float top = lv[c];
+                        for (int off = 8; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+                        const float mn = fmaxf(m, top);       // stays kNoKey while no part has seen a key
+                        w = fast_exp2(lv - mn);
+                        float sum = w;
 #pragma unroll
-                    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-                    const float mn = fmaxf(m[c], top);       // stays kNoKey while no part has seen a key
-                    w[c] = fast_exp2(lv[c] - mn);
-                    float sum = w[c];
+                        for (int off = 8; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+                        const float al = fast_exp2(m - mn);
+                        m = mn;
+                        z = fmaf(z, al, sum);
 #pragma unroll
-                    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-                    const float al = fast_exp2(m[c] - mn);
-                    m[c] = mn;
-                    z[c] = fmaf(z[c], al, sum);
-                    acc[c].x *= al;
-                    acc[c].y *= al;
-                    acc[c].z *= al;
-                    acc[c].w *= al;
-                }
-                for (int j = 0; j < count; j += kAhead * kHalves) {
-                    if (j > 0) load(j);
+                        for (int v = 0; v < kVec; ++v) scale4(acc[v], al);
+                    }
 #pragma unroll
-                    for (int c = 0; c < 2; ++c)
+                    for (int i = 0; i < kAhead; ++i) {
+                        const float wi = __shfl_sync(0xffffffffu, w, (j + i) & 15, 16);
 #pragma unroll
-                        for (int i = 0; i < kAhead; ++i) {
-                            const int kk = j + i * kHalves + half;
-                            const float wk = __shfl_sync(0xffffffffu, w[c], kk & 31);
-                            if (kk < count && c < cols) {
-                                acc[c].x = fmaf(wk, o[c][i].x, acc[c].x);
-                                acc[c].y = fmaf(wk, o[c][i].y, acc[c].y);
-                                acc[c].z = fmaf(wk, o[c][i].z, acc[c].z);
-                                acc[c].w = fmaf(wk, o[c][i].w, acc[c].w);
-                            }
-                        }
+                        for (int v = 0; v < kVec; ++v) fma4(acc[v], wi, o[i][v]);
+                    }
                 }
             }
+            const bool none = m == kNoKey;
+            const float inv = none ? 0.f : 1.f / z;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                if constexpr (kHalves == 2) {
-                    acc[c].x += __shfl_xor_sync(0xffffffffu, acc[c].x, 16);
-                    acc[c].y += __shfl_xor_sync(0xffffffffu, acc[c].y, 16);
-                    acc[c].z += __shfl_xor_sync(0xffffffffu, acc[c].z, 16);
-                    acc[c].w += __shfl_xor_sync(0xffffffffu, acc[c].w, 16);
-                }
-                const bool none = m[c] == kNoKey;
-                const float inv = none ? 0.f : 1.f / z[c];
-                if (half == 0 && c < cols)
-                    store_output(p, output_row(p, it, c0 + kConsumerWarps * c), d0,
-                                 make_float4(acc[c].x * inv, acc[c].y * inv, acc[c].z * inv, acc[c].w * inv),
-                                 none ? -INFINITY : m[c] + log2f(z[c]));
-            }
+            for (int v = 0; v < kVec; ++v) scale4(acc[v], inv);
+            if (live) store_output(p, output_row(p, it, c), acc, none ? -INFINITY : m + fast_log2(z));
         }
     }
 
@@ -796,7 +833,7 @@ struct PagedKernel {
         int merges = 0;
         for (uint32_t i = 0;; ++i) {
             const int slot = i % kItemSlots;
-            if (!mbar_wait_warp(s.ifull0 + 8 * slot, (i / kItemSlots) & 1, p.wait_limit_ns)) {
+            if (!wait_warp(s.ifull0 + 8 * slot, (i / kItemSlots) & 1, p.wait_limit_ns)) {
                 if (lane == 0) flag_error(p.err, DA_DEVERR_TIMEOUT);
                 ok = false;
                 break;
@@ -835,7 +872,7 @@ struct PagedKernel {
 
             for (int t = 0; t < ntiles; ++t) {
                 const uint32_t fb = s.full0 + 8 * st;
-                if (ok && !mbar_wait_warp(fb, ph, p.wait_limit_ns)) {
+                if (ok && !wait_warp(fb, ph, p.wait_limit_ns)) {
                     ok = false;
                     bad_bar = fb;
                     bad_ph = ph;
@@ -950,18 +987,26 @@ struct PagedKernel {
                     for (int off = 4; off < 32; off <<= 1) l[n][c] += __shfl_xor_sync(0xffffffffu, l[n][c], off);
 
             // ---- merge the four warps in the stage that the producer handed over, 8 columns a round
-            if (ok && !mbar_wait_warp(s.full0 + 8 * st, ph, p.wait_limit_ns)) {
+            if (ok && !wait_warp(s.full0 + 8 * st, ph, p.wait_limit_ns)) {
                 ok = false;
                 if (lane == 0) flag_error(p.err, DA_DEVERR_TIMEOUT);
             }
+            // A range ends with the beginning of a sequence, whose end the next range began with: where that is
+            // all of it, it is written by now, and this piece needs no partial result of its own (8-column
+            // kernels: the others have no registers for it).
+            uint32_t* count = p.arrived + item.first_share * kConsumerWarps + warp;
+            const bool two = NT == 1 && item.part >= 0 && (item.part & 1) != 0 && item.nparts == 2;
+            uint32_t arrived = 0;
+            if (two && lane == 0) arrived = ld_acquire(count);
             float* red = reinterpret_cast<float*>(s.smem + st * Sh::kStageBytes);
+            bool direct = false;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 if (n > 0) {
                     // every warp has read the previous round's rows
                     __syncwarp();
                     if (lane == 0) mbar_arrive(s.mdone);
-                    if (ok && !mbar_wait_warp(s.mdone, md & 1, p.wait_limit_ns)) {
+                    if (ok && !wait_warp(s.mdone, md & 1, p.wait_limit_ns)) {
                         ok = false;
                         if (lane == 0) flag_error(p.err, DA_DEVERR_TIMEOUT);
                     }
@@ -988,12 +1033,13 @@ struct PagedKernel {
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(s.mfull);
-                if (ok && !mbar_wait_warp(s.mfull, mz & 1, p.wait_limit_ns)) {
+                if (ok && !wait_warp(s.mfull, mz & 1, p.wait_limit_ns)) {
                     ok = false;
                     if (lane == 0) flag_error(p.err, DA_DEVERR_TIMEOUT);
                 }
                 ++mz;
-                if (ok) write_piece(p, item, red, n);
+                if (NT == 1) direct = __shfl_sync(0xffffffffu, arrived, 0) == 1;
+                if (ok) write_piece(p, item, red, n, direct);
             }
             // release the stage: order these generic-proxy stores before the copy that refills it
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -1004,13 +1050,14 @@ struct PagedKernel {
                 ph ^= 1;
             }
             if (!ok) break;
-            if (item.part >= 0) {
+            if (direct) {
+                if (lane == 0) *count = 0;
+            } else if (item.part >= 0) {
                 // Warp w wrote the same columns of every partial, so the four warps count apart: the
                 // one whose arrival completes the count merges its columns, and sets the count back.
                 uint32_t n = 0;
                 __syncwarp();
                 if (lane == 0) {
-                    uint32_t* count = p.arrived + item.first_share * kConsumerWarps + warp;
                     fence_acq_rel();
                     n = atomicAdd(count, 1u) + 1;
                     if (n == static_cast<uint32_t>(item.nparts)) {
@@ -1033,7 +1080,7 @@ struct PagedKernel {
         for (int i = 0; i < merges; ++i) merge_parts(p, *last_of(s, warp, i));
         // after a timed-out wait, a copy still in flight into this CTA's shared memory gets one more
         // bounded wait before the CTA exits
-        if (!ok && bad_bar != 0) mbar_wait(bad_bar, bad_ph, p.wait_limit_ns);
+        if (!ok && bad_bar != 0) wait_lane(bad_bar, bad_ph, p.wait_limit_ns);
     }
 };
 
