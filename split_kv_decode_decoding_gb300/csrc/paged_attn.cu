@@ -41,7 +41,8 @@ namespace da_impl {
 
 constexpr int kPagedShares = 2048;   // bound of (range, chunk) pairs, each with two partial results
 constexpr size_t kPagedCounterBytes = static_cast<size_t>(kPagedShares) * kConsumerWarps * 4;
-constexpr int kMinRange = 2;         // units per range at least
+constexpr int kMinRange = 2;         // units per range at least (twice as many in a batch of unequal lengths),
+constexpr int kMinCut = 8;           //   where an even batch's sequences have so many: shorter ones stay whole
 constexpr int kAlignRange = 16;      // up to here ranges of an even batch follow its (sequence, head)s
 constexpr int kMaxSlack = 4;         // units that a cut may move to avoid a partial result
 constexpr float kNoKey = -1e30f;     // running maximum of a column that has seen no key (finite: no NaN arises)
@@ -131,7 +132,7 @@ struct Ranges {
         const int by = lane == 0 ? one : slots;
         const int share = (u + by - 1) / by;
         // one range per SM while it is short, then all slots
-        int size = max(kMinRange, __shfl_sync(0xffffffffu, share, 0));
+        int size = max(t >= kMinCut ? kMinRange : 2 * kMinRange, __shfl_sync(0xffffffffu, share, 0));
         if (size > (t >= size ? kAlignRange : short_range)) size = max(short_range, __shfl_sync(0xffffffffu, share, 1));
         const int num = lane == 0 ? u + size - 1 : lane == 1 ? t : size + t - 1;
         const int quot = num / (lane == 2 ? max(t, 1) : size);
@@ -313,7 +314,7 @@ struct PagedKernel {
 
     // Up to this many units a range has an SM to itself, from there on as many run as fit: a stage takes about
     // as long at head size 64 as at 128, for half the bytes.
-    static constexpr int kShortRange = D == 128 ? 8 : 4;
+    static constexpr int kShortRange = D == 128 ? 8 : 3;
 
     static __device__ __forceinline__ Ranges cut(const Layout& s, const PagedParams& p) {
         return Ranges(s.prefix[p.B], s.prefix[p.B + 1], p.slots, p.one, kShortRange);
@@ -588,8 +589,13 @@ struct PagedKernel {
         const int lane = threadIdx.x & 31, mi = lane >> 3, r8 = lane & 7;
         const int row = row0 + (mi & 1) * 8 + r8;
         if constexpr (KV8) {
+            // two chains where there is one n-tile (more give each box as many anyway)
+            constexpr int kChains = NT == 1 ? 2 : 1;
+            float y[NT][kChains][4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) x[n][0] = x[n][1] = x[n][2] = x[n][3] = 0.f;
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int c = 0; c < kChains; ++c) y[n][c][0] = y[n][c][1] = y[n][c][2] = y[n][c][3] = 0.f;
 #pragma unroll
             for (int kk = 0; kk < D / 32; ++kk) {
                 uint32_t w[4];   // rows lo / hi of 16 dims, then of the next 16
@@ -600,9 +606,14 @@ struct PagedKernel {
                     e4m3x4_to_f16(w[2 * h], a[0], a[2]);
                     e4m3x4_to_f16(w[2 * h + 1], a[1], a[3]);
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) mma_16816<DA_F16>(x[n], a, qf[2 * kk + h][n][0], qf[2 * kk + h][n][1]);
+                    for (int n = 0; n < NT; ++n)
+                        mma_16816<DA_F16>(y[n][h % kChains], a, qf[2 * kk + h][n][0], qf[2 * kk + h][n][1]);
                 }
             }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[n][j] = kChains == 2 ? y[n][0][j] + y[n][kChains - 1][j] : y[n][0][j];
         } else {
             float y[NT][4];   // two independent chains
 #pragma unroll
@@ -767,7 +778,7 @@ struct PagedKernel {
     // takes part j's lse and weight, so that every load is issued before any of them is needed; the order
     // of the sums is that of the parts.
     static __device__ __forceinline__ void merge_parts(const PagedParams& p, const PagedItem& it) {
-        constexpr int kAhead = NT == 1 ? 8 / kVec : 4 / kVec;   // parts in flight
+        constexpr int kAhead = NT == 1 ? 16 / kVec : 4 / kVec;   // parts in flight
         const int l16 = threadIdx.x & 15, nparts = it.nparts, nh = it.nh, first_share = it.first_share;
 #pragma unroll 1
         for (int c = (threadIdx.x >> 5) + kConsumerWarps * ((threadIdx.x >> 4) & 1); c - 4 * static_cast<int>((threadIdx.x >> 4) & 1) < nh;

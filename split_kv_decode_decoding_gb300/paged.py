@@ -63,43 +63,28 @@ def _fail(status: int, where: str) -> None:
     raise DecodeAttnError(status, where)
 
 
-_torch = None
+# torch's types and device queries, looked up on first use (importing the binding does not import torch)
+_int32 = _float32 = _codes = _current_device = _current_stream = None
 
 
-def _types():
-    """torch's types by name, looked up on first use (importing the binding does not import torch)."""
-    global _torch
-    if _torch is None:
-        import torch
-        _torch = (torch.int32, torch.float32,
-                  {torch.float16: 0, torch.bfloat16: 1, torch.float8_e4m3fn: DA_E4M3})
-    return _torch
-
-
-def _int32():
-    return _types()[0]
-
-
-def _float32():
-    return _types()[1]
-
-
-def _codes():
-    return _types()[2]
+def _init() -> None:
+    global _int32, _float32, _codes, _current_device, _current_stream
+    import torch
+    _int32, _float32 = torch.int32, torch.float32
+    _current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+    _codes = {torch.float16: 0, torch.bfloat16: 1, torch.float8_e4m3fn: DA_E4M3}
 
 
 def _raw_stream(stream, device: int) -> int:
     if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(device)
+        return _current_stream(device)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _check_device(device: int) -> None:
-    import torch
     if device < 0:
         raise ValueError("tensors must be CUDA tensors")
-    if device != torch._C._cuda_getDevice():
+    if device != _current_device():
         raise ValueError(f"tensors are on cuda:{device}, which is not the current device")
 
 
@@ -112,10 +97,11 @@ class PagedCache:
     """
 
     def __init__(self, k, v, k_scale=None, v_scale=None, *, layout: int = 0):
-        import torch
+        if _codes is None:
+            _init()
         if layout not in (0, 1):
             raise ValueError(f"unknown layout {layout}")
-        code = _codes().get(k.dtype)
+        code = _codes.get(k.dtype)
         if code is None:
             raise TypeError(f"k must be float16, bfloat16 or float8_e4m3fn, not {k.dtype}")
         if v.dtype != k.dtype or v.shape != k.shape or k.dim() != 4:
@@ -129,7 +115,7 @@ class PagedCache:
         page_size, heads = (k.shape[1], k.shape[2]) if layout == 0 else (k.shape[2], k.shape[1])
         if code == DA_E4M3:
             for s in (k_scale, v_scale):
-                if s is None or s.dtype != torch.float32 or tuple(s.shape) != (pages, heads) or not s.is_contiguous() \
+                if s is None or s.dtype is not _float32 or tuple(s.shape) != (pages, heads) or not s.is_contiguous() \
                         or s.get_device() != self.device:
                     raise ValueError("float8 pages need contiguous float32 scales [num_pages, Hkv] on the pages' device")
         else:
@@ -161,6 +147,8 @@ def paged_workspace_size(T_q: int, Hq: int, Hkv: int, D: int) -> int:
 def alloc_paged_workspace(T_q: int, Hq: int, Hkv: int, D: int, device="cuda", stream=None):
     """Allocate (through PyTorch) and initialise a workspace for calls with these heads, of up to T_q query tokens."""
     import torch
+    if _codes is None:
+        _init()
     nbytes = paged_workspace_size(T_q, Hq, Hkv, D)
     if nbytes == 0:
         raise ValueError("paged_workspace_size rejected the sizes")
@@ -172,20 +160,18 @@ def alloc_paged_workspace(T_q: int, Hq: int, Hkv: int, D: int, device="cuda", st
     return ws
 
 
-def _check_sequences(cache, kv_lens, block_table, dev):
+def _check_sequences(kv_lens, block_table, dev):
     """(B, max_pages, table_stride) of kv_lens [B] and block_table [B, max_pages]."""
-    i32 = _int32()
-    if kv_lens.dtype is not i32 or block_table.dtype is not i32:
+    if kv_lens.dtype is not _int32 or block_table.dtype is not _int32:
         raise TypeError("kv_lens and block_table must be int32")
-    shape, stride = block_table.shape, block_table.stride()
-    if len(shape) != 2 or kv_lens.shape != shape[:1]:
+    if block_table.dim() != 2 or kv_lens.shape != block_table.shape[:1]:
         raise ValueError("kv_lens must be [B] and block_table [B, max_pages]")
-    if not kv_lens.is_contiguous() or stride[1] != 1:
+    (B, max_pages), (stride, one) = block_table.shape, block_table.stride()
+    if not kv_lens.is_contiguous() or one != 1:
         raise ValueError("kv_lens and the rows of block_table must be contiguous")
-    if kv_lens.get_device() != dev or block_table.get_device() != dev or cache.device != dev:
+    if kv_lens.get_device() != dev or block_table.get_device() != dev:
         raise ValueError("all tensors must be on one device")
-    # the stride of a single row is any number
-    return shape[0], shape[1], stride[0] if shape[0] > 1 else shape[1]
+    return B, max_pages, stride if B > 1 else max_pages   # the stride of a single row is any number
 
 
 def decode_attn_paged(q, cache: PagedCache, kv_lens, block_table, out, workspace, *, scale: float | None = None, lse=None,
@@ -195,11 +181,15 @@ def decode_attn_paged(q, cache: PagedCache, kv_lens, block_table, out, workspace
     q, out: [B, T_q, Hq, D], or [B, Hq, D] for one query token; lse (optional): float32 of the same
     shape without D. kv_lens: int32 [B]; block_table: int32 [B, max_pages].
     """
+    if _codes is None:
+        _init()
     dev = q.get_device()
     _check_device(dev)
-    B, max_pages, table_stride = _check_sequences(cache, kv_lens, block_table, dev)
+    if cache.device != dev:
+        raise ValueError("the cache must be on the tensors' device")
+    B, max_pages, table_stride = _check_sequences(kv_lens, block_table, dev)
     shape, dtype = q.shape, q.dtype
-    code = _codes().get(dtype, -1)
+    code = _codes.get(dtype, -1)
     if code not in (0, 1):
         raise TypeError(f"q must be float16 or bfloat16, not {dtype}")
     if cache.kv_dtype != DA_E4M3 and cache.kv_dtype != code:
@@ -218,7 +208,7 @@ def decode_attn_paged(q, cache: PagedCache, kv_lens, block_table, out, workspace
         raise ValueError("q and out must be contiguous")
     lse_ptr = 0
     if lse is not None:
-        if lse.shape != shape[:-1] or lse.dtype is not _float32() or not lse.is_contiguous() or lse.get_device() != dev:
+        if lse.shape != shape[:-1] or lse.dtype is not _float32 or not lse.is_contiguous() or lse.get_device() != dev:
             raise ValueError("lse must be contiguous float32 of q's shape without its last dimension")
         lse_ptr = lse.data_ptr()
     if workspace.get_device() != dev:
@@ -226,7 +216,7 @@ def decode_attn_paged(q, cache: PagedCache, kv_lens, block_table, out, workspace
     st = _lib().decode_attn_paged(
         _pack_attn(q.data_ptr(), cache._ref, kv_lens.data_ptr(), block_table.data_ptr(), max_pages, table_stride, B, T_q, Hq,
                    code, 1.0 / math.sqrt(D) if scale is None else scale, out.data_ptr(), lse_ptr, workspace.data_ptr(),
-                   workspace.numel() * workspace.itemsize), _raw_stream(stream, dev))
+                   workspace.nbytes), _raw_stream(stream, dev))
     if st:
         _fail(st, "decode_attn_paged")
     return out
@@ -234,14 +224,14 @@ def decode_attn_paged(q, cache: PagedCache, kv_lens, block_table, out, workspace
 
 def _rows(x, name, T, heads, D, dtype, dev):
     """Check [T, heads, D] rows with contiguous heads; their row stride."""
-    stride = x.stride()
     if x.shape != (T, heads, D):
         raise ValueError(f"{name} must be {(T, heads, D)}, not {tuple(x.shape)}")
-    if stride[2] != 1 or (stride[1] != D and heads > 1):
+    row, head, one = x.stride()
+    if one != 1 or (head != D and heads > 1):
         raise ValueError(f"the heads of a row of {name} must be contiguous")
     if x.dtype is not dtype or x.get_device() != dev:
         raise ValueError(f"{name} must have k's type and device")
-    return stride[0] if T > 1 else heads * D   # the stride of a single row is any number
+    return row if T > 1 else heads * D   # the stride of a single row is any number
 
 
 def decode_attn_paged_append(q, k, v, cache: PagedCache, cu_new, kv_lens, block_table, workspace, *, cos_sin=None,
@@ -253,11 +243,15 @@ def decode_attn_paged_append(q, k, v, cache: PagedCache, cu_new, kv_lens, block_
     [max_pos, rot_dim], or None for no rotation. q_out: like q (q itself to rotate in place);
     returned.
     """
+    if _codes is None:
+        _init()
     dev = k.get_device()
     _check_device(dev)
-    B, max_pages, table_stride = _check_sequences(cache, kv_lens, block_table, dev)
+    if cache.device != dev:
+        raise ValueError("the cache must be on the tensors' device")
+    B, max_pages, table_stride = _check_sequences(kv_lens, block_table, dev)
     dtype = k.dtype
-    code = _codes().get(dtype, -1)
+    code = _codes.get(dtype, -1)
     if code not in (0, 1):
         raise TypeError(f"k must be float16 or bfloat16, not {dtype}")
     if cache.kv_dtype != DA_E4M3 and cache.kv_dtype != code:
@@ -275,15 +269,15 @@ def decode_attn_paged_append(q, k, v, cache: PagedCache, cu_new, kv_lens, block_
         q_stride = _rows(q, "q", T, Hq, D, dtype, dev)
         out_stride = q_stride if q_out is q else _rows(q_out, "q_out", T, Hq, D, dtype, dev)
         q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
-    if cu_new.dtype is not _int32() or cu_new.shape != (B + 1,) or not cu_new.is_contiguous() or cu_new.get_device() != dev:
+    if cu_new.dtype is not _int32 or cu_new.shape != (B + 1,) or not cu_new.is_contiguous() or cu_new.get_device() != dev:
         raise ValueError("cu_new must be contiguous int32 [B + 1]")
     if cos_sin is None:
         rope, cs_ptr, max_pos, rot = DA_ROPE_NONE, 0, 0, 0
     else:
-        if cos_sin.dtype is not _float32() or cos_sin.dim() != 2 or not cos_sin.is_contiguous() or cos_sin.get_device() != dev:
+        if cos_sin.dtype is not _float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous() or cos_sin.get_device() != dev:
             raise ValueError("cos_sin must be contiguous float32 [max_pos, rot_dim]")
         cs_ptr, (max_pos, rot) = cos_sin.data_ptr(), cos_sin.shape
-    if workspace.get_device() != dev or workspace.numel() * workspace.itemsize < 256:
+    if workspace.get_device() != dev or workspace.nbytes < 256:
         raise ValueError("the workspace must be on the tensors' device")
     st = _lib().decode_attn_paged_append(
         _pack_append(q_ptr, k.data_ptr(), v.data_ptr(), q_stride, k_stride, v_stride, cs_ptr, max_pos, rot, rope,
