@@ -43,7 +43,7 @@ constexpr int kPagedShares = 2048;   // bound of (range, chunk) pairs, each with
 constexpr size_t kPagedCounterBytes = static_cast<size_t>(kPagedShares) * kConsumerWarps * 4;
 constexpr int kMinRange = 2;         // units per range at least (twice as many in a batch of unequal lengths),
 constexpr int kMinCut = 8;           //   where an even batch's sequences have so many: shorter ones stay whole
-constexpr int kAlignRange = 16;      // up to here ranges of an even batch follow its (sequence, head)s
+constexpr int kAlignRange = 16;      // up to here ranges of an even batch follow its sequences whatever that leaves idle
 constexpr int kMaxSlack = 4;         // units that a cut may move to avoid a partial result
 constexpr float kNoKey = -1e30f;     // running maximum of a column that has seen no key (finite: no NaN arises)
 
@@ -126,21 +126,25 @@ static_assert(sizeof(PagedItem) <= 64, "PagedItem fits its slot");
 struct Ranges {
     int units, n, w, k, q, rem, split, slack;
     // t: units of every sequence, or 0. slots: ranges that run at once; `one` of them take an
-    // SM each.
-    __device__ __forceinline__ Ranges(int u, int t, int slots, int one, int short_range) : units(u) {
+    // SM each. streams: the bytes bound the kernel (not the 16-column products of e4m3 pages).
+    __device__ __forceinline__ Ranges(int u, int t, int slots, int one, int short_range, bool streams) : units(u) {
         const int lane = threadIdx.x & 31;
         const int by = lane == 0 ? one : slots;
         const int share = (u + by - 1) / by;
         // one range per SM while it is short, then all slots
         int size = max(t >= kMinCut ? kMinRange : 2 * kMinRange, __shfl_sync(0xffffffffu, share, 0));
         if (size > (t >= size ? kAlignRange : short_range)) size = max(short_range, __shfl_sync(0xffffffffu, share, 1));
-        const int num = lane == 0 ? u + size - 1 : lane == 1 ? t : size + t - 1;
-        const int quot = num / (lane == 2 ? max(t, 1) : size);
+        const int num = lane == 0 ? u + size - 1 : lane == 1 ? t : lane == 2 ? size + t - 1 : u;
+        const int quot = num / (lane < 2 ? size : max(t, 1));
         w = units;
         k = min(__shfl_sync(0xffffffffu, quot, 0), slots);
-        if (t > 0 && size <= kAlignRange) {
+        const int parts = __shfl_sync(0xffffffffu, quot, 1);
+        // long ranges too, where four fifths of the slots are enough because the stream bounds them
+        const bool follow = size <= kAlignRange ||
+                            (streams && size < t && 5 * parts * __shfl_sync(0xffffffffu, quot, 3) >= 4 * slots);
+        if (t > 0 && follow) {
             w = size < t ? t : __shfl_sync(0xffffffffu, quot, 2) * t;
-            k = size < t ? __shfl_sync(0xffffffffu, quot, 1) : 1;
+            k = size < t ? parts : 1;
         }
         const int last = (lane == 0 ? units + w - 1 : w) / (lane == 0 ? w : k);
         n = __shfl_sync(0xffffffffu, last, 0) * k;
@@ -317,7 +321,7 @@ struct PagedKernel {
     static constexpr int kShortRange = D == 128 ? 8 : 3;
 
     static __device__ __forceinline__ Ranges cut(const Layout& s, const PagedParams& p) {
-        return Ranges(s.prefix[p.B], s.prefix[p.B + 1], p.slots, p.one, kShortRange);
+        return Ranges(s.prefix[p.B], s.prefix[p.B + 1], p.slots, p.one, kShortRange, !KV8 || NT == 1);
     }
 
     // ------------------------------------------------------------ producer
