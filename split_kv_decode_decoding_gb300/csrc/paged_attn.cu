@@ -250,36 +250,64 @@ struct PagedKernel {
         return reinterpret_cast<PagedItem*>(s.smem + Sh::kLastOff + (2 * warp + i) * Sh::kSlotBytes);
     }
 
-    // Stages per sequence, their running sum, and the stages that all have (prefix[B + 1], 0 where they
-    // differ), by the whole CTA.
+    // A length as it counts, and the stages of sequence b (keeping how many keys its last one lacks).
+    static __device__ __forceinline__ int checked_length(const PagedParams& p, int L) {
+        if (L < 0 || L > static_cast<int64_t>(p.max_pages) * p.P) {
+            if (blockIdx.x == 0) flag_error(p.err, DA_DEVERR_SEQLENS);
+            L = 0;
+        }
+        return L;
+    }
+    static __device__ __forceinline__ int count_stages(const Layout& s, const PagedParams& p, int b, int L) {
+        L = checked_length(p, L);
+        const int n = L == 0 ? 1 : (L + Sh::kKeys - 1) / Sh::kKeys;   // an empty sequence: one empty stage
+        s.pad[b] = static_cast<uint8_t>(n * Sh::kKeys - L);
+        return n;
+    }
+
+    // prefix[b]: stages before sequence b; prefix[B + 1]: the stages that every sequence has, or 0 where they
+    // differ. Up to 32 sequences by the producer warp, which alone needs them, ...
+    static __device__ __forceinline__ void count_units_warp(const Layout& s, const PagedParams& p) {
+        const int lane = threadIdx.x & 31;
+        const int n = lane < p.B ? count_stages(s, p, lane, ld_cg_s32(p.lens + lane)) : 0;
+        int run = n;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, run, off);
+            if (lane >= off) run += y;
+        }
+        const int first = __shfl_sync(0xffffffffu, n, 0);
+        const bool same = __all_sync(0xffffffffu, lane >= p.B || n == first);
+        if (lane < p.B) s.prefix[lane + 1] = run;
+        if (lane == 0) {
+            s.prefix[0] = 0;
+            s.prefix[p.B + 1] = same ? first : 0;
+        }
+        __syncwarp();
+    }
+    // ... more by the whole CTA.
     static __device__ __forceinline__ void count_units(const Layout& s, const PagedParams& p) {
         __shared__ int32_t warp_sum[kThreads / 32];
         const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
         constexpr int kMost = (DA_MAX_PAGED_BATCH + kThreads - 1) / kThreads;
         const int per = (p.B + kThreads - 1) / kThreads, b0 = tid * per;
-        const int64_t most = static_cast<int64_t>(p.max_pages) * p.P;
         int len[kMost], mine = 0;
-        auto stages = [&](int b, int L) {
-            if (L < 0 || L > most) {
-                if (blockIdx.x == 0) flag_error(p.err, DA_DEVERR_SEQLENS);
-                L = 0;
-            }
-            const int n = L == 0 ? 1 : (L + Sh::kKeys - 1) / Sh::kKeys;   // an empty sequence: one empty stage
-            s.pad[b] = static_cast<uint8_t>(n * Sh::kKeys - L);
-            return n;
-        };
+        bool same = true;
+        int first = ld_cg_s32(p.lens);
         if (per == 1) {
-            if (tid < p.B) mine = len[0] = stages(tid, ld_cg_s32(p.lens + tid));
+            if (tid < p.B) mine = len[0] = count_stages(s, p, tid, ld_cg_s32(p.lens + tid));
         } else {
 #pragma unroll
             for (int i = 0; i < kMost; ++i) len[i] = i < per && b0 + i < p.B ? ld_cg_s32(p.lens + b0 + i) : 0;
 #pragma unroll
             for (int i = 0; i < kMost; ++i) {
                 if (i >= per || b0 + i >= p.B) break;
-                len[i] = stages(b0 + i, len[i]);
+                len[i] = count_stages(s, p, b0 + i, len[i]);
                 mine += len[i];
             }
         }
+        first = checked_length(p, first);
+        first = first == 0 ? 1 : (first + Sh::kKeys - 1) / Sh::kKeys;
         int run = mine;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -287,7 +315,13 @@ struct PagedKernel {
             if (lane >= off) run += y;
         }
         if (lane == 31) warp_sum[warp] = run;
-        __syncthreads();
+        if (per == 1) {
+            same = tid >= p.B || len[0] == first;
+        } else {
+#pragma unroll
+            for (int i = 0; i < kMost; ++i) same = same && (i >= per || b0 + i >= p.B || len[i] == first);
+        }
+        same = __syncthreads_and(same);
         int sum = run - mine;
         for (int w = 0; w < warp; ++w) sum += warp_sum[w];
         if (per == 1) {
@@ -300,19 +334,10 @@ struct PagedKernel {
                 s.prefix[b0 + i + 1] = sum;
             }
         }
-        if (tid == 0) s.prefix[0] = 0;
-        // the stages of every sequence, or 0 where they differ
-        __syncthreads();
-        const int first = s.prefix[1];
-        bool same = true;
-        if (per == 1) {
-            same = tid >= p.B || len[0] == first;
-        } else {
-#pragma unroll
-            for (int i = 0; i < kMost; ++i) same = same && (i >= per || b0 + i >= p.B || len[i] == first);
+        if (tid == 0) {
+            s.prefix[0] = 0;
+            s.prefix[p.B + 1] = same ? first : 0;
         }
-        same = __syncthreads_and(same);
-        if (tid == 0) s.prefix[p.B + 1] = same ? first : 0;
         __syncthreads();
     }
 
@@ -330,27 +355,34 @@ struct PagedKernel {
         float ks, lvs;
     };
 
-    static __device__ __forceinline__ Box load_box(const PagedParams& p, const PagedItem& it, int box) {
+    // The block-table entry of this lane's box, and what follows from it: the entry's read is on its way while
+    // other work is done.
+    static __device__ __forceinline__ int box_entry(const PagedParams& p, const PagedItem& it, int box) {
+        const int key = box * p.box_keys;
+        if (static_cast<uint32_t>(key) >= static_cast<uint32_t>(it.nkeys)) return -1;   // (a product past 2^31 is none)
+        return ld_cg_s32(p.table + static_cast<int64_t>(it.b) * p.table_stride + p.page(it.key0 + key));
+    }
+    static __device__ __forceinline__ Box box_of(const PagedParams& p, const PagedItem& it, int box, int entry) {
         Box x;
-        x.page = 0;
+        x.page = p.num_pages;   // a bad page: a coordinate past the cache, which the copy fills with zeros
         x.ks = 0.f;
         x.lvs = -INFINITY;
-        const int key = box * p.box_keys;
-        if (static_cast<uint32_t>(key) < static_cast<uint32_t>(it.nkeys)) {   // (a product past 2^31 is none)
-            const int page = ld_cg_s32(p.table + static_cast<int64_t>(it.b) * p.table_stride + p.page(it.key0 + key));
-            const bool good = page >= 0 && page < p.num_pages;
-            // a bad page: a coordinate past the cache, which the copy fills with zeros
-            x.page = good ? page : p.num_pages;
-            if (!good) flag_error(p.err, DA_DEVERR_PAGE);
+        if (static_cast<uint32_t>(box * p.box_keys) < static_cast<uint32_t>(it.nkeys)) {
+            const bool good = entry >= 0 && entry < p.num_pages;
+            if (good) x.page = entry;
+            else flag_error(p.err, DA_DEVERR_PAGE);
             if constexpr (KV8) {
                 if (good) {
-                    const int64_t at = static_cast<int64_t>(page) * p.Hkv + it.kvh;
+                    const int64_t at = static_cast<int64_t>(entry) * p.Hkv + it.kvh;
                     x.ks = __ldcg(p.ks + at);
                     x.lvs = fast_log2(__ldcg(p.vs + at));
                 }
             }
         }
         return x;
+    }
+    static __device__ __forceinline__ Box load_box(const PagedParams& p, const PagedItem& it, int box) {
+        return box_of(p, it, box, box_entry(p, it, box));
     }
 
     // Copy one box of keys or values to `dst`.
@@ -364,6 +396,7 @@ struct PagedKernel {
     static __device__ void producer(const Layout& s, const PagedParams& p, const CUtensorMap* tmK, const CUtensorMap* tmV,
                                     const CUtensorMap* tmK16, const CUtensorMap* tmV16) {
         const int lane = threadIdx.x & 31;
+        if (p.B <= 32) count_units_warp(s, p);
         const Ranges ranges = cut(s, p);
         const int shares = ranges.n * p.lanes;
 
@@ -457,9 +490,11 @@ struct PagedKernel {
             // the next piece's descriptor, queries and table entries go out before the last one's merge
             PagedItem next;
             next_piece(next);
+            int entry = -1;
+            if (next.valid) entry = box_entry(p, next, lane);
             if (!publish(i, next)) return;
             Box cur = {};
-            if (next.valid) cur = load_box(p, next, lane);
+            if (next.valid) cur = box_of(p, next, lane, entry);
             if (item.valid) {
                 // hand the consumers the next stage, empty, for that merge
                 if (!wait_warp(s.empty0 + 8 * st, ph ^ 1, p.wait_limit_ns)) {
@@ -1123,10 +1158,11 @@ paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CU
         prefetch_tensormap(&tmK16);
         prefetch_tensormap(&tmV16);
     }
+    __syncthreads();
     // From here on this grid touches global memory: wait for the previous kernel.
     grid_dependency_wait();
     if (threadIdx.x == 0) grid_dependents_launch();
-    K::count_units(s, p);   // its barriers also publish the initialised mbarriers
+    if (p.B > 32) K::count_units(s, p);
     if ((threadIdx.x >> 5) == kConsumerWarps) K::producer(s, p, &tmK, &tmV, &tmK16, &tmV16);
     else K::consumer(s, p);
 }
