@@ -571,14 +571,13 @@ __global__ void __launch_bounds__(kAppendThreads, kLanes == 32 ? 2 : 3) append8_
         if (b == p.B - 1) prefix[p.B] = before;
     }
     __syncthreads();
-    const int64_t units = static_cast<int64_t>(prefix[p.B]) * p.Hkv * 2;
+    const uint32_t groups = 2u * p.Hkv, units = prefix[p.B] * groups;   // below 2^31: checked by the host
     constexpr int kPerBlock = kAppendThreads / kLanes;
-    const int64_t step = static_cast<int64_t>(p.page_blocks) * kPerBlock;
+    const uint32_t step = static_cast<uint32_t>(p.page_blocks) * kPerBlock;
     AppendPage<D, DT, HALF, kLanes> page(p, kLanes == 32 ? lane : tid);
     // the bound is uniform over a unit's threads
-    for (int64_t unit = static_cast<int64_t>(blockIdx.x) * kPerBlock + (kLanes == 32 ? warp : 0); unit < units; unit += step) {
-        const int nth = static_cast<int>(unit / (2 * p.Hkv));
-        const int hv = static_cast<int>(unit - static_cast<int64_t>(nth) * 2 * p.Hkv);
+    for (uint32_t unit = blockIdx.x * kPerBlock + (kLanes == 32 ? warp : 0); unit < units; unit += step) {
+        const int nth = static_cast<int>(unit / groups), hv = static_cast<int>(unit - nth * groups);
         int lo = 0, hi = p.B - 1;   // last b with prefix[b] <= nth
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
@@ -626,8 +625,10 @@ da_status run_append(AppendParams& p, bool e4m3, cudaStream_t stream) {
     const int64_t touched = std::min<int64_t>(p.T, p.T / p.P + 2ll * p.B);
     // A warp per page and head while pages get few tokens each, the block where they get many.
     const bool few = p.T < 4 * static_cast<int64_t>(p.B) || p.P <= 16;
-    const int64_t blocks = few ? (touched * p.Hkv * 2 + kAppendThreads / 32 - 1) / (kAppendThreads / 32) : touched * p.Hkv * 2;
-    p.page_blocks = static_cast<int>(std::min<int64_t>(blocks, kMostPageBlocks));
+    const int64_t units = touched * p.Hkv * 2;
+    if (units > 0x3fffffffll) return DA_ERR_INVALID_ARG;
+    constexpr int kWarps = kAppendThreads / 32;
+    p.page_blocks = static_cast<int>(std::min<int64_t>(few ? (units + kWarps - 1) / kWarps : units, kMostPageBlocks));
     return few ? launch_append(append8_kernel<D, DT, HALF, 32>, p.page_blocks + row_blocks, smem, p, stream)
                : launch_append(append8_kernel<D, DT, HALF, kAppendThreads>, p.page_blocks + row_blocks, smem, p, stream);
 }
