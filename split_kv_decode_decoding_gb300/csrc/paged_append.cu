@@ -23,8 +23,9 @@
 // took 20 to 60 % longer.
 //
 // Measured (one GB300): 16-bit pages, 9887 tokens of 32 + 2 x 8 heads in 5 prompts 39.3 us,
-// 6.3 TB/s; 64 tokens, one per sequence, 28 + 2 x 4 heads 2.8 us. e4m3 pages: the same prompts 43.6 us,
-// 5.2 TB/s; 256 tokens, one per sequence, 16 + 2 x 2 heads 4.5 us.
+// 6.3 TB/s; 64 tokens, one per sequence, 28 + 2 x 4 heads 2.8 us. e4m3 pages: the same prompts 43.4 us,
+// 5.2 TB/s (bound by instructions and by the two waits per page and head, not by its bytes); 256 tokens,
+// one per sequence, 16 + 2 x 2 heads 4.3 us.
 
 #include "paged_common.cuh"
 

@@ -8,42 +8,55 @@
 //
 // What bounds it: the K/V bytes. A key costs 4 D (16-bit) or 2 D (e4m3) bytes for 4 D
 // operations per column, far below what the tensor cores deliver, so everything here serves
-// the stream.
+// the stream. Short calls are bound by latency: a chain of kv_lens, block table, first copy,
+// a few stages, the merge of the warps, a partial result's way through the L2. 16-column
+// e4m3 calls by the consumer warps' instructions (39 % of the issue slots at 2.3 warps
+// per scheduler, each waiting for its own results).
 //
-// How the work is cut. The unit is a stage of 64 (e4m3: 128) keys of one sequence and KV
-// head. All units of the batch, in order (sequence, KV head, keys), are cut into about as many
-// equal ranges as there are persistent CTAs, whatever the lengths are: the host knows none of
-// them, and no split count has to be chosen. A range may hold the end of one (sequence, head),
-// several whole ones and the beginning of another; a (sequence, head) that lies in one
-// range is written by it directly, otherwise each of its ranges leaves a partial result (at
-// most two per range, so the workspace does not grow with the batch) and the warp that
-// finishes a column last merges that column's partials, in range order whoever it is: the
-// result does not depend on timing.
+// How the work is cut. The unit is a stage of 64 (e4m3: 128) keys of a sequence. The units of
+// the batch, in order, are cut into about as many equal ranges as there are persistent CTAs
+// per KV head and chunk, whatever the lengths are: the host knows none of them, and no split
+// count has to be chosen. A range may hold the end of one sequence, several whole ones and the
+// beginning of another; a sequence that lies in one range is written by it directly, otherwise
+// each of its ranges leaves a partial result (at most two per range, so the workspace does not
+// grow with the batch) and the warp that finishes a column last merges that column's partials,
+// in range order whoever it is: the result does not depend on timing. Every KV head is cut
+// alike and the heads of a range run at the same time, so that the interleaved rows of a page
+// are read together (16 sequences of 8192 keys, e4m3, tokens outside heads: 68.0 us with one
+// cut through all heads, 51.3 us so).
 //
 // A CTA is one producer warp and four consumer warps around a three-stage ring, as in the
-// split kernel for contiguous caches. The producer's lanes read the block table (and the scales) of the
-// next 32 boxes at once, one batch ahead of the copies, and each lane issues its own box: 64-key
-// TMA boxes (pages smaller than that: their size), 16-key boxes at a sequence's ragged end, so that
-// a box never crosses a page.
+// split kernel for contiguous caches. The producer's lanes read the block table (and the
+// scales) of the next 32 boxes at once, one batch ahead of the copies, and each lane issues its
+// own box: TMA boxes of gcd(page size, stage) keys, 16-key boxes at a sequence's ragged end, so
+// that a box never crosses a page.
 //
 // e4m3 pages. The products run as fp16 tensor-core products: every e4m3 value is an fp16
-// value, and a conversion instruction takes two elements, 2.5 issue slots per key and SM out
-// of the 11 cycles that a key takes to stream (measured: 0.5 cycles per conversion and SM). Queries in bf16
-// are scaled by a power of two per column into the top of the fp16 range (an element below 2^-28 of its
-// column's largest loses bits, by at most 2^-39 of that largest). The order of the dims inside a 16-dim step is free, so
-// one ldmatrix of 16-bit pairs feeds two steps. The scales never touch the elements: ks multiplies the score, and
-// vs goes into the exponent of the weight, 2^(x + log2 vs - mv), with a running maximum mv of
-// its own, so that the fp16 weights keep their precision however unequal the pages' scales are.
+// value, and one conversion takes two elements, 0.5 cycles per SM (measured), 2 of the 11
+// cycles that a key of 2 x 128 bytes takes to stream. Queries in bf16 are scaled by a power of
+// two per column into the top of the fp16 range (an element below 2^-28 of its column's largest
+// loses bits, by at most 2^-39 of that largest). The order of the dims inside a 16-dim step is
+// free, so one ldmatrix of 16-bit pairs feeds two steps. The scales never touch the elements: ks
+// multiplies the score, and vs goes into the exponent of the weight, 2^(x + log2 vs - mv), with
+// a running maximum mv of its own, so that the fp16 weights keep their precision however
+// unequal the pages' scales are.
+//
+// Sums, maxima, accumulators and partial results are float32. Rounded to fewer bits are the
+// weights, to the 16-bit type of the product that they enter, and the outputs, once.
+//
+// Measured (one GB300, mean of a graph of calls): 16 sequences of 131072 keys, 32 / 8 heads, bf16
+// 1197 us, 7.2 TB/s; 64 sequences of 512 to 8192 keys, 28 / 4 heads 89.5 us, 6.2 TB/s, over e4m3
+// pages 51.0 us, 5.4 TB/s; one sequence of 1024 keys 8.7 us, of 8192 keys over e4m3 pages 11.1 us.
 
 #include "paged_common.cuh"
 
 namespace da_impl {
 
-constexpr int kPagedShares = 2048;   // bound of (range, chunk) pairs, each with two partial results
+constexpr int kPagedShares = 2048;   // bound of shares (range, KV head, chunk), each with two partial results
 constexpr size_t kPagedCounterBytes = static_cast<size_t>(kPagedShares) * kConsumerWarps * 4;
 constexpr int kMinRange = 2;         // units per range at least (twice as many in a batch of unequal lengths),
 constexpr int kMinCut = 8;           //   where an even batch's sequences have so many: shorter ones stay whole
-constexpr int kAlignRange = 16;      // up to here ranges of an even batch follow its sequences whatever that leaves idle
+constexpr int kAlignRange = 16;      // ranges of an even batch up to so long follow its sequences in any case
 constexpr int kMaxSlack = 4;         // units that a cut may move to avoid a partial result
 constexpr float kNoKey = -1e30f;     // running maximum of a column that has seen no key (finite: no NaN arises)
 
@@ -113,16 +126,19 @@ struct PagedItem {           // one piece of a (sequence, KV head): what a range
 };
 static_assert(sizeof(PagedItem) <= 64, "PagedItem fits its slot");
 
-// The cut of the batch's `units` into n ranges, for every KV head and chunk alike: k raw cuts at equal distances (q or q + 1 units) in every w units.
-// A batch of unequal lengths is one period of w = units. Where every sequence has the same t
-// units and ranges are short, a period is one of them (cut into k parts) or several whole ones (k = 1),
-// so that no range holds the end of one and the beginning of the next: that costs a second merge of the
-// warps and a partial result, 2 to 3 us against the 1 to 1.5 us that a unit takes to stream with every SM busy
-// (256 sequences of 256 keys, 2 KV heads: 24.0 us with plain equal cuts, 16.6 us with whole heads).
+// The cut of the batch's `units` into n ranges, for every KV head and chunk alike: k raw cuts at equal
+// distances (q or q + 1 units) in every w units.
+//
+// Few units go to one range per SM, more to all the CTAs that run at once. A batch of unequal lengths is
+// one period of w = units. Where every sequence has the same t units and ranges are short, a period
+// is one of them (cut into k parts) or several whole ones (k = 1), so that no range holds the end of one
+// and the beginning of the next: that costs a second merge of the warps and a partial result, 2 to 3 us
+// against the 1 to 1.5 us that a unit takes to stream with every SM busy (256 sequences of 256 keys, 2 KV
+// heads: 24.0 us with plain equal cuts, 16.6 us with whole sequences).
 // Otherwise a raw cut within `slack` units of a border moves there (4 slack <= q keeps the ranges in order).
 //
-// Every method is for a whole warp. A division by a number that is not known at compile time takes some 70 ns
-// and nothing streams before these are done, so independent ones run in different lanes at once.
+// Every method is for a whole warp. A division by a number that is not known at compile time takes some
+// 70 ns and nothing streams before these are done, so independent ones run in different lanes at once.
 struct Ranges {
     int units, n, w, k, q, rem, split, slack;
     // t: units of every sequence, or 0. slots: ranges that run at once; `one` of them take an
@@ -167,8 +183,8 @@ struct Ranges {
     // Ranges that hold parts of the sequence of units [a, b): the first, and their number.
     __device__ __forceinline__ void parts(int a, int b, int& first, int& count) const {
         const int r = first_from((threadIdx.x & 31) == 0 ? a + slack + 1 : b - slack);
-        const int lo = __shfl_sync(0xffffffffu, r, 0), end = __shfl_sync(0xffffffffu, r, 1);   // cuts lo .. end - 1 lie inside
-        first = lo - 1;
+        const int lo = __shfl_sync(0xffffffffu, r, 0), end = __shfl_sync(0xffffffffu, r, 1);
+        first = lo - 1;                // cuts lo .. end - 1 lie inside
         count = max(end - lo, 0) + 1;
     }
 };
@@ -762,7 +778,8 @@ struct PagedKernel {
             const int64_t at = part_row(p, it.first_share, 1, col);
             lse1 = __ldcg(p.part_lse + at);
 #pragma unroll
-            for (int v = 0; v < kVec; ++v) o1[v] = __ldcg(reinterpret_cast<const float4*>(p.part + at * D + 64 * v + 4 * l16));
+            for (int v = 0; v < kVec; ++v)
+                o1[v] = __ldcg(reinterpret_cast<const float4*>(p.part + at * D + 64 * v + 4 * l16));
         }
         float M = kNoKey, Mv = kNoKey;
 #pragma unroll
@@ -783,8 +800,8 @@ struct PagedKernel {
 #pragma unroll
             for (int v = 0; v < kVec; ++v) fma4(o[v], wt, *reinterpret_cast<const float4*>(row + 64 * v));
         }
-        const bool none = M == kNoKey;   // the column saw no key: output 0, lse -inf
-        // l >= 1 otherwise (the key that set M weighs 1). In 8-bit pages o is relative to Mv, l to M.
+        const bool none = M == kNoKey && l == 0.f;   // the column saw no key: output 0, lse -inf
+        // (NaN scores leave M alone and make l NaN.) l >= 1 otherwise (the key that set M weighs 1). In 8-bit pages o is relative to Mv, l to M.
         float inv = none ? 0.f : 1.f / l;
         if constexpr (KV8) inv *= Mv == kNoKey ? 0.f : fast_exp2(Mv - M);
 #pragma unroll
@@ -794,14 +811,15 @@ struct PagedKernel {
         if (direct) {
             const float m = fmaxf(kNoKey, fmaxf(lse2, lse1));
             const float w0 = fast_exp2(lse2 - m), w1 = fast_exp2(lse1 - m), z = w0 + w1;
-            const float by = m == kNoKey ? 0.f : 1.f / z;
+            const bool empty = m == kNoKey && z == 0.f;
+            const float by = empty ? 0.f : 1.f / z;
 #pragma unroll
             for (int v = 0; v < kVec; ++v) {
                 scale4(o[v], w0);
                 fma4(o[v], w1, o1[v]);
                 scale4(o[v], by);
             }
-            lse2 = m == kNoKey ? -INFINITY : m + fast_log2(z);
+            lse2 = empty ? -INFINITY : m + fast_log2(z);
         }
         if (it.part < 0 || direct) {
             store_output(p, output_row(p, it, col), o, lse2);
@@ -820,8 +838,8 @@ struct PagedKernel {
         constexpr int kAhead = NT == 1 ? 16 / kVec : 4 / kVec;   // parts in flight
         const int l16 = threadIdx.x & 15, nparts = it.nparts, nh = it.nh, first_share = it.first_share;
 #pragma unroll 1
-        for (int c = (threadIdx.x >> 5) + kConsumerWarps * ((threadIdx.x >> 4) & 1); c - 4 * static_cast<int>((threadIdx.x >> 4) & 1) < nh;
-             c += 8) {
+        for (int c0 = threadIdx.x >> 5; c0 < nh; c0 += 2 * kConsumerWarps) {
+            const int c = c0 + kConsumerWarps * ((threadIdx.x >> 4) & 1);
             const bool live = c < nh;
             float m = kNoKey, z = 0.f;
             float4 acc[kVec];
@@ -840,7 +858,8 @@ struct PagedKernel {
                         const float* at = p.part + part_row(p, first_share, j0 + j + i, c) * D + 4 * l16;
 #pragma unroll
                         for (int v = 0; v < kVec; ++v)
-                            o[i][v] = j + i < count ? __ldcg(reinterpret_cast<const float4*>(at + 64 * v)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                            o[i][v] = j + i < count ? __ldcg(reinterpret_cast<const float4*>(at + 64 * v))
+                                                    : make_float4(0.f, 0.f, 0.f, 0.f);
                     }
                     if (j == 0) {
                         float top = lv;
@@ -865,7 +884,7 @@ struct PagedKernel {
                     }
                 }
             }
-            const bool none = m == kNoKey;
+            const bool none = m == kNoKey && z == 0.f;
             const float inv = none ? 0.f : 1.f / z;
 #pragma unroll
             for (int v = 0; v < kVec; ++v) scale4(acc[v], inv);
@@ -1088,7 +1107,10 @@ struct PagedKernel {
                     if (lane == 0) flag_error(p.err, DA_DEVERR_TIMEOUT);
                 }
                 ++mz;
-                if (NT == 1) direct = __shfl_sync(0xffffffffu, arrived, 0) == 1;
+                if (NT == 1) {
+                    direct = __shfl_sync(0xffffffffu, arrived, 0) == 1;
+                    __syncwarp();
+                }
                 if (ok) write_piece(p, item, red, n, direct);
             }
             // release the stage: order these generic-proxy stores before the copy that refills it
@@ -1244,7 +1266,8 @@ da_status launch_paged(const da_paged_cache& c, PagedParams& p, cudaStream_t str
     p.slots = std::max(1, std::min(resident, kPagedShares) / p.lanes);
     p.one = std::max(1, device_sms() / p.lanes);
     // CTAs for the most ranges that the kernel can make of these units (see Ranges)
-    const int64_t most = units <= static_cast<int64_t>(p.one) * PagedKernel<D, DT, KV8, NT>::kShortRange ? p.one : p.slots;
+    const bool few = units <= static_cast<int64_t>(p.one) * PagedKernel<D, DT, KV8, NT>::kShortRange;
+    const int64_t most = few ? p.one : p.slots;
     const int grid = static_cast<int>(std::min<int64_t>(most, (units + kMinRange - 1) / kMinRange)) * p.lanes;
     cudaLaunchAttribute attrs[1] = {pdl_attr()};
     cudaLaunchConfig_t cfg = {};

@@ -191,6 +191,60 @@ def test_nan_of_a_visible_key_reaches_only_its_sequence_and_head():
         check(out, lse, ref, "bf16")
 
 
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_nan_scores_are_not_taken_for_masked_ones(kv):
+    """A query of NaN, a key of NaN that is all a sequence has, and one among others in a later piece."""
+    p = Paged([700, 1, 90], 2, 64, kv, 16, BHSD, seed=14)
+    q = queries(p, 3, 1, 4, "bf16")
+    ref = attend64(q, p)
+    q[0, 0, 1, 5] = math.nan
+    raw = p.k.view(torch.uint8 if kv == "e4m3" else torch.int16)
+    code = 0x7F if kv == "e4m3" else 0x7FC0
+    token_view(raw, BHSD)[p.table[1, 0].long(), 0, 0, 3] = code      # sequence 1's only key, KV head 0
+    token_view(raw, BHSD)[p.table[2, 5].long(), 9, 1, 0] = code      # sequence 2's last one, KV head 1
+    out, lse, err = attend(p, q)
+    assert err == 0
+    bad = np.zeros((3, 1, 4), dtype=bool)
+    bad[0, 0, 1] = bad[1, 0, :2] = bad[2, 0, 2:] = True
+    assert np.isnan(out[bad]).all() and np.isnan(lse[bad]).all()
+    out[bad], lse[bad] = ref[0][bad], ref[1][bad]
+    check(out, lse, ref, "bf16")
+
+
+def test_a_capture_as_the_very_first_call():
+    """A process whose first calls are captured: what a call looks up once per device is no obstacle."""
+    import subprocess
+    import sys
+    code = """
+import torch
+import split_kv_decode_decoding_gb300 as da
+da.load()
+dev = "cuda"
+for dtype in (torch.float16, torch.float8_e4m3fn):
+    cache = da.PagedCache.empty(4, 16, 1, 64, dtype)
+    kv_lens = torch.tensor([20, 1], dtype=torch.int32, device=dev)
+    table = torch.tensor([[2, 0], [3, 1]], dtype=torch.int32, device=dev)
+    cu = torch.tensor([0, 20, 21], dtype=torch.int32, device=dev)
+    x = torch.randn(21, 4, 64, device=dev).half()
+    out = torch.empty(2, 2, 64, dtype=torch.float16, device=dev)
+    ws = da.alloc_paged_workspace(1, 2, 1, 64)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        da.decode_attn_paged_append(None, x[:, 2:3], x[:, 3:], cache, cu, kv_lens, table, ws)
+        da.decode_attn_paged(x[:2, :2].contiguous(), cache, kv_lens, table, out, ws)
+    g.replay()
+    torch.cuda.synchronize()
+    assert da.decode_attn_splitkv_get_error(ws) == 0
+    assert torch.isfinite(out).all()
+    first = out[1].float()                       # one key: its value, in fp16 or rounded to e4m3
+    assert torch.allclose(first[0], x[20, 3].float(), rtol=2 ** -4, atol=2 ** -8), (first[0], x[20, 3])
+print("captured")
+"""
+    got = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert got.returncode == 0 and "captured" in got.stdout, got.stderr[-2000:]
+
+
 def test_shared_pages_and_a_wide_strided_table():
     p = Paged([100, 164], 2, 64, "f16", 32, VARLEN, seed=10, extra_pages=3)
     p.table[1, :2] = p.table[0, :2]      # a common prefix of 64 tokens
