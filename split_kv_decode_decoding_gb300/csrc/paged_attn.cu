@@ -137,39 +137,30 @@ static_assert(sizeof(PagedItem) <= 64, "PagedItem fits its slot");
 // heads: 24.0 us with plain equal cuts, 16.6 us with whole sequences).
 // Otherwise a raw cut within `slack` units of a border moves there (4 slack <= q keeps the ranges in order).
 //
-// Every method is for a whole warp. A division by a number that is not known at compile time takes some
-// 70 ns and nothing streams before these are done, so independent ones run in different lanes at once.
+// A division by a number that is not known at compile time takes some 70 ns and nothing streams before
+// these are done, so independent ones stand together, where they overlap.
 struct Ranges {
     int units, n, w, k, q, rem, split, slack;
     // t: units of every sequence, or 0. slots: ranges that run at once; `one` of them take an
     // SM each. streams: the bytes bound the kernel (not the 16-column products of e4m3 pages).
     __device__ __forceinline__ Ranges(int u, int t, int slots, int one, int short_range, bool streams) : units(u) {
-        const int lane = threadIdx.x & 31;
-        const int by = lane == 0 ? one : slots;
-        const int share = (u + by - 1) / by;
+        const int share1 = (u + one - 1) / one, share = (u + slots - 1) / slots;
         // one range per SM while it is short, then all slots
-        int size = max(t >= kMinCut ? kMinRange : 2 * kMinRange, __shfl_sync(0xffffffffu, share, 0));
-        if (size > (t >= size ? kAlignRange : short_range)) size = max(short_range, __shfl_sync(0xffffffffu, share, 1));
-        const int num = lane == 0 ? u + size - 1 : lane == 1 ? t : lane == 2 ? size + t - 1 : u;
-        const int quot = num / (lane < 2 ? size : max(t, 1));
-        w = units;
-        k = min(__shfl_sync(0xffffffffu, quot, 0), slots);
-        const int parts = __shfl_sync(0xffffffffu, quot, 1);
+        int size = max(t >= kMinCut ? kMinRange : 2 * kMinRange, share1);
+        if (size > (t >= size ? kAlignRange : short_range)) size = max(short_range, share);
+        const int cuts = (u + size - 1) / size, parts = t / size, whole = (size + t - 1) / max(t, 1), seqs = u / max(t, 1);
         // long ranges too, where four fifths of the slots are enough because the stream bounds them
-        const bool follow = size <= kAlignRange ||
-                            (streams && size < t && 5 * parts * __shfl_sync(0xffffffffu, quot, 3) >= 4 * slots);
-        if (t > 0 && follow) {
-            w = size < t ? t : __shfl_sync(0xffffffffu, quot, 2) * t;
-            k = size < t ? parts : 1;
-        }
-        const int last = (lane == 0 ? units + w - 1 : w) / (lane == 0 ? w : k);
-        n = __shfl_sync(0xffffffffu, last, 0) * k;
-        q = __shfl_sync(0xffffffffu, last, 1);
+        const bool follow = t > 0 && (size <= kAlignRange || (streams && size < t && 5 * parts * seqs >= 4 * slots));
+        w = !follow ? units : size < t ? t : whole * t;
+        k = !follow ? min(cuts, slots) : size < t ? parts : 1;
+        const int periods = (units + w - 1) / w;
+        q = w / k;
+        n = periods * k;
         rem = w - q * k;
         split = rem * (q + 1);
         slack = min(q / 4, kMaxSlack);
     }
-    // (per lane) cut r, and the first r with raw(r) >= x
+    // cut r, and the first r with raw(r) >= x
     __device__ __forceinline__ int raw(int r) const {
         const int p = r / k, j = r - p * k;
         return p * w + j * q + min(j, rem);
@@ -182,8 +173,7 @@ struct Ranges {
     }
     // Ranges that hold parts of the sequence of units [a, b): the first, and their number.
     __device__ __forceinline__ void parts(int a, int b, int& first, int& count) const {
-        const int r = first_from((threadIdx.x & 31) == 0 ? a + slack + 1 : b - slack);
-        const int lo = __shfl_sync(0xffffffffu, r, 0), end = __shfl_sync(0xffffffffu, r, 1);
+        const int lo = first_from(a + slack + 1), end = first_from(b - slack);
         first = lo - 1;                // cuts lo .. end - 1 lie inside
         count = max(end - lo, 0) + 1;
     }
@@ -368,7 +358,7 @@ struct PagedKernel {
     // ------------------------------------------------------------ producer
     struct Box {        // what a lane knows of its box: one page and head
         int page;
-        float ks, lvs;
+        float ks, vs;
     };
 
     // The block-table entry of this lane's box, and what follows from it: the entry's read is on its way while
@@ -382,7 +372,7 @@ struct PagedKernel {
         Box x;
         x.page = p.num_pages;   // a bad page: a coordinate past the cache, which the copy fills with zeros
         x.ks = 0.f;
-        x.lvs = -INFINITY;
+        x.vs = 0.f;
         if (static_cast<uint32_t>(box * p.box_keys) < static_cast<uint32_t>(it.nkeys)) {
             const bool good = entry >= 0 && entry < p.num_pages;
             if (good) x.page = entry;
@@ -391,7 +381,7 @@ struct PagedKernel {
                 if (good) {
                     const int64_t at = static_cast<int64_t>(entry) * p.Hkv + it.kvh;
                     x.ks = __ldcg(p.ks + at);
-                    x.lvs = fast_log2(__ldcg(p.vs + at));
+                    x.vs = __ldcg(p.vs + at);   // its logarithm waits until the copies are on their way
                 }
             }
         }
@@ -559,8 +549,8 @@ struct PagedKernel {
                     // the scales of the stage's 16-key boxes
                     const int from = (in32 + lane * 16 / p.box_keys) & 31;
                     const float ks = __shfl_sync(0xffffffffu, cur.ks, from);
-                    const float lvs = __shfl_sync(0xffffffffu, cur.lvs, from);
-                    if (lane < Sh::kKeys / 16) s.scales[st * (Sh::kKeys / 16) + lane] = make_float2(ks, lvs);
+                    const float vs = __shfl_sync(0xffffffffu, cur.vs, from);
+                    if (lane < Sh::kKeys / 16) s.scales[st * (Sh::kKeys / 16) + lane] = make_float2(ks, fast_log2(vs));
                     __syncwarp();
                 }
                 if (lane == 0) mbar_arrive(fb);
