@@ -13,7 +13,7 @@
 // e4m3 calls by the consumer warps' instructions (39 % of the issue slots at 2.3 warps
 // per scheduler, each waiting for its own results).
 //
-// How the work is cut. The unit is a stage of 64 (e4m3: 128) keys of a sequence. The units of
+// How the work is cut. The unit is a stage of 64 or 128 keys of a sequence. The units of
 // the batch, in order, are cut into about as many equal ranges as there are persistent CTAs
 // per KV head and chunk, whatever the lengths are: the host knows none of them, and no split
 // count has to be chosen. A range may hold the end of one sequence, several whole ones and the
@@ -25,11 +25,16 @@
 // are read together (16 sequences of 8192 keys, e4m3, tokens outside heads: 68.0 us with one
 // cut through all heads, 51.3 us so).
 //
-// A CTA is one producer warp and four consumer warps around a three-stage ring, as in the
-// split kernel for contiguous caches. The producer's lanes read the block table (and the
-// scales) of the next 32 boxes at once, one batch ahead of the copies, and each lane issues its
-// own box: TMA boxes of gcd(page size, stage) keys, 16-key boxes at a sequence's ragged end, so
-// that a box never crosses a page.
+// A CTA is one producer warp and four or eight consumer warps around a ring of stages, as in the
+// split kernel for contiguous caches. With four, two CTAs share an SM (three at head size 64).
+// 16-bit pages of head size 128 have one CTA of eight per SM: as many warps on half as many ranges, so
+// half the partial results, and a short range streams twice as fast (16 x 131072 keys 1189 -> 1153 us,
+// the ragged batch 89 -> 85 us, one sequence of 32768 keys 31.0 -> 28.5 us), unless the table's rows hold
+// few keys (256 sequences of 256: 18.5 us against 16.5, where two CTAs cover each other's
+// ends). e4m3 pages, whose consumers work harder, lose by it (four tokens 198 us against 174), as does
+// head size 64. The producer's lanes read the block table (and the scales) of the next 32 boxes at
+// once, one batch ahead of the copies, and each lane issues its own box: TMA boxes of gcd(page
+// size, stage) keys, 16-key boxes at a sequence's ragged end, so that a box never crosses a page.
 //
 // e4m3 pages. The products run as fp16 tensor-core products: every e4m3 value is an fp16
 // value, and one conversion takes two elements, 0.5 cycles per SM (measured), 2 of the 11
@@ -45,47 +50,55 @@
 // weights, to the 16-bit type of the product that they enter, and the outputs, once.
 //
 // Measured (one GB300, mean of a graph of calls): 16 sequences of 131072 keys, 32 / 8 heads, bf16
-// 1197 us, 7.2 TB/s; 64 sequences of 512 to 8192 keys, 28 / 4 heads 89.5 us, 6.2 TB/s, over e4m3
-// pages 51.0 us, 5.4 TB/s; one sequence of 1024 keys 8.7 us, of 8192 keys over e4m3 pages 11.1 us.
+// 1153 us, 7.4 TB/s; 64 sequences of 512 to 8192 keys, 28 / 4 heads 85.1 us, 6.5 TB/s, over e4m3
+// pages 50.8 us, 5.5 TB/s; one sequence of 1024 keys 8.8 us, of 8192 keys over e4m3 pages 11.0 us.
 
 #include "paged_common.cuh"
 
 namespace da_impl {
 
 constexpr int kPagedShares = 2048;   // bound of shares (range, KV head, chunk), each with two partial results
-constexpr size_t kPagedCounterBytes = static_cast<size_t>(kPagedShares) * kConsumerWarps * 4;
-constexpr int kMinRange = 2;         // units per range at least (twice as many in a batch of unequal lengths),
-constexpr int kMinCut = 8;           //   where an even batch's sequences have so many: shorter ones stay whole
+constexpr int kWriters = 4;          // consumer warps that write a piece's columns, two of every eight each
+constexpr size_t kPagedCounterBytes = static_cast<size_t>(kPagedShares) * kWriters * 4;
 constexpr int kAlignRange = 16;      // ranges of an even batch up to so long follow its sequences in any case
 constexpr int kMaxSlack = 4;         // units that a cut may move to avoid a partial result
+constexpr int kFewUnits = 8;         // units per SM of a full table up to which CTAs have an SM each
+constexpr int kShortCapacity = 1023; // keys of the block table's rows up to which CTAs of four consumer warps do better
 constexpr float kNoKey = -1e30f;     // running maximum of a column that has seen no key (finite: no NaN arises)
 
-template <int D, bool KV8, int NT>
+template <int D, bool KV8, int NT, int NW>
 struct PagedShape {
-    static constexpr int kKeys = KV8 ? 128 : 64;                    // keys per stage
-    static constexpr int kBoxes = kKeys / kConsumerWarps / 16;      // 16-key boxes per consumer warp
+    static constexpr int kWarps = NW;                               // consumer warps
+    static constexpr int kThreads = (kWarps + 1) * 32;
+    static constexpr int kKeys = kWarps == 8 || KV8 ? 128 : 64;     // keys per stage
+    static constexpr int kBoxes = kKeys / kWarps / 16;              // 16-key boxes per consumer warp
     static constexpr int kRowBytes = KV8 ? D : 2 * D;
     static constexpr int kSliceRow = kRowBytes < 128 ? kRowBytes : 128;   // bytes per row of a TMA box
     static constexpr int kSlices = kRowBytes / kSliceRow;
     static constexpr int kSliceBytes = kKeys * kSliceRow;
     static constexpr int kTileBytes = kSlices * kSliceBytes;
     static constexpr int kStageBytes = 2 * kTileBytes;
-    static constexpr int kRingBytes = kStages * kStageBytes;
+    static constexpr int kRing = kWarps == 8 ? (196608 / kStageBytes < 8 ? 196608 / kStageBytes : 8) : 3;
+    static constexpr int kRingBytes = kRing * kStageBytes;
     static constexpr int kCols = 8 * NT;
-    // the merge of the four warps, in a ring stage: [warp][8][D + 4] accumulators, then [warp][8]
-    // maxima, maxima of the weights, and sums
-    static constexpr int kMergeRow = D + 4;
-    static constexpr int kMergeFloats = kConsumerWarps * 8 * kMergeRow;
-    static_assert((kMergeFloats + 3 * kConsumerWarps * 8) * 4 <= kStageBytes, "item merge must fit in one ring stage");
+    static constexpr int kLeast = kKeys == 64 || KV8 ? 2 : 1;       // units of a range at least (see Ranges)
+    // the merge of the warps, in a ring stage: [warp][8] rows of accumulators, free of bank conflicts both ways by
+    // four floats of padding, or where the stage has no room for it, by dim d of column c at d ^ 4 (c % 8); and
+    // beside the ring [warp][8] maxima, maxima of the weights, sums
+    static constexpr int kMergeRow = kWarps == 8 ? D : D + 4;
+    static __device__ __forceinline__ int merge_dim(int d, int col) { return kWarps == 8 ? d ^ (4 * (col & 7)) : d; }
+    static_assert(kWarps * 8 * kMergeRow * 4 <= kStageBytes, "item merge must fit in one ring stage");
     static constexpr int kQBytes = kCols * D * 2;
     static constexpr int kQOff = kRingBytes;
     static constexpr int kSlotOff = kQOff + kItemSlots * kQBytes;
     static constexpr int kSlotBytes = 64;
     static constexpr int kScaleOff = kSlotOff + kItemSlots * kSlotBytes;   // [stage][box] {ks, log2 vs}
-    static constexpr int kScaleBytes = KV8 ? kStages * (kKeys / 16) * 8 : 0;
-    static constexpr int kLastOff = kScaleOff + kScaleBytes;               // [consumer warp][2] merges to do
-    static constexpr int kBarOff = kLastOff + kConsumerWarps * 2 * kSlotBytes;
-    static constexpr int kNumBars = 2 * kStages + 2 * kItemSlots + 2;
+    static constexpr int kScaleBytes = KV8 ? kRing * (kKeys / 16) * 8 : 0;
+    static constexpr int kRedOff = kScaleOff + kScaleBytes;
+    static constexpr int kRedFloats = 3 * kWarps * 8;                      // twice, used in turn
+    static constexpr int kLastOff = kRedOff + 2 * kRedFloats * 4;          // [writer][2] merges to do
+    static constexpr int kBarOff = kLastOff + kWriters * 2 * kSlotBytes;
+    static constexpr int kNumBars = 2 * kRing + 2 * kItemSlots + 2;
     static constexpr int kSeqOff = kBarOff + kNumBars * 8;                 // prefix[B + 1], even, then pad[B]
     static constexpr int smem_bytes(int B) { return 1024 + kSeqOff + (4 * (B + 2) + B + 15) / 16 * 16; }
 };
@@ -141,12 +154,15 @@ static_assert(sizeof(PagedItem) <= 64, "PagedItem fits its slot");
 // these are done, so independent ones stand together, where they overlap.
 struct Ranges {
     int units, n, w, k, q, rem, split, slack;
-    // t: units of every sequence, or 0. slots: ranges that run at once; `one` of them take an
-    // SM each. streams: the bytes bound the kernel (not the 16-column products of e4m3 pages).
-    __device__ __forceinline__ Ranges(int u, int t, int slots, int one, int short_range, bool streams) : units(u) {
+    // t: units of every sequence, or 0. slots: ranges that run at once; `one` of them take an SM each. least:
+    // units of a range at least where every sequence has eight or more of them (two where it has sixteen, twice
+    // as many in a batch of unequal lengths, and sequences shorter than that stay whole). streams: the bytes bound the kernel (not the 16-column products of e4m3 pages).
+    __device__ __forceinline__ Ranges(int u, int t, int slots, int one, int short_range, int least,
+                                      bool streams)
+        : units(u) {
         const int share1 = (u + one - 1) / one, share = (u + slots - 1) / slots;
         // one range per SM while it is short, then all slots
-        int size = max(t >= kMinCut ? kMinRange : 2 * kMinRange, share1);
+        int size = max(t >= 16 ? 2 : t >= 8 ? least : 2 * least, share1);
         if (size > (t >= size ? kAlignRange : short_range)) size = max(short_range, share);
         const int cuts = (u + size - 1) / size, parts = t / size, whole = (size + t - 1) / max(t, 1), seqs = u / max(t, 1);
         // long ranges too, where four fifths of the slots are enough because the stream bounds them
@@ -217,9 +233,9 @@ __device__ __forceinline__ void e4m3x4_to_f16(uint32_t x, uint32_t& lo, uint32_t
         : "r"(x));
 }
 
-template <int D, int DT, bool KV8, int NT>
+template <int D, int DT, bool KV8, int NT, int NW>
 struct PagedKernel {
-    using Sh = PagedShape<D, KV8, NT>;
+    using Sh = PagedShape<D, KV8, NT, NW>;
 
     struct Layout {
         uint8_t* smem;
@@ -240,8 +256,8 @@ struct PagedKernel {
         s.ring = smem_addr(s.smem);
         s.qbuf = s.ring + Sh::kQOff;
         s.full0 = s.ring + Sh::kBarOff;
-        s.empty0 = s.full0 + 8 * kStages;
-        s.ifull0 = s.empty0 + 8 * kStages;
+        s.empty0 = s.full0 + 8 * Sh::kRing;
+        s.ifull0 = s.empty0 + 8 * Sh::kRing;
         s.iempty0 = s.ifull0 + 8 * kItemSlots;
         s.mfull = s.iempty0 + 8 * kItemSlots;
         s.mdone = s.mfull + 8;
@@ -293,6 +309,7 @@ struct PagedKernel {
     }
     // ... more by the whole CTA.
     static __device__ __forceinline__ void count_units(const Layout& s, const PagedParams& p) {
+        constexpr int kThreads = Sh::kThreads;
         __shared__ int32_t warp_sum[kThreads / 32];
         const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
         constexpr int kMost = (DA_MAX_PAGED_BATCH + kThreads - 1) / kThreads;
@@ -347,12 +364,12 @@ struct PagedKernel {
         __syncthreads();
     }
 
-    // Up to this many units a range has an SM to itself, from there on as many run as fit: a stage takes about
-    // as long at head size 64 as at 128, for half the bytes.
-    static constexpr int kShortRange = D == 128 ? 8 : 3;
+    // Up to this many units a range has an SM to itself in a batch of unequal lengths, from there on as many run as
+    // fit (200 sequences of 25 to 400 keys: 18.5 us with 8, 16.8 with 4).
+    static constexpr int kShortRange = D == 128 ? 4 : 3;
 
     static __device__ __forceinline__ Ranges cut(const Layout& s, const PagedParams& p) {
-        return Ranges(s.prefix[p.B], s.prefix[p.B + 1], p.slots, p.one, kShortRange, !KV8 || NT == 1);
+        return Ranges(s.prefix[p.B], s.prefix[p.B + 1], p.slots, p.one, kShortRange, Sh::kLeast, !KV8 || NT == 1);
     }
 
     // ------------------------------------------------------------ producer
@@ -508,7 +525,7 @@ struct PagedKernel {
                     return;
                 }
                 if (lane == 0) mbar_arrive(s.full0 + 8 * st);
-                if (++st == kStages) {
+                if (++st == Sh::kRing) {
                     st = 0;
                     ph ^= 1;
                 }
@@ -554,7 +571,7 @@ struct PagedKernel {
                     __syncwarp();
                 }
                 if (lane == 0) mbar_arrive(fb);
-                if (++st == kStages) {
+                if (++st == Sh::kRing) {
                     st = 0;
                     ph ^= 1;
                 }
@@ -754,13 +771,12 @@ struct PagedKernel {
 
     // Columns 8n .. 8n + 7 of a piece from the four warps' states. With `direct` the piece is the first of two
     // parts and the second one is written: they are merged here, in the order and with the roundings of merge_parts.
-    static __device__ __forceinline__ void write_piece(const PagedParams& p, const PagedItem& it, const float* red_acc, int n,
-                                                       bool direct) {
-        const float* red_m = red_acc + Sh::kMergeFloats;
-        const float* red_mv = red_m + kConsumerWarps * 8;
-        const float* red_l = red_mv + kConsumerWarps * 8;
+    static __device__ __forceinline__ void write_piece(const PagedParams& p, const PagedItem& it, const float* red_acc,
+                                                       const float* red_m, int n, bool direct) {
+        const float* red_mv = red_m + Sh::kWarps * 8;
+        const float* red_l = red_mv + Sh::kWarps * 8;
         const int l16 = threadIdx.x & 15;
-        const int hh = (threadIdx.x >> 5) + kConsumerWarps * ((threadIdx.x >> 4) & 1), col = 8 * n + hh;
+        const int hh = (threadIdx.x >> 5) + kWriters * ((threadIdx.x >> 4) & 1), col = 8 * n + hh;
         const bool live = col < it.nh;
         float lse1 = -INFINITY;
         float4 o1[kVec];
@@ -773,7 +789,7 @@ struct PagedKernel {
         }
         float M = kNoKey, Mv = kNoKey;
 #pragma unroll
-        for (int w = 0; w < kConsumerWarps; ++w) {
+        for (int w = 0; w < Sh::kWarps; ++w) {
             M = fmaxf(M, red_m[w * 8 + hh]);
             if constexpr (KV8) Mv = fmaxf(Mv, red_mv[w * 8 + hh]);
         }
@@ -782,11 +798,11 @@ struct PagedKernel {
         for (int v = 0; v < kVec; ++v) o[v] = make_float4(0.f, 0.f, 0.f, 0.f);
         float l = 0.f;
 #pragma unroll
-        for (int w = 0; w < kConsumerWarps; ++w) {
+        for (int w = 0; w < Sh::kWarps; ++w) {
             const float wl = fast_exp2(red_m[w * 8 + hh] - M);
             const float wt = KV8 ? fast_exp2(red_mv[w * 8 + hh] - Mv) : wl;
             l = fmaf(wl, red_l[w * 8 + hh], l);
-            const float* row = red_acc + (w * 8 + hh) * Sh::kMergeRow + 4 * l16;
+            const float* row = red_acc + (w * 8 + hh) * Sh::kMergeRow + Sh::merge_dim(4 * l16, hh);
 #pragma unroll
             for (int v = 0; v < kVec; ++v) fma4(o[v], wt, *reinterpret_cast<const float4*>(row + 64 * v));
         }
@@ -828,8 +844,8 @@ struct PagedKernel {
         constexpr int kAhead = NT == 1 ? 16 / kVec : 4 / kVec;   // parts in flight
         const int l16 = threadIdx.x & 15, nparts = it.nparts, nh = it.nh, first_share = it.first_share;
 #pragma unroll 1
-        for (int c0 = threadIdx.x >> 5; c0 < nh; c0 += 2 * kConsumerWarps) {
-            const int c = c0 + kConsumerWarps * ((threadIdx.x >> 4) & 1);
+        for (int c0 = threadIdx.x >> 5; c0 < nh; c0 += 2 * kWriters) {
+            const int c = c0 + kWriters * ((threadIdx.x >> 4) & 1);
             const bool live = c < nh;
             float m = kNoKey, z = 0.f;
             float4 acc[kVec];
@@ -1033,7 +1049,7 @@ struct PagedKernel {
                 if (zeroed) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) mbar_arrive(s.empty0 + 8 * st);
-                if (++st == kStages) {
+                if (++st == Sh::kRing) {
                     st = 0;
                     ph ^= 1;
                 }
@@ -1053,8 +1069,9 @@ struct PagedKernel {
             // A range ends with the beginning of a sequence, whose end the next range began with: where that is
             // all of it, it is written by now, and this piece needs no partial result of its own (8-column
             // kernels: the others have no registers for it).
-            uint32_t* count = p.arrived + item.first_share * kConsumerWarps + warp;
-            const bool two = NT == 1 && item.part >= 0 && (item.part & 1) != 0 && item.nparts == 2;
+            uint32_t* count = p.arrived + item.first_share * kWriters + warp;   // (a writer's)
+            const bool writer = Sh::kWarps == kWriters || warp < kWriters;
+            const bool two = NT == 1 && writer && item.part >= 0 && (item.part & 1) != 0 && item.nparts == 2;
             uint32_t arrived = 0;
             if (two && lane == 0) arrived = ld_acquire(count);
             float* red = reinterpret_cast<float*>(s.smem + st * Sh::kStageBytes);
@@ -1071,22 +1088,24 @@ struct PagedKernel {
                     }
                     ++md;
                 }
+                // in turn: a warp may be a round ahead of one that still reads the last
+                float* red_m = reinterpret_cast<float*>(s.smem + Sh::kRedOff) + (mz & 1) * Sh::kRedFloats;
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     const int col = warp * 8 + 2 * t4 + c;
                     if (g == 0) {
-                        red[Sh::kMergeFloats + col] = m[n][c];
-                        red[Sh::kMergeFloats + kConsumerWarps * 8 + col] = mv[n][c];
-                        red[Sh::kMergeFloats + 2 * kConsumerWarps * 8 + col] = l[n][c];
+                        red_m[col] = m[n][c];
+                        red_m[Sh::kWarps * 8 + col] = mv[n][c];
+                        red_m[2 * Sh::kWarps * 8 + col] = l[n][c];
                     }
                     float* row = red + col * Sh::kMergeRow;
 #pragma unroll
                     for (int a = 0; a < D / 16; ++a) {
                         if constexpr (KV8) {
-                            *reinterpret_cast<float2*>(row + a * 16 + 2 * g) = make_float2(acc[a][n][c], acc[a][n][c + 2]);
+                            *reinterpret_cast<float2*>(row + Sh::merge_dim(a * 16 + 2 * g, col)) = make_float2(acc[a][n][c], acc[a][n][c + 2]);
                         } else {
-                            row[a * 16 + g] = acc[a][n][c];
-                            row[a * 16 + g + 8] = acc[a][n][c + 2];
+                            row[Sh::merge_dim(a * 16 + g, col)] = acc[a][n][c];
+                            row[Sh::merge_dim(a * 16 + g + 8, col)] = acc[a][n][c + 2];
                         }
                     }
                 }
@@ -1101,21 +1120,21 @@ struct PagedKernel {
                     direct = __shfl_sync(0xffffffffu, arrived, 0) == 1;
                     __syncwarp();
                 }
-                if (ok) write_piece(p, item, red, n, direct);
+                if (ok && writer) write_piece(p, item, red, red_m, n, direct);
             }
             // release the stage: order these generic-proxy stores before the copy that refills it
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) mbar_arrive(s.empty0 + 8 * st);
-            if (++st == kStages) {
+            if (++st == Sh::kRing) {
                 st = 0;
                 ph ^= 1;
             }
             if (!ok) break;
             if (direct) {
                 if (lane == 0) *count = 0;
-            } else if (item.part >= 0) {
-                // Warp w wrote the same columns of every partial, so the four warps count apart: the
+            } else if (writer && item.part >= 0) {
+                // Warp w wrote the same columns of every partial, so the writers count apart: the
                 // one whose arrival completes the count merges its columns, and sets the count back.
                 uint32_t n = 0;
                 __syncwarp();
@@ -1146,24 +1165,25 @@ struct PagedKernel {
     }
 };
 
-template <int D, int DT, bool KV8, int NT>
-__global__ void __launch_bounds__(kThreads, kMinBlocksPerSm)
+template <int D, int DT, bool KV8, int NT, int NW>
+__global__ void __launch_bounds__(PagedShape<D, KV8, NT, NW>::kThreads, NW == 8 ? 1 : 2)
 paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
              const __grid_constant__ CUtensorMap tmK16, const __grid_constant__ CUtensorMap tmV16, const PagedParams p) {
-    using K = PagedKernel<D, DT, KV8, NT>;
+    using K = PagedKernel<D, DT, KV8, NT, NW>;
+    using Sh = typename K::Sh;
     extern __shared__ uint8_t smem_raw[];
     const auto s = K::layout(smem_raw, p);
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kStages; ++i) {
+        for (int i = 0; i < Sh::kRing; ++i) {
             mbar_init(s.full0 + 8 * i, 1);
-            mbar_init(s.empty0 + 8 * i, kConsumerWarps);
+            mbar_init(s.empty0 + 8 * i, Sh::kWarps);
         }
         for (int i = 0; i < kItemSlots; ++i) {
             mbar_init(s.ifull0 + 8 * i, 1);
-            mbar_init(s.iempty0 + 8 * i, kConsumerWarps);
+            mbar_init(s.iempty0 + 8 * i, Sh::kWarps);
         }
-        mbar_init(s.mfull, kConsumerWarps);
-        mbar_init(s.mdone, kConsumerWarps);
+        mbar_init(s.mfull, Sh::kWarps);
+        mbar_init(s.mdone, Sh::kWarps);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         prefetch_tensormap(&tmK);
         prefetch_tensormap(&tmV);
@@ -1175,7 +1195,7 @@ paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CU
     grid_dependency_wait();
     if (threadIdx.x == 0) grid_dependents_launch();
     if (p.B > 32) K::count_units(s, p);
-    if ((threadIdx.x >> 5) == kConsumerWarps) K::producer(s, p, &tmK, &tmV, &tmK16, &tmV16);
+    if ((threadIdx.x >> 5) == Sh::kWarps) K::producer(s, p, &tmK, &tmV, &tmK16, &tmV16);
     else K::consumer(s, p);
 }
 
@@ -1233,9 +1253,9 @@ inline int device_sms() {
     return sms;
 }
 
-template <int D, int DT, bool KV8, int NT>
+template <int D, int DT, bool KV8, int NT, int NW>
 da_status launch_paged(const da_paged_cache& c, PagedParams& p, cudaStream_t stream) {
-    using Sh = PagedShape<D, KV8, NT>;
+    using Sh = PagedShape<D, KV8, NT, NW>;
     constexpr int kInner = Sh::kSliceRow / (KV8 ? 1 : 2);
     p.chunks = (p.G * p.tq + Sh::kCols - 1) / Sh::kCols;
     p.box_keys = gcd_of(c.page_size, Sh::kKeys);
@@ -1247,22 +1267,23 @@ da_status launch_paged(const da_paged_cache& c, PagedParams& p, cudaStream_t str
     const int64_t stages = (static_cast<int64_t>(p.max_pages) * p.P + Sh::kKeys - 1) / Sh::kKeys;
     const int64_t units = static_cast<int64_t>(p.B) * stages, lanes = static_cast<int64_t>(p.Hkv) * p.chunks;
     if (units > 0x3fff0000ll || lanes > 0x1000000ll) return DA_ERR_INVALID_ARG;
-    auto kern = paged_kernel<D, DT, KV8, NT>;
+    auto kern = paged_kernel<D, DT, KV8, NT, NW>;
     static DeviceCache cache;
     int resident = 0;
-    if (persistent_grid(kern, kThreads, Sh::smem_bytes(DA_MAX_PAGED_BATCH), cache, &resident) != cudaSuccess)
+    if (persistent_grid(kern, Sh::kThreads, Sh::smem_bytes(DA_MAX_PAGED_BATCH), cache, &resident) != cudaSuccess)
         return DA_ERR_CUDA;
     p.lanes = static_cast<int>(lanes);
     p.slots = std::max(1, std::min(resident, kPagedShares) / p.lanes);
     p.one = std::max(1, device_sms() / p.lanes);
+    // A table whose rows hold few keys gets one CTA per SM (idle ones beside it cost a short call 1.7 us of 12).
+    if (units <= static_cast<int64_t>(p.one) * kFewUnits) p.slots = p.one;
     // CTAs for the most ranges that the kernel can make of these units (see Ranges)
-    const bool few = units <= static_cast<int64_t>(p.one) * PagedKernel<D, DT, KV8, NT>::kShortRange;
-    const int64_t most = few ? p.one : p.slots;
-    const int grid = static_cast<int>(std::min<int64_t>(most, (units + kMinRange - 1) / kMinRange)) * p.lanes;
+    const int64_t most = std::min<int64_t>(p.slots, (units + Sh::kLeast - 1) / Sh::kLeast);
+    const int grid = static_cast<int>(most) * p.lanes;
     cudaLaunchAttribute attrs[1] = {pdl_attr()};
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(Sh::kThreads);
     cfg.dynamicSmemBytes = Sh::smem_bytes(p.B);
     cfg.stream = stream;
     cfg.attrs = attrs;
@@ -1270,11 +1291,20 @@ da_status launch_paged(const da_paged_cache& c, PagedParams& p, cudaStream_t str
     return cudaLaunchKernelEx(&cfg, kern, mk, mv, mk16, mv16, p) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
 }
 
+template <int D, int DT, bool KV8, int NT>
+da_status launch_paged_warps(const da_paged_cache& c, PagedParams& p, cudaStream_t s) {
+    if constexpr (D == 128 && !KV8) {
+        if (static_cast<int64_t>(p.max_pages) * p.P > kShortCapacity) return launch_paged<D, DT, KV8, NT, 8>(c, p, s);
+    }
+    return launch_paged<D, DT, KV8, NT, 4>(c, p, s);
+}
+
 template <int D, int DT>
 da_status launch_paged_any(const da_paged_cache& c, PagedParams& p, cudaStream_t s) {
     const bool wide = item_cols(static_cast<int64_t>(p.G) * p.tq) > kHeadsPerCta;
-    if (c.kv_dtype == DA_E4M3) return wide ? launch_paged<D, DT, true, 2>(c, p, s) : launch_paged<D, DT, true, 1>(c, p, s);
-    return wide ? launch_paged<D, DT, false, 2>(c, p, s) : launch_paged<D, DT, false, 1>(c, p, s);
+    if (c.kv_dtype == DA_E4M3)
+        return wide ? launch_paged_warps<D, DT, true, 2>(c, p, s) : launch_paged_warps<D, DT, true, 1>(c, p, s);
+    return wide ? launch_paged_warps<D, DT, false, 2>(c, p, s) : launch_paged_warps<D, DT, false, 1>(c, p, s);
 }
 
 }  // namespace da_impl
