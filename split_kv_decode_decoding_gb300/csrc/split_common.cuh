@@ -2,8 +2,9 @@
 // (decode_attn_splitkv.cu) and the comparison arms (comparison_arms.cu):
 // work-item decoding, PTX wrappers, the producer warp that feeds the K/V ring,
 // the write-out of a merged item, and the host-side helpers (tensor maps,
-// argument checks, launch facts). Included by exactly those two translation
-// units; it defines no kernel.
+// argument checks, launch facts). Included by those two translation units and,
+// for the wrappers, the error word and the launch helpers, by the paged-cache
+// ones (paged_attn.cu, paged_append.cu); it defines no kernel.
 #ifndef DECODE_ATTN_SPLITKV_SPLIT_COMMON_CUH
 #define DECODE_ATTN_SPLITKV_SPLIT_COMMON_CUH
 
