@@ -109,6 +109,43 @@ def test_attention_over_many_pieces(kv, lens):
     check(out, lse, attend64(q, p), "bf16")
 
 
+@pytest.mark.parametrize("page", [16, 32, 48, 64, 96, 128, 256, 1008])
+@pytest.mark.parametrize("T,Hq,Hkv,layout", [(1, 8, 2, VARLEN), (3, 6, 1, BHSD), (1, 1, 1, BHSD), (2, 20, 1, VARLEN)])
+def test_long_tables_of_16_bit_pages(page, T, Hq, Hkv, layout):
+    """Head size 128 with tables of more than a thousand keys (CTAs of eight consumer warps): every page size, one
+    and two n-tiles, pieces that begin and end anywhere, and a sequence without keys."""
+    lens = [1100, 0, 2, 129, 1023, 640, 4000]
+    p = Paged(lens, Hkv, 128, "bf16" if page % 32 else "f16", page, layout, seed=page + T)
+    q = queries(p, len(lens), T, Hq, p.kv, page)
+    out, lse, err = attend(p, q)
+    assert err == 0
+    check(out, lse, attend64(q, p), p.kv)
+
+
+@pytest.mark.parametrize("kv", ["f16", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_short_sequences_under_a_very_wide_table_and_none_at_all(kv, D):
+    p = Paged([5, 0, 17], 2, D, kv, 16, VARLEN, seed=15, width=9000)
+    q = queries(p, 3, 1, 4, "f16")
+    out, lse, err = attend(p, q)
+    assert err == 0
+    check(out, lse, attend64(q, p), "f16")
+    cache, lens, table = on_gpu(p)
+    lens.zero_()
+    out, lse, err = attend(p, q, tensors=(cache, lens, table))
+    assert err == 0 and np.all(out == 0) and np.all(np.isneginf(lse))
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3])
+def test_scales_that_are_not_positive(scale):
+    for kv in ("bf16", "e4m3"):
+        p = Paged([70, 333], 1, 64, kv, 32, BHSD, seed=16)
+        q = queries(p, 2, 2, 4, "bf16")
+        out, lse, err = attend(p, q, scale=scale)
+        assert err == 0
+        check(out, lse, attend64(q, p, scale), "bf16")
+
+
 def test_a_batch_of_the_largest_size():
     lens = [(7 * i) % 40 for i in range(da.DA_MAX_PAGED_BATCH)]
     for kv in ("f16", "e4m3"):
@@ -517,6 +554,50 @@ def test_a_page_scale_grows_and_earlier_elements_follow():
     for i, x in enumerate(rows):
         r = x[0, 0].double()
         assert torch.all((got[i] - r).abs() <= torch.maximum(r.abs() * 2 * 2.0 ** -4, torch.tensor(s * 2.0 ** -9))), i
+
+
+@pytest.mark.parametrize("D,page", [(128, 64), (64, 256), (128, 1024)])
+def test_many_tokens_of_growing_size_into_a_begun_page(D, page):
+    """Chunks of a prompt, each larger in value than the one before, several rows per thread and pages of
+    more rows than a block holds at once: the begun page is rounded again each time."""
+    chunks = [7, 150, 33, 900]
+    total = sum(chunks)
+    p = Paged([total], 2, D, "e4m3", page, VARLEN, seed=74)
+    cache, _, table = on_gpu(p)
+    ws, cs = da.alloc_paged_workspace(1, 2, 2, D), table_of(total, D)
+    at = 0
+    for i, m in enumerate(chunks):
+        at += m
+        q, k, v = fused_rows(m, 2, 2, D, "bf16", 75 + i)
+        k, v = k * 4.0 ** i, v * 4.0 ** i
+        cu = torch.tensor([0, m], dtype=torch.int32, device="cuda")
+        out = torch.empty(m, 2, D, dtype=torch.bfloat16, device="cuda")
+        da.decode_attn_paged_append(q.cuda(), k.cuda(), v.cuda(), cache, cu, torch.tensor([at], dtype=torch.int32, device="cuda"),
+                                    table, ws, cos_sin=cs.cuda(), q_out=out)
+        assert da.decode_attn_splitkv_get_error(ws) == 0
+        check_append(p, out, cache, append32(p, q, k, v, [at], [m], cs, 1), m)
+
+
+@pytest.mark.parametrize("kv", ["f16", "e4m3"])
+def test_append_to_the_largest_batch(kv):
+    B = da.DA_MAX_PAGED_BATCH
+    new = [(i * 5) % 4 for i in range(B)]
+    lens = [n + (i * 11) % 40 for i, n in enumerate(new)]
+    p = Paged(lens, 1, 64, kv, 16, BHSD, seed=76)
+    q, k, v = fused_rows(sum(new), 2, 1, 64, "f16", 77)
+    cs = table_of(64, 64)
+    got, cache, err = run_append(p, q, k, v, lens, new, cs, 2)
+    assert err == 0
+    check_append(p, got, cache, append32(p, q, k, v, lens, new, cs, 2), sum(new))
+
+
+def test_a_batch_without_new_tokens_changes_nothing():
+    for kv in ("bf16", "e4m3"):
+        p = Paged([20, 0], 1, 64, kv, 16, VARLEN, seed=78)
+        q, k, v = fused_rows(3, 2, 1, 64, "bf16", 79)
+        got, cache, err = run_append(p, q, k, v, [20, 0], [0, 0], table_of(32, 64), 1)
+        assert err == 0 and torch.all(got == -3.0)
+        assert same_bits(cache.k, p.k) and same_bits(cache.v, p.v)
 
 
 def test_scales_that_are_no_powers_of_two_and_stale_scales_of_fresh_pages():
