@@ -141,12 +141,13 @@ struct Turn {
     uint64_t c[4], s[4];
 };
 
+// (Plain loads: the table may come from the kernel before, whose end this kernel awaits while it runs.)
 __device__ __forceinline__ void load_turn(Turn& t, const float* cos_sin, int rot, int pos, int u) {
     const float* at = cos_sin + static_cast<int64_t>(pos) * rot + 8 * u;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const ulonglong2 c = __ldg(reinterpret_cast<const ulonglong2*>(at) + i);
-        const ulonglong2 s = __ldg(reinterpret_cast<const ulonglong2*>(at + rot / 2) + i);
+        const ulonglong2 c = reinterpret_cast<const ulonglong2*>(at)[i];
+        const ulonglong2 s = reinterpret_cast<const ulonglong2*>(at + rot / 2)[i];
         t.c[2 * i] = c.x;
         t.c[2 * i + 1] = c.y;
         t.s[2 * i] = s.x;
