@@ -98,7 +98,7 @@ typedef struct {
                                     DA_DEVERR_SEQLENS */
     const int32_t* block_table;  /* device, int32 [B][table_stride], the first max_pages entries of a row
                                     readable; only the entries of a sequence's own tokens are read */
-    int max_pages;               /* >= 1 */
+    int max_pages;               /* >= 1; max_pages * page_size <= 0x7fffff00, and B times that <= 2^35 */
     int table_stride;            /* >= max_pages */
     int B;                       /* in [1, DA_MAX_PAGED_BATCH] */
     int T_q;                     /* in [1, DA_MAX_QUERY_TOKENS] */

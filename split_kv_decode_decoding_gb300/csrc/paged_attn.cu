@@ -42,9 +42,10 @@
 // two per column into the top of the fp16 range (an element below 2^-28 of its column's largest
 // loses bits, by at most 2^-39 of that largest). The order of the dims inside a 16-dim step is
 // free, so one ldmatrix of 16-bit pairs feeds two steps. The scales never touch the elements: ks
-// multiplies the score, and vs goes into the exponent of the weight, 2^(x + log2 vs - mv), with
-// a running maximum mv of its own, so that the fp16 weights keep their precision however
-// unequal the pages' scales are.
+// multiplies the score, and vs goes into the exponent of the weight, 2^((x - m) + (log2 vs - dv)),
+// with m + dv a running maximum of its own, so that the fp16 weights keep their precision however
+// unequal the pages' scales are. It is held as its distance dv from m: beside a large score log2 vs
+// would lose its last bits.
 //
 // Sums, maxima, accumulators and partial results are float32. Rounded to fewer bits are the
 // weights, to the 16-bit type of the product that they enter, and the outputs, once.
@@ -64,7 +65,8 @@ constexpr int kAlignRange = 16;      // ranges of an even batch up to so long fo
 constexpr int kMaxSlack = 4;         // units that a cut may move to avoid a partial result
 constexpr int kFewUnits = 8;         // units per SM of a full table up to which CTAs have an SM each
 constexpr int kShortCapacity = 1023; // keys of the block table's rows up to which CTAs of four consumer warps do better
-constexpr float kNoKey = -1e30f;     // running maximum of a column that has seen no key (finite: no NaN arises)
+constexpr float kNoKey = -3.402823466e38f;   // running maximum of a column that has seen no key: the least finite
+                                             // value, so that every finite score is above it and no NaN arises
 
 template <int D, bool KV8, int NT, int NW>
 struct PagedShape {
@@ -84,7 +86,7 @@ struct PagedShape {
     static constexpr int kLeast = kKeys == 64 || KV8 ? 2 : 1;       // units of a range at least (see Ranges)
     // the merge of the warps, in a ring stage: [warp][8] rows of accumulators, free of bank conflicts both ways by
     // four floats of padding, or where the stage has no room for it, by dim d of column c at d ^ 4 (c % 8); and
-    // beside the ring [warp][8] maxima, maxima of the weights, sums
+    // beside the ring [warp][8] maxima, the weights' distance from them, sums
     static constexpr int kMergeRow = kWarps == 8 ? D : D + 4;
     static __device__ __forceinline__ int merge_dim(int d, int col) { return kWarps == 8 ? d ^ (4 * (col & 7)) : d; }
     static_assert(kWarps * 8 * kMergeRow * 4 <= kStageBytes, "item merge must fit in one ring stage");
@@ -113,8 +115,9 @@ struct PagedParams {
     float* lse;              // or nullptr
     uint32_t* err;
     uint32_t* arrived;       // [share][consumer warp] partials written, at the share that begins a (sequence, head)
-    float* part_lse;         // [2 * share][columns], log2
-    float* part;             // [2 * share][columns][D]
+    float2* part_sum;        // [2 * share][columns] {maximum m, sum of 2^(x - m)}: a logarithm of the sum would lose
+                             // its last bits beside a large m
+    float* part;             // [2 * share][columns][D], sums of weighted values relative to the same m
     int B, tq, Hq, Hkv, G, P, max_pages, table_stride, num_pages, layout, chunks;
     int lanes;               // CTAs per range: Hkv * chunks
     int slots, one;          // ranges that run at once, and ranges that have an SM to themselves
@@ -740,22 +743,6 @@ struct PagedKernel {
     // n-tile. A lane has kVec times four dims, 64 v + 4 (lane % 16) on.
     static constexpr int kVec = D / 64;
 
-    // One finished column: its output, and its lse (log2).
-    static __device__ __forceinline__ void store_output(const PagedParams& p, int64_t row, const float4 (&o)[kVec], float lse2) {
-        const int l16 = threadIdx.x & 15;
-#pragma unroll
-        for (int v = 0; v < kVec; ++v)
-            *reinterpret_cast<uint2*>(p.out + row * D + 64 * v + 4 * l16) =
-                make_uint2(pack2<DT>(o[v].x, o[v].y), pack2<DT>(o[v].z, o[v].w));
-        if (p.lse != nullptr && l16 == 0) p.lse[row] = lse2 * kLn2;
-    }
-
-    // Where part j of a (sequence, head)'s column lies, in units of columns: j = 0 is the part with the first
-    // key, which its range left in its second place (a range's first place is for the end of a sequence).
-    static __device__ __forceinline__ int64_t part_row(const PagedParams& p, int first_share, int j, int col) {
-        return static_cast<int64_t>(j == 0 ? 2 * first_share + 1 : 2 * (first_share + j * p.lanes)) * Sh::kCols + col;
-    }
-
     static __device__ __forceinline__ void scale4(float4& a, float by) {
         a.x *= by;
         a.y *= by;
@@ -769,29 +756,51 @@ struct PagedKernel {
         a.w = fmaf(w, b.w, a.w);
     }
 
+    // One column whose sums o and l, relative to m, are complete: its output and its lse. One that saw no key has
+    // output 0 and lse -inf. (NaN scores leave m alone and make l NaN.) l >= 1 otherwise (the key that set m weighs 1).
+    static __device__ __forceinline__ void finish_column(const PagedParams& p, int64_t row, float4 (&o)[kVec], float m, float l) {
+        const int l16 = threadIdx.x & 15;
+        const bool none = m == kNoKey && l == 0.f;
+        const float by = none ? 0.f : 1.f / l, lse2 = none ? -INFINITY : m + fast_log2(l);
+#pragma unroll
+        for (int v = 0; v < kVec; ++v) {
+            scale4(o[v], by);
+            *reinterpret_cast<uint2*>(p.out + row * D + 64 * v + 4 * l16) =
+                make_uint2(pack2<DT>(o[v].x, o[v].y), pack2<DT>(o[v].z, o[v].w));
+        }
+        if (p.lse != nullptr && l16 == 0) p.lse[row] = lse2 * kLn2;
+    }
+
+    // Where part j of a (sequence, head)'s column lies, in units of columns: j = 0 is the part with the first
+    // key, which its range left in its second place (a range's first place is for the end of a sequence).
+    static __device__ __forceinline__ int64_t part_row(const PagedParams& p, int first_share, int j, int col) {
+        return static_cast<int64_t>(j == 0 ? 2 * first_share + 1 : 2 * (first_share + j * p.lanes)) * Sh::kCols + col;
+    }
+
     // Columns 8n .. 8n + 7 of a piece from the four warps' states. With `direct` the piece is the first of two
     // parts and the second one is written: they are merged here, in the order and with the roundings of merge_parts.
     static __device__ __forceinline__ void write_piece(const PagedParams& p, const PagedItem& it, const float* red_acc,
                                                        const float* red_m, int n, bool direct) {
-        const float* red_mv = red_m + Sh::kWarps * 8;
-        const float* red_l = red_mv + Sh::kWarps * 8;
+        const float* red_dv = red_m + Sh::kWarps * 8;
+        const float* red_l = red_dv + Sh::kWarps * 8;
         const int l16 = threadIdx.x & 15;
         const int hh = (threadIdx.x >> 5) + kWriters * ((threadIdx.x >> 4) & 1), col = 8 * n + hh;
         const bool live = col < it.nh;
-        float lse1 = -INFINITY;
+        float2 sum1 = make_float2(kNoKey, 0.f);
         float4 o1[kVec];
         if (direct && live) {
             const int64_t at = part_row(p, it.first_share, 1, col);
-            lse1 = __ldcg(p.part_lse + at);
+            sum1 = __ldcg(p.part_sum + at);
 #pragma unroll
             for (int v = 0; v < kVec; ++v)
                 o1[v] = __ldcg(reinterpret_cast<const float4*>(p.part + at * D + 64 * v + 4 * l16));
         }
-        float M = kNoKey, Mv = kNoKey;
+        float M = kNoKey, dV = kNoKey;
 #pragma unroll
-        for (int w = 0; w < Sh::kWarps; ++w) {
-            M = fmaxf(M, red_m[w * 8 + hh]);
-            if constexpr (KV8) Mv = fmaxf(Mv, red_mv[w * 8 + hh]);
+        for (int w = 0; w < Sh::kWarps; ++w) M = fmaxf(M, red_m[w * 8 + hh]);
+        if constexpr (KV8) {
+#pragma unroll
+            for (int w = 0; w < Sh::kWarps; ++w) dV = fmaxf(dV, (red_m[w * 8 + hh] - M) + red_dv[w * 8 + hh]);
         }
         float4 o[kVec];
 #pragma unroll
@@ -800,45 +809,40 @@ struct PagedKernel {
 #pragma unroll
         for (int w = 0; w < Sh::kWarps; ++w) {
             const float wl = fast_exp2(red_m[w * 8 + hh] - M);
-            const float wt = KV8 ? fast_exp2(red_mv[w * 8 + hh] - Mv) : wl;
+            const float wt = KV8 ? fast_exp2((red_m[w * 8 + hh] - M) + (red_dv[w * 8 + hh] - dV)) : wl;
             l = fmaf(wl, red_l[w * 8 + hh], l);
             const float* row = red_acc + (w * 8 + hh) * Sh::kMergeRow + Sh::merge_dim(4 * l16, hh);
 #pragma unroll
             for (int v = 0; v < kVec; ++v) fma4(o[v], wt, *reinterpret_cast<const float4*>(row + 64 * v));
         }
-        const bool none = M == kNoKey && l == 0.f;   // the column saw no key: output 0, lse -inf
-        // (NaN scores leave M alone and make l NaN.) l >= 1 otherwise (the key that set M weighs 1). In 8-bit pages o is relative to Mv, l to M.
-        float inv = none ? 0.f : 1.f / l;
-        if constexpr (KV8) inv *= Mv == kNoKey ? 0.f : fast_exp2(Mv - M);
-#pragma unroll
-        for (int v = 0; v < kVec; ++v) scale4(o[v], inv);
-        float lse2 = none ? -INFINITY : M + fast_log2(l);
         if (!live) return;
+        if constexpr (KV8) {   // o is relative to M + dV, l to M
+            const float by = fast_exp2(dV);
+#pragma unroll
+            for (int v = 0; v < kVec; ++v) scale4(o[v], by);
+        }
         if (direct) {
-            const float m = fmaxf(kNoKey, fmaxf(lse2, lse1));
-            const float w0 = fast_exp2(lse2 - m), w1 = fast_exp2(lse1 - m), z = w0 + w1;
-            const bool empty = m == kNoKey && z == 0.f;
-            const float by = empty ? 0.f : 1.f / z;
+            const float m = fmaxf(M, sum1.x), w0 = fast_exp2(M - m), w1 = fast_exp2(sum1.x - m);
 #pragma unroll
             for (int v = 0; v < kVec; ++v) {
                 scale4(o[v], w0);
                 fma4(o[v], w1, o1[v]);
-                scale4(o[v], by);
             }
-            lse2 = empty ? -INFINITY : m + fast_log2(z);
+            l = __fadd_rn(__fmul_rn(w0, l), __fmul_rn(w1, sum1.y));
+            M = m;
         }
         if (it.part < 0 || direct) {
-            store_output(p, output_row(p, it, col), o, lse2);
+            finish_column(p, output_row(p, it, col), o, M, l);
         } else {
             const int64_t at = static_cast<int64_t>(it.part) * Sh::kCols + col;
 #pragma unroll
             for (int v = 0; v < kVec; ++v) *reinterpret_cast<float4*>(p.part + at * D + 64 * v + 4 * l16) = o[v];
-            if (l16 == 0) p.part_lse[at] = lse2;
+            if (l16 == 0) p.part_sum[at] = make_float2(M, l);
         }
     }
 
     // Merge this warp's columns of a (sequence, head) whose partials are all written. Lane j of a half warp
-    // takes part j's lse and weight, so that every load is issued before any of them is needed; the order
+    // takes part j's maximum, sum and weight, so that every load is issued before any of them is needed; the order
     // of the sums is that of the parts.
     static __device__ __forceinline__ void merge_parts(const PagedParams& p, const PagedItem& it) {
         constexpr int kAhead = NT == 1 ? 16 / kVec : 4 / kVec;   // parts in flight
@@ -854,7 +858,8 @@ struct PagedKernel {
 #pragma unroll 1
             for (int j0 = 0; j0 < nparts; j0 += 16) {
                 const int count = live ? min(16, nparts - j0) : 0;
-                const float lv = l16 < count ? __ldcg(p.part_lse + part_row(p, first_share, j0 + l16, c)) : -INFINITY;
+                const float2 part = l16 < count ? __ldcg(p.part_sum + part_row(p, first_share, j0 + l16, c))
+                                                : make_float2(kNoKey, 0.f);
                 float w = 0.f;
 #pragma unroll 1
                 for (int j = 0; j < min(16, nparts - j0); j += kAhead) {
@@ -868,12 +873,12 @@ struct PagedKernel {
                                                     : make_float4(0.f, 0.f, 0.f, 0.f);
                     }
                     if (j == 0) {
-                        float top = lv;
+                        float top = part.x;
 #pragma unroll
                         for (int off = 8; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
                         const float mn = fmaxf(m, top);       // stays kNoKey while no part has seen a key
-                        w = fast_exp2(lv - mn);
-                        float sum = w;
+                        w = fast_exp2(part.x - mn);
+                        float sum = __fmul_rn(w, part.y);
 #pragma unroll
                         for (int off = 8; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
                         const float al = fast_exp2(m - mn);
@@ -890,11 +895,7 @@ struct PagedKernel {
                     }
                 }
             }
-            const bool none = m == kNoKey && z == 0.f;
-            const float inv = none ? 0.f : 1.f / z;
-#pragma unroll
-            for (int v = 0; v < kVec; ++v) scale4(acc[v], inv);
-            if (live) store_output(p, output_row(p, it, c), acc, none ? -INFINITY : m + fast_log2(z));
+            if (live) finish_column(p, output_row(p, it, c), acc, m, z);
         }
     }
 
@@ -935,14 +936,15 @@ struct PagedKernel {
             for (int a = 0; a < D / 16; ++a)
 #pragma unroll
                 for (int n = 0; n < NT; ++n) acc[a][n][0] = acc[a][n][1] = acc[a][n][2] = acc[a][n][3] = 0.f;
-            // running maximum of the scores and (8-bit) of the weights, this thread's share of the sum
-            float m[NT][2], mv[NT][2], l[NT][2];
+            // running maximum of the scores, (8-bit) how far that of the weights is above it, this thread's share of
+            // the sum
+            float m[NT][2], dv[NT][2], l[NT][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    m[n][c] = mv[n][c] = kNoKey;
-                    l[n][c] = 0.f;
+                    m[n][c] = kNoKey;
+                    dv[n][c] = l[n][c] = 0.f;
                 }
 
             for (int t = 0; t < ntiles; ++t) {
@@ -990,8 +992,8 @@ struct PagedKernel {
                                 const float f = KV8 ? qs[n][j & 1] * ks : qs[n][j & 1];
                                 const bool seen = key + 8 * (j >> 1) < vis[n][j & 1];
                                 x[bx][n][j] = seen ? x[bx][n][j] * f : -INFINITY;
-                                move = move || x[bx][n][j] > m[n][j & 1] + kLazyRescale;
-                                if constexpr (KV8) move = move || x[bx][n][j] + lv[bx] > mv[n][j & 1] + kLazyRescale;
+                                const float above = KV8 ? fmaxf(lv[bx] - dv[n][j & 1], 0.f) : 0.f;
+                                move = move || x[bx][n][j] - m[n][j & 1] > kLazyRescale - above;
                             }
                     }
                     // The reference of a column moves only when a score passes it by more than
@@ -1002,22 +1004,26 @@ struct PagedKernel {
                         for (int n = 0; n < NT; ++n)
 #pragma unroll
                             for (int c = 0; c < 2; ++c) {
-                                float top = m[n][c], topv = mv[n][c];
+                                float top = m[n][c];
 #pragma unroll
-                                for (int bx = 0; bx < Sh::kBoxes; ++bx) {
-                                    const float y = fmaxf(x[bx][n][c], x[bx][n][c + 2]);
-                                    top = fmaxf(top, y);
-                                    topv = fmaxf(topv, y + lv[bx]);
-                                }
+                                for (int bx = 0; bx < Sh::kBoxes; ++bx)
+                                    top = fmaxf(top, fmaxf(x[bx][n][c], x[bx][n][c + 2]));
 #pragma unroll
-                                for (int off = 4; off < 32; off <<= 1) {
-                                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-                                    if constexpr (KV8) topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, off));
-                                }
+                                for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
                                 const float al = fast_exp2(m[n][c] - top);
-                                const float av = KV8 ? fast_exp2(mv[n][c] - topv) : al;
+                                float av = al;
+                                if constexpr (KV8) {
+                                    float dnew = fmaxf(kNoKey, (m[n][c] - top) + dv[n][c]);
+#pragma unroll
+                                    for (int bx = 0; bx < Sh::kBoxes; ++bx)
+                                        dnew = fmaxf(dnew, (fmaxf(x[bx][n][c], x[bx][n][c + 2]) - top) + lv[bx]);
+#pragma unroll
+                                    for (int off = 4; off < 32; off <<= 1)
+                                        dnew = fmaxf(dnew, __shfl_xor_sync(0xffffffffu, dnew, off));
+                                    av = fast_exp2((m[n][c] - top) + (dv[n][c] - dnew));
+                                    dv[n][c] = dnew;
+                                }
                                 m[n][c] = top;
-                                mv[n][c] = KV8 ? topv : top;
                                 l[n][c] *= al;
 #pragma unroll
                                 for (int a = 0; a < D / 16; ++a) {
@@ -1034,9 +1040,10 @@ struct PagedKernel {
                             float w[4];
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
-                                w[j] = fast_exp2(x[bx][n][j] - m[n][j & 1]);
+                                const float d = x[bx][n][j] - m[n][j & 1];
+                                w[j] = fast_exp2(d);
                                 l[n][j & 1] += w[j];
-                                if constexpr (KV8) w[j] = fast_exp2(x[bx][n][j] + (lv[bx] - mv[n][j & 1]));
+                                if constexpr (KV8) w[j] = fast_exp2(d + (lv[bx] - dv[n][j & 1]));
                             }
                             // the weights are rounded to the 16-bit type of the product's other operand
                             pb[n][0] = movmatrix_trans(pack2<KV8 ? DA_F16 : DT>(w[0], w[1]));
@@ -1095,7 +1102,7 @@ struct PagedKernel {
                     const int col = warp * 8 + 2 * t4 + c;
                     if (g == 0) {
                         red_m[col] = m[n][c];
-                        red_m[Sh::kWarps * 8 + col] = mv[n][c];
+                        red_m[Sh::kWarps * 8 + col] = dv[n][c];
                         red_m[2 * Sh::kWarps * 8 + col] = l[n][c];
                     }
                     float* row = red + col * Sh::kMergeRow;
@@ -1316,7 +1323,7 @@ extern "C" {
 size_t decode_attn_paged_workspace_size(int T_q, int Hq, int Hkv, int D) {
     if (T_q < 1 || T_q > DA_MAX_QUERY_TOKENS || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || (D != 64 && D != 128)) return 0;
     const int cols = item_cols(static_cast<int64_t>(Hq / Hkv) * T_q);
-    return kPagedHeaderBytes + kPagedCounterBytes + static_cast<size_t>(2 * kPagedShares) * cols * (D + 1) * 4;
+    return kPagedHeaderBytes + kPagedCounterBytes + static_cast<size_t>(2 * kPagedShares) * cols * (D + 2) * 4;
 }
 
 da_status decode_attn_paged_workspace_init(void* workspace, size_t workspace_bytes, void* stream) {
@@ -1351,7 +1358,7 @@ da_status decode_attn_paged(const da_paged_attn* args, void* stream) {
     p.G = a.Hq / c.Hkv;
     const int cols = item_cols(static_cast<int64_t>(p.G) * a.T_q);
     p.part = reinterpret_cast<float*>(ws + kPagedHeaderBytes + kPagedCounterBytes);
-    p.part_lse = p.part + static_cast<size_t>(2 * kPagedShares) * cols * c.D;
+    p.part_sum = reinterpret_cast<float2*>(p.part + static_cast<size_t>(2 * kPagedShares) * cols * c.D);
     p.B = a.B;
     p.tq = a.T_q;
     p.Hq = a.Hq;

@@ -146,6 +146,38 @@ def test_scales_that_are_not_positive(scale):
         check(out, lse, attend64(q, p, scale), "bf16")
 
 
+@pytest.mark.parametrize("kv,q_size,k_size,scale", [
+    ("bf16", -2.0 ** 60, 2.0 ** 60, 0.125),      # scores of -2^123 and below: still above a column without keys
+    ("f16", 2.0 ** 12, 2.0 ** 12, 1.0), ("e4m3", -2.0 ** 100, 2.0 ** 8, 0.125), ("e4m3", 2.0 ** 10, 2.0, 1.0)])
+@pytest.mark.parametrize("T,lens", [(1, [1, 50, 300, 0]), (3, [2, 700])])
+def test_equal_scores_of_any_size_give_the_mean(kv, q_size, k_size, scale, T, lens):
+    """Every key alike: the output is the mean of the values that a token sees, whatever the score. The products are
+    powers of two, so every score is the same float; a weight is 1 or, of an e4m3 value, its page's scale relative to
+    the largest in sight, rounded to fp16 (2^-11); sums of n float32 terms are off by n 2^-24, log2, exp2 and their
+    arguments by less than 2^-17 for these scales."""
+    q_type = "f16" if kv == "f16" else "bf16"
+    p = Paged(lens, 1, 64, kv, 16, VARLEN, seed=17)
+    p.k = torch.full_like(p.k.float(), k_size).to(p.k.dtype)
+    if kv == "e4m3":
+        p.k_scale = torch.ones_like(p.k_scale)
+        p.v_scale = torch.rand(p.v_scale.shape, generator=torch.Generator().manual_seed(18)) * 3 + 0.3
+    q = torch.full((len(lens), T, 2, 64), q_size).to(DTYPES[q_type])
+    out, lse, err = attend(p, q, scale=scale)
+    assert err == 0
+    x = q_size * k_size * 64 * scale
+    for b, L in enumerate(lens):
+        v = p.sequence(b)[1].numpy()[:, 0] if L else None
+        for t in range(T):
+            n = L - T + 1 + t
+            if n <= 0:
+                assert np.all(out[b, t] == 0) and np.all(np.isneginf(lse[b, t]))
+                continue
+            mean, size = v[:n].mean(0), np.abs(v[:n]).mean(0)
+            tol = half_step(mean, DTYPES[q_type]) + size * (2.0 ** -11 * (kv == "e4m3") + n * 2.0 ** -24 + 2.0 ** -17)
+            assert np.all(np.abs(out[b, t] - mean) <= tol), (b, t)
+            assert np.all(np.abs(lse[b, t] - (x + math.log(n))) <= 2.0 ** -21 * abs(x) + 1e-5)
+
+
 def test_a_batch_of_the_largest_size():
     lens = [(7 * i) % 40 for i in range(da.DA_MAX_PAGED_BATCH)]
     for kv in ("f16", "e4m3"):
