@@ -10,7 +10,7 @@
 // operations per column, far below what the tensor cores deliver, so everything here serves
 // the stream. Short calls are bound by latency: a chain of kv_lens, block table, first copy,
 // a few stages, the merge of the warps, a partial result's way through the L2. 16-column
-// e4m3 calls by the consumer warps' instructions (39 % of the issue slots at 2.3 warps
+// e4m3 calls by the consumer warps' instructions (40 % of the issue slots at 2.4 warps
 // per scheduler, each waiting for its own results).
 //
 // How the work is cut. The unit is a stage of 64 or 128 keys of a sequence. The units of
@@ -31,7 +31,7 @@
 // half the partial results, and a short range streams twice as fast (16 x 131072 keys 1189 -> 1153 us,
 // the ragged batch 89 -> 85 us, one sequence of 32768 keys 31.0 -> 28.5 us), unless the table's rows hold
 // few keys (256 sequences of 256: 18.5 us against 16.5, where two CTAs cover each other's
-// ends). e4m3 pages, whose consumers work harder, lose by it (four tokens 198 us against 174), as does
+// ends). e4m3 pages, whose consumers work harder, lose by it (four tokens 191 us against 169), as does
 // head size 64. The producer's lanes read the block table (and the scales) of the next 32 boxes at
 // once, one batch ahead of the copies, and each lane issues its own box: TMA boxes of gcd(page
 // size, stage) keys, 16-key boxes at a sequence's ragged end, so that a box never crosses a page.
@@ -47,7 +47,8 @@
 // unequal the pages' scales are. It is held as its distance dv from m: beside a large score log2 vs
 // would lose its last bits.
 //
-// Sums, maxima, accumulators and partial results are float32. Rounded to fewer bits are the
+// Sums, maxima, accumulators and partial results are float32. A partial result keeps its maximum and its
+// sum apart, so that scores of any size are joined with no more loss than they were computed with. Rounded to fewer bits are the
 // weights, to the 16-bit type of the product that they enter, and the outputs, once.
 //
 // Measured (one GB300, mean of a graph of calls): 16 sequences of 131072 keys, 32 / 8 heads, bf16
@@ -159,7 +160,8 @@ struct Ranges {
     int units, n, w, k, q, rem, split, slack;
     // t: units of every sequence, or 0. slots: ranges that run at once; `one` of them take an SM each. least:
     // units of a range at least where every sequence has eight or more of them (two where it has sixteen, twice
-    // as many in a batch of unequal lengths, and sequences shorter than that stay whole). streams: the bytes bound the kernel (not the 16-column products of e4m3 pages).
+    // as many in a batch of unequal lengths, and sequences shorter than that stay whole). streams: the bytes bound
+    // the kernel (not the 16-column products of e4m3 pages).
     __device__ __forceinline__ Ranges(int u, int t, int slots, int one, int short_range, int least,
                                       bool streams)
         : units(u) {
