@@ -23,9 +23,9 @@
 // took 20 to 60 % longer.
 //
 // Measured (one GB300): 16-bit pages, 9887 tokens of 32 + 2 x 8 heads in 5 prompts 39.3 us,
-// 6.3 TB/s; 64 tokens, one per sequence, 28 + 2 x 4 heads 2.8 us. e4m3 pages: the same prompts 43.4 us,
-// 5.2 TB/s (bound by instructions and by the two waits per page and head, not by its bytes); 256 tokens,
-// one per sequence, 16 + 2 x 2 heads 4.3 us.
+// 6.3 TB/s; 64 tokens, one per sequence, 28 + 2 x 4 heads 2.8 us. e4m3 pages: the same prompts 41.2 us,
+// 5.5 TB/s (bound by instructions and by the two waits per page and head, not by its bytes); 256 tokens,
+// one per sequence, 16 + 2 x 2 heads 4.0 us.
 
 #include "paged_common.cuh"
 
@@ -174,11 +174,39 @@ __device__ __forceinline__ void unit_dims(const AppendParams& p, int u, int& da,
     db = paired ? p.rot / 2 + 8 * u : 16 * u + 8;
 }
 
-// Stage cu_new and kv_lens in shared memory.
+// Stage cu_new and kv_lens in shared memory; AT_ONCE: every read on its way before the first is waited for
+// (256 tokens, one per sequence, into e4m3 pages 4.2 -> 4.1 us; 9887 tokens 43.6 -> 42.2). Where the threads hold rows
+// meanwhile and few registers are left (16-bit pages, the rows of a decode step) it costs more than it gives:
+// 9887 tokens into 16-bit pages 39.5 -> 41.3 us.
+template <bool AT_ONCE>
 __device__ __forceinline__ void stage_sequences(const AppendParams& p, int32_t* cu, int32_t* lens) {
-    for (int i = threadIdx.x; i <= p.B; i += kAppendThreads) {
-        cu[i] = ld_cg_s32(p.cu + i);
-        if (i < p.B) lens[i] = ld_cg_s32(p.lens + i);
+    if constexpr (AT_ONCE) {
+        constexpr int kMost = (DA_MAX_PAGED_BATCH + kAppendThreads - 1) / kAppendThreads;
+        const int tid = threadIdx.x;
+        int32_t c[kMost], l[kMost], c0 = 0;
+        if (tid == 0) c0 = ld_cg_s32(p.cu);
+#pragma unroll
+        for (int k = 0; k < kMost; ++k) {
+            const int i = tid + k * kAppendThreads;
+            if (i < p.B) {
+                c[k] = ld_cg_s32(p.cu + i + 1);
+                l[k] = ld_cg_s32(p.lens + i);
+            }
+        }
+        if (tid == 0) cu[0] = c0;
+#pragma unroll
+        for (int k = 0; k < kMost; ++k) {
+            const int i = tid + k * kAppendThreads;
+            if (i < p.B) {
+                cu[i + 1] = c[k];
+                lens[i] = l[k];
+            }
+        }
+    } else {
+        for (int i = threadIdx.x; i <= p.B; i += kAppendThreads) {
+            cu[i] = ld_cg_s32(p.cu + i);
+            if (i < p.B) lens[i] = ld_cg_s32(p.lens + i);
+        }
     }
     __syncthreads();
 }
@@ -209,7 +237,8 @@ __device__ __forceinline__ int page_of(const AppendParams& p, int b, int pos) {
 template <int D, int DT, bool HALF, bool KV16>
 struct AppendRows {
     static constexpr int kUnits = D / 16;
-    static constexpr int kAhead = 2;   // query heads in flight
+    // query heads in flight: as many as the registers hold (e4m3 pages, 9887 tokens: 42.2 us with two, 41.5 with four)
+    static constexpr int kAhead = KV16 ? 2 : 4;
     struct Chunk {
         uint4 a, b;
     };
@@ -312,7 +341,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append16_kernel(const Appen
     grid_dependency_wait();
     if (threadIdx.x == 0) grid_dependents_launch();
     AppendRows<D, DT, HALF, true> rows(p, blockIdx.x);
-    stage_sequences(p, cu, lens);
+    stage_sequences<false>(p, cu, lens);
     if (blockIdx.x == 0) flag_bad_sequences(p, cu, lens);
     rows.finish(cu, lens);
 }
@@ -398,12 +427,15 @@ __device__ __forceinline__ float grow_scale(const AppendParams& p, const PagePar
 
 // A unit is the new tokens of one page and KV head, keys or values, by kLanes threads: a warp for the few
 // tokens of a decode step, the block for prompts. A thread holds kKeep rows in registers between the
-// pass that finds the largest element and the one that rounds (further rows are read twice).
+// pass that finds the largest element and the one that rounds (further rows are read twice): rotated, in
+// float32, where it is one row (256 tokens, one per sequence: 4.2 us against 4.3), as they were read where
+// twice as many such registers would cost a third of the blocks (9887 tokens: 43.3 us against 49).
 template <int D, int DT, bool HALF, int kLanes>
 struct AppendPage {
     static constexpr int kUnits = D / 16;
     static constexpr int kRows = kLanes / kUnits;   // rows at once
     static constexpr int kKeep = kLanes == 32 ? 1 : 2;
+    static constexpr bool kKeepTurned = kKeep == 1;
     struct Chunk {
         uint4 a, b;
     };
@@ -416,6 +448,7 @@ struct AppendPage {
     const uint16_t* src;   // the first new row
     int64_t stride;
     Chunk kept[kKeep];
+    Chunk16 kept_turned[kKeepTurned ? kKeep : 1];
 
     __device__ __forceinline__ AppendPage(const AppendParams& params, int l) : p(params), lane(l), u(l % kUnits), r0(l / kUnits) {
         unit_dims<HALF>(p, u, da, db);
@@ -452,7 +485,8 @@ struct AppendPage {
         for (int i = 0; i < kKeep; ++i)
             if (r0 + i * kRows < x.n) {
                 Chunk16 e;
-                turned(kept[i], r0 + i * kRows, e);
+                if constexpr (kKeepTurned) e = kept_turned[i];
+                else turned(kept[i], r0 + i * kRows, e);
                 f(r0 + i * kRows, e);
             }
         for (int r = r0 + kKeep * kRows; r < x.n; r += kRows) {
@@ -513,6 +547,11 @@ struct AppendPage {
         const bool is_v = (hv & 1) != 0;
         const float* scale_at = (is_v ? p.vs : p.ks) + static_cast<int64_t>(x.page) * p.Hkv + head;
         const float before = x.slot0 > 0 ? *reinterpret_cast<const volatile float*>(scale_at) : 0.f;
+        if constexpr (kKeepTurned) {
+#pragma unroll
+            for (int i = 0; i < kKeep; ++i)
+                if (r0 + i * kRows < x.n) turned(kept[i], r0 + i * kRows, kept_turned[i]);
+        }
         float amax = largest<false>(red);
         if (amax == INFINITY) amax = largest<true>(red);   // the same for every thread
         // every thread has read `before` by now
@@ -539,11 +578,11 @@ __global__ void __launch_bounds__(kAppendThreads, kLanes == 32 ? 2 : 3) append8_
     if (tid == 0) grid_dependents_launch();
     if (static_cast<int>(blockIdx.x) >= p.page_blocks) {
         AppendRows<D, DT, HALF, false> rows(p, blockIdx.x - p.page_blocks);
-        stage_sequences(p, cu, lens);
+        stage_sequences<(kLanes > 32)>(p, cu, lens);
         rows.finish(cu, lens);
         return;
     }
-    stage_sequences(p, cu, lens);
+    stage_sequences<true>(p, cu, lens);
     if (blockIdx.x == 0) flag_bad_sequences(p, cu, lens);
     // running count of touched pages: each thread sums its run of sequences, then one scan
     const int per = (p.B + kAppendThreads - 1) / kAppendThreads;
@@ -605,7 +644,13 @@ da_status launch_append(K kern, int grid, size_t smem, const AppendParams& p, cu
     return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
 }
 
-constexpr int kMostPageBlocks = 152 * 2;     // blocks for pages; beyond, each takes several
+// Blocks for pages: what fits the GPU at once, times the pages' share of the work, an element of theirs taken for
+// kPageWeight of a query's. Each takes several units, so that rows, which are bound by bytes, run beside pages,
+// which are bound by instructions, from the first to the last (7200 tokens of 3 x 32 128-dim heads: 66.2 us, with
+// two thirds for pages 92.5, with all 68.4; 9887 tokens of 32 + 2 x 8 heads 41.2, all 43.0, a block for each unit
+// 49.8). Rows take over what pages leave, not the other way round, hence the large weight (8; 3 or 4: 5.8 us
+// where 8 has 4.3, 200 tokens of 28 + 2 x 4 heads).
+constexpr int kPageWeight = 8;
 constexpr int kManyHeads = 8;                // heads per thread where there are many tokens
 constexpr int64_t kManyThreads = 152 * 512;  // threads that keep the GPU busy
 
@@ -630,7 +675,9 @@ da_status run_append(AppendParams& p, bool e4m3, cudaStream_t stream) {
     const int64_t units = touched * p.Hkv * 2;
     if (units > 0x3fffffffll) return DA_ERR_INVALID_ARG;
     constexpr int kWarps = kAppendThreads / 32;
-    p.page_blocks = static_cast<int>(std::min<int64_t>(few ? (units + kWarps - 1) / kWarps : units, kMostPageBlocks));
+    const int64_t page_work = 2ll * kPageWeight * p.Hkv, resident = 152 * (few ? 2 : 3);
+    const int64_t most = std::max<int64_t>(1, resident * page_work / (page_work + p.Hq));
+    p.page_blocks = static_cast<int>(std::min<int64_t>(few ? (units + kWarps - 1) / kWarps : units, most));
     return few ? launch_append(append8_kernel<D, DT, HALF, 32>, p.page_blocks + row_blocks, smem, p, stream)
                : launch_append(append8_kernel<D, DT, HALF, kAppendThreads>, p.page_blocks + row_blocks, smem, p, stream);
 }
