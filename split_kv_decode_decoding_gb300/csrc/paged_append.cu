@@ -425,8 +425,15 @@ __device__ __forceinline__ float grow_scale(const AppendParams& p, const PagePar
     return scale;
 }
 
+// Barrier of a unit's threads.
+template <int kLanes>
+__device__ __forceinline__ void unit_sync() {
+    if constexpr (kLanes == kAppendThreads) __syncthreads();
+    else asm volatile("bar.sync %0, %1;" ::"r"(1 + static_cast<int>(threadIdx.x) / kLanes), "n"(kLanes) : "memory");
+}
+
 // A unit is the new tokens of one page and KV head, keys or values, by kLanes threads: a warp for the few
-// tokens of a decode step, the block for prompts. A thread holds kKeep rows in registers between the
+// tokens of a decode step, up to the block for prompts (run_append). A thread holds kKeep rows in registers between the
 // pass that finds the largest element and the one that rounds (further rows are read twice): rotated, in
 // float32, where it is one row (256 tokens, one per sequence: 4.2 us against 4.3), as they were read where
 // twice as many such registers would cost a third of the blocks (9887 tokens: 43.3 us against 49).
@@ -510,11 +517,10 @@ struct AppendPage {
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
         if constexpr (kLanes > 32) {
-            if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = amax;
-            __syncthreads();
+            if ((threadIdx.x & 31) == 0) red[lane >> 5] = amax;
+            unit_sync<kLanes>();
 #pragma unroll
             for (int w = 0; w < kLanes / 32; ++w) amax = fmaxf(amax, red[w]);
-            __syncthreads();   // `red` is free again
         } else {
             __syncwarp();
         }
@@ -540,7 +546,7 @@ struct AppendPage {
         });
     }
 
-    // red: shared, a float per warp.
+    // red: shared, a float per warp of the unit, not the one of the call before.
     __device__ __forceinline__ void finish(float* red) {
         if (!x.check(p, lane == 0)) return;   // for the whole unit
         const int head = hv >> 1;
@@ -553,7 +559,10 @@ struct AppendPage {
                 if (r0 + i * kRows < x.n) turned(kept[i], r0 + i * kRows, kept_turned[i]);
         }
         float amax = largest<false>(red);
-        if (amax == INFINITY) amax = largest<true>(red);   // the same for every thread
+        if (amax == INFINITY) {   // the same for every thread
+            if constexpr (kLanes > 32) unit_sync<kLanes>();   // `red` has been read
+            amax = largest<true>(red);
+        }
         // every thread has read `before` by now
         const float scale = grow_scale<D, kLanes>(p, x, head, is_v, before, amax, lane);
         uint8_t* to = (is_v ? p.vc : p.kc) + page_row(p.layout, x.page, x.slot0, head, p.P, p.Hkv) * D;
@@ -569,7 +578,7 @@ template <int D, int DT, bool HALF, int kLanes>
 __global__ void __launch_bounds__(kAppendThreads, kLanes == 32 ? 2 : 3) append8_kernel(const AppendParams p) {
     extern __shared__ int32_t append_smem[];
     __shared__ int32_t warp_sum[kAppendThreads / 32];
-    __shared__ float red[kAppendThreads / 32];
+    __shared__ float red[2][kAppendThreads / 32];   // used in turn
     int32_t* cu = append_smem;
     int32_t* lens = cu + p.B + 1;
     int32_t* prefix = lens + p.B;      // touched pages before sequence b, [B + 1]
@@ -615,9 +624,11 @@ __global__ void __launch_bounds__(kAppendThreads, kLanes == 32 ? 2 : 3) append8_
     const uint32_t groups = 2u * p.Hkv, units = prefix[p.B] * groups;   // below 2^31: checked by the host
     constexpr int kPerBlock = kAppendThreads / kLanes;
     const uint32_t step = static_cast<uint32_t>(p.page_blocks) * kPerBlock;
-    AppendPage<D, DT, HALF, kLanes> page(p, kLanes == 32 ? lane : tid);
+    AppendPage<D, DT, HALF, kLanes> page(p, tid % kLanes);
+    const int sub = tid / kLanes;
+    int turn = 0;
     // the bound is uniform over a unit's threads
-    for (uint32_t unit = blockIdx.x * kPerBlock + (kLanes == 32 ? warp : 0); unit < units; unit += step) {
+    for (uint32_t unit = blockIdx.x * kPerBlock + sub; unit < units; unit += step, turn ^= 1) {
         const int nth = static_cast<int>(unit / groups), hv = static_cast<int>(unit - nth * groups);
         int lo = 0, hi = p.B - 1;   // last b with prefix[b] <= nth
         while (lo < hi) {
@@ -626,7 +637,7 @@ __global__ void __launch_bounds__(kAppendThreads, kLanes == 32 ? 2 : 3) append8_
             else hi = mid - 1;
         }
         page.load(new_tokens(p, cu[lo], cu[lo + 1], lens[lo]), lo, nth - prefix[lo], hv);
-        page.finish(red);
+        page.finish(&red[turn][sub * (kLanes / 32)]);
     }
 }
 
@@ -670,16 +681,22 @@ da_status run_append(AppendParams& p, bool e4m3, cudaStream_t stream) {
     if (!e4m3) return launch_append(append16_kernel<D, DT, HALF>, row_blocks, smem, p, stream);
     // a sequence's n new tokens touch at most min(n, n / P + 2) pages
     const int64_t touched = std::min<int64_t>(p.T, p.T / p.P + 2ll * p.B);
-    // A warp per page and head while pages get few tokens each, the block where they get many.
-    const bool few = p.T < 4 * static_cast<int64_t>(p.B) || p.P <= 16;
+    // Threads per page and head: a warp while pages get few tokens each, else as many as hold a page of 32 or of
+    // 64 tokens in registers: fewer read rows twice (pages of 64 tokens, half the threads: 18.7 us against 17.8, and
+    // 15.3 against 9.3), more idle and have fewer bytes in flight (pages of 32 tokens, twice the threads: 16.6 us
+    // against 14.2; 64-dim heads, pages of 64, the whole block: 51.9 against 37.6).
+    const bool few = p.T < 4 * static_cast<int64_t>(p.B);
+    const int lanes = few ? 32 : p.P <= 32 ? D : 2 * D;
     const int64_t units = touched * p.Hkv * 2;
     if (units > 0x3fffffffll) return DA_ERR_INVALID_ARG;
-    constexpr int kWarps = kAppendThreads / 32;
     const int64_t page_work = 2ll * kPageWeight * p.Hkv, resident = 152 * (few ? 2 : 3);
     const int64_t most = std::max<int64_t>(1, resident * page_work / (page_work + p.Hq));
-    p.page_blocks = static_cast<int>(std::min<int64_t>(few ? (units + kWarps - 1) / kWarps : units, most));
-    return few ? launch_append(append8_kernel<D, DT, HALF, 32>, p.page_blocks + row_blocks, smem, p, stream)
-               : launch_append(append8_kernel<D, DT, HALF, kAppendThreads>, p.page_blocks + row_blocks, smem, p, stream);
+    const int per_block = kAppendThreads / lanes;
+    p.page_blocks = static_cast<int>(std::min<int64_t>((units + per_block - 1) / per_block, most));
+    const int grid = p.page_blocks + row_blocks;
+    if (lanes == 32) return launch_append(append8_kernel<D, DT, HALF, 32>, grid, smem, p, stream);
+    if (lanes == D) return launch_append(append8_kernel<D, DT, HALF, D>, grid, smem, p, stream);
+    return launch_append(append8_kernel<D, DT, HALF, 2 * D>, grid, smem, p, stream);
 }
 
 template <int D, int DT>

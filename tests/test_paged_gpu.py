@@ -588,7 +588,30 @@ def test_a_page_scale_grows_and_earlier_elements_follow():
         assert torch.all((got[i] - r).abs() <= torch.maximum(r.abs() * 2 * 2.0 ** -4, torch.tensor(s * 2.0 ** -9))), i
 
 
-@pytest.mark.parametrize("D,page", [(128, 64), (64, 256), (128, 1024)])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("page,layout", [(16, VARLEN), (32, BHSD), (48, VARLEN), (64, BHSD), (96, VARLEN), (256, BHSD)])
+@pytest.mark.parametrize("rope,rot", [(0, 0), (1, 64), (2, 32)])
+def test_prompts_with_infinities_and_nan_in_8_bit_pages(D, page, layout, rope, rot):
+    """Units of every number of threads, each page several times what a block holds at once or less than that; some
+    pages of some heads have an infinity (their threads look for the largest finite element again), some a NaN."""
+    lens, new = [333, 70, 5, 600], [333, 33, 5, 401]
+    p = Paged(lens, 3, D, "e4m3", page, layout, seed=80 + page)
+    q, k, v = fused_rows(sum(new), 6, 3, D, "bf16", 81)
+    k, v = k.clone(), v.clone()
+    gen = torch.Generator().manual_seed(82)
+    for x in (k, v):
+        for value in (math.inf, -math.inf, math.nan):
+            for row in torch.randint(0, sum(new), (4,), generator=gen).tolist():
+                x[row, row % 3, -1 if rot < D else 5] = value        # dims past a part rotation, or values, stay as they are
+    if rope and rot == D:
+        k = torch.where(torch.isfinite(k), k, torch.ones_like(k))    # a rotated infinity may meet another: keys stay finite
+    cs = None if rope == 0 else table_of(700, rot)
+    got, cache, err = run_append(p, q, k, v, lens, new, cs, rope)
+    assert err == 0
+    check_append(p, got, cache, append32(p, q, k, v, lens, new, cs, rope), sum(new))
+
+
+@pytest.mark.parametrize("D,page", [(64, 16), (64, 32), (64, 64), (64, 256), (128, 32), (128, 64), (128, 1024)])
 def test_many_tokens_of_growing_size_into_a_begun_page(D, page):
     """Chunks of a prompt, each larger in value than the one before, several rows per thread and pages of
     more rows than a block holds at once: the begun page is rounded again each time."""
