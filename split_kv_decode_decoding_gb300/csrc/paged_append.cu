@@ -24,7 +24,7 @@
 //
 // Measured (one GB300): 16-bit pages, 9887 tokens of 32 + 2 x 8 heads in 5 prompts 39.3 us,
 // 6.3 TB/s; 64 tokens, one per sequence, 28 + 2 x 4 heads 2.8 us. e4m3 pages: the same prompts 41.2 us,
-// 5.5 TB/s (bound by instructions and by the two waits per page and head, not by its bytes); 256 tokens,
+// 5.5 TB/s (bound by the latency of a page's two passes and by instructions, not by its bytes); 256 tokens,
 // one per sequence, 16 + 2 x 2 heads 4.0 us.
 
 #include "paged_common.cuh"
@@ -87,6 +87,11 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b, uint64_t minus_
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     uint64_t d;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
 __device__ __forceinline__ float lo2(uint64_t a) { return __uint_as_float(static_cast<uint32_t>(a)); }
@@ -158,8 +163,7 @@ __device__ __forceinline__ void load_turn(Turn& t, const float* cos_sin, int rot
 __device__ __forceinline__ void rotate(Chunk16& e, const Turn& t, uint64_t minus_zero) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint64_t minus = t.s[i] ^ 0x8000000080000000ull;
-        const uint64_t x = add2(mul2(e.x[i], t.c[i], minus_zero), mul2(e.y[i], minus, minus_zero));
+        const uint64_t x = sub2(mul2(e.x[i], t.c[i], minus_zero), mul2(e.y[i], t.s[i], minus_zero));
         e.y[i] = add2(mul2(e.y[i], t.c[i], minus_zero), mul2(e.x[i], t.s[i], minus_zero));
         e.x[i] = x;
     }
@@ -657,7 +661,7 @@ da_status launch_append(K kern, int grid, size_t smem, const AppendParams& p, cu
 
 // Blocks for pages: what fits the GPU at once, times the pages' share of the work, an element of theirs taken for
 // kPageWeight of a query's. Each takes several units, so that rows, which are bound by bytes, run beside pages,
-// which are bound by instructions, from the first to the last (7200 tokens of 3 x 32 128-dim heads: 66.2 us, with
+// which are bound by latency and instructions, from the first to the last (7200 tokens of 3 x 32 128-dim heads: 66.2 us, with
 // two thirds for pages 92.5, with all 68.4; 9887 tokens of 32 + 2 x 8 heads 41.2, all 43.0, a block for each unit
 // 49.8). Rows take over what pages leave, not the other way round, hence the large weight (8; 3 or 4: 5.8 us
 // where 8 has 4.3, 200 tokens of 28 + 2 x 4 heads).
