@@ -661,10 +661,10 @@ da_status launch_append(K kern, int grid, size_t smem, const AppendParams& p, cu
 
 // Blocks for pages: what fits the GPU at once, times the pages' share of the work, an element of theirs taken for
 // kPageWeight of a query's. Each takes several units, so that rows, which are bound by bytes, run beside pages,
-// which are bound by latency and instructions, from the first to the last (7200 tokens of 3 x 32 128-dim heads: 66.2 us, with
-// two thirds for pages 92.5, with all 68.4; 9887 tokens of 32 + 2 x 8 heads 41.2, all 43.0, a block for each unit
-// 49.8). Rows take over what pages leave, not the other way round, hence the large weight (8; 3 or 4: 5.8 us
-// where 8 has 4.3, 200 tokens of 28 + 2 x 4 heads).
+// which are bound by latency and instructions, from the first to the last (7200 tokens of 3 x 32 128-dim heads:
+// 66.2 us, with two thirds for pages 92.5, with all 68.4; 9887 tokens of 32 + 2 x 8 heads 41.2, all 43.0, a block
+// for each unit 49.8). Rows take over what pages leave, not the other way round, hence the large weight (8; 3 or 4:
+// 5.8 us where 8 has 4.3, 200 tokens of 28 + 2 x 4 heads).
 constexpr int kPageWeight = 8;
 constexpr int kManyHeads = 8;                // heads per thread where there are many tokens
 constexpr int64_t kManyThreads = 152 * 512;  // threads that keep the GPU busy
