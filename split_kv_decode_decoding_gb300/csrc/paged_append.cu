@@ -550,9 +550,10 @@ struct AppendPage {
         });
     }
 
-    // red: shared, a float per warp of the unit, not the one of the call before.
-    __device__ __forceinline__ void finish(float* red) {
-        if (!x.check(p, lane == 0)) return;   // for the whole unit
+    // red: shared, a float per warp of the unit, not the one that the last call used. Whether this one used it: a unit
+    // that is left out returns before its barrier, with the last call's maxima perhaps still being read.
+    __device__ __forceinline__ bool finish(float* red) {
+        if (!x.check(p, lane == 0)) return false;   // for the whole unit
         const int head = hv >> 1;
         const bool is_v = (hv & 1) != 0;
         const float* scale_at = (is_v ? p.vs : p.ks) + static_cast<int64_t>(x.page) * p.Hkv + head;
@@ -573,6 +574,7 @@ struct AppendPage {
         const int64_t row_step = static_cast<int64_t>(p.layout == DA_LAYOUT_VARLEN ? p.Hkv : 1) * D;
         if ((__float_as_uint(scale) & 0x7fffffu) == 0) write<true>(to, row_step, scale);
         else write<false>(to, row_step, scale);
+        return true;
     }
 };
 
@@ -632,7 +634,7 @@ __global__ void __launch_bounds__(kAppendThreads, kLanes == 32 ? 2 : 3) append8_
     const int sub = tid / kLanes;
     int turn = 0;
     // the bound is uniform over a unit's threads
-    for (uint32_t unit = blockIdx.x * kPerBlock + sub; unit < units; unit += step, turn ^= 1) {
+    for (uint32_t unit = blockIdx.x * kPerBlock + sub; unit < units; unit += step) {
         const int nth = static_cast<int>(unit / groups), hv = static_cast<int>(unit - nth * groups);
         int lo = 0, hi = p.B - 1;   // last b with prefix[b] <= nth
         while (lo < hi) {
@@ -641,7 +643,7 @@ __global__ void __launch_bounds__(kAppendThreads, kLanes == 32 ? 2 : 3) append8_
             else hi = mid - 1;
         }
         page.load(new_tokens(p, cu[lo], cu[lo + 1], lens[lo]), lo, nth - prefix[lo], hv);
-        page.finish(&red[turn][sub * (kLanes / 32)]);
+        if (page.finish(&red[turn][sub * (kLanes / 32)])) turn ^= 1;
     }
 }
 
