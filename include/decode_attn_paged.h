@@ -83,7 +83,8 @@ da_status decode_attn_paged_workspace_init(void* workspace, size_t workspace_byt
  *
  * with the scales of key j's page and head (1 in 16-bit pages). A token that sees no key
  * gets out = 0 and lse = -inf. Memory in a page behind a sequence's last token may hold
- * anything. The results do not depend on timing: the same inputs on the same device give
+ * anything. A NaN or an infinity among keys or values reaches the tokens that see it and no
+ * others (nor other heads). The results do not depend on timing: the same inputs on the same device give
  * the same bits.
  *
  * The call's arguments are the fields of a struct (host memory, read during the call).

@@ -230,6 +230,15 @@ __device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
     return v;
 }
 
+// yes ? a : b, kept a selection: of several from one array the compiler makes an index, and the array goes to local memory.
+__device__ __forceinline__ float select(bool yes, float a, float b) {
+    float r;
+    asm("{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %3, 0;\n\tselp.f32 %0, %1, %2, p;\n\t}"
+        : "=f"(r)
+        : "f"(a), "f"(b), "r"(static_cast<int>(yes)));
+    return r;
+}
+
 // Two e4m3 values to two fp16 values (exact).
 __device__ __forceinline__ void e4m3x4_to_f16(uint32_t x, uint32_t& lo, uint32_t& hi) {
     asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
@@ -736,6 +745,65 @@ struct PagedKernel {
         }
     }
 
+    // A token does not see the keys of the tokens after it, and its weights for them are 0; but 0 * NaN and 0 * Inf
+    // are not, so a value row of theirs that holds either must not enter the product. Such rows are rare: they are
+    // looked for where a stage has keys that some column does not see (at most T_q - 1, at a sequence's end), taken
+    // into the columns that see them one by one, and zeroed before the product. Rows are rows of the tile. (The search and
+    // the registers of the rare case cost four tokens over e4m3 pages 1.5 %: 169.4 -> 171.9 us; one token nothing.)
+    static __device__ __forceinline__ bool any_non_finite(uint32_t vtile, int from, int to) {
+        constexpr int kPerRow = Sh::kRowBytes / 16;
+        constexpr uint32_t kOnes = KV8 ? 0x7f7f7f7fu : DT == DA_BF16 ? 0x7f807f80u : 0x7c007c00u;
+        uint32_t found = 0;
+        for (int c = threadIdx.x & 31; c < (to - from) * kPerRow; c += 32) {
+            uint32_t w[4];
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                         : "r"(chunk_addr(vtile, from + c / kPerRow, c % kPerRow)));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) found |= KV8 ? __vcmpeq4(w[i] & kOnes, kOnes) : __vcmpeq2(w[i] & kOnes, kOnes);
+        }
+        return __any_sync(0xffffffffu, found != 0);
+    }
+    static __device__ __forceinline__ void zero_rows(uint32_t vtile, int from, int to) {
+        constexpr int kPerRow = Sh::kRowBytes / 16;
+        for (int c = threadIdx.x & 31; c < (to - from) * kPerRow; c += 32)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
+                             chunk_addr(vtile, from + c / kPerRow, c % kPerRow)),
+                         "r"(0u)
+                         : "memory");
+        __syncwarp();
+    }
+    // acc += w[n][c] v over the columns with sees[n][c], v the value row `row`.
+    static __device__ __forceinline__ void weigh_row(uint32_t vtile, int row, const float (&w)[NT][2], const bool (&sees)[NT][2],
+                                                     float (&acc)[D / 16][NT][4]) {
+        const int g = (threadIdx.x & 31) >> 2;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+            float v[2];   // of the dims that acc[i][n][0 .. 1] and acc[i][n][2 .. 3] hold
+            uint16_t x, y;
+            if constexpr (KV8) {
+                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(chunk_addr(vtile, row, i) + 2 * g));
+                uint32_t h2;
+                asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(x));
+                v[0] = bits_to_f32<DA_F16>(h2 & 0xffffu);
+                v[1] = bits_to_f32<DA_F16>(h2 >> 16);
+            } else {
+                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(chunk_addr(vtile, row, 2 * i) + 2 * g));
+                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(y) : "r"(chunk_addr(vtile, row, 2 * i + 1) + 2 * g));
+                v[0] = bits_to_f32<DT>(x);
+                v[1] = bits_to_f32<DT>(y);
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    if (sees[n][c]) {
+                        acc[i][n][c] = fmaf(w[n][c], v[0], acc[i][n][c]);
+                        acc[i][n][c + 2] = fmaf(w[n][c], v[1], acc[i][n][c + 2]);
+                    }
+        }
+    }
+
     static __device__ __forceinline__ int64_t output_row(const PagedParams& p, const PagedItem& it, int col) {
         const int c = it.c0 + col;
         return (static_cast<int64_t>(it.b) * p.tq + c / p.G) * p.Hq + it.kvh * p.G + c % p.G;
@@ -924,6 +992,8 @@ struct PagedKernel {
             float qs[NT][2];
             load_queries(p, s.qbuf + slot * Sh::kQBytes, item.nh, qf, qs);
             const int nkeys = item.nkeys, ntiles = item.ntiles;
+            const int hide = item.vis0 - warp * kRows;   // this warp's first row that token 0 does not see, from the first
+                                                         // stage on (with one token: past the last)
 
             int vis[NT][2];   // keys of the piece that this thread's columns may see
 #pragma unroll
@@ -965,14 +1035,8 @@ struct PagedKernel {
                     const uint32_t vtile = ktile + Sh::kTileBytes;
                     if (valid < kRows) {
                         // rows past the end hold anything: their weight is 0, but 0 * NaN is not
-                        constexpr int kPerRow = Sh::kRowBytes / 16;
-                        for (int c = lane; c < (kRows - valid) * kPerRow; c += 32)
-                            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                             chunk_addr(vtile, warp * kRows + valid + c / kPerRow, c % kPerRow)),
-                                         "r"(0u)
-                                         : "memory");
+                        zero_rows(vtile, warp * kRows + valid, (warp + 1) * kRows);
                         zeroed = true;
-                        __syncwarp();
                     }
                     float x[Sh::kBoxes][NT][4], lv[Sh::kBoxes];
                     bool move = false;
@@ -1033,6 +1097,31 @@ struct PagedKernel {
                                     acc[a][n][c + 2] *= av;
                                 }
                             }
+                    }
+                    const int hidden = max(hide - t * Sh::kKeys, 0), rows = min(valid, kRows);
+                    if (hidden < rows && any_non_finite(vtile, warp * kRows + hidden, warp * kRows + rows)) {
+#pragma unroll 1
+                        for (int r = hidden; r < rows; ++r) {
+                            float w[NT][2], lr = lv[0];
+                            bool sees[NT][2];
+                            if constexpr (Sh::kBoxes == 2) lr = r < 16 ? lv[0] : lv[Sh::kBoxes - 1];
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                for (int c = 0; c < 2; ++c) {
+                                    float score = x[0][n][c];
+#pragma unroll
+                                    for (int k = 1; k < 2 * Sh::kBoxes; ++k)
+                                        score = select(r >> 3 == k, x[k >> 1][n][2 * (k & 1) + c], score);
+                                    const float d = __shfl_sync(0xffffffffu, score, 4 * (r & 7) + t4) - m[n][c];
+                                    w[n][c] = fast_exp2(KV8 ? d + (lr - dv[n][c]) : d);
+                                    sees[n][c] = t * Sh::kKeys + warp * kRows + r < vis[n][c];
+                                }
+                            weigh_row(vtile, warp * kRows + r, w, sees, acc);
+                        }
+                        __syncwarp();
+                        zero_rows(vtile, warp * kRows + hidden, warp * kRows + rows);
+                        zeroed = true;
                     }
 #pragma unroll
                     for (int bx = 0; bx < Sh::kBoxes; ++bx) {

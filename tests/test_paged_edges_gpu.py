@@ -8,8 +8,8 @@ import pytest
 import torch
 
 import split_kv_decode_decoding_gb300 as da
-from paged_ref import BHSD, VARLEN, Paged, append32, table_of
-from test_paged_gpu import _lib, fused_rows, on_gpu  # noqa: F401
+from paged_ref import BHSD, VARLEN, Paged, append32, attend64, table_of, token_view
+from test_paged_gpu import _lib, attend, check, fused_rows, on_gpu, queries  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -57,3 +57,37 @@ def test_prompts_with_pages_that_are_left_out_between_others(D, page, layout):
             raw = torch.uint8 if x.element_size() == 1 else torch.int32
             assert torch.equal(getattr(cache, name).view(raw), x.view(raw)), name
     assert da.decode_attn_splitkv_get_error(ws) == da.DA_DEVERR_PAGE | da.DA_DEVERR_POSITION
+
+
+@pytest.mark.parametrize("kv,value", [("bf16", math.nan), ("bf16", -math.inf), ("f16", math.nan), ("f16", math.inf), ("e4m3", math.nan)])
+@pytest.mark.parametrize("T,Hq,Hkv,D,page,layout,longest", [
+    (4, 4, 2, 128, 64, BHSD, 700), (4, 8, 2, 64, 16, VARLEN, 1100), (16, 2, 2, 64, 48, BHSD, 700), (5, 6, 2, 128, 32, VARLEN, 700),
+    (4, 4, 2, 128, 64, VARLEN, 1100), (3, 16, 2, 128, 128, BHSD, 1100), (16, 4, 2, 128, 256, VARLEN, 1100)])
+def test_values_of_later_tokens_that_are_not_finite(kv, value, T, Hq, Hkv, D, page, layout, longest):
+    """A NaN or an infinity among the values of a key reaches the query tokens that see the key and no other, wherever
+    the last keys lie in their box, stage and page: sequences that end everywhere in a stage, one shorter than its query
+    tokens, one in several pieces. (16-bit pages of head size 128 have four consumer warps up to 1023 keys, then eight.)"""
+    lens = [130, 128, 129, 127, 66, 65, 18, 17, 16, 2, longest, T]
+    spoilt = {(b, n - 1 - (b * 5) % min(T, n)) for b, n in enumerate(lens)} | {(0, 129), (10, longest - T), (4, 65), (4, 64)}
+    p = Paged(lens, Hkv, D, kv, page, layout, seed=110)
+    rng = np.random.default_rng(111)
+    where = [(b, j, int(rng.integers(Hkv)), int(rng.integers(D))) for b, j in sorted(spoilt)]
+    code = 0x7F if kv == "e4m3" else int(torch.tensor(value).to(p.v.dtype).view(torch.int16))
+    raw = token_view(p.v.view(torch.uint8 if kv == "e4m3" else torch.int16), layout)
+    sound = p.v.clone()
+    for b, j, h, d in where:
+        raw[p.table[b, j // page].long(), j % page, h, d] = code
+    q = queries(p, len(lens), T, Hq, "f16" if kv == "f16" else "bf16", 112)
+    out, lse, err = attend(p, q)
+    assert err == 0
+    p.v = sound
+    ref = attend64(q, p)
+    hit = np.zeros(out.shape, dtype=bool)
+    for b, j, h, d in where:
+        for t in range(T):
+            if j <= lens[b] - T + t:
+                hit[b, t, h * Hq // Hkv:(h + 1) * Hq // Hkv, d] = True
+    assert hit.any() and not np.isfinite(out[hit]).any()
+    assert np.isnan(out[hit]).all() or math.isinf(value) and (out[hit] == value).all()
+    out[hit] = ref[0][hit]
+    check(out, lse, ref, "f16" if kv == "f16" else "bf16")
