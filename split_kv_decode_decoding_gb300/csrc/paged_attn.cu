@@ -239,6 +239,13 @@ __device__ __forceinline__ float select(bool yes, float a, float b) {
     return r;
 }
 
+// log2 of a scale, a subnormal one too (-inf of 0).
+__device__ __forceinline__ float log2_of_scale(float x) {
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // Two e4m3 values to two fp16 values (exact).
 __device__ __forceinline__ void e4m3x4_to_f16(uint32_t x, uint32_t& lo, uint32_t& hi) {
     asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
@@ -581,7 +588,7 @@ struct PagedKernel {
                     const int from = (in32 + lane * 16 / p.box_keys) & 31;
                     const float ks = __shfl_sync(0xffffffffu, cur.ks, from);
                     const float vs = __shfl_sync(0xffffffffu, cur.vs, from);
-                    if (lane < Sh::kKeys / 16) s.scales[st * (Sh::kKeys / 16) + lane] = make_float2(ks, fast_log2(vs));
+                    if (lane < Sh::kKeys / 16) s.scales[st * (Sh::kKeys / 16) + lane] = make_float2(ks, log2_of_scale(vs));
                     __syncwarp();
                 }
                 if (lane == 0) mbar_arrive(fb);
@@ -886,10 +893,13 @@ struct PagedKernel {
             for (int v = 0; v < kVec; ++v) fma4(o[v], wt, *reinterpret_cast<const float4*>(row + 64 * v));
         }
         if (!live) return;
-        if constexpr (KV8) {   // o is relative to M + dV, l to M
-            const float by = fast_exp2(dV);
+        if constexpr (KV8) {   // o is relative to M + dV, l to M: in two steps, which stay normal floats for every scale
+            const float by = fast_exp2(0.5f * dV);
 #pragma unroll
-            for (int v = 0; v < kVec; ++v) scale4(o[v], by);
+            for (int v = 0; v < kVec; ++v) {
+                scale4(o[v], by);
+                scale4(o[v], by);
+            }
         }
         if (direct) {
             const float m = fmaxf(M, sum1.x), w0 = fast_exp2(M - m), w1 = fast_exp2(sum1.x - m);

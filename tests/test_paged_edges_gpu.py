@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import split_kv_decode_decoding_gb300 as da
-from paged_ref import BHSD, VARLEN, Paged, append32, attend64, table_of, token_view
+from paged_ref import BHSD, VARLEN, Paged, append32, attend64, half_step, table_of, token_view
 from test_paged_gpu import _lib, attend, check, fused_rows, on_gpu, queries  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -91,3 +91,22 @@ def test_values_of_later_tokens_that_are_not_finite(kv, value, T, Hq, Hkv, D, pa
     assert np.isnan(out[hit]).all() or math.isinf(value) and (out[hit] == value).all()
     out[hit] = ref[0][hit]
     check(out, lse, ref, "f16" if kv == "f16" else "bf16")
+
+
+@pytest.mark.parametrize("lens", [[200, 7, 64], [1, 3000]])
+@pytest.mark.parametrize("power", [-149, -140, -130, -126, 100])
+def test_value_scales_from_the_least_float_on(power, lens):
+    """Outputs follow the value scales, powers of two, down to subnormal ones (bf16 outputs reach as far). Relative to
+    the same values at scale 1, whose tolerance is scaled alike; float32 itself ends at 2^-149."""
+    p = Paged(lens, 2, 128, "e4m3", 64, BHSD, seed=120)
+    p.v_scale.masked_fill_(~p.v_scale.isnan(), 1.0)
+    q = queries(p, len(lens), 2, 8, "bf16", 121)
+    ro, rl, to, tl = attend64(q, p)
+    p.v_scale.masked_fill_(~p.v_scale.isnan(), 2.0 ** power)
+    out, lse, err = attend(p, q)
+    assert err == 0
+    s = 2.0 ** power
+    off = np.abs(out - ro * s) - half_step(ro * s, torch.bfloat16) - to * s - 4 * 2.0 ** -149
+    assert np.all(off <= 0), off.max()
+    assert np.abs(out).max() > 0 or 448 * s < 2.0 ** -134       # below half of the least bfloat16 everything is 0
+    check(ro, lse, (ro, rl, to, tl), "bf16")
