@@ -258,6 +258,20 @@ template <int D, int DT, bool KV8, int NT, int NW>
 struct PagedKernel {
     using Sh = PagedShape<D, KV8, NT, NW>;
 
+    // A weight enters its product as 2^kLift times itself, and is at most 2^kHeadroom times the largest one at the time
+    // that its column's reference was set (a larger one moves the reference). bf16 holds any of them. fp16 ends at 2^-24,
+    // and at 2^16: lifted by 11 to the top of it, weights keep all their bits down to 2^-25 of the largest, and count down
+    // to 2^-36. (Unlifted, down to 2^-14 and 2^-25: 10^5 keys of 2^-26 beside one are 2^-9 of the sum, and went missing.)
+    // Less headroom means more moves, which the 16-column kernel of 8-bit pages feels: four tokens 172.4 us with 8 and
+    // 7, 176.3 with 4 and 11, 171.7 unlifted; it is given the first, 2^-21 and 2^-32. One token: 50.7, 50.9 and 50.6.
+    static constexpr bool kFp16Weights = KV8 || DT == DA_F16;
+    static constexpr bool kFewMoves = KV8 && NT == 2;
+    static constexpr float kHeadroom = kFp16Weights && !kFewMoves ? 4.f : kLazyRescale;
+    static constexpr float kLift = kFp16Weights ? 15.f - kHeadroom : 0.f;
+    // In 16-bit pages a factor of the weights (2^kLift), beside the sum that keeps them as they are (fp16, four tokens 116.3 ->
+    // 118.2 us, one token 86.5 both); in 8-bit pages, whose weights have a reference of their own, part of that one (dv).
+    static constexpr float kLiftBy = !KV8 && kFp16Weights ? 2048.f : 1.f;
+
     struct Layout {
         uint8_t* smem;
         PagedItem* slots;
@@ -886,7 +900,7 @@ struct PagedKernel {
 #pragma unroll
         for (int w = 0; w < Sh::kWarps; ++w) {
             const float wl = fast_exp2(red_m[w * 8 + hh] - M);
-            const float wt = KV8 ? fast_exp2((red_m[w * 8 + hh] - M) + (red_dv[w * 8 + hh] - dV)) : wl;
+            const float wt = KV8 ? fast_exp2((red_m[w * 8 + hh] - M) + (red_dv[w * 8 + hh] - dV)) : wl * (1.f / kLiftBy);
             l = fmaf(wl, red_l[w * 8 + hh], l);
             const float* row = red_acc + (w * 8 + hh) * Sh::kMergeRow + Sh::merge_dim(4 * l16, hh);
 #pragma unroll
@@ -1018,15 +1032,16 @@ struct PagedKernel {
             for (int a = 0; a < D / 16; ++a)
 #pragma unroll
                 for (int n = 0; n < NT; ++n) acc[a][n][0] = acc[a][n][1] = acc[a][n][2] = acc[a][n][3] = 0.f;
-            // running maximum of the scores, (8-bit) how far that of the weights is above it, this thread's share of
-            // the sum
+            // running maximum of the scores, (8-bit) how far that of the weights is above it, less kLift, this thread's
+            // share of the sum
             float m[NT][2], dv[NT][2], l[NT][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     m[n][c] = kNoKey;
-                    dv[n][c] = l[n][c] = 0.f;
+                    dv[n][c] = KV8 ? -kLift : 0.f;
+                    l[n][c] = 0.f;
                 }
 
             for (int t = 0; t < ntiles; ++t) {
@@ -1068,13 +1083,12 @@ struct PagedKernel {
                                 const float f = KV8 ? qs[n][j & 1] * ks : qs[n][j & 1];
                                 const bool seen = key + 8 * (j >> 1) < vis[n][j & 1];
                                 x[bx][n][j] = seen ? x[bx][n][j] * f : -INFINITY;
-                                const float above = KV8 ? fmaxf(lv[bx] - dv[n][j & 1], 0.f) : 0.f;
-                                move = move || x[bx][n][j] - m[n][j & 1] > kLazyRescale - above;
+                                const float above = KV8 ? fmaxf(lv[bx] - dv[n][j & 1], kLift) : kLift;
+                                move = move || x[bx][n][j] - m[n][j & 1] > kHeadroom + kLift - above;
                             }
                     }
                     // The reference of a column moves only when a score passes it by more than
-                    // kLazyRescale, so the shuffles and the rescale run on a few stages per piece; the
-                    // weights stay below 2^8.
+                    // kHeadroom, so the shuffles and the rescale run on a few stages per piece.
                     if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
                         for (int n = 0; n < NT; ++n)
@@ -1092,7 +1106,7 @@ struct PagedKernel {
                                     float dnew = fmaxf(kNoKey, (m[n][c] - top) + dv[n][c]);
 #pragma unroll
                                     for (int bx = 0; bx < Sh::kBoxes; ++bx)
-                                        dnew = fmaxf(dnew, (fmaxf(x[bx][n][c], x[bx][n][c + 2]) - top) + lv[bx]);
+                                        dnew = fmaxf(dnew, (fmaxf(x[bx][n][c], x[bx][n][c + 2]) - top) + (lv[bx] - kLift));
 #pragma unroll
                                     for (int off = 4; off < 32; off <<= 1)
                                         dnew = fmaxf(dnew, __shfl_xor_sync(0xffffffffu, dnew, off));
@@ -1124,7 +1138,7 @@ struct PagedKernel {
                                     for (int k = 1; k < 2 * Sh::kBoxes; ++k)
                                         score = select(r >> 3 == k, x[k >> 1][n][2 * (k & 1) + c], score);
                                     const float d = __shfl_sync(0xffffffffu, score, 4 * (r & 7) + t4) - m[n][c];
-                                    w[n][c] = fast_exp2(KV8 ? d + (lr - dv[n][c]) : d);
+                                    w[n][c] = fast_exp2(KV8 ? d + (lr - dv[n][c]) : d) * kLiftBy;
                                     sees[n][c] = t * Sh::kKeys + warp * kRows + r < vis[n][c];
                                 }
                             weigh_row(vtile, warp * kRows + r, w, sees, acc);
@@ -1145,6 +1159,7 @@ struct PagedKernel {
                                 w[j] = fast_exp2(d);
                                 l[n][j & 1] += w[j];
                                 if constexpr (KV8) w[j] = fast_exp2(d + (lv[bx] - dv[n][j & 1]));
+                                else w[j] *= kLiftBy;
                             }
                             // the weights are rounded to the 16-bit type of the product's other operand
                             pb[n][0] = movmatrix_trans(pack2<KV8 ? DA_F16 : DT>(w[0], w[1]));

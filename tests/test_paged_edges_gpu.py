@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import split_kv_decode_decoding_gb300 as da
-from paged_ref import BHSD, VARLEN, Paged, append32, attend64, half_step, table_of, token_view
+from paged_ref import BHSD, DTYPES, VARLEN, Paged, append32, attend64, half_step, table_of, token_view
 from test_paged_gpu import _lib, attend, check, fused_rows, on_gpu, queries  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -110,3 +110,41 @@ def test_value_scales_from_the_least_float_on(power, lens):
     assert np.all(off <= 0), off.max()
     assert np.abs(out).max() > 0 or 448 * s < 2.0 ** -134       # below half of the least bfloat16 everything is 0
     check(ro, lse, (ro, rl, to, tl), "bf16")
+
+
+@pytest.mark.parametrize("kv,Hq,T,D,n", [("f16", 4, 1, 128, 40000), ("f16", 16, 1, 128, 9000), ("f16", 2, 1, 64, 20000), ("f16", 8, 2, 64, 900),
+                                         ("f16", 2, 1, 128, 1000), ("e4m3", 4, 1, 128, 40000), ("e4m3", 4, 4, 128, 9000),
+                                         ("e4m3", 2, 1, 64, 20000)])
+@pytest.mark.parametrize("below", [13.3, 20.3, 24.5, 27.0, 31.7, 34.0])
+def test_many_keys_far_below_a_few_with_small_values(kv, Hq, T, D, n, below):
+    """Attention sinks: every sixteenth key outweighs the others by 2^`below` and has values of zero, so that the output
+    is what the others leave. Relative to that, a weight is off by a rounding to fp16, 2^-11, or, below 2^-25 of the
+    largest, by half of 2^-35 of that one (fp16 ends at 2^-24, the weights enter as 2^11 times theirs; with more than
+    eight columns over 8-bit pages as 2^7 times theirs, hence 2^-31); its score by 2^-21 a unit; sums of n terms by
+    n 2^-24."""
+    p = Paged([n], 1, D, kv, 64, BHSD, seed=130)
+    sink = torch.zeros(p.k.shape[0], p.page, dtype=torch.bool)
+    for j in range(3, n, 16):
+        sink[p.table[0, j // p.page].long(), j % p.page] = True
+    values = (torch.rand(p.v.shape, generator=torch.Generator().manual_seed(131)) + 0.5) * (20000 if kv == "f16" else 200)
+    values[(sink[:, None, :, None]).expand_as(values)] = 0
+    p.v = values.to(p.v.dtype)
+    p.k = sink[:, None, :, None].expand(p.k.shape).float().to(p.k.dtype).contiguous()
+    if kv == "e4m3":
+        p.k_scale.fill_(1.0)
+        p.v_scale.fill_(2.0)
+    q_type = "f16" if kv == "f16" else "bf16"
+    q = torch.ones(1, T, Hq, D, dtype=DTYPES[q_type])
+    scale = float(np.float32(below * math.log(2) / D))
+    out, lse, err = attend(p, q, scale=scale)
+    assert err == 0
+    v = p.sequence(0)[1][:, 0].numpy()
+    for t in range(T):
+        m = n - T + 1 + t
+        heavy = len(range(3, m, 16))
+        w = math.exp(-scale * D)
+        ref = w * v[:m].sum(0) / (heavy + (m - heavy) * w)
+        rel = max(2.0 ** -11, 2.0 ** (-32 if kv == "e4m3" and Hq * T > 8 else -36) / w) + 2.0 ** -21 * (1 + 2 * below) + 2 * m * 2.0 ** -24
+        off = np.abs(out[0, t] - ref) - half_step(ref, DTYPES[q_type]) - rel * ref
+        assert np.all(off <= 0), (t, (np.abs(out[0, t] - ref) / ref).max(), rel)
+        assert np.all(np.abs(lse[0, t] - (scale * D + math.log(heavy + (m - heavy) * w))) <= 2.0 ** -20 * (1 + below) + m * 2.0 ** -24)
