@@ -49,7 +49,7 @@
 //
 // Sums, maxima, accumulators and partial results are float32. A partial result keeps its maximum and its
 // sum apart, so that scores of any size are joined with no more loss than they were computed with. Rounded to fewer bits are the
-// weights, to the 16-bit type of the product that they enter, and the outputs, once.
+// weights, in 16-bit pages to two terms of their type and in 8-bit pages to one of fp16 (weights16), and the outputs, once.
 //
 // Measured (one GB300, mean of a graph of calls): 16 sequences of 131072 keys, 32 / 8 heads, bf16
 // 1153 us, 7.4 TB/s; 64 sequences of 512 to 8192 keys, 28 / 4 heads 85.1 us, 6.5 TB/s, over e4m3
@@ -244,6 +244,15 @@ __device__ __forceinline__ float log2_of_scale(float x) {
     float y;
     asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// pack2, rounded towards zero.
+template <int DT>
+__device__ __forceinline__ uint32_t pack2_down(float a, float b) {
+    uint32_t r;
+    if constexpr (DT == DA_F16) asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    else asm("cvt.rz.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
 }
 
 // Two e4m3 values to two fp16 values (exact).
@@ -734,9 +743,32 @@ struct PagedKernel {
         }
     }
 
+    // Weights to the type of their product. In 16-bit pages a weight enters as two terms, a 16-bit value and what it
+    // leaves: off by 2^-15 of itself in bf16, in fp16 by 2^-21, or 2^-36 of the largest. One term, off by 2^-8 and 2^-11,
+    // made the outputs' error 1.2 to 1.4 times that of float32 weights. The first is rounded down (in fp16 from 2^-20 of
+    // the weight and the least fp16 below it) and the second (in bf16 of 2^-20 of the weight more) is above 0: an infinite
+    // value stays one, as it meets no 0 and no other sign. The second products cost one token next to nothing
+    // (16 x 131072 keys 1154 -> 1156 us, the ragged batch 86.7 both), 16 columns 1 to 7 % (16 x 8192 keys, four tokens, bf16
+    // 81.9 -> 82.7 us; 64 ragged sequences, fp16 117.9 -> 125.6). 8-bit pages, bound by instructions, have one (fp16)
+    // term: a second takes four tokens from 172.6 to 201.2 us and 16 x 32768 keys of head size 64 from 94.1 to 97.4.
+    static constexpr int kTerms = KV8 ? 1 : 2;
+    static __device__ __forceinline__ void weights16(float a, float b, uint32_t (&term)[kTerms]) {
+        if constexpr (KV8) {
+            term[0] = pack2<DA_F16>(a, b);
+        } else if constexpr (DT == DA_F16) {
+            constexpr float kLess = 1.f - 0x1p-20f, kLeast = 0x1p-24f;
+            term[0] = pack2_down<DT>(fmaxf(fmaf(a, kLess, -kLeast), 0.f), fmaxf(fmaf(b, kLess, -kLeast), 0.f));
+            term[1] = pack2<DT>(a - bits_to_f32<DT>(term[0] & 0xffffu), b - bits_to_f32<DT>(term[0] >> 16));
+        } else {
+            constexpr float kMore = 1.f + 0x1p-20f;
+            term[0] = pack2_down<DT>(a, b);
+            term[1] = pack2<DT>(fmaf(a, kMore, -bits_to_f32<DT>(term[0] & 0xffffu)), fmaf(b, kMore, -bits_to_f32<DT>(term[0] >> 16)));
+        }
+    }
+
     // O^T[D, 8 columns per n-tile] += V^T P^T of box `row0`; in 8-bit tiles rows g and g + 8 of
     // step i are dims 16 i + 2 g and 16 i + 2 g + 1, in 16-bit tiles 16 i + g and 16 i + g + 8.
-    static __device__ __forceinline__ void weigh(uint32_t tile, int row0, const uint32_t (&pb)[NT][2],
+    static __device__ __forceinline__ void weigh(uint32_t tile, int row0, const uint32_t (&pb)[kTerms][NT][2],
                                                  float (&acc)[D / 16][NT][4]) {
         const int lane = threadIdx.x & 31, mi = lane >> 3, r8 = lane & 7;
         if constexpr (KV8) {
@@ -751,7 +783,7 @@ struct PagedKernel {
                     e4m3x4_to_f16(__byte_perm(w[2 * h], 0, 0x3120), a[0], a[1]);
                     e4m3x4_to_f16(__byte_perm(w[2 * h + 1], 0, 0x3120), a[2], a[3]);
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) mma_16816<DA_F16>(acc[2 * ii + h][n], a, pb[n][0], pb[n][1]);
+                    for (int n = 0; n < NT; ++n) mma_16816<DA_F16>(acc[2 * ii + h][n], a, pb[0][n][0], pb[0][n][1]);
                 }
             }
         } else {
@@ -761,7 +793,9 @@ struct PagedKernel {
                 uint32_t a[4];
                 ldsm_x4_trans(chunk_addr(tile, row, 2 * i + (mi & 1)), a);
 #pragma unroll
-                for (int n = 0; n < NT; ++n) mma_16816<DT>(acc[i][n], a, pb[n][0], pb[n][1]);
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int k = 0; k < kTerms; ++k) mma_16816<DT>(acc[i][n], a, pb[k][n][0], pb[k][n][1]);
             }
         }
     }
@@ -1149,7 +1183,7 @@ struct PagedKernel {
                     }
 #pragma unroll
                     for (int bx = 0; bx < Sh::kBoxes; ++bx) {
-                        uint32_t pb[NT][2];
+                        uint32_t pb[kTerms][NT][2];
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
                             float w[4];
@@ -1161,9 +1195,14 @@ struct PagedKernel {
                                 if constexpr (KV8) w[j] = fast_exp2(d + (lv[bx] - dv[n][j & 1]));
                                 else w[j] *= kLiftBy;
                             }
-                            // the weights are rounded to the 16-bit type of the product's other operand
-                            pb[n][0] = movmatrix_trans(pack2<KV8 ? DA_F16 : DT>(w[0], w[1]));
-                            pb[n][1] = movmatrix_trans(pack2<KV8 ? DA_F16 : DT>(w[2], w[3]));
+                            uint32_t lo[kTerms], hi[kTerms];
+                            weights16(w[0], w[1], lo);
+                            weights16(w[2], w[3], hi);
+#pragma unroll
+                            for (int k = 0; k < kTerms; ++k) {
+                                pb[k][n][0] = movmatrix_trans(lo[k]);
+                                pb[k][n][1] = movmatrix_trans(hi[k]);
+                            }
                         }
                         weigh(vtile, warp * kRows + bx * 16, pb, acc);
                     }

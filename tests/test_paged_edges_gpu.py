@@ -148,3 +148,27 @@ def test_many_keys_far_below_a_few_with_small_values(kv, Hq, T, D, n, below):
         off = np.abs(out[0, t] - ref) - half_step(ref, DTYPES[q_type]) - rel * ref
         assert np.all(off <= 0), (t, (np.abs(out[0, t] - ref) / ref).max(), rel)
         assert np.all(np.abs(lse[0, t] - (scale * D + math.log(heavy + (m - heavy) * w))) <= 2.0 ** -20 * (1 + below) + m * 2.0 ** -24)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "f16"])
+@pytest.mark.parametrize("T,Hq,Hkv,D,width", [(1, 8, 2, 128, None), (1, 8, 2, 128, 20), (4, 6, 2, 128, None), (4, 6, 2, 128, 20),
+                                              (1, 8, 2, 64, None), (5, 8, 4, 64, None)])
+def test_weights_of_16_bit_pages_keep_more_bits_than_the_pages(kv, T, Hq, Hkv, D, width):
+    """The output is off by its own rounding and little else: a weight enters as the sum of two 16-bit values, the first
+    rounded down: off by 2^-15 of itself in bf16 (2^-8 of what that leaves, 2^-7) and by 2^-20 for the second's sign, by 2^-21
+    (2^-11 of 2^-10) and 2^-34 of the largest in fp16. Small queries, so that the bound of the scores' error is no larger."""
+    lens = [5, 6, 7, 9, 12, 17, 40, 3, 100]
+    p = Paged(lens, Hkv, D, kv, 64, BHSD, seed=140, width=width)
+    q = queries(p, len(lens), T, Hq, kv, 141, size=0.02)
+    out, lse, err = attend(p, q)
+    assert err == 0
+    ro, rl, to, tl = attend64(q, p)
+    # attend64's bound without its term for the weights' one rounding, 2^-8 or 2^-11 of the largest value
+    once, twice = (2.0 ** -8, 2.0 ** -15 + 2.0 ** -20) if kv == "bf16" else (2.0 ** -11, 2.0 ** -21 + 2.0 ** -34)
+    for b in range(len(lens)):
+        v = p.sequence(b)[1].abs().numpy()
+        for t, h in itertools.product(range(T), range(Hq)):
+            n = lens[b] - T + t + 1
+            if n > 0:
+                to[b, t, h] -= (once - twice) * v[:n, h * Hkv // Hq].max()
+    check(out, lse, (ro, rl, to, tl), kv)
