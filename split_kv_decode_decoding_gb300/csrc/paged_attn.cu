@@ -953,8 +953,10 @@ struct PagedKernel {
             const float m = fmaxf(M, sum1.x), w0 = fast_exp2(M - m), w1 = fast_exp2(sum1.x - m);
 #pragma unroll
             for (int v = 0; v < kVec; ++v) {
-                scale4(o[v], w0);
-                fma4(o[v], w1, o1[v]);
+                float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);   // (merge_parts' first term: a product of -0 becomes +0)
+                fma4(sum, w0, o[v]);
+                fma4(sum, w1, o1[v]);
+                o[v] = sum;
             }
             l = __fadd_rn(__fmul_rn(w0, l), __fmul_rn(w1, sum1.y));
             M = m;
