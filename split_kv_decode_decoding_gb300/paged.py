@@ -167,7 +167,7 @@ def _check_sequences(kv_lens, block_table, dev):
     if block_table.dim() != 2 or kv_lens.shape != block_table.shape[:1]:
         raise ValueError("kv_lens must be [B] and block_table [B, max_pages]")
     (B, max_pages), (stride, one) = block_table.shape, block_table.stride()
-    if not kv_lens.is_contiguous() or one != 1:
+    if not kv_lens.is_contiguous() or (one != 1 and max_pages > 1):   # (a row of one entry: any stride)
         raise ValueError("kv_lens and the rows of block_table must be contiguous")
     if kv_lens.get_device() != dev or block_table.get_device() != dev:
         raise ValueError("all tensors must be on one device")
