@@ -213,10 +213,13 @@ def decode_attn_paged(q, cache: PagedCache, kv_lens, block_table, out, workspace
         lse_ptr = lse.data_ptr()
     if workspace.get_device() != dev:
         raise ValueError("the workspace must be on q's device")
-    st = _lib().decode_attn_paged(
-        _pack_attn(q.data_ptr(), cache._ref, kv_lens.data_ptr(), block_table.data_ptr(), max_pages, table_stride, B, T_q, Hq,
-                   code, 1.0 / math.sqrt(D) if scale is None else scale, out.data_ptr(), lse_ptr, workspace.data_ptr(),
-                   workspace.nbytes), _raw_stream(stream, dev))
+    try:
+        args = _pack_attn(q.data_ptr(), cache._ref, kv_lens.data_ptr(), block_table.data_ptr(), max_pages, table_stride, B, T_q,
+                          Hq, code, 1.0 / math.sqrt(D) if scale is None else scale, out.data_ptr(), lse_ptr,
+                          workspace.data_ptr(), workspace.nbytes)
+    except struct.error as e:
+        raise ValueError(f"scale, or a size, is no number of its C type: {e}") from None
+    st = _lib().decode_attn_paged(args, _raw_stream(stream, dev))
     if st:
         _fail(st, "decode_attn_paged")
     return out
@@ -279,10 +282,13 @@ def decode_attn_paged_append(q, k, v, cache: PagedCache, cu_new, kv_lens, block_
         cs_ptr, (max_pos, rot) = cos_sin.data_ptr(), cos_sin.shape
     if workspace.get_device() != dev or workspace.nbytes < 256:
         raise ValueError("the workspace must be on the tensors' device")
-    st = _lib().decode_attn_paged_append(
-        _pack_append(q_ptr, k.data_ptr(), v.data_ptr(), q_stride, k_stride, v_stride, cs_ptr, max_pos, rot, rope,
-                     cu_new.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), max_pages, table_stride, B, T, Hq, code,
-                     cache._ref, out_ptr, out_stride, workspace.data_ptr()), _raw_stream(stream, dev))
+    try:
+        args = _pack_append(q_ptr, k.data_ptr(), v.data_ptr(), q_stride, k_stride, v_stride, cs_ptr, max_pos, rot, rope,
+                            cu_new.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), max_pages, table_stride, B, T, Hq,
+                            code, cache._ref, out_ptr, out_stride, workspace.data_ptr())
+    except struct.error as e:
+        raise ValueError(f"rope, or a size, is no number of its C type: {e}") from None
+    st = _lib().decode_attn_paged_append(args, _raw_stream(stream, dev))
     if st:
         _fail(st, "decode_attn_paged_append")
     return q_out

@@ -172,3 +172,23 @@ def test_weights_of_16_bit_pages_keep_more_bits_than_the_pages(kv, T, Hq, Hkv, D
             if n > 0:
                 to[b, t, h] -= (once - twice) * v[:n, h * Hkv // Hq].max()
     check(out, lse, (ro, rl, to, tl), kv)
+
+
+def test_numbers_that_are_none_of_their_c_types():
+    """Refused as other arguments are: a scale past float32, or none at all, and a rotation that is no integer."""
+    p = Paged([20, 9], 2, 64, "f16", 16, VARLEN, seed=150)
+    cache, lens, table = on_gpu(p)
+    ws = da.alloc_paged_workspace(1, 4, 2, 64)
+    q = queries(p, 2, 1, 4, "f16").cuda()
+    out = torch.full_like(q, 7.0)
+    for scale in (1e39, -1e300, "0.1", 1 + 2j, math.inf, math.nan):
+        with pytest.raises((ValueError, TypeError, da.DecodeAttnError)):
+            da.decode_attn_paged(q, cache, lens, table, out, ws, scale=scale)
+    k = torch.zeros(2, 2, 64, dtype=torch.float16, device="cuda")
+    cu = torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda")
+    before = cache.k.clone()
+    for rope in ("half", 1 << 40, None):
+        with pytest.raises((ValueError, TypeError)):
+            da.decode_attn_paged_append(None, k, k, cache, cu, lens, table, ws, cos_sin=table_of(32, 64).cuda(), rope=rope)
+    assert torch.all(out == 7.0) and torch.equal(cache.k.view(torch.int16), before.view(torch.int16))
+    assert da.decode_attn_splitkv_get_error(ws) == 0
