@@ -106,7 +106,7 @@ typedef struct {
     int table_stride;            /* >= max_pages */
     int B;                       /* in [1, DA_MAX_PAGED_BATCH] */
     int T_q;                     /* in [1, DA_MAX_QUERY_TOKENS] */
-    int Hq;                      /* a multiple of the cache's Hkv */
+    int Hq;                      /* a multiple of the cache's Hkv; B * T_q * Hq * D <= 0x7fffffff */
     int dtype;                   /* DA_F16 or DA_BF16 */
     float scale;                 /* finite */
     void* out;                   /* device, [B, T_q, Hq, D] elements of `dtype`, 16-byte aligned */
@@ -155,13 +155,16 @@ typedef struct {
     int max_pos;
     int rot_dim;                 /* a multiple of 16 in [16, D] (ignored without rotation) */
     int rope;                    /* da_rope */
-    const int32_t* cu_new;       /* device, int32 [B+1], non-decreasing; rows from cu_new[B] on are left alone */
+    const int32_t* cu_new;       /* device, int32 [B+1], non-decreasing; rows from cu_new[B] on are left alone. (Where it
+                                    decreases, that sequence is left out, and so may be others; a row that two of the
+                                    rest claim goes to either or to both.) */
     const int32_t* kv_lens;      /* device, int32 [B], the new tokens counted */
     const int32_t* block_table;  /* as above */
     int max_pages;
     int table_stride;
     int B;
-    int T_new;                   /* rows that q, k and v hold, >= 0; a sequence whose rows lie outside them, or
+    int T_new;                   /* rows that q, k and v hold, >= 0 (0: nothing is enqueued, nor flagged; 8-bit pages:
+                                    T_new * Hkv <= 0x1fffffff); a sequence whose rows lie outside them, or
                                     whose kv_lens is smaller than its new tokens or larger than max_pages *
                                     page_size, is left out and sets DA_DEVERR_SEQLENS */
     int Hq;

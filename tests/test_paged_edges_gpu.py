@@ -8,8 +8,8 @@ import pytest
 import torch
 
 import split_kv_decode_decoding_gb300 as da
-from paged_ref import BHSD, DTYPES, VARLEN, Paged, append32, attend64, half_step, table_of, token_view
-from test_paged_gpu import _lib, attend, check, fused_rows, on_gpu, queries  # noqa: F401
+from paged_ref import BHSD, DTYPES, VARLEN, Paged, append32, attend64, half_step, table_of, token_view, turned
+from test_paged_gpu import _lib, attend, check, fused_rows, on_gpu, queries, same_bits  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -192,3 +192,56 @@ def test_numbers_that_are_none_of_their_c_types():
             da.decode_attn_paged_append(None, k, k, cache, cu, lens, table, ws, cos_sin=table_of(32, 64).cuda(), rope=rope)
     assert torch.all(out == 7.0) and torch.equal(cache.k.view(torch.int16), before.view(torch.int16))
     assert da.decode_attn_splitkv_get_error(ws) == 0
+
+
+@pytest.mark.parametrize("kv", ["f16", "bf16", "e4m3"])
+@pytest.mark.parametrize("bounds,done,claimed_twice", [
+    ([0, 3, 2, 5], {0: range(0, 3), 2: range(2, 5)}, 2), ([0, 2, 3, 9], {0: range(0, 2), 1: range(2, 3)}, None),
+    ([-1, 2, 3, 5], {1: range(2, 3), 2: range(3, 5)}, None), ([1 << 30, -(1 << 31), 4, 5], {2: range(4, 5)}, None),
+    ([0, 2, 5, 5], {0: range(0, 2), 1: range(2, 5)}, None), ([0, 5, 6, 5], {0: range(0, 5)}, None)])
+def test_rows_of_sequences_that_cannot_be(kv, bounds, done, claimed_twice):
+    """cu_new that decreases or leaves the rows: what the other sequences append is right, and nothing else changes, in the
+    pages, the scales, the rotated queries, and memory around them. (A row that two sequences claim, and the page that
+    one of them has for it, are left aside.)"""
+    dt = "bf16" if kv == "bf16" else "f16"
+    lens = [10, 10, 10]
+    p = Paged(lens, 2, 64, kv, 16, VARLEN, seed=160)
+    q, k, v = fused_rows(5, 4, 2, 64, dt, 161)
+    cs = table_of(16, 64)
+    cache, kv_lens, table = on_gpu(p)
+    n = p.k.shape[0]
+    raw = torch.uint8 if kv == "e4m3" else torch.int16
+    guarded = []
+    for x in (cache.k, cache.v):                                # pages with as many guard pages on either side
+        big = torch.full((3 * n, *x.shape[1:]), 0x55, dtype=raw, device="cuda").view(x.dtype)
+        big.view(raw)[n:2 * n] = x.view(raw)
+        guarded.append(big)
+    cache = da.PagedCache(*(x[n:2 * n] for x in guarded), cache.k_scale, cache.v_scale, layout=VARLEN)
+    out = torch.full((15, 4, 64), -3.0, dtype=DTYPES[dt], device="cuda")
+    ws = da.alloc_paged_workspace(1, 4, 2, 64)
+    da.decode_attn_paged_append(q.cuda(), k.cuda(), v.cuda(), cache, torch.tensor(bounds, dtype=torch.int32, device="cuda"), kv_lens,
+                                table, ws, cos_sin=cs.cuda(), q_out=out[5:10])
+    err = da.decode_attn_splitkv_get_error(ws)
+    assert err == (0 if bounds[-2:] == [5, 5] else da.DA_DEVERR_SEQLENS)
+    out = out.cpu()
+    tables = p.table
+    left_alone = set(range(15))
+    for b, rows in done.items():
+        r = torch.tensor(list(rows))
+        at = torch.arange(10 - len(rows), 10)
+        p.table = tables[b:b + 1]
+        append32(p, None, k[r], v[r], [10], [len(rows)], cs, 1)
+        want = turned(q[r], cs, at, 1, torch.float32).to(q.dtype)
+        for i, row in enumerate(rows):
+            left_alone.discard(5 + row)
+            if row != claimed_twice:
+                assert same_bits(out[5 + row], want[i]), row
+    assert torch.all(out[sorted(left_alone)] == -3.0)
+    same = torch.ones(n, dtype=torch.bool)
+    if claimed_twice is not None:
+        same[tables[2, 0].long()] = False
+    for name, big in zip(("k", "v"), guarded):
+        assert torch.all(big.view(raw)[:n] == 0x55) and torch.all(big.view(raw)[2 * n:] == 0x55)
+        assert torch.equal(big.view(raw)[n:2 * n].cpu()[same], getattr(p, name).view(raw)[same]), name
+        if kv == "e4m3":
+            assert same_bits(getattr(cache, name + "_scale").cpu()[same], getattr(p, name + "_scale")[same])
