@@ -682,7 +682,7 @@ da_status run_append(AppendParams& p, bool e4m3, cudaStream_t stream) {
            (p.head_lanes * kManyHeads < heads || static_cast<int64_t>(p.T) * kUnits * p.head_lanes < kManyThreads))
         p.head_lanes *= 2;
     const int tokens = kAppendThreads / kUnits / p.head_lanes;
-    const int row_blocks = e4m3 && p.Hq == 0 ? 0 : (p.T + tokens - 1) / tokens;
+    const int row_blocks = e4m3 && p.Hq == 0 ? 0 : 1 + (p.T - 1) / tokens;   // (T >= 1, up to 2^31 - 1)
     const size_t smem = (3 * p.B + 2) * sizeof(int32_t);
     if (!e4m3) return launch_append(append16_kernel<D, DT, HALF>, row_blocks, smem, p, stream);
     // a sequence's n new tokens touch at most min(n, n / P + 2) pages
