@@ -81,14 +81,17 @@ da_status decode_attn_paged_workspace_init(void* workspace, size_t workspace_byt
  *     x_j = scale * k_scale * (q . k_j)              j <= L_b - T_q + t
  *     out = sum_j softmax(x)_j * v_scale * v_j,      lse = ln sum_j exp(x_j)
  *
- * with the scales of key j's page and head (1 in 16-bit pages). Scores, maxima and sums are
- * float32. A key's weight is rounded before it meets the value: in 16-bit pages to within 2^-15
- * of itself (bf16), 2^-21 or 2^-36 of the largest one of its token and head (fp16); in 8-bit
- * pages it times v_scale to fp16, 2^-11 of itself or 2^-32 of the largest one. A token that sees no key
+ * with the scales of key j's page and head (1 in 16-bit pages). A token that sees no key
  * gets out = 0 and lse = -inf. Memory in a page behind a sequence's last token may hold
- * anything. A NaN or an infinity among keys or values reaches the tokens that see it and no
- * others (nor other heads). The results do not depend on timing: the same inputs on the same device give
- * the same bits.
+ * anything. A NaN or an infinity among keys or values reaches the tokens that see it and
+ * no others, nor other heads. The results do not depend on timing: the same inputs on the
+ * same device give the same bits.
+ *
+ * Scores, maxima and sums are float32. A key's weight is rounded before it meets the value:
+ * in 16-bit pages to within 2^-15 of itself (bf16), 2^-21 or 2^-36 of the largest one of its
+ * token and head (fp16); in 8-bit pages it times v_scale to fp16, 2^-11 of itself or 2^-32
+ * of the largest one. (An infinite value whose weight is below 2^-34
+ * of the largest one may give NaN.)
  *
  * The call's arguments are the fields of a struct (host memory, read during the call).
  * Errors (nothing enqueued): DA_ERR_INVALID_ARG, DA_ERR_UNSUPPORTED (D, or a batch

@@ -23,9 +23,9 @@
 // took 20 to 60 % longer.
 //
 // Measured (one GB300): 16-bit pages, 9887 tokens of 32 + 2 x 8 heads in 5 prompts 39.3 us,
-// 6.3 TB/s; 64 tokens, one per sequence, 28 + 2 x 4 heads 2.8 us. e4m3 pages: the same prompts 41.2 us,
+// 6.3 TB/s; 64 tokens, one per sequence, 28 + 2 x 4 heads 2.8 us. e4m3 pages: the same prompts 40.8 us,
 // 5.5 TB/s (bound by the latency of a page's two passes and by instructions, not by its bytes); 256 tokens,
-// one per sequence, 16 + 2 x 2 heads 4.0 us.
+// one per sequence, 16 + 2 x 2 heads 4.1 us.
 
 #include "paged_common.cuh"
 
@@ -691,6 +691,8 @@ da_status run_append(AppendParams& p, bool e4m3, cudaStream_t stream) {
     // 64 tokens in registers: fewer read rows twice (pages of 64 tokens, half the threads: 18.7 us against 17.8, and
     // 15.3 against 9.3), more idle and have fewer bytes in flight (pages of 32 tokens, twice the threads: 16.6 us
     // against 14.2; 64-dim heads, pages of 64, the whole block: 51.9 against 37.6).
+    // (A warp for up to three tokens per sequence: 64 sequences of 3 tokens, 32 + 2 x 8 heads, 4.2 us against 8.7. It is
+    // ahead further than that: of 4 tokens 5.1 against 8.7, of 16 8.2 against 11.6; of 32 17.5 against 16.7.)
     const bool few = p.T < 4 * static_cast<int64_t>(p.B);
     const int lanes = few ? 32 : p.P <= 32 ? D : 2 * D;
     const int64_t units = touched * p.Hkv * 2;

@@ -30,9 +30,10 @@
 // 16-bit pages of head size 128 have one CTA of eight per SM: as many warps on half as many ranges, so
 // half the partial results, and a short range streams twice as fast (16 x 131072 keys 1189 -> 1153 us,
 // the ragged batch 89 -> 85 us, one sequence of 32768 keys 31.0 -> 28.5 us), unless the table's rows hold
-// few keys (256 sequences of 256: 18.5 us against 16.5, where two CTAs cover each other's
-// ends). e4m3 pages, whose consumers work harder, lose by it (four tokens 191 us against 169), as does
-// head size 64. The producer's lanes read the block table (and the scales) of the next 32 boxes at
+// few keys (256 sequences of 256: 18.6 us against 16.3, 64 of 512: 25.8 against 25.4, of 960: 45.3 against
+// 42.8, where two CTAs cover each other's ends; of 1024: 46.0 against 44.6, but 16 of 1024 15.3 against 16.4
+// and 16 of 2048 24.5 against 27.4). e4m3 pages, whose consumers work harder, lose by it (four tokens
+// 191 us against 169), as does head size 64. The producer's lanes read the block table (and the scales) of the next 32 boxes at
 // once, one batch ahead of the copies, and each lane issues its own box: TMA boxes of gcd(page
 // size, stage) keys, 16-key boxes at a sequence's ragged end, so that a box never crosses a page.
 //
@@ -52,8 +53,8 @@
 // weights, in 16-bit pages to two terms of their type and in 8-bit pages to one of fp16 (weights16), and the outputs, once.
 //
 // Measured (one GB300, mean of a graph of calls): 16 sequences of 131072 keys, 32 / 8 heads, bf16
-// 1153 us, 7.4 TB/s; 64 sequences of 512 to 8192 keys, 28 / 4 heads 85.1 us, 6.5 TB/s, over e4m3
-// pages 50.8 us, 5.5 TB/s; one sequence of 1024 keys 8.8 us, of 8192 keys over e4m3 pages 11.0 us.
+// 1156 us, 7.4 TB/s; 64 sequences of 512 to 8192 keys, 28 / 4 heads 86.2 us, 6.4 TB/s, over e4m3
+// pages 51.3 us, 5.4 TB/s; one sequence of 1024 keys 9.0 us, of 8192 keys over e4m3 pages 11.1 us.
 
 #include "paged_common.cuh"
 
@@ -902,7 +903,7 @@ struct PagedKernel {
         return static_cast<int64_t>(j == 0 ? 2 * first_share + 1 : 2 * (first_share + j * p.lanes)) * Sh::kCols + col;
     }
 
-    // Columns 8n .. 8n + 7 of a piece from the four warps' states. With `direct` the piece is the first of two
+    // Columns 8n .. 8n + 7 of a piece from the consumer warps' states. With `direct` the piece is the first of two
     // parts and the second one is written: they are merged here, in the order and with the roundings of merge_parts.
     static __device__ __forceinline__ void write_piece(const PagedParams& p, const PagedItem& it, const float* red_acc,
                                                        const float* red_m, int n, bool direct) {
@@ -1225,7 +1226,7 @@ struct PagedKernel {
 #pragma unroll
                     for (int off = 4; off < 32; off <<= 1) l[n][c] += __shfl_xor_sync(0xffffffffu, l[n][c], off);
 
-            // ---- merge the four warps in the stage that the producer handed over, 8 columns a round
+            // ---- merge the consumer warps in the stage that the producer handed over, 8 columns a round
             if (ok && !wait_warp(s.full0 + 8 * st, ph, p.wait_limit_ns)) {
                 ok = false;
                 if (lane == 0) flag_error(p.err, DA_DEVERR_TIMEOUT);
