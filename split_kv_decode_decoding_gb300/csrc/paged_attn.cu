@@ -33,9 +33,10 @@
 // few keys (256 sequences of 256: 18.6 us against 16.3, 64 of 512: 25.8 against 25.4, of 960: 45.3 against
 // 42.8, where two CTAs cover each other's ends; of 1024: 46.0 against 44.6, but 16 of 1024 15.3 against 16.4
 // and 16 of 2048 24.5 against 27.4). e4m3 pages, whose consumers work harder, lose by it (four tokens
-// 191 us against 169), as does head size 64. The producer's lanes read the block table (and the scales) of the next 32 boxes at
-// once, one batch ahead of the copies, and each lane issues its own box: TMA boxes of gcd(page
-// size, stage) keys, 16-key boxes at a sequence's ragged end, so that a box never crosses a page.
+// 191 us against 169), as does head size 64. The producer's lanes read the block table (and the
+// scales) of the next 32 boxes at once, one batch ahead of the copies, and each lane issues its own
+// box: TMA boxes of gcd(page size, stage) keys, 16-key boxes at a sequence's ragged end, so that a
+// box never crosses a page.
 //
 // e4m3 pages. The products run as fp16 tensor-core products: every e4m3 value is an fp16
 // value, and one conversion takes two elements, 0.5 cycles per SM (measured), 2 of the 11
@@ -281,6 +282,7 @@ struct PagedKernel {
     // In 16-bit pages a factor of the weights (2^kLift), beside the sum that keeps them as they are (fp16, four tokens 116.3 ->
     // 118.2 us, one token 86.5 both); in 8-bit pages, whose weights have a reference of their own, part of that one (dv).
     static constexpr float kLiftBy = !KV8 && kFp16Weights ? 2048.f : 1.f;
+    static_assert(kLiftBy == 1.f || kLift == 11.f, "kLiftBy is 2^kLift");
 
     struct Layout {
         uint8_t* smem;
