@@ -181,6 +181,135 @@ typedef struct {
 
 da_status decode_attn_paged_append(const da_paged_append* args, void* stream);
 
+/*
+ * decode_attn_paged of a model with a sliding window: the token at position p sees key j where
+ * j <= p and (j > p - window or j < sinks): itself and the window - 1 tokens before it, and the
+ * sequence's first `sinks` tokens, which stay visible however long it gets. Only pages that hold a
+ * key which some token sees are read (block-table entries of the others are not, and may hold
+ * anything). window in [1, 0x7fffffff], sinks in [0, 0x7fffffff]; arguments, results, workspace and
+ * errors otherwise as decode_attn_paged.
+ */
+da_status decode_attn_paged_window(const da_paged_attn* args, int window, int sinks, void* stream);
+
+/*
+ * Attention of a chunk of new tokens of each sequence over its pages: a prompt, a part of one, a
+ * drafted continuation or a single token, in any mixture. As in decode_attn_paged_append sequence
+ * b's tokens are rows cu_new[b] .. cu_new[b+1] - 1 of q, and row i of them sits at position
+ * p = kv_lens[b] - (cu_new[b+1] - cu_new[b]) + i (kv_lens counts them already, and their keys and
+ * values are in the pages). A row sees key j where
+ *
+ *     j <= p  and  (window = 0  or  j > p - window  or  j < sinks)
+ *
+ * and gets out and lse as decode_attn_paged defines them; a row that sees no key (p < 0, an empty
+ * sequence) gets out = 0 and lse = -inf. Rows that belong to no sequence are left alone, in out and
+ * lse alike. What a page holds behind a sequence's end, or block-table entries of pages that no row
+ * sees, may be anything. A NaN or an infinity among keys or values reaches the rows that see it and no
+ * others, nor other heads. The results do not depend on timing: the same inputs on the same device
+ * give the same bits.
+ *
+ * Scores, maxima, sums and accumulators are float32. A key's weight is rounded once before it meets
+ * the value: in bf16 pages to bf16, in fp16 pages to fp16 and in 8-bit pages (with v_scale) to fp16,
+ * both lifted by 2^11 towards the top of that type, so that weights count down to 2^-36 of the
+ * largest one of the row. Over 8-bit pages queries enter as fp16 scaled by a power of two per row (an
+ * element below 2^-28 of its row's largest loses bits). (An infinite value whose weight is below that,
+ * and a value of 8-bit pages whose weight without v_scale is below 2^-126, may count as none or give NaN.)
+ */
+typedef struct {
+    const void* q;               /* device, T_new rows of Hq heads of D contiguous elements of `dtype`, 16-byte aligned, */
+    int64_t q_stride;            /*   rows q_stride elements apart (a multiple of 8, >= Hq * D)             */
+    const da_paged_cache* cache; /* host; 16-bit pages hold elements of `dtype` */
+    const int32_t* cu_new;       /* device, int32 [B+1], non-decreasing; a sequence whose rows are not within 0 .. T_new, or
+                                    end before they begin, is left out and sets DA_DEVERR_SEQLENS. (A row that two
+                                    sequences claim then goes to either or to both.) */
+    const int32_t* kv_lens;      /* device, int32 [B], the new tokens counted. A length below 0 or above max_pages *
+                                    page_size counts as 0 and sets DA_DEVERR_SEQLENS */
+    const int32_t* block_table;  /* as above; an entry outside [0, num_pages) sets DA_DEVERR_PAGE, its keys and values
+                                    read as zeros */
+    int max_pages;
+    int table_stride;
+    int B;                       /* in [1, DA_MAX_PAGED_BATCH] */
+    int T_new;                   /* rows that q and out hold, >= 0 (0: nothing is enqueued) */
+    int Hq;                      /* a multiple of the cache's Hkv; T_new * Hq / Hkv <= 0x3fffffff */
+    int dtype;                   /* DA_F16 or DA_BF16 */
+    float scale;                 /* finite */
+    int window;                  /* >= 1, or 0: no limit */
+    int sinks;                   /* >= 0 (ignored where window is 0) */
+    void* out;                   /* device, rows like q's, out_stride elements apart; no overlap with q */
+    int64_t out_stride;
+    float* lse;                  /* device, float32 [T_new, Hq], or NULL */
+    void* workspace;             /* decode_attn_paged_chunk_workspace_size(Hq, Hkv, D) bytes, initialised once by */
+    size_t workspace_bytes;      /*   decode_attn_paged_workspace_init; serves the other calls too, if large enough */
+} da_paged_chunk;
+
+/* Workspace of decode_attn_paged_chunk, for any batch and any lengths with these heads; 0 if an argument is out of range. */
+size_t decode_attn_paged_chunk_workspace_size(int Hq, int Hkv, int D);
+
+da_status decode_attn_paged_chunk(const da_paged_chunk* args, void* stream);
+
+/*
+ * Managing the pages. The block table and the lengths say which pages are in use: page p of the first
+ * ceil(kv_lens[b] / page_size) entries of row b. Nothing else is kept, so a sequence is freed by
+ * setting its length to 0 (or leaving its row out), and
+ *
+ *     decode_attn_paged_free_pages     lists the pages that no row uses,
+ *     decode_attn_paged_fork           makes rows that continue other rows and share their pages,
+ *     decode_attn_paged_compact        moves the pages in use to the front of the cache.
+ *
+ * They read one table and write another one, which must not overlap it, and can be captured and repeated.
+ * A length below 0 or above max_pages * page_size counts as 0 and sets DA_DEVERR_SEQLENS; an entry
+ * outside [0, num_pages) is used by no one, is copied as it is, and sets DA_DEVERR_PAGE. The results do not
+ * depend on timing.
+ */
+typedef struct {
+    const int32_t* kv_lens;      /* device, int32 [B] */
+    const int32_t* block_table;  /* device, int32 [B][table_stride]; only the entries in use are read */
+    int max_pages;               /* >= 1; max_pages * page_size <= 0x7fffff00 */
+    int table_stride;            /* >= max_pages */
+    int B;                       /* in [1, 65536]; B * max_pages <= 0x7fffffff */
+    int page_size;               /* a multiple of 16 in [16, DA_MAX_PAGE_SIZE]; the cache's own where there is one */
+    int num_pages;               /* >= 1, num_pages * page_size <= 0x7fffff00; the cache's own where there is one */
+    void* workspace;             /* decode_attn_paged_pages_workspace_size(num_pages) bytes, initialised once by */
+    size_t workspace_bytes;      /*   decode_attn_paged_workspace_init; serves the other calls too, if large enough */
+} da_paged_rows;
+
+/* Largest B of the calls below. */
+#define DA_MAX_PAGED_ROWS 65536
+
+/* Workspace of the calls below; 0 if num_pages is out of range. */
+size_t decode_attn_paged_pages_workspace_size(int num_pages);
+
+/*
+ * free_pages[0 .. n-1] = the pages that no row uses, ascending; num_free[0] = n. Entries of free_pages
+ * (device, int32 [num_pages]) from n on are left alone.
+ */
+da_status decode_attn_paged_free_pages(const da_paged_rows* rows, int32_t* free_pages, int32_t* num_free, void* stream);
+
+/*
+ * Row i of block_table_out (i < n_out) continues row parents[i]: it gets its length and its pages. Where
+ * new_pages[i] >= 0 and the length is no multiple of the page size, new_pages[i] takes the place of the last,
+ * partly filled page, and that page's tokens (keys, values and 8-bit pages' scales) are copied to it, so that both
+ * rows can be appended to; with new_pages[i] < 0 the last page is shared like the others (one row at most may
+ * append to it). A parent outside [0, B) sets DA_DEVERR_SEQLENS and gives a row of length 0; a new page outside the
+ * cache sets DA_DEVERR_PAGE and is not written. Entries behind a row's pages are left alone. The new pages must be
+ * distinct, and none of them in use.
+ *   parents, new_pages   device, int32 [n_out], n_out in [1, 65536]
+ *   kv_lens_out          device, int32 [n_out]; block_table_out device, int32 [n_out][table_out_stride],
+ *                        table_out_stride >= max_pages; neither overlaps an input
+ *   rows                 page_size and num_pages must be the cache's
+ */
+da_status decode_attn_paged_fork(const da_paged_rows* rows, const da_paged_cache* cache, const int32_t* parents,
+                                 const int32_t* new_pages, int n_out, int32_t* kv_lens_out, int32_t* block_table_out,
+                                 int table_out_stride, void* stream);
+
+/*
+ * With n pages in use, the pages in use from n on move to the free ones before n, in ascending order both, and
+ * num_used[0] = n; pages n .. num_pages - 1 are free afterwards. block_table_out (device, int32 [B][table_out_stride])
+ * gets the rows' entries with the pages' new numbers; entries behind a row's pages are left alone, and a page that
+ * several rows share moves once. The lengths stay as they are.
+ */
+da_status decode_attn_paged_compact(const da_paged_rows* rows, const da_paged_cache* cache, int32_t* block_table_out,
+                                    int table_out_stride, int32_t* num_used, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -15,9 +15,11 @@ import os
 
 from . import paged as _paged
 from .build import LIB, build
-from .paged import (DA_DEVERR_PAGE, DA_DEVERR_POSITION, DA_E4M3, DA_MAX_PAGE_SIZE, DA_MAX_PAGED_BATCH, DA_ROPE_HALF,
-                    DA_ROPE_INTERLEAVED, DA_ROPE_NONE, EXPORTED_PAGED, PagedCache, alloc_paged_workspace,
-                    decode_attn_paged, decode_attn_paged_append, paged_workspace_size)
+from .paged import (DA_DEVERR_PAGE, DA_DEVERR_POSITION, DA_E4M3, DA_MAX_PAGE_SIZE, DA_MAX_PAGED_BATCH, DA_MAX_PAGED_ROWS,
+                    DA_ROPE_HALF, DA_ROPE_INTERLEAVED, DA_ROPE_NONE, EXPORTED_PAGED, PagedCache, alloc_paged_chunk_workspace,
+                    alloc_paged_pages_workspace, alloc_paged_workspace, decode_attn_paged, decode_attn_paged_append,
+                    decode_attn_paged_chunk, decode_attn_paged_compact, decode_attn_paged_fork, decode_attn_paged_free_pages,
+                    decode_attn_paged_window, paged_chunk_workspace_size, paged_pages_workspace_size, paged_workspace_size)
 
 DA_OK, DA_ERR_INVALID_ARG, DA_ERR_UNSUPPORTED, DA_ERR_ALIGNMENT = 0, 1, 2, 3
 DA_ERR_WORKSPACE_TOO_SMALL, DA_ERR_CUDA, DA_ERR_SCRATCH_LIMIT, DA_ERR_DEVICE_TIMEOUT = 4, 5, 6, 7

@@ -9,6 +9,11 @@
 namespace da_impl {
 
 constexpr size_t kPagedHeaderBytes = kHeaderBytes;
+constexpr int kPagedShares = 2048;   // decode attention: bound of shares (range, KV head, chunk), each with two partial results
+constexpr int kWriters = 4;          // consumer warps that write a piece's columns, two of every eight each
+constexpr size_t kPagedCounterBytes = static_cast<size_t>(kPagedShares) * kWriters * 4;
+// what workspace_init clears: every workspace begins so, whichever call it is for, so that one can serve them all
+constexpr size_t kPagedHeadBytes = kPagedHeaderBytes + kPagedCounterBytes;
 
 // Host checks of a cache description and of the block table's geometry, for calls
 // whose queries and new tokens are `dt`.

@@ -13,11 +13,14 @@ import struct
 DA_E4M3 = 2
 DA_DEVERR_PAGE, DA_DEVERR_POSITION = 0x4, 0x8
 DA_MAX_PAGED_BATCH, DA_MAX_PAGE_SIZE = 1024, 1024
+DA_MAX_PAGED_ROWS = 65536
 DA_ROPE_NONE, DA_ROPE_HALF, DA_ROPE_INTERLEAVED = 0, 1, 2
 
 EXPORTED_PAGED = [
     "decode_attn_paged_workspace_size", "decode_attn_paged_workspace_init", "decode_attn_paged",
-    "decode_attn_paged_append",
+    "decode_attn_paged_append", "decode_attn_paged_window", "decode_attn_paged_chunk_workspace_size",
+    "decode_attn_paged_chunk", "decode_attn_paged_pages_workspace_size", "decode_attn_paged_free_pages",
+    "decode_attn_paged_fork", "decode_attn_paged_compact",
 ]
 
 
@@ -39,16 +42,25 @@ def declare(lib) -> None:
     lib.decode_attn_paged_workspace_size.restype = SZ
     lib.decode_attn_paged_workspace_init.argtypes = [P, SZ, P]
     lib.decode_attn_paged_workspace_init.restype = I
-    for f in (lib.decode_attn_paged, lib.decode_attn_paged_append):
-        f.argtypes = [ctypes.c_char_p, P]
+    lib.decode_attn_paged_chunk_workspace_size.argtypes = [I, I, I]
+    lib.decode_attn_paged_chunk_workspace_size.restype = SZ
+    lib.decode_attn_paged_pages_workspace_size.argtypes = [I]
+    lib.decode_attn_paged_pages_workspace_size.restype = SZ
+    S = ctypes.c_char_p
+    for f, more in ((lib.decode_attn_paged, []), (lib.decode_attn_paged_append, []), (lib.decode_attn_paged_window, [I, I]),
+                    (lib.decode_attn_paged_chunk, []), (lib.decode_attn_paged_free_pages, [P, P]),
+                    (lib.decode_attn_paged_fork, [P, P, P, I, P, P, I]), (lib.decode_attn_paged_compact, [P, P, I, P])):
+        f.argtypes = [S, *more, P]
         f.restype = I
     _handle = lib
 
 
-# da_paged_attn and da_paged_append, field by field: packing a struct costs a third of what ctypes
+# da_paged_attn, da_paged_append, da_paged_chunk and da_paged_rows, field by field: packing a struct costs a third of what ctypes
 # takes to convert as many arguments
 _pack_attn = struct.Struct("@PPPPiiiiiifPPPN").pack
 _pack_append = struct.Struct("@PPPqqqPiiiPPPiiiiiiPPqP").pack
+_pack_chunk = struct.Struct("@PqPPPPiiiiiifiiPqPPN").pack
+_pack_rows = struct.Struct("@PPiiiiiPN").pack
 
 
 def _lib():
@@ -144,20 +156,41 @@ def paged_workspace_size(T_q: int, Hq: int, Hkv: int, D: int) -> int:
     return _lib().decode_attn_paged_workspace_size(T_q, Hq, Hkv, D)
 
 
-def alloc_paged_workspace(T_q: int, Hq: int, Hkv: int, D: int, device="cuda", stream=None):
-    """Allocate (through PyTorch) and initialise a workspace for calls with these heads, of up to T_q query tokens."""
+def _alloc(nbytes: int, device, stream):
     import torch
     if _codes is None:
         _init()
-    nbytes = paged_workspace_size(T_q, Hq, Hkv, D)
     if nbytes == 0:
-        raise ValueError("paged_workspace_size rejected the sizes")
+        raise ValueError("the workspace size was rejected: a size is out of range")
     ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
     _check_device(ws.get_device())
     st = _lib().decode_attn_paged_workspace_init(ws.data_ptr(), nbytes, _raw_stream(stream, ws.get_device()))
     if st:
         _fail(st, "decode_attn_paged_workspace_init")
     return ws
+
+
+def alloc_paged_workspace(T_q: int, Hq: int, Hkv: int, D: int, device="cuda", stream=None):
+    """Allocate (through PyTorch) and initialise a workspace for calls with these heads, of up to T_q query tokens."""
+    return _alloc(paged_workspace_size(T_q, Hq, Hkv, D), device, stream)
+
+
+def paged_chunk_workspace_size(Hq: int, Hkv: int, D: int) -> int:
+    return _lib().decode_attn_paged_chunk_workspace_size(Hq, Hkv, D)
+
+
+def paged_pages_workspace_size(num_pages: int) -> int:
+    return _lib().decode_attn_paged_pages_workspace_size(num_pages)
+
+
+def alloc_paged_chunk_workspace(Hq: int, Hkv: int, D: int, device="cuda", stream=None):
+    """Allocate and initialise a workspace for decode_attn_paged_chunk with these heads."""
+    return _alloc(paged_chunk_workspace_size(Hq, Hkv, D), device, stream)
+
+
+def alloc_paged_pages_workspace(num_pages: int, device="cuda", stream=None):
+    """Allocate and initialise a workspace for free_pages, fork and compact over a cache of num_pages pages."""
+    return _alloc(paged_pages_workspace_size(num_pages), device, stream)
 
 
 def _check_sequences(kv_lens, block_table, dev):
@@ -174,13 +207,8 @@ def _check_sequences(kv_lens, block_table, dev):
     return B, max_pages, stride if B > 1 else max_pages   # the stride of a single row is any number
 
 
-def decode_attn_paged(q, cache: PagedCache, kv_lens, block_table, out, workspace, *, scale: float | None = None, lse=None,
-                      stream=None):
-    """out = decode attention of q over a paged cache; see the C header.
-
-    q, out: [B, T_q, Hq, D], or [B, Hq, D] for one query token; lse (optional): float32 of the same
-    shape without D. kv_lens: int32 [B]; block_table: int32 [B, max_pages].
-    """
+def _decode_args(q, cache: PagedCache, kv_lens, block_table, out, workspace, scale, lse):
+    """(packed da_paged_attn, device) of a decode call."""
     if _codes is None:
         _init()
     dev = q.get_device()
@@ -219,9 +247,37 @@ def decode_attn_paged(q, cache: PagedCache, kv_lens, block_table, out, workspace
                           workspace.data_ptr(), workspace.nbytes)
     except struct.error as e:
         raise ValueError(f"scale, or a size, is no number of its C type: {e}") from None
+    return args, dev
+
+
+def decode_attn_paged(q, cache: PagedCache, kv_lens, block_table, out, workspace, *, scale: float | None = None, lse=None,
+                      stream=None):
+    """out = decode attention of q over a paged cache; see the C header.
+
+    q, out: [B, T_q, Hq, D], or [B, Hq, D] for one query token; lse (optional): float32 of the same
+    shape without D. kv_lens: int32 [B]; block_table: int32 [B, max_pages].
+    """
+    args, dev = _decode_args(q, cache, kv_lens, block_table, out, workspace, scale, lse)
     st = _lib().decode_attn_paged(args, _raw_stream(stream, dev))
     if st:
         _fail(st, "decode_attn_paged")
+    return out
+
+
+def _int32_of(x, name):
+    """x as a C int."""
+    if isinstance(x, bool) or not isinstance(x, int) or not -(1 << 31) <= x < 1 << 31:
+        raise ValueError(f"{name} must be a whole number of 32 bits, not {x!r}")
+    return x
+
+
+def decode_attn_paged_window(q, cache: PagedCache, kv_lens, block_table, out, workspace, *, window: int, sinks: int = 0,
+                             scale: float | None = None, lse=None, stream=None):
+    """decode_attn_paged where a token sees itself, the window - 1 tokens before it and the first `sinks` tokens."""
+    args, dev = _decode_args(q, cache, kv_lens, block_table, out, workspace, scale, lse)
+    st = _lib().decode_attn_paged_window(args, _int32_of(window, "window"), _int32_of(sinks, "sinks"), _raw_stream(stream, dev))
+    if st:
+        _fail(st, "decode_attn_paged_window")
     return out
 
 
@@ -292,3 +348,136 @@ def decode_attn_paged_append(q, k, v, cache: PagedCache, cu_new, kv_lens, block_
     if st:
         _fail(st, "decode_attn_paged_append")
     return q_out
+
+
+def decode_attn_paged_chunk(q, cache: PagedCache, cu_new, kv_lens, block_table, out, workspace, *, scale: float | None = None,
+                            window: int | None = None, sinks: int = 0, lse=None, stream=None):
+    """out = attention of a chunk of new tokens of each sequence over the paged cache; see the C header.
+
+    q, out: [T, Hq, D], rows may be strided; cu_new: int32 [B + 1]; kv_lens: int32 [B], the new
+    tokens counted (their keys and values are in the pages); block_table: int32 [B, max_pages];
+    lse (optional): float32 [T, Hq]. window None or 0: no limit.
+    """
+    if _codes is None:
+        _init()
+    dev = q.get_device()
+    _check_device(dev)
+    if cache.device != dev:
+        raise ValueError("the cache must be on the tensors' device")
+    B, max_pages, table_stride = _check_sequences(kv_lens, block_table, dev)
+    dtype, D = q.dtype, cache.D
+    code = _codes.get(dtype, -1)
+    if code not in (0, 1):
+        raise TypeError(f"q must be float16 or bfloat16, not {dtype}")
+    if cache.kv_dtype != DA_E4M3 and cache.kv_dtype != code:
+        raise TypeError(f"q is {dtype}, the cache {cache.dtype}")
+    if q.dim() != 3:
+        raise ValueError(f"q must be [T, Hq, D], not {tuple(q.shape)}")
+    T, Hq = q.shape[0], q.shape[1]
+    q_stride = _rows(q, "q", T, Hq, D, dtype, dev)
+    out_stride = _rows(out, "out", T, Hq, D, dtype, dev)
+    if cu_new.dtype is not _int32 or cu_new.shape != (B + 1,) or not cu_new.is_contiguous() or cu_new.get_device() != dev:
+        raise ValueError("cu_new must be contiguous int32 [B + 1]")
+    lse_ptr = 0
+    if lse is not None:
+        if lse.shape != (T, Hq) or lse.dtype is not _float32 or not lse.is_contiguous() or lse.get_device() != dev:
+            raise ValueError("lse must be contiguous float32 [T, Hq]")
+        lse_ptr = lse.data_ptr()
+    if workspace.get_device() != dev:
+        raise ValueError("the workspace must be on q's device")
+    try:
+        args = _pack_chunk(q.data_ptr(), q_stride, cache._ref, cu_new.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(),
+                           max_pages, table_stride, B, T, Hq, code, 1.0 / math.sqrt(D) if scale is None else scale,
+                           0 if window is None else window, sinks, out.data_ptr(), out_stride, lse_ptr, workspace.data_ptr(),
+                           workspace.nbytes)
+    except struct.error as e:
+        raise ValueError(f"scale, window, sinks, or a size, is no number of its C type: {e}") from None
+    st = _lib().decode_attn_paged_chunk(args, _raw_stream(stream, dev))
+    if st:
+        _fail(st, "decode_attn_paged_chunk")
+    return out
+
+
+# ------------------------------------------------------------ managing the pages
+def _rows_args(kv_lens, block_table, workspace, page_size, num_pages):
+    """(packed da_paged_rows, B, max_pages, device)"""
+    if _codes is None:
+        _init()
+    dev = kv_lens.get_device()
+    _check_device(dev)
+    B, max_pages, table_stride = _check_sequences(kv_lens, block_table, dev)
+    if workspace.get_device() != dev:
+        raise ValueError("the workspace must be on the tensors' device")
+    try:
+        args = _pack_rows(kv_lens.data_ptr(), block_table.data_ptr(), max_pages, table_stride, B, page_size, num_pages,
+                          workspace.data_ptr(), workspace.nbytes)
+    except struct.error as e:
+        raise ValueError(f"page_size, or a size, is no number of its C type: {e}") from None
+    return args, B, max_pages, dev
+
+
+def _list(x, name, n, dev):
+    """Check a contiguous int32 [n] tensor; its address."""
+    if x.dtype is not _int32 or x.shape != (n,) or not x.is_contiguous() or x.get_device() != dev:
+        raise ValueError(f"{name} must be contiguous int32 [{n}] on the tensors' device")
+    return x.data_ptr()
+
+
+def _table_out(x, B, max_pages, dev):
+    """Check a block table to write; its row stride."""
+    if x.dtype is not _int32 or x.dim() != 2 or x.shape[0] != B or x.shape[1] < max_pages or x.get_device() != dev:
+        raise ValueError(f"block_table_out must be int32 [{B}, max_pages] on the tensors' device, with max_pages >= {max_pages}")
+    stride, one = x.stride()
+    if (one != 1 and x.shape[1] > 1) or (B > 1 and stride < x.shape[1]):
+        raise ValueError("the rows of block_table_out must be contiguous and apart")
+    return stride if B > 1 else x.shape[1]
+
+
+def decode_attn_paged_free_pages(kv_lens, block_table, free_pages, num_free, workspace, *, page_size: int, stream=None):
+    """free_pages[:n] = the pages that no sequence uses, ascending, num_free[0] = n; see the C header.
+
+    kv_lens: int32 [B]; block_table: int32 [B, max_pages]; free_pages: int32 [num_pages] of the cache;
+    num_free: int32 [1]. Returned.
+    """
+    args, _, _, dev = _rows_args(kv_lens, block_table, workspace, page_size, free_pages.shape[0])
+    st = _lib().decode_attn_paged_free_pages(args, _list(free_pages, "free_pages", free_pages.shape[0], dev),
+                                             _list(num_free, "num_free", 1, dev), _raw_stream(stream, dev))
+    if st:
+        _fail(st, "decode_attn_paged_free_pages")
+    return free_pages, num_free
+
+
+def decode_attn_paged_fork(cache: PagedCache, kv_lens, block_table, parents, new_pages, kv_lens_out, block_table_out, workspace,
+                           *, stream=None):
+    """Rows that continue other rows of a block table and share their pages; see the C header.
+
+    parents, new_pages, kv_lens_out: int32 [n]; block_table_out: int32 [n, max_pages]. Returned:
+    kv_lens_out, block_table_out.
+    """
+    args, _, max_pages, dev = _rows_args(kv_lens, block_table, workspace, cache.page_size, cache.num_pages)
+    if cache.device != dev:
+        raise ValueError("the cache must be on the tensors' device")
+    n = parents.shape[0]
+    stride = _table_out(block_table_out, n, max_pages, dev)
+    st = _lib().decode_attn_paged_fork(args, cache._ref, _list(parents, "parents", n, dev), _list(new_pages, "new_pages", n, dev), n,
+                                       _list(kv_lens_out, "kv_lens_out", n, dev), block_table_out.data_ptr(), stride,
+                                       _raw_stream(stream, dev))
+    if st:
+        _fail(st, "decode_attn_paged_fork")
+    return kv_lens_out, block_table_out
+
+
+def decode_attn_paged_compact(cache: PagedCache, kv_lens, block_table, block_table_out, num_used, workspace, *, stream=None):
+    """Move the n pages in use to the front of the cache; block_table_out names them there, num_used[0] = n.
+
+    block_table_out: int32 [B, max_pages], another tensor than block_table; num_used: int32 [1]. Returned.
+    """
+    args, B, max_pages, dev = _rows_args(kv_lens, block_table, workspace, cache.page_size, cache.num_pages)
+    if cache.device != dev:
+        raise ValueError("the cache must be on the tensors' device")
+    stride = _table_out(block_table_out, B, max_pages, dev)
+    st = _lib().decode_attn_paged_compact(args, cache._ref, block_table_out.data_ptr(), stride, _list(num_used, "num_used", 1, dev),
+                                          _raw_stream(stream, dev))
+    if st:
+        _fail(st, "decode_attn_paged_compact")
+    return block_table_out, num_used
