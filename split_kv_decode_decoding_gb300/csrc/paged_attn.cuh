@@ -69,8 +69,6 @@ constexpr int kAlignRange = 16;      // ranges of an even batch up to so long fo
 constexpr int kMaxSlack = 4;         // units that a cut may move to avoid a partial result
 constexpr int kFewUnits = 8;         // units per SM of a full table up to which CTAs have an SM each
 constexpr int kShortCapacity = 1023; // keys of the block table's rows up to which CTAs of four consumer warps do better
-constexpr float kNoKey = -3.402823466e38f;   // running maximum of a column that has seen no key: the least finite
-                                             // value, so that every finite score is above it and no NaN arises
 
 template <int D, bool KV8, int NT, int NW, bool WIN>
 struct PagedShape {
@@ -207,28 +205,6 @@ struct Ranges {
     }
 };
 
-// mbar_wait and mbar_wait_warp with their loop kept a loop: unrolled at some twenty places it makes up a
-// third of the kernel's code, and a call on a short sequence spends a microsecond fetching code.
-__device__ __forceinline__ bool wait_lane(uint32_t bar, uint32_t parity, unsigned long long limit_ns) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const unsigned long long t0 = global_ns();
-#pragma unroll 1
-    do {
-#pragma unroll 1
-        for (int i = 0; i < 32; ++i)
-            if (mbar_try_wait(bar, parity)) return true;
-    } while (global_ns() - t0 <= limit_ns);
-    return false;
-}
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, unsigned long long limit_ns) {
-    const bool ok = wait_lane(bar, parity, limit_ns);
-    return __all_sync(0xffffffffu, ok);
-}
-
-__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-
 __device__ __forceinline__ void fence_acq_rel() { asm volatile("fence.acq_rel.gpu;" ::: "memory"); }
 
 __device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
@@ -246,13 +222,6 @@ __device__ __forceinline__ float select(bool yes, float a, float b) {
     return r;
 }
 
-// log2 of a scale, a subnormal one too (-inf of 0).
-__device__ __forceinline__ float log2_of_scale(float x) {
-    float y;
-    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // pack2, rounded towards zero.
 template <int DT>
 __device__ __forceinline__ uint32_t pack2_down(float a, float b) {
@@ -260,14 +229,6 @@ __device__ __forceinline__ uint32_t pack2_down(float a, float b) {
     if constexpr (DT == DA_F16) asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
     else asm("cvt.rz.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
     return r;
-}
-
-// Two e4m3 values to two fp16 values (exact).
-__device__ __forceinline__ void e4m3x4_to_f16(uint32_t x, uint32_t& lo, uint32_t& hi) {
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(x));
 }
 
 template <int D, int DT, bool KV8, int NT, int NW, bool WIN>
@@ -1427,59 +1388,6 @@ paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CU
 }
 
 // ------------------------------------------------------------ host side
-inline int gcd_of(int a, int b) {
-    while (b) {
-        const int r = a % b;
-        a = b;
-        b = r;
-    }
-    return a;
-}
-
-// Tensor map of a cache's keys or values: boxes of `rows` tokens of one head, slices of `inner` elements.
-inline bool make_page_map(CUtensorMap* map, const void* base, const da_paged_cache& c, int inner, int rows) {
-    auto fn = encode_fn();
-    if (!fn) return false;
-    const cuuint64_t size = c.kv_dtype == DA_E4M3 ? 1 : 2;
-    cuuint64_t dims[3], strides[2];
-    cuuint32_t box[3], step[3] = {1, 1, 1};
-    dims[0] = c.D;
-    strides[0] = c.D * size;
-    box[0] = inner;
-    if (c.layout == DA_LAYOUT_VARLEN) {
-        dims[1] = c.Hkv;
-        dims[2] = static_cast<cuuint64_t>(c.num_pages) * c.page_size;
-        strides[1] = static_cast<cuuint64_t>(c.Hkv) * c.D * size;
-        box[1] = 1;
-        box[2] = rows;
-    } else {
-        dims[1] = c.page_size;
-        dims[2] = static_cast<cuuint64_t>(c.num_pages) * c.Hkv;
-        strides[1] = static_cast<cuuint64_t>(c.page_size) * c.D * size;
-        box[1] = rows;
-        box[2] = 1;
-    }
-    const CUtensorMapDataType type = c.kv_dtype == DA_E4M3   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                                     : c.kv_dtype == DA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                                             : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    return fn(map, type, 3, const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              inner * size == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// SMs of the current device (152 if it cannot be queried).
-inline int device_sms() {
-    static std::atomic<int> known[64] = {};
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 152;
-    sms = known[dev].load(std::memory_order_relaxed);
-    if (sms == 0) {
-        if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) return 152;
-        known[dev].store(sms, std::memory_order_relaxed);
-    }
-    return sms;
-}
-
 // Keys of a sequence that its tokens see at most, in stages of `keys` keys.
 template <bool WIN>
 int64_t most_stages(const PagedParams& p, int keys) {

@@ -1,118 +1,1101 @@
 // Attention of a chunk of new tokens of each sequence over the paged KV cache
-// (decode_attn_paged.h): a warp per (token, query head), in one pass over the keys that the
-// token sees with a running maximum m,
+// (decode_attn_paged.h) on the Blackwell tensor cores, for GB300 / sm_103a.
 //
-//     x_j = scale * ks * (q . k_j),   out = sum_j e^(x_j - m) vs v_j / sum_j e^(x_j - m).
+// An item is 256 rows of one sequence and KV head, a row one (token, query head of the group)
+// pair, in two tiles of 128 rows that take turns on the tensor cores. Over the 128-key tiles that
+// some row sees, in one pass with a running maximum m per row,
 //
-// A lane holds D / 32 dims of the query and of the accumulator. All of it is float32.
+//     S = Q K^T,   P = 2^(S scale log2e - m),   O += P V,   l += sum P;   out = O / l.
+//
+// S, P and O live in tensor memory (S and P in the same columns), Q, K and V in shared memory.
+// One thread per row holds the row's scores in registers. One warp copies K and V by TMA, a box
+// per page, or per 16 to 128 keys of it; one thread issues the products:
+//
+//     ... P0(j) V(j), Q0 K(j+1), P1(j) V(j), Q1 K(j+1), P0(j+1) V(j+1) ...
+//
+// so that the softmax of one row tile runs beside the products of the other.
+//
+// The work of the whole call, in units of a key tile of an item, is cut into as many equal ranges
+// as there are CTAs, one per SM, whatever the lengths, the causal triangle and the window leave of it. An item that lies in
+// one range is written by it; otherwise each of its ranges leaves a partial result (two per range at
+// most), and a second kernel joins them, in the order of the ranges: the results do not depend on timing.
+//
+// A tile is special if some row does not see some of its keys. There the scores of the others are taken
+// out, values that no row sees are zeroed, and so are elements that are not finite (0 times NaN is no
+// zero), which the end of the piece then adds to the rows that see them.
+//
+// e4m3 pages: four warps convert each tile to fp16, exactly. Queries enter as fp16 (load_queries of the
+// decode kernel has the reasons); ks multiplies the scores and vs the weights, page by page, relative to
+// a reference per row (`dv`) that keeps the fp16 weights in range.
 
 #include "paged_common.cuh"
+#include "tcgen05.cuh"
 
 namespace da_impl {
 
-constexpr int kRowWarps = 8;
+constexpr int kTileRows = 128;
+constexpr int kItemRows = 2 * kTileRows;
+constexpr int kTileKeys = 128;
+constexpr int kMaxRanges = 160;       // CTAs at most (GB300 has 152 SMs)
+constexpr int kItemCost = 2;          // an item's begin and end, in key tiles
+constexpr int kLeastCost = 6;         // of a range
+constexpr int kLeastPart = 2;         // key tiles of a partial result at least
+constexpr int kScaleRing = 4;         // tiles whose scales are in shared memory
+constexpr int kJoinSlices = 8;        // blocks that join one split item, 32 rows each
+
+template <int D, bool KV8>
+struct ChunkShape {
+    static constexpr int kThreads = KV8 ? 512 : 320;
+    static constexpr int kSlices = D / 64;                     // 128-byte columns of a tile in 16 bits
+    static constexpr int kSliceBytes = 128 * 128;
+    static constexpr int kTileBytes = kSlices * kSliceBytes;
+    static constexpr int kRing = KV8 ? 3 : (D == 128 ? 5 : 8); // K and V tiles in 16 bits
+    static constexpr int kRawBytes = KV8 ? kTileKeys * D : 0;  // and as they come, in 8
+    static constexpr int kRaw = KV8 ? 4 : 0;
+    static constexpr int kRawRow = D;
+    static constexpr int kQOff = 0;
+    static constexpr int kRingOff = 2 * kTileBytes;
+    static constexpr int kRawOff = kRingOff + kRing * kTileBytes;
+    static constexpr int kScaleOff = kRawOff + kRaw * kRawBytes;          // [tile][16-key box] {ks, log2 vs}
+    static constexpr int kBarOff = kScaleOff + (KV8 ? kScaleRing * 8 * 8 : 0);
+    static constexpr int kNumBars = 2 * kRing + 2 * kRaw + 2 * kScaleRing + 9;
+    static constexpr int kSmemBytes = 1024 + kBarOff + kNumBars * 8;
+    static constexpr int kPlanBytes = (DA_MAX_PAGED_BATCH + 1) * 8 + DA_MAX_PAGED_BATCH * 12;
+    static_assert(kPlanBytes <= kRing * kTileBytes, "the plan is made where the ring is later");
+    // tensor memory
+    static constexpr int kCols = 512, kO = 2 * kTileKeys;      // S0, S1, O0, O1
+};
+
+struct ChunkCut {            // a place in the order of the work: before key tile `tile` of an item
+    int b, kvh, rt, tile;
+};
+
+struct ChunkJoin {           // a split item, at the range that holds its first part
+    int parts;               // 0: none
+    int n, r0, kvh, rt, pad[3];
+};
 
 struct ChunkParams {
     const uint16_t* q;
-    const uint8_t *k, *v;
+    const uint8_t* v;
     const float *ks, *vs;
     const int32_t *cu, *lens, *table;
     uint16_t* out;
     float* lse;              // or nullptr
     uint32_t* err;
+    ChunkJoin* join;         // [ranges]
+    float2* part_sum;        // [2 * range][row] {m, l}
+    float4* part;            // [2 * range][D / 4][row], sums of weighted values relative to m
     int64_t q_stride, out_stride;
     int B, T, Hq, Hkv, G, P, max_pages, table_stride, num_pages, layout, window, sinks;
-    float scale;
+    int box_keys;            // keys of a TMA box: gcd(page size, 128)
+    uint32_t q_and, q_xor;   // on two query elements: zeroes them if the scale is 0, and takes its sign
+    float scale_log2;        // |scale| log2e (1 if it is 0)
+    unsigned long long wait_limit_ns;
 };
 
-template <int D, int DT, bool KV8>
-__global__ void __launch_bounds__(kRowWarps * 32) chunk_row_kernel(const ChunkParams p) {
-    constexpr int kDims = D / 32;
-    grid_dependency_wait();
-    if (threadIdx.x == 0) grid_dependents_launch();
-    const int lane = threadIdx.x & 31;
-    const int64_t warp = static_cast<int64_t>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
-    const int64_t warps = static_cast<int64_t>(gridDim.x) * kRowWarps;
-    auto element = [&](const uint8_t* base, int64_t at) {
-        if constexpr (KV8) {
-            uint32_t h2;
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(base[at])));
-            return bits_to_f32<DA_F16>(h2 & 0xffffu);
+struct ChunkSeq {
+    int n, L, r0;            // rows (0: none, or none that can be), keys, first row
+};
+
+__device__ __forceinline__ ChunkSeq chunk_seq(const ChunkParams& p, int b, bool flag) {
+    ChunkSeq s;
+    s.r0 = ld_cg_s32(p.cu + b);
+    const int r1 = ld_cg_s32(p.cu + b + 1);
+    s.L = ld_cg_s32(p.lens + b);
+    s.n = r1 - s.r0;
+    if (s.r0 < 0 || r1 < s.r0 || r1 > p.T) {
+        if (flag) flag_error(p.err, DA_DEVERR_SEQLENS);
+        s.n = 0;
+    }
+    if (s.L < 0 || s.L > static_cast<int64_t>(p.max_pages) * p.P) {
+        if (flag) flag_error(p.err, DA_DEVERR_SEQLENS);
+        s.L = 0;
+    }
+    return s;
+}
+
+// The key tiles of an item: 0 .. ns - 1 (first tokens), then lo on, nt in all (one, all of it hidden, if no row sees a key).
+struct ChunkTiles {
+    int first, last;         // positions of its first and last token (may be < 0)
+    int low;                 // the first key that the first token sees through the window
+    int ns, lo, nt;
+
+    __device__ __forceinline__ ChunkTiles(const ChunkParams& p, const ChunkSeq& s, int rt) {
+        const int f = rt * kItemRows;
+        first = s.L - s.n + f / p.G;
+        last = s.L - s.n + min(s.n - 1, (f + kItemRows - 1) / p.G);
+        low = p.window ? max(0, max(first, 0) - p.window + 1) : 0;
+        ns = (min(p.sinks, low) + kTileKeys - 1) / kTileKeys;
+        lo = max(ns, low / kTileKeys);
+        nt = ns + max(last, 0) / kTileKeys - lo + 1;
+    }
+    __device__ __forceinline__ int key(int tile) const { return (tile < ns ? tile : lo + tile - ns) * kTileKeys; }
+    // whether every row sees every key of the tile at key k0
+    __device__ __forceinline__ bool plain(const ChunkParams& p, int k0) const {
+        const int end = k0 + kTileKeys - 1;
+        return first >= end && (p.window == 0 || last - k0 < p.window || end < p.sinks);
+    }
+    // whether some row sees a key in [k, k + keys), or the key k
+    __device__ __forceinline__ bool wanted(const ChunkParams& p, int k, int keys) const {
+        return k <= last && (k + keys > low || k < p.sinks);
+    }
+};
+
+__device__ __forceinline__ int chunk_items(const ChunkParams& p, int n) { return (n * p.G + kItemRows - 1) / kItemRows; }
+
+// Where a cut at distance x into an item falls: the item's begin, a key tile of it, or (nt) its end.
+__device__ __forceinline__ int cut_tile(int x, int nt) {
+    const int tile = x - kItemCost;
+    return tile < kLeastPart ? 0 : nt - tile < kLeastPart ? nt : tile;
+}
+
+// The pieces of a range, one after the other.
+struct ChunkPiece {
+    ChunkSeq s;
+    int b, kvh, rt, t0, t1, nt;
+};
+
+struct ChunkWalk {
+    ChunkCut at, end;
+    ChunkSeq s;
+    __device__ __forceinline__ ChunkWalk(const ChunkParams& p, const ChunkCut* cuts) : at(cuts[0]), end(cuts[1]) {
+        if (at.b < p.B) s = chunk_seq(p, at.b, false);
+    }
+    __device__ __forceinline__ bool next(const ChunkParams& p, ChunkPiece& x) {
+        if (at.b >= p.B || (at.b == end.b && at.kvh == end.kvh && at.rt == end.rt && at.tile >= end.tile)) return false;
+        const ChunkTiles tiles(p, s, at.rt);
+        x.s = s;
+        x.b = at.b;
+        x.kvh = at.kvh;
+        x.rt = at.rt;
+        x.t0 = at.tile;
+        x.nt = x.t1 = tiles.nt;
+        if (at.b == end.b && at.kvh == end.kvh && at.rt == end.rt) {
+            x.t1 = end.tile;
+            at.tile = end.tile;
         } else {
-            return bits_to_f32<DT>(reinterpret_cast<const uint16_t*>(base)[at]);
-        }
-    };
-    for (int b = 0; b < p.B; ++b) {
-        const int r0 = ld_cg_s32(p.cu + b), r1 = ld_cg_s32(p.cu + b + 1);
-        if (r0 < 0 || r1 < r0 || r1 > p.T) {
-            if (lane == 0) flag_error(p.err, DA_DEVERR_SEQLENS);
-            continue;
-        }
-        int L = ld_cg_s32(p.lens + b);
-        if (L < 0 || L > static_cast<int64_t>(p.max_pages) * p.P) {
-            if (lane == 0) flag_error(p.err, DA_DEVERR_SEQLENS);
-            L = 0;
-        }
-        for (int64_t i = warp; i < static_cast<int64_t>(r1 - r0) * p.Hq; i += warps) {
-            const int t = static_cast<int>(i / p.Hq), h = static_cast<int>(i - static_cast<int64_t>(t) * p.Hq), kvh = h / p.G;
-            const int pos = L - (r1 - r0) + t;
-            const int low = p.window ? max(0, pos - p.window + 1) : 0, sinks = min(p.sinks, low);
-            float q[kDims], acc[kDims], m = -INFINITY, l = 0.f;
-#pragma unroll
-            for (int d = 0; d < kDims; ++d) {
-                q[d] = bits_to_f32<DT>(p.q[(r0 + t) * p.q_stride + static_cast<int64_t>(h) * D + 32 * d + lane]);
-                acc[d] = 0.f;
-            }
-            for (int j = 0; j <= pos; ++j) {
-                if (j == sinks) j = low;
-                const int page = ld_cg_s32(p.table + static_cast<int64_t>(b) * p.table_stride + j / p.P);
-                const bool good = page >= 0 && page < p.num_pages;
-                if (!good && lane == 0) flag_error(p.err, DA_DEVERR_PAGE);
-                const int64_t at = page_row(p.layout, good ? page : 0, j % p.P, kvh, p.P, p.Hkv) * D + lane;
-                float x = 0.f, ks = 1.f, vs = 1.f;
-                if constexpr (KV8) {
-                    ks = good ? p.ks[static_cast<int64_t>(page) * p.Hkv + kvh] : 0.f;
-                    vs = good ? p.vs[static_cast<int64_t>(page) * p.Hkv + kvh] : 0.f;
+            at.tile = 0;
+            if (++at.rt == chunk_items(p, s.n)) {
+                at.rt = 0;
+                if (++at.kvh == p.Hkv) {
+                    at.kvh = 0;
+                    do {
+                        if (++at.b >= p.B) break;
+                        s = chunk_seq(p, at.b, false);
+                    } while (s.n == 0);
                 }
-#pragma unroll
-                for (int d = 0; d < kDims; ++d) x = fmaf(q[d], good ? element(p.k, at + 32 * d) : 0.f, x);
-#pragma unroll
-                for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-                x *= p.scale * ks;
-                const float top = fmaxf(m, x), none = top == -INFINITY ? 0.f : top;
-                const float old = expf(m - none), w = expf(x - none);
-                m = top;
-                l = fmaf(l, old, w);
-#pragma unroll
-                for (int d = 0; d < kDims; ++d)
-                    acc[d] = fmaf(acc[d], old, good ? w * (vs * element(p.v, at + 32 * d)) : 0.f);
             }
-            const bool none = m == -INFINITY && l == 0.f;
-            const int64_t row = (r0 + t) * p.out_stride + static_cast<int64_t>(h) * D;
-#pragma unroll
-            for (int d = 0; d < kDims; ++d) p.out[row + 32 * d + lane] = to_bits<DT>(none ? 0.f : acc[d] / l);
-            if (p.lse != nullptr && lane == 0)
-                p.lse[static_cast<int64_t>(r0 + t) * p.Hq + h] = none ? -INFINITY : m + logf(l);
         }
+        return true;
+    }
+};
+
+// ------------------------------------------------------------ the plan
+// This CTA's range: its cuts, and the split item that begins in it (by all threads; `space` is shared memory that
+// the pipeline uses later).
+struct ChunkPlan {
+    ChunkCut cuts[2];
+    int ranges;
+    ChunkJoin join;
+};
+
+template <int THREADS>
+__device__ void chunk_plan(const ChunkParams& p, uint8_t* space, ChunkPlan& plan) {
+    int64_t* pre = reinterpret_cast<int64_t*>(space);                    // [B + 1] cost before a sequence
+    ChunkSeq* seqs = reinterpret_cast<ChunkSeq*>(pre + p.B + 1);         // [B]
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr int kFew = 4;                                              // items that a thread counts by itself
+    for (int b = threadIdx.x; b < p.B; b += THREADS) {
+        const ChunkSeq s = chunk_seq(p, b, blockIdx.x == 0);
+        seqs[b] = s;
+        const int items = chunk_items(p, s.n);
+        int64_t cost = 0;
+        for (int rt = 0; rt < min(items, kFew); ++rt) cost += ChunkTiles(p, s, rt).nt + kItemCost;
+        pre[b + 1] = items > kFew ? -1 : cost * p.Hkv;
+    }
+    __syncthreads();
+    for (int b = warp; b < p.B; b += THREADS / 32) {
+        if (pre[b + 1] >= 0) continue;
+        const ChunkSeq s = seqs[b];
+        int64_t cost = 0;
+        for (int rt = lane; rt < chunk_items(p, s.n); rt += 32) cost += ChunkTiles(p, s, rt).nt + kItemCost;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) cost += __shfl_xor_sync(0xffffffffu, cost, off);
+        if (lane == 0) pre[b + 1] = cost * p.Hkv;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        int64_t before = 0;
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+            int64_t run = b0 + lane < p.B ? pre[b0 + lane + 1] : 0;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, run, off);
+                if (lane >= off) run += y;
+            }
+            if (b0 + lane < p.B) pre[b0 + lane + 1] = before + run;
+            before += __shfl_sync(0xffffffffu, run, 31);
+        }
+        if (lane == 0) pre[0] = 0;
+    }
+    __syncthreads();
+    const int64_t all = pre[p.B];
+    const int ranges = static_cast<int>(max(int64_t(1), min(static_cast<int64_t>(gridDim.x), all / kLeastCost)));
+    const int64_t q = all / ranges;
+    const int rem = static_cast<int>(all - q * ranges);
+    auto raw = [&](int r) { return r * q + min(r, rem); };
+    if (warp < 2) {
+        // warp 0 the range's begin, warp 1 its end and what follows from it
+        const int r = static_cast<int>(blockIdx.x) + warp;
+        ChunkCut cut = {p.B, 0, 0, 0};
+        ChunkJoin join = {};
+        if (r < ranges && all > 0) {         // (no rows at all: no work, and nothing to divide by)
+            const int64_t at = raw(r);
+            int lo = 0, hi = p.B - 1;       // last b with pre[b] <= at
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (pre[mid] <= at) lo = mid;
+                else hi = mid - 1;
+            }
+            const ChunkSeq s = seqs[lo];
+            const int64_t head = (pre[lo + 1] - pre[lo]) / p.Hkv;
+            const int items = chunk_items(p, s.n);
+            cut.b = lo;
+            cut.kvh = static_cast<int>((at - pre[lo]) / head);
+            int64_t begin = pre[lo] + cut.kvh * head;
+            int nt = 0;
+            for (int rt0 = 0; rt0 < items; rt0 += 32) {
+                const int mine = rt0 + lane < items ? ChunkTiles(p, s, rt0 + lane).nt : 0;
+                int64_t run = mine + (rt0 + lane < items ? kItemCost : 0);
+#pragma unroll
+                for (int off = 1; off < 32; off <<= 1) {
+                    const int64_t y = __shfl_up_sync(0xffffffffu, run, off);
+                    if (lane >= off) run += y;
+                }
+                const uint32_t past = __ballot_sync(0xffffffffu, begin + run > at);
+                if (past != 0) {
+                    const int i = __ffs(past) - 1;
+                    cut.rt = rt0 + i;
+                    nt = __shfl_sync(0xffffffffu, mine, i);
+                    begin += __shfl_sync(0xffffffffu, run, i) - nt - kItemCost;
+                    break;
+                }
+                begin += __shfl_sync(0xffffffffu, run, 31);
+            }
+            cut.tile = cut_tile(static_cast<int>(at - begin), nt);
+            if (warp == 1 && cut.tile > 0 && cut.tile < nt) {
+                // the cuts of other ranges in the same item
+                int inside = 0;
+                bool more = true;
+                for (int r0 = r + 1; more; r0 += 32) {
+                    const int64_t x = r0 + lane < ranges ? raw(r0 + lane) - begin : int64_t(1) << 40;
+                    int tile = nt;
+                    if (x < nt + kItemCost) tile = cut_tile(static_cast<int>(x), nt);
+                    const uint32_t in = __ballot_sync(0xffffffffu, tile < nt);
+                    inside += __popc(in);
+                    more = in == 0xffffffffu;
+                }
+                join.parts = 2 + inside;
+                join.n = s.n;
+                join.r0 = s.r0;
+                join.kvh = cut.kvh;
+                join.rt = cut.rt;
+            }
+            if (cut.tile == nt) {            // the next item's begin
+                cut.tile = 0;
+                if (++cut.rt == items) {
+                    cut.rt = 0;
+                    if (++cut.kvh == p.Hkv) {
+                        cut.kvh = 0;
+                        do ++cut.b;
+                        while (cut.b < p.B && pre[cut.b + 1] == pre[cut.b]);
+                    }
+                }
+            }
+        }
+        if (lane == 0) {
+            plan.cuts[warp] = cut;
+            if (warp == 1) plan.join = join;
+        }
+    }
+    __syncthreads();
+    // the first part begins in this range, unless the item did in an earlier one
+    if (threadIdx.x == 0) {
+        const ChunkCut &a = plan.cuts[0], &e = plan.cuts[1];
+        const bool earlier = a.b == e.b && a.kvh == e.kvh && a.rt == e.rt && a.tile > 0;
+        if (earlier) plan.join.parts = 0;
+        p.join[blockIdx.x] = plan.join;
     }
 }
 
+// ------------------------------------------------------------ arithmetic on pairs
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// tmem_ld32 and tmem_st16 without the wait.
+__device__ __forceinline__ void tmem_ld32_start(uint32_t taddr, float* r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+                 : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]), "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]), "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+                 : "r"(taddr));
+}
+// Nothing that reads the values moves before this.
+__device__ __forceinline__ void hold32(float* r) {
+    asm volatile("" : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]), "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15]), "+f"(r[16]), "+f"(r[17]), "+f"(r[18]), "+f"(r[19]), "+f"(r[20]), "+f"(r[21]), "+f"(r[22]), "+f"(r[23]), "+f"(r[24]), "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]), "+f"(r[29]), "+f"(r[30]), "+f"(r[31]));
+}
+__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_st16_start(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+                 ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 x;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(a));
+    return x;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint4 x) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
+}
+
 template <int D, int DT, bool KV8>
-da_status launch_chunk(const ChunkParams& p, cudaStream_t stream) {
+struct ChunkKernel {
+    using Sh = ChunkShape<D, KV8>;
+    static constexpr int MT = KV8 ? DA_F16 : DT;                 // type of the products
+    // A weight enters its product as 2^kLift times itself and is at most 2^kHeadroom times the largest one at the
+    // time that its row's reference was set; fp16 then holds all bits of a weight down to 2^-25 of the largest (bf16 any).
+    static constexpr float kHeadroom = MT == DA_F16 ? 4.f : 8.f;
+    static constexpr float kLift = MT == DA_F16 ? 15.f - kHeadroom : 0.f;
+    static constexpr uint32_t kIdS = umma_idesc<MT>(kTileRows, kTileKeys, false);
+    static constexpr uint32_t kIdPV = umma_idesc<MT>(kTileRows, D, true);
+
+    struct Ctx {
+        uint8_t* smem;
+        uint32_t base, tmem;
+        uint32_t kv_full, kv_empty, raw_full, raw_empty, sc_full, sc_empty, q_full, s_full, p_full, pv_done, fin;
+        const ChunkCut* cuts;
+        volatile int* dirty;     // [piece & 3]: number + 1 of the last such piece that had values that are not finite
+    };
+
+    static __device__ __forceinline__ uint32_t ring(const Ctx& c, int i) { return c.base + Sh::kRingOff + i * Sh::kTileBytes; }
+    // 16-byte chunk `chunk` of row `row` of a 16-bit tile
+    static __device__ __forceinline__ uint32_t tile_addr(uint32_t tile, int row, int chunk) {
+        return tile + (chunk >> 3) * Sh::kSliceBytes + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+    }
+    static __device__ __forceinline__ bool wait(const ChunkParams& p, uint32_t bar, uint32_t parity) {
+        const bool ok = wait_warp(bar, parity, p.wait_limit_ns);
+        if (!ok && (threadIdx.x & 31) == 0) flag_error(p.err, DA_DEVERR_TIMEOUT);
+        return ok;
+    }
+
+    // ------------------------------------------------------------ copies
+    static __device__ void producer(const Ctx& c, const ChunkParams& p, const CUtensorMap* tmK, const CUtensorMap* tmV) {
+        constexpr uint32_t kSlots = KV8 ? Sh::kRaw : Sh::kRing;
+        uint32_t slot = 0;             // K and V tiles so far
+        if (copy_tiles(c, p, tmK, tmV, slot)) return;
+        // after a wait that timed out, copies still in flight into this CTA's shared memory get another bounded one each
+        for (uint32_t i = slot < kSlots ? 0 : slot - kSlots; i < slot; ++i)
+            wait_lane((KV8 ? c.raw_full : c.kv_full) + 8 * (i % kSlots), (i / kSlots) & 1, p.wait_limit_ns);
+    }
+
+    static __device__ __forceinline__ bool copy_tiles(const Ctx& c, const ChunkParams& p, const CUtensorMap* tmK, const CUtensorMap* tmV,
+                                                      uint32_t& slot) {
+        constexpr int kSlots = KV8 ? Sh::kRaw : Sh::kRing;
+        constexpr int kBytes = KV8 ? Sh::kRawBytes : Sh::kTileBytes;
+        constexpr int kRow = KV8 ? Sh::kRawRow : 128;                       // bytes of a row of a box
+        const uint32_t space = c.base + (KV8 ? Sh::kRawOff : Sh::kRingOff);
+        const uint32_t full = KV8 ? c.raw_full : c.kv_full, empty = KV8 ? c.raw_empty : c.kv_empty;
+        const int lane = threadIdx.x & 31;
+        const int boxes = kTileKeys / p.box_keys, batch = 32 / boxes;       // tiles whose boxes the lanes look up at once
+        const int my_tile = lane / boxes, my_box = lane - my_tile * boxes;
+        ChunkWalk walk(p, c.cuts);
+        ChunkPiece x;
+        uint32_t count = 0;                // key tiles so far
+        while (walk.next(p, x)) {
+            const ChunkTiles tiles(p, x.s, x.rt);
+            const int32_t* row = p.table + static_cast<int64_t>(x.b) * p.table_stride;
+            auto entry = [&](int t) {      // block-table entry of this lane's box of tile t + my_tile, or -1
+                t += my_tile;
+                if (t >= x.t1) return -1;
+                const int k = tiles.key(t) + my_box * p.box_keys;
+                return tiles.wanted(p, k, p.box_keys) ? ld_cg_s32(row + k / p.P) : -1;
+            };
+            int ahead = entry(x.t0);
+            for (int t0 = x.t0; t0 < x.t1; t0 += batch) {
+                int page = ahead;
+                const int mine = t0 + my_tile;
+                const bool want = mine < x.t1 && tiles.wanted(p, tiles.key(mine) + my_box * p.box_keys, p.box_keys);
+                const bool good = page >= 0 && page < p.num_pages;
+                if (want && !good) flag_error(p.err, DA_DEVERR_PAGE);
+                if (!good) page = p.num_pages;     // past the cache, which the copy fills with zeros
+                ahead = entry(t0 + batch);
+                float ks = 0.f, lv = 0.f;
+                if constexpr (KV8) {
+                    float vs = 0.f;
+                    if (good) {
+                        const int64_t at = static_cast<int64_t>(page) * p.Hkv + x.kvh;
+                        ks = __ldcg(p.ks + at);
+                        vs = __ldcg(p.vs + at);
+                    }
+                    lv = log2_of_scale(vs);
+                }
+                for (int t = t0; t < min(t0 + batch, x.t1); ++t) {
+                    const int k0 = tiles.key(t);
+                    const int from = (t - t0) * boxes;      // this tile's lanes
+                    if constexpr (KV8) {
+                        const int at = count % kScaleRing;
+                        if (!wait(p, c.sc_empty + 8 * at, ((count / kScaleRing) & 1) ^ 1)) return false;
+                        const int owner = (from + (lane * 16) / p.box_keys) & 31;
+                        const float a = __shfl_sync(0xffffffffu, ks, owner), b = __shfl_sync(0xffffffffu, lv, owner);
+                        if (lane < 8) reinterpret_cast<float2*>(c.smem + Sh::kScaleOff)[at * 8 + lane] = make_float2(a, b);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(c.sc_full + 8 * at);
+                        ++count;
+                    }
+                    const int my_page = __shfl_sync(0xffffffffu, page, (from + lane) & 31);
+                    const int pos = k0 + lane * p.box_keys, in_page = pos % p.P;
+                    const bool thd = p.layout == DA_LAYOUT_VARLEN;
+                    // (a box of a page that is none starts past the last page)
+                    const bool none = my_page == p.num_pages;
+                    const int c1 = thd ? x.kvh : in_page;
+                    const int c2 = thd ? my_page * p.P + (none ? 0 : in_page) : my_page * p.Hkv + (none ? 0 : x.kvh);
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv, ++slot) {
+                        const int at = slot % kSlots;
+                        if (!wait(p, empty + 8 * at, ((slot / kSlots) & 1) ^ 1)) return false;
+                        const uint32_t bar = full + 8 * at;
+                        if (lane == 0) mbar_arrive_expect_tx(bar, kBytes);
+                        __syncwarp();
+                        if (lane < boxes) {
+                            const uint32_t dst = space + at * kBytes + lane * p.box_keys * kRow;
+                            const CUtensorMap* map = kv ? tmV : tmK;
+                            if constexpr (KV8) {
+                                tma_load_3d(dst, map, 0, c1, c2, bar);
+                            } else {
+#pragma unroll
+                                for (int sl = 0; sl < Sh::kSlices; ++sl) tma_load_3d(dst + sl * Sh::kSliceBytes, map, sl * 64, c1, c2, bar);
+                            }
+                        }
+                    }
+                }
+            }
+        }
+        return true;
+    }
+
+    // ------------------------------------------------------------ e4m3 to fp16
+    static __device__ void converter(const Ctx& c, const ChunkParams& p) {
+        constexpr int kChunks = D / 16;                        // 16-byte chunks of a raw row
+        const int tid = threadIdx.x & 127, lane = threadIdx.x & 31;
+        ChunkWalk walk(p, c.cuts);
+        ChunkPiece x;
+        uint32_t slot = 0;
+        for (int piece = 0; walk.next(p, x); ++piece) {
+            const ChunkTiles tiles(p, x.s, x.rt);
+            for (int t = x.t0; t < x.t1; ++t) {
+                const int k0 = tiles.key(t);
+                const bool plain = tiles.plain(p, k0);
+#pragma unroll 1
+                for (int kv = 0; kv < 2; ++kv, ++slot) {
+                    const int from = slot % Sh::kRaw, to = slot % Sh::kRing;
+                    if (!wait(p, c.raw_full + 8 * from, (slot / Sh::kRaw) & 1)) return;
+                    if (!wait(p, c.kv_empty + 8 * to, ((slot / Sh::kRing) & 1) ^ 1)) return;
+                    const uint32_t src = c.base + Sh::kRawOff + from * Sh::kRawBytes, dst = ring(c, to);
+                    const bool clean = kv == 1 && !plain;
+                    uint32_t found = 0;
+                    constexpr int kPer = kTileKeys * kChunks / 128;    // chunks per thread
+#pragma unroll
+                    for (int i0 = 0; i0 < kPer; i0 += 4) {
+                        uint4 w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int u = (i0 + i) * 128 + tid, r = u / kChunks, ch = u % kChunks;
+                            const int sw = kChunks == 8 ? r & 7 : (r >> 1) & 3;    // the copy's swizzle
+                            w[i] = lds128(src + r * Sh::kRawRow + ((ch ^ sw) << 4));
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int u = (i0 + i) * 128 + tid, r = u / kChunks, ch = u % kChunks;
+                            uint32_t in[4] = {w[i].x, w[i].y, w[i].z, w[i].w}, o[8];
+                            if (clean) {
+                                const bool seen = tiles.wanted(p, k0 + r, 1);
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) {
+                                    const uint32_t bad = __vcmpeq4(in[j] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                                    if (seen) found |= bad;
+                                    in[j] = seen ? in[j] & ~bad : 0u;
+                                }
+                            }
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) e4m3x4_to_f16(in[j], o[2 * j], o[2 * j + 1]);
+                            const uint4 a = make_uint4(o[0], o[1], o[2], o[3]), b = make_uint4(o[4], o[5], o[6], o[7]);
+                            // lanes of the two slices write their halves in opposite order, which spreads the banks
+                            const bool second = kChunks == 8 && ch >= 4;
+                            sts128(tile_addr(dst, r, 2 * ch + (second ? 1 : 0)), second ? b : a);
+                            sts128(tile_addr(dst, r, 2 * ch + (second ? 0 : 1)), second ? a : b);
+                        }
+                    }
+                    if (found) c.dirty[piece & 3] = piece + 1;
+                    proxy_fence();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(c.raw_empty + 8 * from);
+                        mbar_arrive(c.kv_full + 8 * to);
+                    }
+                }
+            }
+        }
+    }
+
+    // ------------------------------------------------------------ products (one thread)
+    static __device__ void multiplier(const Ctx& c, const ChunkParams& p) {
+        multiply(c, p);
+        // nothing is in flight when the tensor memory is freed, after a wait that timed out neither
+        umma_commit(c.fin);
+        wait_lane(c.fin, 0, p.wait_limit_ns);
+    }
+
+    static __device__ __forceinline__ void multiply(const Ctx& c, const ChunkParams& p) {
+        const uint64_t q0 = umma_desc_sw128(c.base + Sh::kQOff, 16, 1024);
+        ChunkWalk walk(p, c.cuts);
+        ChunkPiece x;
+        uint32_t slot = 0, pieces = 0, tiles = 0;
+        auto ready = [&](uint32_t bar, uint32_t parity) {
+            const bool ok = wait_lane(bar, parity, p.wait_limit_ns);
+            if (!ok) flag_error(p.err, DA_DEVERR_TIMEOUT);
+            tmem_fence_after_sync();
+            return ok;
+        };
+        auto landed = [&](uint32_t i) { return ready(c.kv_full + 8 * (i % Sh::kRing), (i / Sh::kRing) & 1); };
+        auto scores = [&](int w, uint32_t i) {
+            const uint64_t kd = umma_desc_sw128(ring(c, i % Sh::kRing), 16, 1024), qd = q0 + ((w * Sh::kTileBytes) >> 4);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                const uint32_t off = ((k >> 2) * Sh::kSliceBytes + (k & 3) * 32) >> 4;
+                umma_ss(c.tmem + w * kTileKeys, qd + off, kd + off, kIdS, k > 0);
+            }
+            umma_commit(c.s_full + 8 * w);
+        };
+        auto weigh = [&](int w, uint32_t i, bool first) {
+            const uint64_t vd = umma_desc_sw128(ring(c, i % Sh::kRing), Sh::kSliceBytes, 1024);
+#pragma unroll
+            for (int k = 0; k < kTileKeys / 16; ++k)
+                umma_ts(c.tmem + Sh::kO + w * D, c.tmem + w * kTileKeys + k * 8, vd + ((k * 16 * 128) >> 4), kIdPV, !(first && k == 0));
+            umma_commit(c.pv_done + 8 * w);
+        };
+        while (walk.next(p, x)) {
+            // slots: K, V, K, V ...
+            if (!landed(slot)) return;
+            for (int w = 0; w < 2; ++w) {
+                if (!ready(c.q_full + 8 * w, pieces & 1)) return;
+                scores(w, slot);
+            }
+            umma_commit(c.kv_empty + 8 * (slot % Sh::kRing));
+            ++slot;
+            for (int t = x.t0; t < x.t1; ++t, ++tiles) {
+                const uint32_t v = slot++, k = v + 1;
+                const bool more = t + 1 < x.t1;
+                if (!landed(v)) return;
+                for (int w = 0; w < 2; ++w) {
+                    if (!ready(c.p_full + 8 * w, tiles & 1)) return;
+                    weigh(w, v, t == x.t0);
+                    if (w == 1) umma_commit(c.kv_empty + 8 * (v % Sh::kRing));
+                    if (more) {
+                        if (w == 0 && !landed(k)) return;
+                        scores(w, k);
+                        if (w == 1) umma_commit(c.kv_empty + 8 * (k % Sh::kRing));
+                    }
+                }
+                if (more) ++slot;
+            }
+            ++pieces;
+        }
+    }
+
+    // ------------------------------------------------------------ rows
+    // Rows of this warp's quarter of tile w into shared memory (32 rows; float32 factor per row to `factors` of e4m3 calls).
+    static __device__ __forceinline__ void load_queries(const Ctx& c, const ChunkParams& p, const ChunkPiece& x, int w, float& factor) {
+        const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3;
+        constexpr int kChunks = D / 8, kPerPass = 32 / kChunks, kPasses = 32 / kPerPass, kBatch = 8;
+        const uint32_t tile = c.base + Sh::kQOff + w * Sh::kTileBytes;
+        const int ch = lane % kChunks, sub = lane / kChunks;
+        const int rows = x.s.n * p.G, row0 = x.rt * kItemRows + w * kTileRows + quarter * 32;
+#pragma unroll 1
+        for (int i0 = 0; i0 < kPasses; i0 += kBatch) {
+            uint4 v[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int f = row0 + (i0 + i) * kPerPass + sub;
+                v[i] = make_uint4(0, 0, 0, 0);
+                if (f < rows) {
+                    const int t = f / p.G, g = f - t * p.G;
+                    v[i] = __ldg(reinterpret_cast<const uint4*>(p.q + (x.s.r0 + t) * p.q_stride + (static_cast<int64_t>(x.kvh) * p.G + g) * D) + ch);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int r = (i0 + i) * kPerPass + sub;
+                uint32_t e[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) e[j] = (e[j] & p.q_and) ^ p.q_xor;
+                if constexpr (KV8 && DT == DA_BF16) {
+                    uint32_t top = 0;   // largest exponent field of the row
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) top = max(top, max((e[j] >> 7) & 0xffu, (e[j] >> 23) & 0xffu));
+#pragma unroll
+                    for (int off = 1; off < kChunks; off <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
+                    // 2^e takes the largest element to [2^14, 2^15); an infinity or a NaN stays one
+                    const int field = top == 255 ? 127 : min(max(268 - static_cast<int>(top), 14), 240);
+                    const float up = __uint_as_float(static_cast<uint32_t>(field) << 23);
+                    const float down = __uint_as_float(static_cast<uint32_t>(254 - field) << 23);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        e[j] = pack2<DA_F16>(__uint_as_float(e[j] << 16) * up, __uint_as_float(e[j] & 0xffff0000u) * up);
+#pragma unroll
+                    for (int s = 0; s < kPerPass; ++s) {
+                        const float y = __shfl_sync(0xffffffffu, down, s * kChunks);
+                        if (lane == (i0 + i) * kPerPass + s) factor = y;
+                    }
+                }
+                sts128(tile_addr(tile, quarter * 32 + r, ch), make_uint4(e[0], e[1], e[2], e[3]));
+            }
+        }
+    }
+
+    // A special tile's values, 16-bit pages (by the threads of row tile 0): zeros for what no row sees and for what is not finite.
+    static __device__ __forceinline__ bool clean_values(const ChunkParams& p, const ChunkTiles& tiles, int k0, uint32_t tile) {
+        constexpr int kChunks = D / 8;
+        constexpr uint32_t kExp = MT == DA_BF16 ? 0x7f807f80u : 0x7c007c00u;
+        bool found = false;
+#pragma unroll 4
+        for (int i = 0; i < kChunks; ++i) {
+            const int u = i * 128 + static_cast<int>(threadIdx.x & 127), r = u / kChunks, ch = u % kChunks;
+            const uint32_t at = tile_addr(tile, r, ch);
+            const uint4 v = lds128(at);
+            const uint32_t bad[4] = {__vcmpeq2(v.x & kExp, kExp), __vcmpeq2(v.y & kExp, kExp), __vcmpeq2(v.z & kExp, kExp),
+                                     __vcmpeq2(v.w & kExp, kExp)};
+            const bool seen = tiles.wanted(p, k0 + r, 1), any = (bad[0] | bad[1] | bad[2] | bad[3]) != 0;
+            if (!seen) sts128(at, make_uint4(0, 0, 0, 0));
+            else if (any) sts128(at, make_uint4(v.x & ~bad[0], v.y & ~bad[1], v.z & ~bad[2], v.w & ~bad[3]));
+            found = found || (seen && any);
+        }
+        proxy_fence();
+        return found;
+    }
+
+    // Adds to dims d0 .. d0 + 31 of a row what clean_values took out of the values that the row sees.
+    static __device__ __noinline__ void add_non_finite(const ChunkParams& p, const ChunkPiece& x, int pos, int d0, float* o) {
+        const ChunkTiles tiles(p, x.s, x.rt);
+        for (int t = x.t0; t < x.t1; ++t) {
+            const int k0 = tiles.key(t);
+            if (tiles.plain(p, k0)) continue;
+            for (int k = k0; k <= min(k0 + kTileKeys - 1, pos); ++k) {
+                if (p.window && k <= pos - p.window && k >= p.sinks) continue;
+                const int page = ld_cg_s32(p.table + static_cast<int64_t>(x.b) * p.table_stride + k / p.P);
+                if (page < 0 || page >= p.num_pages) continue;
+                const int64_t at = page_row(p.layout, page, k % p.P, x.kvh, p.P, p.Hkv) * D + d0;
+                for (int d = 0; d < 32; ++d) {
+                    float v;
+                    if constexpr (KV8) v = (p.v[at + d] & 0x7f) == 0x7f ? NAN : 0.f;
+                    else v = bits_to_f32<DT>(reinterpret_cast<const uint16_t*>(p.v)[at + d]);
+                    if (!isfinite(v)) o[d] += v;
+                }
+            }
+        }
+    }
+
+    static __device__ void rows(const Ctx& c, const ChunkParams& p, int w) {
+        const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, r = quarter * 32 + lane;
+        const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+        const uint32_t ts = c.tmem + lanes + w * kTileKeys, to = c.tmem + lanes + Sh::kO + w * D;
+        ChunkWalk walk(p, c.cuts);
+        ChunkPiece x;
+        uint32_t count = 0;            // key tiles so far
+        for (int piece = 0; walk.next(p, x); ++piece) {
+            const ChunkTiles tiles(p, x.s, x.rt);
+            float factor = 1.f;
+            load_queries(c, p, x, w, factor);
+            proxy_fence();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(c.q_full + 8 * w);
+            factor *= p.scale_log2;
+            const int f = x.rt * kItemRows + w * kTileRows + r, token = f / p.G;
+            const bool live = f < x.s.n * p.G;
+            const int pos = live ? x.s.L - x.s.n + token : -1;
+            // references: scores' maximum m (16-bit pages: less kLift), and (8-bit pages) dv, how far the weights' is above it
+            float m = kNoKey, dv = 0.f, l = 0.f;
+            for (int t = x.t0; t < x.t1; ++t, ++count) {
+                const int k0 = tiles.key(t);
+                const bool plain = tiles.plain(p, k0), first = t == x.t0;
+                if (!wait(p, c.s_full + 8 * w, count & 1)) return;
+                tmem_fence_after_sync();
+                float s[kTileKeys];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) tmem_ld32_start(ts + 32 * i, s + 32 * i);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) hold32(s + 32 * i);
+                const float2* sc = reinterpret_cast<const float2*>(c.smem + Sh::kScaleOff) + (count % kScaleRing) * 8;
+                if constexpr (KV8) {
+                    if (!wait(p, c.sc_full + 8 * (count % kScaleRing), (count / kScaleRing) & 1)) return;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float by = factor * sc[i].x;
+                        const uint64_t by2 = pair(by, by);
+#pragma unroll
+                        for (int j = 0; j < 16; j += 2) {
+                            const uint64_t y = mul2(pair(s[16 * i + j], s[16 * i + j + 1]), by2);
+                            unpair(y, s[16 * i + j], s[16 * i + j + 1]);
+                        }
+                    }
+                }
+                if (!plain) {
+                    const int hi = pos - k0;
+                    if (p.window == 0) {
+#pragma unroll
+                        for (int i = 0; i < kTileKeys; ++i) s[i] = i <= hi ? s[i] : -INFINITY;
+                    } else {
+                        const int low = max(pos, 0) - p.window + 1 - k0, sink = p.sinks - k0;
+#pragma unroll
+                        for (int i = 0; i < kTileKeys; ++i) s[i] = i <= hi && (i >= low || i < sink) ? s[i] : -INFINITY;
+                    }
+                }
+                // maxima of 16 keys, the size of the smallest page
+                float top[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    float a = fmaxf(s[16 * i], s[16 * i + 1]), b = fmaxf(s[16 * i + 2], s[16 * i + 3]);
+#pragma unroll
+                    for (int j = 4; j < 16; j += 4) {
+                        a = fmaxf(a, fmaxf(s[16 * i + j], s[16 * i + j + 1]));
+                        b = fmaxf(b, fmaxf(s[16 * i + j + 2], s[16 * i + j + 3]));
+                    }
+                    top[i] = fmaxf(a, b);
+                }
+                float best = top[0];
+#pragma unroll
+                for (int i = 1; i < 8; ++i) best = fmaxf(best, top[i]);
+                bool move;
+                if constexpr (KV8) {
+                    move = best - m > kHeadroom;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) move = move || (top[i] - m) + (sc[i].y - dv) > kHeadroom + kLift;
+                } else {
+                    best *= factor;
+                    move = best - m > kHeadroom + kLift;
+                }
+                if (first || __any_sync(0xffffffffu, move)) {
+                    float al = 1.f, av = 1.f;     // factors of the sum and of the accumulator
+                    if (first || move) {
+                        if constexpr (KV8) {
+                            const float mn = fmaxf(m, best);
+                            float dn = first ? kNoKey : (m - mn) + dv;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) dn = fmaxf(dn, (top[i] - mn) + (sc[i].y - kLift));
+                            al = fast_exp2(m - mn);
+                            av = fast_exp2((m - mn) + (dv - dn));
+                            m = mn;
+                            dv = dn;
+                        } else {
+                            const float mn = fmaxf(m, best - kLift);
+                            al = av = fast_exp2(m - mn);
+                            m = mn;
+                        }
+                    }
+                    if (!first) {
+                        l *= al;
+                        // the accumulator: its last product is done, the next one waits for this tile's weights
+                        if (!wait(p, c.pv_done + 8 * w, (count - 1) & 1)) return;
+                        tmem_fence_after_sync();
+#pragma unroll 1
+                        for (int d = 0; d < D; d += 32) {
+                            float o[32];
+                            tmem_ld32_start(to + d, o);
+                            tmem_ld_wait();
+                            hold32(o);
+                            uint32_t x0[16], x1[16];
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                x0[j] = __float_as_uint(o[j] * av);
+                                x1[j] = __float_as_uint(o[j + 16] * av);
+                            }
+                            tmem_st16_start(to + d, x0);
+                            tmem_st16_start(to + d + 16, x1);
+                        }
+                    }
+                }
+                if constexpr (!KV8) {
+                    if (w == 0 && !plain) {
+                        const uint32_t v = 2 * count + 1;
+                        if (!wait(p, c.kv_full + 8 * (v % Sh::kRing), (v / Sh::kRing) & 1)) return;
+                        if (clean_values(p, tiles, k0, ring(c, v % Sh::kRing))) c.dirty[piece & 3] = piece + 1;
+                    }
+                }
+                uint64_t sum0 = 0, sum1 = 0;
+                float lift = 1.f;
+                const uint64_t by2 = pair(factor, factor), m2 = pair(-m, -m);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t o[16];
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        const int k = 32 * i + j;
+                        const uint64_t y = KV8 ? add2(pair(s[k], s[k + 1]), m2) : fma2(pair(s[k], s[k + 1]), by2, m2);
+                        float a, b;
+                        unpair(y, a, b);
+                        a = fast_exp2(a);
+                        b = fast_exp2(b);
+                        uint64_t e = pair(a, b);
+                        if (j & 2) sum1 = add2(sum1, e);
+                        else sum0 = add2(sum0, e);
+                        if constexpr (KV8) {
+                            if (j % 16 == 0) lift = fast_exp2(fminf(sc[k / 16].y - dv, 127.f));
+                            e = mul2(e, pair(lift, lift));
+                            unpair(e, a, b);
+                        }
+                        o[j / 2] = pack2<MT>(a, b);
+                    }
+                    tmem_st16_start(ts + 16 * i, o);
+                }
+                float a, b;
+                unpair(add2(sum0, sum1), a, b);
+                l += a + b;
+                tmem_st_wait();
+                tmem_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(c.p_full + 8 * w);
+                    if constexpr (KV8) mbar_arrive(c.sc_empty + 8 * (count % kScaleRing));
+                }
+            }
+            // ---- the piece's end
+            if (!wait(p, c.pv_done + 8 * w, (count - 1) & 1)) return;
+            tmem_fence_after_sync();
+            const bool whole = x.t0 == 0 && x.t1 == x.nt, dirty = c.dirty[piece & 3] == piece + 1;
+            const bool none = m == kNoKey && l == 0.f;
+            const float by = whole ? (none ? 0.f : 1.f / l) : 1.f;
+            const int64_t row = x.s.r0 + token, head = static_cast<int64_t>(x.kvh) * p.G + (f - token * p.G);
+            const int slot = 2 * static_cast<int>(blockIdx.x) + (x.t0 == 0 ? 1 : 0);
+            const float half = KV8 ? fast_exp2(0.5f * dv) : 1.f;   // 2^dv in two steps, which stay normal floats for every scale
+#pragma unroll 1
+            for (int d = 0; d < D; d += 32) {
+                float o[32];
+                tmem_ld32_start(to + d, o);
+                tmem_ld_wait();
+                hold32(o);
+                if (dirty && live) add_non_finite(p, x, pos, d, o);
+                if constexpr (KV8) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) o[j] = o[j] * half * half;
+                }
+                if (whole) {
+                    if (live) {
+                        uint4* out = reinterpret_cast<uint4*>(p.out + row * p.out_stride + head * D + d);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            out[j] = make_uint4(pack2<DT>(o[8 * j] * by, o[8 * j + 1] * by), pack2<DT>(o[8 * j + 2] * by, o[8 * j + 3] * by),
+                                                pack2<DT>(o[8 * j + 4] * by, o[8 * j + 5] * by), pack2<DT>(o[8 * j + 6] * by, o[8 * j + 7] * by));
+                    }
+                } else {
+                    float4* out = p.part + (static_cast<int64_t>(slot) * (D / 4) + d / 4) * kItemRows + w * kTileRows + r;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        out[j * kItemRows] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                }
+            }
+            if (!whole) p.part_sum[static_cast<int64_t>(slot) * kItemRows + w * kTileRows + r] = make_float2(m, l);
+            else if (p.lse != nullptr && live) p.lse[row * p.Hq + head] = none ? -INFINITY : (m + fast_log2(l)) * kLn2;
+            tmem_fence_before_sync();
+        }
+    }
+};
+
+template <int D, int DT, bool KV8>
+__global__ void __launch_bounds__(ChunkShape<D, KV8>::kThreads, 1)
+chunk_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const ChunkParams p) {
+    using K = ChunkKernel<D, DT, KV8>;
+    using Sh = typename K::Sh;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ ChunkPlan plan;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int dirty[4];
+    typename K::Ctx c;
+    c.smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    c.base = smem_addr(c.smem);
+    uint32_t bar = c.base + Sh::kBarOff;
+    auto bars = [&](int n) {
+        const uint32_t at = bar;
+        bar += 8 * n;
+        return at;
+    };
+    c.kv_full = bars(Sh::kRing);
+    c.kv_empty = bars(Sh::kRing);
+    c.raw_full = bars(Sh::kRaw);
+    c.raw_empty = bars(Sh::kRaw);
+    c.sc_full = bars(kScaleRing);
+    c.sc_empty = bars(kScaleRing);
+    c.q_full = bars(2);
+    c.s_full = bars(2);
+    c.p_full = bars(2);
+    c.pv_done = bars(2);
+    c.fin = bars(1);
+    c.cuts = plan.cuts;
+    c.dirty = dirty;
+    const int warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < Sh::kRing; ++i) {
+            mbar_init(c.kv_full + 8 * i, KV8 ? 4 : 1);
+            mbar_init(c.kv_empty + 8 * i, 1);
+        }
+        for (int i = 0; i < Sh::kRaw; ++i) {
+            mbar_init(c.raw_full + 8 * i, 1);
+            mbar_init(c.raw_empty + 8 * i, 4);
+        }
+        for (int i = 0; i < kScaleRing; ++i) {
+            mbar_init(c.sc_full + 8 * i, 1);
+            mbar_init(c.sc_empty + 8 * i, 8);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(c.q_full + 8 * i, 4);
+            mbar_init(c.s_full + 8 * i, 1);
+            mbar_init(c.p_full + 8 * i, 4);
+            mbar_init(c.pv_done + 8 * i, 1);
+        }
+        mbar_init(c.fin, 1);
+        for (int i = 0; i < 4; ++i) dirty[i] = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        prefetch_tensormap(&tmK);
+        prefetch_tensormap(&tmV);
+    }
+    if (warp == 9) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_slot)), "r"(Sh::kCols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    // From here on this grid touches global memory: wait for the previous kernel.
+    grid_dependency_wait();
+    if (threadIdx.x == 0) grid_dependents_launch();
+    chunk_plan<Sh::kThreads>(p, c.smem + Sh::kRingOff, plan);
+    proxy_fence();                 // the plan's memory is the ring from here on
+    tmem_fence_before_sync();
+    __syncthreads();
+    tmem_fence_after_sync();
+    c.tmem = tmem_slot;
+    if constexpr (KV8) {
+        // of the launch's 512 x 128 registers the rows' threads take 192 each, the others 64
+        if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    }
+    if (warp < 8) K::rows(c, p, warp >> 2);
+    else if (warp == 8) K::producer(c, p, &tmK, &tmV);
+    else if (warp == 9) {
+        if ((threadIdx.x & 31) == 0) K::multiplier(c, p);
+        __syncwarp();
+    }
+    if constexpr (KV8) {
+        if (warp >= 12) K::converter(c, p);
+    }
+    tmem_fence_before_sync();
+    __syncthreads();
+    if (warp == 9) {
+        tmem_fence_after_sync();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(c.tmem), "r"(Sh::kCols));
+    }
+}
+
+// Joins the parts of the split items: block (range, slice) 32 rows of the item whose first part that range holds, a
+// thread 16 dims of a row.
+template <int D, int DT>
+__global__ void __launch_bounds__(32 * D / 16) chunk_join_kernel(const ChunkParams p) {
+    grid_dependency_wait();
+    if (threadIdx.x == 0) grid_dependents_launch();
+    const int range = blockIdx.x / kJoinSlices, slice = blockIdx.x % kJoinSlices;
+    const ChunkJoin join = p.join[range];
+    const int r = slice * 32 + (threadIdx.x & 31), f = join.rt * kItemRows + r, d = threadIdx.x / 32 * 16;
+    if (join.parts == 0 || f >= join.n * p.G) return;
+    auto slot = [&](int j) { return static_cast<int64_t>(j == 0 ? 2 * range + 1 : 2 * (range + j)); };
+    float m = kNoKey;
+    for (int j = 0; j < join.parts; ++j) m = fmaxf(m, __ldcg(p.part_sum + slot(j) * kItemRows + r).x);
+    float l = 0.f, o[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i] = 0.f;
+    for (int j = 0; j < join.parts; ++j) {
+        const float2 sum = __ldcg(p.part_sum + slot(j) * kItemRows + r);
+        const float w = fast_exp2(sum.x - m);
+        l = fmaf(w, sum.y, l);
+        const float4* part = p.part + (slot(j) * (D / 4) + d / 4) * kItemRows + r;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4 x = __ldcg(part + i * kItemRows);
+            o[4 * i] = fmaf(w, x.x, o[4 * i]);
+            o[4 * i + 1] = fmaf(w, x.y, o[4 * i + 1]);
+            o[4 * i + 2] = fmaf(w, x.z, o[4 * i + 2]);
+            o[4 * i + 3] = fmaf(w, x.w, o[4 * i + 3]);
+        }
+    }
+    const bool none = m == kNoKey && l == 0.f;
+    const float by = none ? 0.f : 1.f / l;
+    const int token = f / p.G;
+    const int64_t row = join.r0 + token, head = static_cast<int64_t>(join.kvh) * p.G + (f - token * p.G);
+    uint4* out = reinterpret_cast<uint4*>(p.out + row * p.out_stride + head * D + d);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        out[j] = make_uint4(pack2<DT>(o[8 * j] * by, o[8 * j + 1] * by), pack2<DT>(o[8 * j + 2] * by, o[8 * j + 3] * by),
+                            pack2<DT>(o[8 * j + 4] * by, o[8 * j + 5] * by), pack2<DT>(o[8 * j + 6] * by, o[8 * j + 7] * by));
+    if (p.lse != nullptr && d == 0) p.lse[row * p.Hq + head] = none ? -INFINITY : (m + fast_log2(l)) * kLn2;
+}
+
+template <int D, int DT, bool KV8>
+da_status launch_chunk(const da_paged_cache& c, ChunkParams& p, cudaStream_t stream) {
+    using Sh = ChunkShape<D, KV8>;
+    constexpr int kInner = KV8 ? D : 64;
+    p.box_keys = gcd_of(c.page_size, kTileKeys);
+    CUtensorMap mk, mv;
+    if (!make_page_map(&mk, c.k, c, kInner, p.box_keys) || !make_page_map(&mv, c.v, c, kInner, p.box_keys)) return DA_ERR_CUDA;
+    auto kern = chunk_kernel<D, DT, KV8>;
+    static DeviceCache cache;
+    int resident = 0;
+    if (persistent_grid(kern, Sh::kThreads, Sh::kSmemBytes, cache, &resident) != cudaSuccess) return DA_ERR_CUDA;
+    const int grid = std::min(std::min(resident, device_sms()), kMaxRanges);
     cudaLaunchAttribute attrs[1] = {pdl_attr()};
     cudaLaunchConfig_t cfg = {};
-    const int64_t rows = static_cast<int64_t>(p.T) * p.Hq;
-    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(152 * 8, (rows + kRowWarps - 1) / kRowWarps)));
-    cfg.blockDim = dim3(kRowWarps * 32);
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(Sh::kThreads);
+    cfg.dynamicSmemBytes = Sh::kSmemBytes;
     cfg.stream = stream;
     cfg.attrs = attrs;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, chunk_row_kernel<D, DT, KV8>, p) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, kern, mk, mv, p) != cudaSuccess) return DA_ERR_CUDA;
+    cfg.gridDim = dim3(grid * kJoinSlices);
+    cfg.blockDim = dim3(32 * D / 16);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, chunk_join_kernel<D, DT>, p) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
 }
 
 template <int D, int DT>
-da_status launch_chunk_any(const ChunkParams& p, bool kv8, cudaStream_t s) {
-    return kv8 ? launch_chunk<D, DT, true>(p, s) : launch_chunk<D, DT, false>(p, s);
+da_status launch_chunk_any(const da_paged_cache& c, ChunkParams& p, cudaStream_t s) {
+    return c.kv_dtype == DA_E4M3 ? launch_chunk<D, DT, true>(c, p, s) : launch_chunk<D, DT, false>(c, p, s);
 }
 
 }  // namespace da_impl
@@ -123,7 +1106,8 @@ extern "C" {
 
 size_t decode_attn_paged_chunk_workspace_size(int Hq, int Hkv, int D) {
     if (Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || (D != 64 && D != 128)) return 0;
-    return kPagedHeadBytes;
+    return kPagedHeadBytes + round_up(kMaxRanges * sizeof(ChunkJoin), 256) +
+           static_cast<size_t>(2 * kMaxRanges) * kItemRows * (sizeof(float2) + D * sizeof(float));
 }
 
 da_status decode_attn_paged_chunk(const da_paged_chunk* args, void* stream) {
@@ -138,15 +1122,15 @@ da_status decode_attn_paged_chunk(const da_paged_chunk* args, void* stream) {
     const int64_t row = static_cast<int64_t>(a.Hq) * c.D;
     if (a.q_stride < row || a.out_stride < row) return DA_ERR_INVALID_ARG;
     if (a.q_stride % 8 || a.out_stride % 8) return DA_ERR_ALIGNMENT;
-    // rows of the accumulators' tiles, one per (token, head of a group)
+    // rows of the items are numbered in 32 bits
     if (static_cast<int64_t>(a.T_new) * (a.Hq / c.Hkv) > 0x3fffffffll) return DA_ERR_INVALID_ARG;
     if (!aligned(a.q, 16) || !aligned(a.out, 16) || !aligned(a.lse, 4)) return DA_ERR_ALIGNMENT;
     if (a.workspace_bytes < decode_attn_paged_chunk_workspace_size(a.Hq, c.Hkv, c.D)) return DA_ERR_WORKSPACE_TOO_SMALL;
     if (a.T_new == 0) return DA_OK;
     if (!a.q || !a.out) return DA_ERR_INVALID_ARG;
     ChunkParams p;
+    uint8_t* ws = static_cast<uint8_t*>(a.workspace);
     p.q = static_cast<const uint16_t*>(a.q);
-    p.k = static_cast<const uint8_t*>(c.k);
     p.v = static_cast<const uint8_t*>(c.v);
     p.ks = c.k_scale;
     p.vs = c.v_scale;
@@ -155,7 +1139,10 @@ da_status decode_attn_paged_chunk(const da_paged_chunk* args, void* stream) {
     p.table = a.block_table;
     p.out = static_cast<uint16_t*>(a.out);
     p.lse = a.lse;
-    p.err = static_cast<uint32_t*>(a.workspace);
+    p.err = reinterpret_cast<uint32_t*>(ws);
+    p.join = reinterpret_cast<ChunkJoin*>(ws + kPagedHeadBytes);
+    p.part = reinterpret_cast<float4*>(ws + kPagedHeadBytes + round_up(kMaxRanges * sizeof(ChunkJoin), 256));
+    p.part_sum = reinterpret_cast<float2*>(p.part + static_cast<size_t>(2 * kMaxRanges) * kItemRows * (c.D / 4));
     p.q_stride = a.q_stride;
     p.out_stride = a.out_stride;
     p.B = a.B;
@@ -168,13 +1155,17 @@ da_status decode_attn_paged_chunk(const da_paged_chunk* args, void* stream) {
     p.table_stride = a.table_stride;
     p.num_pages = c.num_pages;
     p.layout = c.layout;
-    p.window = a.window;
+    p.window = std::min(a.window, 0x7fffff00);   // (no sequence is longer; the kernel subtracts it)
     p.sinks = a.sinks;
-    p.scale = a.scale;
-    const bool kv8 = c.kv_dtype == DA_E4M3;
+    p.scale_log2 = std::fabs(a.scale) * kLog2e;
+    const bool zero = p.scale_log2 == 0.f;       // (a factor of 0 would make NaN of the scores taken out)
+    if (zero) p.scale_log2 = 1.f;
+    p.q_and = zero ? 0u : 0xffffffffu;
+    p.q_xor = !zero && a.scale < 0.f ? 0x80008000u : 0u;
+    p.wait_limit_ns = kWaitLimitNs;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (c.D == 128) return a.dtype == DA_F16 ? launch_chunk_any<128, DA_F16>(p, kv8, s) : launch_chunk_any<128, DA_BF16>(p, kv8, s);
-    return a.dtype == DA_F16 ? launch_chunk_any<64, DA_F16>(p, kv8, s) : launch_chunk_any<64, DA_BF16>(p, kv8, s);
+    if (c.D == 128) return a.dtype == DA_F16 ? launch_chunk_any<128, DA_F16>(c, p, s) : launch_chunk_any<128, DA_BF16>(c, p, s);
+    return a.dtype == DA_F16 ? launch_chunk_any<64, DA_F16>(c, p, s) : launch_chunk_any<64, DA_BF16>(c, p, s);
 }
 
 }  // extern "C"
