@@ -41,11 +41,15 @@ constexpr int kItemCost = 2;          // an item's begin and end, in key tiles
 constexpr int kLeastCost = 6;         // of a range
 constexpr int kLeastPart = 2;         // key tiles of a partial result at least
 constexpr int kScaleRing = 4;         // tiles whose scales are in shared memory
+constexpr int kPieceRing = 4;         // pieces whose description is
 constexpr int kJoinSlices = 8;        // blocks that join one split item, 32 rows each
 
 template <int D, bool KV8>
 struct ChunkShape {
-    static constexpr int kThreads = KV8 ? 512 : 320;
+    // warps: 0 - 7 rows, 8 copies, 9 products, 12 - 15 conversion. The rows' threads take most of the launch's registers.
+    static constexpr int kThreads = KV8 ? 512 : 384;
+    static constexpr int kRowRegs = KV8 ? 192 : 208, kOtherRegs = KV8 ? 64 : 88;
+    static_assert(256 * kRowRegs + (kThreads - 256) * kOtherRegs <= kThreads * (65536 / kThreads / 8 * 8), "registers of the launch");
     static constexpr int kSlices = D / 64;                     // 128-byte columns of a tile in 16 bits
     static constexpr int kSliceBytes = 128 * 128;
     static constexpr int kTileBytes = kSlices * kSliceBytes;
@@ -58,7 +62,8 @@ struct ChunkShape {
     static constexpr int kRawOff = kRingOff + kRing * kTileBytes;
     static constexpr int kScaleOff = kRawOff + kRaw * kRawBytes;          // [tile][16-key box] {ks, log2 vs}
     static constexpr int kBarOff = kScaleOff + (KV8 ? kScaleRing * 8 * 8 : 0);
-    static constexpr int kNumBars = 2 * kRing + 2 * kRaw + 2 * kScaleRing + 9;
+    static constexpr int kNumBars = 2 * kRing + 2 * kRaw + 2 * kScaleRing + 2 * kPieceRing + 9;
+    static constexpr int kPieceReaders = 9 + (KV8 ? 4 : 0);               // warps
     static constexpr int kSmemBytes = 1024 + kBarOff + kNumBars * 8;
     static constexpr int kPlanBytes = (DA_MAX_PAGED_BATCH + 1) * 8 + DA_MAX_PAGED_BATCH * 12;
     static_assert(kPlanBytes <= kRing * kTileBytes, "the plan is made where the ring is later");
@@ -117,9 +122,11 @@ __device__ __forceinline__ ChunkSeq chunk_seq(const ChunkParams& p, int b, bool 
 
 // The key tiles of an item: 0 .. ns - 1 (first tokens), then lo on, nt in all (one, all of it hidden, if no row sees a key).
 struct ChunkTiles {
+    ChunkTiles() = default;
     int first, last;         // positions of its first and last token (may be < 0)
     int low;                 // the first key that the first token sees through the window
     int ns, lo, nt;
+    int from, to;            // tiles of which every row sees every key (besides those of the first tokens)
 
     __device__ __forceinline__ ChunkTiles(const ChunkParams& p, const ChunkSeq& s, int rt) {
         const int f = rt * kItemRows;
@@ -129,13 +136,14 @@ struct ChunkTiles {
         ns = (min(p.sinks, low) + kTileKeys - 1) / kTileKeys;
         lo = max(ns, low / kTileKeys);
         nt = ns + max(last, 0) / kTileKeys - lo + 1;
+        // tiles from lo on that end at or before the first token, and begin in the last token's window
+        to = ns + max((first + 1) / kTileKeys - lo, 0);
+        from = ns;
+        if (p.window) from += max((max(0, last - p.window + 1) + kTileKeys - 1) / kTileKeys - lo, 0);
     }
     __device__ __forceinline__ int key(int tile) const { return (tile < ns ? tile : lo + tile - ns) * kTileKeys; }
-    // whether every row sees every key of the tile at key k0
-    __device__ __forceinline__ bool plain(const ChunkParams& p, int k0) const {
-        const int end = k0 + kTileKeys - 1;
-        return first >= end && (p.window == 0 || last - k0 < p.window || end < p.sinks);
-    }
+    // (k0 + 127 <= first, and last - k0 < window)
+    __device__ __forceinline__ bool plain(int tile) const { return tile >= from && tile < to; }
     // whether some row sees a key in [k, k + keys), or the key k
     __device__ __forceinline__ bool wanted(const ChunkParams& p, int k, int keys) const {
         return k <= last && (k + keys > low || k < p.sinks);
@@ -150,10 +158,13 @@ __device__ __forceinline__ int cut_tile(int x, int nt) {
     return tile < kLeastPart ? 0 : nt - tile < kLeastPart ? nt : tile;
 }
 
-// The pieces of a range, one after the other.
+// A piece: key tiles t0 .. t1 - 1 of an item. The warp that copies tiles walks through the range and leaves the pieces'
+// descriptions in shared memory, where the others read them when they need them: their registers are the rows'.
 struct ChunkPiece {
+    int valid, b, kvh, rt, t0, t1;
     ChunkSeq s;
-    int b, kvh, rt, t0, t1, nt;
+    ChunkTiles tiles;
+    int dirty;               // special tiles had values that are not finite
 };
 
 struct ChunkWalk {
@@ -164,13 +175,15 @@ struct ChunkWalk {
     }
     __device__ __forceinline__ bool next(const ChunkParams& p, ChunkPiece& x) {
         if (at.b >= p.B || (at.b == end.b && at.kvh == end.kvh && at.rt == end.rt && at.tile >= end.tile)) return false;
-        const ChunkTiles tiles(p, s, at.rt);
+        x.tiles = ChunkTiles(p, s, at.rt);
         x.s = s;
         x.b = at.b;
         x.kvh = at.kvh;
         x.rt = at.rt;
         x.t0 = at.tile;
-        x.nt = x.t1 = tiles.nt;
+        x.t1 = x.tiles.nt;
+        x.valid = 1;
+        x.dirty = 0;
         if (at.b == end.b && at.kvh == end.kvh && at.rt == end.rt) {
             x.t1 = end.tile;
             at.tile = end.tile;
@@ -394,9 +407,9 @@ struct ChunkKernel {
     struct Ctx {
         uint8_t* smem;
         uint32_t base, tmem;
-        uint32_t kv_full, kv_empty, raw_full, raw_empty, sc_full, sc_empty, q_full, s_full, p_full, pv_done, fin;
+        uint32_t kv_full, kv_empty, raw_full, raw_empty, sc_full, sc_empty, x_full, x_empty, q_full, s_full, p_full, pv_done, fin;
         const ChunkCut* cuts;
-        volatile int* dirty;     // [piece & 3]: number + 1 of the last such piece that had values that are not finite
+        ChunkPiece* pieces;
     };
 
     static __device__ __forceinline__ uint32_t ring(const Ctx& c, int i) { return c.base + Sh::kRingOff + i * Sh::kTileBytes; }
@@ -408,6 +421,17 @@ struct ChunkKernel {
         const bool ok = wait_warp(bar, parity, p.wait_limit_ns);
         if (!ok && (threadIdx.x & 31) == 0) flag_error(p.err, DA_DEVERR_TIMEOUT);
         return ok;
+    }
+
+    // Piece number i, or nullptr after the last one (or a wait that timed out); it is given back with drop_piece.
+    static __device__ __forceinline__ ChunkPiece* take_piece(const Ctx& c, const ChunkParams& p, uint32_t i) {
+        const bool ok = wait_lane(c.x_full + 8 * (i % kPieceRing), (i / kPieceRing) & 1, p.wait_limit_ns);
+        if (!ok) flag_error(p.err, DA_DEVERR_TIMEOUT);
+        ChunkPiece* x = c.pieces + i % kPieceRing;
+        return ok && x->valid ? x : nullptr;
+    }
+    static __device__ __forceinline__ void drop_piece(const Ctx& c, uint32_t i) {   // (one lane of a warp)
+        mbar_arrive(c.x_empty + 8 * (i % kPieceRing));
     }
 
     // ------------------------------------------------------------ copies
@@ -431,10 +455,20 @@ struct ChunkKernel {
         const int boxes = kTileKeys / p.box_keys, batch = 32 / boxes;       // tiles whose boxes the lanes look up at once
         const int my_tile = lane / boxes, my_box = lane - my_tile * boxes;
         ChunkWalk walk(p, c.cuts);
-        ChunkPiece x;
         uint32_t count = 0;                // key tiles so far
-        while (walk.next(p, x)) {
-            const ChunkTiles tiles(p, x.s, x.rt);
+        for (uint32_t piece = 0;; ++piece) {
+            ChunkPiece x;
+            x.valid = 0;
+            walk.next(p, x);
+            const int place = piece % kPieceRing;
+            if (!wait(p, c.x_empty + 8 * place, ((piece / kPieceRing) & 1) ^ 1)) return false;
+            if (lane == 0) {
+                c.pieces[place] = x;
+                mbar_arrive(c.x_full + 8 * place);
+            }
+            __syncwarp();
+            if (!x.valid) break;
+            const ChunkTiles& tiles = x.tiles;
             const int32_t* row = p.table + static_cast<int64_t>(x.b) * p.table_stride;
             auto entry = [&](int t) {      // block-table entry of this lane's box of tile t + my_tile, or -1
                 t += my_tile;
@@ -509,14 +543,14 @@ struct ChunkKernel {
     static __device__ void converter(const Ctx& c, const ChunkParams& p) {
         constexpr int kChunks = D / 16;                        // 16-byte chunks of a raw row
         const int tid = threadIdx.x & 127, lane = threadIdx.x & 31;
-        ChunkWalk walk(p, c.cuts);
-        ChunkPiece x;
         uint32_t slot = 0;
-        for (int piece = 0; walk.next(p, x); ++piece) {
-            const ChunkTiles tiles(p, x.s, x.rt);
-            for (int t = x.t0; t < x.t1; ++t) {
+        for (uint32_t piece = 0;; ++piece) {
+            ChunkPiece* x = take_piece(c, p, piece);
+            if (!x) break;
+            const ChunkTiles& tiles = x->tiles;
+            for (int t = x->t0, t1 = x->t1; t < t1; ++t) {
                 const int k0 = tiles.key(t);
-                const bool plain = tiles.plain(p, k0);
+                const bool plain = tiles.plain(t);
 #pragma unroll 1
                 for (int kv = 0; kv < 2; ++kv, ++slot) {
                     const int from = slot % Sh::kRaw, to = slot % Sh::kRing;
@@ -557,7 +591,7 @@ struct ChunkKernel {
                             sts128(tile_addr(dst, r, 2 * ch + (second ? 0 : 1)), second ? a : b);
                         }
                     }
-                    if (found) c.dirty[piece & 3] = piece + 1;
+                    if (found) x->dirty = 1;
                     proxy_fence();
                     __syncwarp();
                     if (lane == 0) {
@@ -566,6 +600,8 @@ struct ChunkKernel {
                     }
                 }
             }
+            __syncwarp();
+            if (lane == 0) drop_piece(c, piece);
         }
     }
 
@@ -579,9 +615,7 @@ struct ChunkKernel {
 
     static __device__ __forceinline__ void multiply(const Ctx& c, const ChunkParams& p) {
         const uint64_t q0 = umma_desc_sw128(c.base + Sh::kQOff, 16, 1024);
-        ChunkWalk walk(p, c.cuts);
-        ChunkPiece x;
-        uint32_t slot = 0, pieces = 0, tiles = 0;
+        uint32_t slot = 0, tiles = 0;
         auto ready = [&](uint32_t bar, uint32_t parity) {
             const bool ok = wait_lane(bar, parity, p.wait_limit_ns);
             if (!ok) flag_error(p.err, DA_DEVERR_TIMEOUT);
@@ -605,22 +639,26 @@ struct ChunkKernel {
                 umma_ts(c.tmem + Sh::kO + w * D, c.tmem + w * kTileKeys + k * 8, vd + ((k * 16 * 128) >> 4), kIdPV, !(first && k == 0));
             umma_commit(c.pv_done + 8 * w);
         };
-        while (walk.next(p, x)) {
+        for (uint32_t piece = 0;; ++piece) {
+            const ChunkPiece* x = take_piece(c, p, piece);
+            if (!x) return;
+            const int t0 = x->t0, t1 = x->t1;
+            drop_piece(c, piece);
             // slots: K, V, K, V ...
             if (!landed(slot)) return;
             for (int w = 0; w < 2; ++w) {
-                if (!ready(c.q_full + 8 * w, pieces & 1)) return;
+                if (!ready(c.q_full + 8 * w, piece & 1)) return;
                 scores(w, slot);
             }
             umma_commit(c.kv_empty + 8 * (slot % Sh::kRing));
             ++slot;
-            for (int t = x.t0; t < x.t1; ++t, ++tiles) {
+            for (int t = t0; t < t1; ++t, ++tiles) {
                 const uint32_t v = slot++, k = v + 1;
-                const bool more = t + 1 < x.t1;
+                const bool more = t + 1 < t1;
                 if (!landed(v)) return;
                 for (int w = 0; w < 2; ++w) {
                     if (!ready(c.p_full + 8 * w, tiles & 1)) return;
-                    weigh(w, v, t == x.t0);
+                    weigh(w, v, t == t0);
                     if (w == 1) umma_commit(c.kv_empty + 8 * (v % Sh::kRing));
                     if (more) {
                         if (w == 0 && !landed(k)) return;
@@ -630,7 +668,6 @@ struct ChunkKernel {
                 }
                 if (more) ++slot;
             }
-            ++pieces;
         }
     }
 
@@ -705,24 +742,37 @@ struct ChunkKernel {
         return found;
     }
 
-    // Adds to dims d0 .. d0 + 31 of a row what clean_values took out of the values that the row sees.
-    static __device__ __noinline__ void add_non_finite(const ChunkParams& p, const ChunkPiece& x, int pos, int d0, float* o) {
-        const ChunkTiles tiles(p, x.s, x.rt);
-        for (int t = x.t0; t < x.t1; ++t) {
-            const int k0 = tiles.key(t);
-            if (tiles.plain(p, k0)) continue;
-            for (int k = k0; k <= min(k0 + kTileKeys - 1, pos); ++k) {
-                if (p.window && k <= pos - p.window && k >= p.sinks) continue;
-                const int page = ld_cg_s32(p.table + static_cast<int64_t>(x.b) * p.table_stride + k / p.P);
-                if (page < 0 || page >= p.num_pages) continue;
-                const int64_t at = page_row(p.layout, page, k % p.P, x.kvh, p.P, p.Hkv) * D + d0;
-                for (int d = 0; d < 32; ++d) {
-                    float v;
-                    if constexpr (KV8) v = (p.v[at + d] & 0x7f) == 0x7f ? NAN : 0.f;
-                    else v = bits_to_f32<DT>(reinterpret_cast<const uint16_t*>(p.v)[at + d]);
-                    if (!isfinite(v)) o[d] += v;
+    // Adds to the accumulator `to` of this warp's rows what was taken out of the special tiles' values that a row sees.
+    static __device__ __noinline__ void add_non_finite(const ChunkParams& p, const ChunkPiece& x, int pos, uint32_t to) {
+        const ChunkTiles& tiles = x.tiles;
+        for (int d0 = 0; d0 < D; d0 += 16) {
+            uint32_t o[16];
+            tmem_ld16(to + d0, o);
+            float add[16];
+#pragma unroll
+            for (int d = 0; d < 16; ++d) add[d] = 0.f;
+            for (int t = x.t0; t < x.t1; ++t) {
+                const int k0 = tiles.key(t);
+                if (tiles.plain(t)) continue;
+                for (int k = k0; k <= min(k0 + kTileKeys - 1, pos); ++k) {
+                    if (p.window && k <= pos - p.window && k >= p.sinks) continue;
+                    const int page = ld_cg_s32(p.table + static_cast<int64_t>(x.b) * p.table_stride + k / p.P);
+                    if (page < 0 || page >= p.num_pages) continue;
+                    const int64_t at = page_row(p.layout, page, k % p.P, x.kvh, p.P, p.Hkv) * D + d0;
+#pragma unroll
+                    for (int d = 0; d < 16; ++d) {
+                        float v;
+                        if constexpr (KV8) v = (p.v[at + d] & 0x7f) == 0x7f ? NAN : 0.f;
+                        else v = bits_to_f32<DT>(reinterpret_cast<const uint16_t*>(p.v)[at + d]);
+                        if (!isfinite(v)) add[d] += v;
+                    }
                 }
             }
+            __syncwarp();
+#pragma unroll
+            for (int d = 0; d < 16; ++d) o[d] = __float_as_uint(__uint_as_float(o[d]) + add[d]);
+            tmem_st16_start(to + d0, o);
+            tmem_st_wait();
         }
     }
 
@@ -730,11 +780,11 @@ struct ChunkKernel {
         const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, r = quarter * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
         const uint32_t ts = c.tmem + lanes + w * kTileKeys, to = c.tmem + lanes + Sh::kO + w * D;
-        ChunkWalk walk(p, c.cuts);
-        ChunkPiece x;
         uint32_t count = 0;            // key tiles so far
-        for (int piece = 0; walk.next(p, x); ++piece) {
-            const ChunkTiles tiles(p, x.s, x.rt);
+        for (uint32_t piece = 0;; ++piece) {
+            ChunkPiece* const taken = take_piece(c, p, piece);
+            if (!taken) return;
+            ChunkPiece& x = *taken;
             float factor = 1.f;
             load_queries(c, p, x, w, factor);
             proxy_fence();
@@ -746,9 +796,9 @@ struct ChunkKernel {
             const int pos = live ? x.s.L - x.s.n + token : -1;
             // references: scores' maximum m (16-bit pages: less kLift), and (8-bit pages) dv, how far the weights' is above it
             float m = kNoKey, dv = 0.f, l = 0.f;
-            for (int t = x.t0; t < x.t1; ++t, ++count) {
-                const int k0 = tiles.key(t);
-                const bool plain = tiles.plain(p, k0), first = t == x.t0;
+            const int t0 = x.t0, t1 = x.t1, plain0 = x.tiles.from, plain1 = x.tiles.to;
+            for (int t = t0; t < t1; ++t, ++count) {
+                const bool plain = t >= plain0 && t < plain1, first = t == t0;
                 if (!wait(p, c.s_full + 8 * w, count & 1)) return;
                 tmem_fence_after_sync();
                 float s[kTileKeys];
@@ -772,7 +822,7 @@ struct ChunkKernel {
                     }
                 }
                 if (!plain) {
-                    const int hi = pos - k0;
+                    const int k0 = x.tiles.key(t), hi = pos - k0;
                     if (p.window == 0) {
 #pragma unroll
                         for (int i = 0; i < kTileKeys; ++i) s[i] = i <= hi ? s[i] : -INFINITY;
@@ -850,7 +900,7 @@ struct ChunkKernel {
                     if (w == 0 && !plain) {
                         const uint32_t v = 2 * count + 1;
                         if (!wait(p, c.kv_full + 8 * (v % Sh::kRing), (v / Sh::kRing) & 1)) return;
-                        if (clean_values(p, tiles, k0, ring(c, v % Sh::kRing))) c.dirty[piece & 3] = piece + 1;
+                        if (clean_values(p, x.tiles, x.tiles.key(t), ring(c, v % Sh::kRing))) x.dirty = 1;
                     }
                 }
                 uint64_t sum0 = 0, sum1 = 0;
@@ -893,11 +943,12 @@ struct ChunkKernel {
             // ---- the piece's end
             if (!wait(p, c.pv_done + 8 * w, (count - 1) & 1)) return;
             tmem_fence_after_sync();
-            const bool whole = x.t0 == 0 && x.t1 == x.nt, dirty = c.dirty[piece & 3] == piece + 1;
+            const bool whole = t0 == 0 && t1 == x.tiles.nt, dirty = *static_cast<volatile int*>(&x.dirty) != 0;
+            if (dirty) add_non_finite(p, x, pos, to);
             const bool none = m == kNoKey && l == 0.f;
             const float by = whole ? (none ? 0.f : 1.f / l) : 1.f;
             const int64_t row = x.s.r0 + token, head = static_cast<int64_t>(x.kvh) * p.G + (f - token * p.G);
-            const int slot = 2 * static_cast<int>(blockIdx.x) + (x.t0 == 0 ? 1 : 0);
+            const int slot = 2 * static_cast<int>(blockIdx.x) + (t0 == 0 ? 1 : 0);
             const float half = KV8 ? fast_exp2(0.5f * dv) : 1.f;   // 2^dv in two steps, which stay normal floats for every scale
 #pragma unroll 1
             for (int d = 0; d < D; d += 32) {
@@ -905,7 +956,6 @@ struct ChunkKernel {
                 tmem_ld32_start(to + d, o);
                 tmem_ld_wait();
                 hold32(o);
-                if (dirty && live) add_non_finite(p, x, pos, d, o);
                 if constexpr (KV8) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) o[j] = o[j] * half * half;
@@ -928,6 +978,8 @@ struct ChunkKernel {
             if (!whole) p.part_sum[static_cast<int64_t>(slot) * kItemRows + w * kTileRows + r] = make_float2(m, l);
             else if (p.lse != nullptr && live) p.lse[row * p.Hq + head] = none ? -INFINITY : (m + fast_log2(l)) * kLn2;
             tmem_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) drop_piece(c, piece);
         }
     }
 };
@@ -940,7 +992,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CU
     extern __shared__ uint8_t smem_raw[];
     __shared__ ChunkPlan plan;
     __shared__ uint32_t tmem_slot;
-    __shared__ int dirty[4];
+    __shared__ ChunkPiece pieces[kPieceRing];
     typename K::Ctx c;
     c.smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     c.base = smem_addr(c.smem);
@@ -956,13 +1008,15 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CU
     c.raw_empty = bars(Sh::kRaw);
     c.sc_full = bars(kScaleRing);
     c.sc_empty = bars(kScaleRing);
+    c.x_full = bars(kPieceRing);
+    c.x_empty = bars(kPieceRing);
     c.q_full = bars(2);
     c.s_full = bars(2);
     c.p_full = bars(2);
     c.pv_done = bars(2);
     c.fin = bars(1);
     c.cuts = plan.cuts;
-    c.dirty = dirty;
+    c.pieces = pieces;
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         for (int i = 0; i < Sh::kRing; ++i) {
@@ -984,7 +1038,10 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CU
             mbar_init(c.pv_done + 8 * i, 1);
         }
         mbar_init(c.fin, 1);
-        for (int i = 0; i < 4; ++i) dirty[i] = 0;
+        for (int i = 0; i < kPieceRing; ++i) {
+            mbar_init(c.x_full + 8 * i, 1);
+            mbar_init(c.x_empty + 8 * i, Sh::kPieceReaders);
+        }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         prefetch_tensormap(&tmK);
         prefetch_tensormap(&tmV);
@@ -1002,11 +1059,8 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CU
     __syncthreads();
     tmem_fence_after_sync();
     c.tmem = tmem_slot;
-    if constexpr (KV8) {
-        // of the launch's 512 x 128 registers the rows' threads take 192 each, the others 64
-        if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
-        else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    }
+    if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Sh::kRowRegs));
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Sh::kOtherRegs));
     if (warp < 8) K::rows(c, p, warp >> 2);
     else if (warp == 8) K::producer(c, p, &tmK, &tmV);
     else if (warp == 9) {
