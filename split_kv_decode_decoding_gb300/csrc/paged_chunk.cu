@@ -44,33 +44,6 @@ constexpr int kScaleRing = 4;         // tiles whose scales are in shared memory
 constexpr int kPieceRing = 4;         // pieces whose description is
 constexpr int kJoinSlices = 8;        // blocks that join one split item, 32 rows each
 
-template <int D, bool KV8>
-struct ChunkShape {
-    // warps: 0 - 7 rows, 8 copies, 9 products, 12 - 15 conversion. The rows' threads take most of the launch's registers.
-    static constexpr int kThreads = KV8 ? 512 : 384;
-    static constexpr int kRowRegs = KV8 ? 192 : 208, kOtherRegs = KV8 ? 64 : 88;
-    static_assert(256 * kRowRegs + (kThreads - 256) * kOtherRegs <= kThreads * (65536 / kThreads / 8 * 8), "registers of the launch");
-    static constexpr int kSlices = D / 64;                     // 128-byte columns of a tile in 16 bits
-    static constexpr int kSliceBytes = 128 * 128;
-    static constexpr int kTileBytes = kSlices * kSliceBytes;
-    static constexpr int kRing = KV8 ? 3 : (D == 128 ? 5 : 8); // K and V tiles in 16 bits
-    static constexpr int kRawBytes = KV8 ? kTileKeys * D : 0;  // and as they come, in 8
-    static constexpr int kRaw = KV8 ? 4 : 0;
-    static constexpr int kRawRow = D;
-    static constexpr int kQOff = 0;
-    static constexpr int kRingOff = 2 * kTileBytes;
-    static constexpr int kRawOff = kRingOff + kRing * kTileBytes;
-    static constexpr int kScaleOff = kRawOff + kRaw * kRawBytes;          // [tile][16-key box] {ks, log2 vs}
-    static constexpr int kBarOff = kScaleOff + (KV8 ? kScaleRing * 8 * 8 : 0);
-    static constexpr int kNumBars = 2 * kRing + 2 * kRaw + 2 * kScaleRing + 2 * kPieceRing + 9;
-    static constexpr int kPieceReaders = 9 + (KV8 ? 4 : 0);               // warps
-    static constexpr int kSmemBytes = 1024 + kBarOff + kNumBars * 8;
-    static constexpr int kPlanBytes = (DA_MAX_PAGED_BATCH + 1) * 8 + DA_MAX_PAGED_BATCH * 12;
-    static_assert(kPlanBytes <= kRing * kTileBytes, "the plan is made where the ring is later");
-    // tensor memory
-    static constexpr int kCols = 512, kO = 2 * kTileKeys;      // S0, S1, O0, O1
-};
-
 struct ChunkCut {            // a place in the order of the work: before key tile `tile` of an item
     int b, kvh, rt, tile;
 };
@@ -211,6 +184,37 @@ struct ChunkPlan {
     ChunkCut cuts[2];
     int ranges;
     ChunkJoin join;
+};
+
+template <int D, bool KV8>
+struct ChunkShape {
+    // warps: 0 - 7 rows, 8 copies, 9 products, 12 - 15 conversion. The rows' threads take most of the launch's registers.
+    static constexpr int kRowWarps = 8, kThreads = KV8 ? 512 : 384;
+    static constexpr int kRowRegs = KV8 ? 192 : 208, kOtherRegs = KV8 ? 64 : 88;
+    static_assert(256 * kRowRegs + (kThreads - 256) * kOtherRegs <= kThreads * (65536 / kThreads / 8 * 8), "registers of the launch");
+    static constexpr int kSlices = D / 64;                     // 128-byte columns of a tile in 16 bits
+    static constexpr int kSliceBytes = 128 * 128;
+    static constexpr int kTileBytes = kSlices * kSliceBytes;
+    static constexpr int kRing = KV8 ? 3 : (D == 128 ? 5 : 8); // K and V tiles in 16 bits
+    static constexpr int kRawBytes = KV8 ? kTileKeys * D : 0;  // and as they come, in 8
+    static constexpr int kRaw = KV8 ? (D == 128 ? 4 : 6) : 0;
+    static constexpr int kRawRow = D;
+    static constexpr int kQOff = 0;
+    static constexpr int kRingOff = 2 * kTileBytes;
+    static constexpr int kRawOff = kRingOff + kRing * kTileBytes;
+    static constexpr int kScaleOff = kRawOff + kRaw * kRawBytes;          // [tile][16-key box] {ks, log2 vs}
+    static constexpr int kFactorOff = kScaleOff + (KV8 ? kScaleRing * 8 * 8 : 0);   // [row] factor of a row's scores
+    static constexpr int kPieceOff = kFactorOff + (KV8 ? kItemRows * 4 : 0);
+    static constexpr int kPlanOff = kPieceOff + (kPieceRing * static_cast<int>(sizeof(ChunkPiece)) + 7) / 8 * 8;
+    static constexpr int kBarOff = kPlanOff + (static_cast<int>(sizeof(ChunkPlan)) + 7) / 8 * 8;
+    static constexpr int kNumBars = 2 * kRing + 2 * kRaw + 2 * kScaleRing + 2 * kPieceRing + 11;
+    static constexpr int kPieceReaders = kRowWarps + 1 + (KV8 ? 4 : 0);               // warps
+    static constexpr int kTmemOff = kBarOff + kNumBars * 8;               // where the tensor memory begins
+    static constexpr int kSmemBytes = kTmemOff + 8;
+    static constexpr int kPlanBytes = (DA_MAX_PAGED_BATCH + 1) * 8 + DA_MAX_PAGED_BATCH * 12;
+    static_assert(kPlanBytes <= kRing * kTileBytes, "the plan is made where the ring is later");
+    // tensor memory
+    static constexpr int kCols = 512, kO = 2 * kTileKeys;      // S0, S1, O0, O1
 };
 
 template <int THREADS>
@@ -393,6 +397,15 @@ __device__ __forceinline__ void sts128(uint32_t a, uint4 x) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
 }
 
+// 0 times two 16-bit elements, added to y.
+template <int DT>
+__device__ __forceinline__ uint32_t zero_times(uint32_t x, uint32_t y) {
+    uint32_t r;
+    if constexpr (DT == DA_F16) asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(y));
+    else asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(y));
+    return r;
+}
+
 template <int D, int DT, bool KV8>
 struct ChunkKernel {
     using Sh = ChunkShape<D, KV8>;
@@ -407,7 +420,7 @@ struct ChunkKernel {
     struct Ctx {
         uint8_t* smem;
         uint32_t base, tmem;
-        uint32_t kv_full, kv_empty, raw_full, raw_empty, sc_full, sc_empty, x_full, x_empty, q_full, s_full, p_full, pv_done, fin;
+        uint32_t kv_full, kv_empty, raw_full, raw_empty, sc_full, sc_empty, x_full, x_empty, q_full, s_full, p_half, p_full, pv_done, fin;
         const ChunkCut* cuts;
         ChunkPiece* pieces;
     };
@@ -632,12 +645,15 @@ struct ChunkKernel {
             }
             umma_commit(c.s_full + 8 * w);
         };
-        auto weigh = [&](int w, uint32_t i, bool first) {
+        // (a half of the tile's keys at a time: the second half's weights are computed beside the first product)
+        auto weigh = [&](int w, uint32_t i, int half, bool first) {
             const uint64_t vd = umma_desc_sw128(ring(c, i % Sh::kRing), Sh::kSliceBytes, 1024);
 #pragma unroll
-            for (int k = 0; k < kTileKeys / 16; ++k)
+            for (int j = 0; j < kTileKeys / 32; ++j) {
+                const int k = half * (kTileKeys / 32) + j;
                 umma_ts(c.tmem + Sh::kO + w * D, c.tmem + w * kTileKeys + k * 8, vd + ((k * 16 * 128) >> 4), kIdPV, !(first && k == 0));
-            umma_commit(c.pv_done + 8 * w);
+            }
+            if (half == 1) umma_commit(c.pv_done + 8 * w);
         };
         for (uint32_t piece = 0;; ++piece) {
             const ChunkPiece* x = take_piece(c, p, piece);
@@ -657,8 +673,10 @@ struct ChunkKernel {
                 const bool more = t + 1 < t1;
                 if (!landed(v)) return;
                 for (int w = 0; w < 2; ++w) {
+                    if (!ready(c.p_half + 8 * w, tiles & 1)) return;
+                    weigh(w, v, 0, t == t0);
                     if (!ready(c.p_full + 8 * w, tiles & 1)) return;
-                    weigh(w, v, t == t0);
+                    weigh(w, v, 1, false);
                     if (w == 1) umma_commit(c.kv_empty + 8 * (v % Sh::kRing));
                     if (more) {
                         if (w == 0 && !landed(k)) return;
@@ -672,32 +690,33 @@ struct ChunkKernel {
     }
 
     // ------------------------------------------------------------ rows
-    // Rows of this warp's quarter of tile w into shared memory (32 rows; float32 factor per row to `factors` of e4m3 calls).
-    static __device__ __forceinline__ void load_queries(const Ctx& c, const ChunkParams& p, const ChunkPiece& x, int w, float& factor) {
-        const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3;
-        constexpr int kChunks = D / 8, kPerPass = 32 / kChunks, kPasses = 32 / kPerPass, kBatch = 8;
+    // 32 rows of tile w into shared memory, this warp's quarter of it.
+    static __device__ __forceinline__ void load_queries(const Ctx& c, const ChunkParams& p, const ChunkPiece& x, int w, int quarter) {
+        const int lane = threadIdx.x & 31;
+        constexpr int kChunks = D / 8, kPerPass = 32 / kChunks, kPasses = 32 / kPerPass;
         const uint32_t tile = c.base + Sh::kQOff + w * Sh::kTileBytes;
         const int ch = lane % kChunks, sub = lane / kChunks;
         const int rows = x.s.n * p.G, row0 = x.rt * kItemRows + w * kTileRows + quarter * 32;
-#pragma unroll 1
-        for (int i0 = 0; i0 < kPasses; i0 += kBatch) {
-            uint4 v[kBatch];
+        const uint16_t* q = p.q + static_cast<int64_t>(x.kvh) * p.G * D + ch * 8;
+        uint4 v[kPasses];
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const int f = row0 + (i0 + i) * kPerPass + sub;
-                v[i] = make_uint4(0, 0, 0, 0);
-                if (f < rows) {
-                    const int t = f / p.G, g = f - t * p.G;
-                    v[i] = __ldg(reinterpret_cast<const uint4*>(p.q + (x.s.r0 + t) * p.q_stride + (static_cast<int64_t>(x.kvh) * p.G + g) * D) + ch);
-                }
+        for (int i = 0; i < kPasses; ++i) {
+            const int f = row0 + i * kPerPass + sub;
+            v[i] = make_uint4(0, 0, 0, 0);
+            if (f < rows) {
+                const int t = f / p.G, g = f - t * p.G;
+                v[i] = __ldg(reinterpret_cast<const uint4*>(q + (x.s.r0 + t) * p.q_stride + g * D));
             }
+        }
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const int r = (i0 + i) * kPerPass + sub;
-                uint32_t e[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        for (int i = 0; i < kPasses; ++i) {
+            const int r = quarter * 32 + i * kPerPass + sub;
+            uint32_t e[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) e[j] = (e[j] & p.q_and) ^ p.q_xor;
-                if constexpr (KV8 && DT == DA_BF16) {
+            for (int j = 0; j < 4; ++j) e[j] = (e[j] & p.q_and) ^ p.q_xor;
+            if constexpr (KV8) {
+                float down = 1.f;
+                if constexpr (DT == DA_BF16) {
                     uint32_t top = 0;   // largest exponent field of the row
 #pragma unroll
                     for (int j = 0; j < 4; ++j) top = max(top, max((e[j] >> 7) & 0xffu, (e[j] >> 23) & 0xffu));
@@ -706,37 +725,46 @@ struct ChunkKernel {
                     // 2^e takes the largest element to [2^14, 2^15); an infinity or a NaN stays one
                     const int field = top == 255 ? 127 : min(max(268 - static_cast<int>(top), 14), 240);
                     const float up = __uint_as_float(static_cast<uint32_t>(field) << 23);
-                    const float down = __uint_as_float(static_cast<uint32_t>(254 - field) << 23);
+                    down = __uint_as_float(static_cast<uint32_t>(254 - field) << 23);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         e[j] = pack2<DA_F16>(__uint_as_float(e[j] << 16) * up, __uint_as_float(e[j] & 0xffff0000u) * up);
-#pragma unroll
-                    for (int s = 0; s < kPerPass; ++s) {
-                        const float y = __shfl_sync(0xffffffffu, down, s * kChunks);
-                        if (lane == (i0 + i) * kPerPass + s) factor = y;
-                    }
                 }
-                sts128(tile_addr(tile, quarter * 32 + r, ch), make_uint4(e[0], e[1], e[2], e[3]));
+                if (ch == 0) reinterpret_cast<float*>(c.smem + Sh::kFactorOff)[w * kTileRows + r] = down * p.scale_log2;
             }
+            sts128(tile_addr(tile, r, ch), make_uint4(e[0], e[1], e[2], e[3]));
         }
     }
 
-    // A special tile's values, 16-bit pages (by the threads of row tile 0): zeros for what no row sees and for what is not finite.
+    // A special tile's values, 16-bit pages (by the 128 threads of row tile 0): zeros for what no row sees and for what
+    // is not finite.
     static __device__ __forceinline__ bool clean_values(const ChunkParams& p, const ChunkTiles& tiles, int k0, uint32_t tile) {
-        constexpr int kChunks = D / 8;
-        constexpr uint32_t kExp = MT == DA_BF16 ? 0x7f807f80u : 0x7c007c00u;
-        bool found = false;
+        constexpr int kChunks = D / 8, kStep = 128 / kChunks, kTimes = kTileKeys / kStep;
+        const int tid = threadIdx.x & 127, ch = tid % kChunks, r0 = tid / kChunks;
+        uint32_t probe = 0;      // a sum of zero times the elements that some row sees: 0, or NaN
 #pragma unroll 4
-        for (int i = 0; i < kChunks; ++i) {
-            const int u = i * 128 + static_cast<int>(threadIdx.x & 127), r = u / kChunks, ch = u % kChunks;
+        for (int i = 0; i < kTimes; ++i) {
+            const int r = r0 + i * kStep;
             const uint32_t at = tile_addr(tile, r, ch);
-            const uint4 v = lds128(at);
-            const uint32_t bad[4] = {__vcmpeq2(v.x & kExp, kExp), __vcmpeq2(v.y & kExp, kExp), __vcmpeq2(v.z & kExp, kExp),
-                                     __vcmpeq2(v.w & kExp, kExp)};
-            const bool seen = tiles.wanted(p, k0 + r, 1), any = (bad[0] | bad[1] | bad[2] | bad[3]) != 0;
-            if (!seen) sts128(at, make_uint4(0, 0, 0, 0));
-            else if (any) sts128(at, make_uint4(v.x & ~bad[0], v.y & ~bad[1], v.z & ~bad[2], v.w & ~bad[3]));
-            found = found || (seen && any);
+            if (tiles.wanted(p, k0 + r, 1)) {
+                const uint4 v = lds128(at);
+                probe = zero_times<MT>(v.x, zero_times<MT>(v.y, zero_times<MT>(v.z, zero_times<MT>(v.w, probe))));
+            } else {
+                sts128(at, make_uint4(0, 0, 0, 0));
+            }
+        }
+        const bool found = (probe & 0x7fff7fffu) != 0;
+        if (found) {
+            constexpr uint32_t kExp = MT == DA_BF16 ? 0x7f807f80u : 0x7c007c00u;
+#pragma unroll 1
+            for (int i = 0; i < kTimes; ++i) {
+                const int r = r0 + i * kStep;
+                const uint32_t at = tile_addr(tile, r, ch);
+                if (!tiles.wanted(p, k0 + r, 1)) continue;
+                const uint4 v = lds128(at);
+                sts128(at, make_uint4(v.x & ~__vcmpeq2(v.x & kExp, kExp), v.y & ~__vcmpeq2(v.y & kExp, kExp),
+                                      v.z & ~__vcmpeq2(v.z & kExp, kExp), v.w & ~__vcmpeq2(v.w & kExp, kExp)));
+            }
         }
         proxy_fence();
         return found;
@@ -776,8 +804,37 @@ struct ChunkKernel {
         }
     }
 
-    static __device__ void rows(const Ctx& c, const ChunkParams& p, int w) {
-        const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, r = quarter * 32 + lane;
+    // Multiplies the accumulator of this warp's rows, at `to`, by `by`: its last product is done then, the next one waits
+    // for this tile's weights.
+    static __device__ __forceinline__ bool rescale(const Ctx& c, const ChunkParams& p, uint32_t to, uint32_t done, uint32_t count, float by) {
+        if (!wait(p, done, (count - 1) & 1)) return false;
+        tmem_fence_after_sync();
+#pragma unroll 1
+        for (int d = 0; d < D; d += 16) {
+            uint32_t u[16];
+            tmem_ld16(to + d, u);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) asm volatile("" : "+r"(u[j]));
+#pragma unroll
+            for (int j = 0; j < 16; ++j) u[j] = __float_as_uint(__uint_as_float(u[j]) * by);
+            tmem_st16_start(to + d, u);
+        }
+        tmem_st_wait();
+        return true;
+    }
+
+    static __device__ __forceinline__ float max16(const float* s) {
+        float a = fmaxf(s[0], s[1]), b = fmaxf(s[2], s[3]);
+#pragma unroll
+        for (int j = 4; j < 16; j += 4) {
+            a = fmaxf(a, fmaxf(s[j], s[j + 1]));
+            b = fmaxf(b, fmaxf(s[j + 2], s[j + 3]));
+        }
+        return fmaxf(a, b);
+    }
+
+    static __device__ void rows(const Ctx& c, const ChunkParams& p) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
         const uint32_t ts = c.tmem + lanes + w * kTileKeys, to = c.tmem + lanes + Sh::kO + w * D;
         uint32_t count = 0;            // key tiles so far
@@ -785,12 +842,12 @@ struct ChunkKernel {
             ChunkPiece* const taken = take_piece(c, p, piece);
             if (!taken) return;
             ChunkPiece& x = *taken;
-            float factor = 1.f;
-            load_queries(c, p, x, w, factor);
+            load_queries(c, p, x, w, quarter);
             proxy_fence();
             __syncwarp();
             if (lane == 0) mbar_arrive(c.q_full + 8 * w);
-            factor *= p.scale_log2;
+            float factor = p.scale_log2;
+            if constexpr (KV8) factor = reinterpret_cast<const float*>(c.smem + Sh::kFactorOff)[w * kTileRows + r];
             const int f = x.rt * kItemRows + w * kTileRows + r, token = f / p.G;
             const bool live = f < x.s.n * p.G;
             const int pos = live ? x.s.L - x.s.n + token : -1;
@@ -815,10 +872,7 @@ struct ChunkKernel {
                         const float by = factor * sc[i].x;
                         const uint64_t by2 = pair(by, by);
 #pragma unroll
-                        for (int j = 0; j < 16; j += 2) {
-                            const uint64_t y = mul2(pair(s[16 * i + j], s[16 * i + j + 1]), by2);
-                            unpair(y, s[16 * i + j], s[16 * i + j + 1]);
-                        }
+                        for (int j = 16 * i; j < 16 * i + 16; j += 2) unpair(mul2(pair(s[j], s[j + 1]), by2), s[j], s[j + 1]);
                     }
                 }
                 if (!plain) {
@@ -835,68 +889,36 @@ struct ChunkKernel {
                 // maxima of 16 keys, the size of the smallest page
                 float top[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    float a = fmaxf(s[16 * i], s[16 * i + 1]), b = fmaxf(s[16 * i + 2], s[16 * i + 3]);
-#pragma unroll
-                    for (int j = 4; j < 16; j += 4) {
-                        a = fmaxf(a, fmaxf(s[16 * i + j], s[16 * i + j + 1]));
-                        b = fmaxf(b, fmaxf(s[16 * i + j + 2], s[16 * i + j + 3]));
-                    }
-                    top[i] = fmaxf(a, b);
-                }
-                float best = top[0];
-#pragma unroll
-                for (int i = 1; i < 8; ++i) best = fmaxf(best, top[i]);
-                bool move;
+                for (int i = 0; i < 8; ++i) top[i] = max16(s + 16 * i);
+                float best = fmaxf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), fmaxf(fmaxf(top[4], top[5]), fmaxf(top[6], top[7])));
                 if constexpr (KV8) {
-                    move = best - m > kHeadroom;
+                    // a weight that is too large moves the references as a score does
+                    bool move = best - m > kHeadroom;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) move = move || (top[i] - m) + (sc[i].y - dv) > kHeadroom + kLift;
+                    if (first || __any_sync(0xffffffffu, move)) {
+                        const float mn = fmaxf(m, best);
+                        float dn = first ? kNoKey : (m - mn) + dv;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) dn = fmaxf(dn, (top[i] - mn) + (sc[i].y - kLift));
+                        if (!first) {
+                            l *= fast_exp2(m - mn);
+                            if (!rescale(c, p, to, c.pv_done + 8 * w, count, fast_exp2((m - mn) + (dv - dn)))) return;
+                        }
+                        m = mn;
+                        dv = dn;
+                    }
                 } else {
                     best *= factor;
-                    move = best - m > kHeadroom + kLift;
-                }
-                if (first || __any_sync(0xffffffffu, move)) {
-                    float al = 1.f, av = 1.f;     // factors of the sum and of the accumulator
-                    if (first || move) {
-                        if constexpr (KV8) {
-                            const float mn = fmaxf(m, best);
-                            float dn = first ? kNoKey : (m - mn) + dv;
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) dn = fmaxf(dn, (top[i] - mn) + (sc[i].y - kLift));
-                            al = fast_exp2(m - mn);
-                            av = fast_exp2((m - mn) + (dv - dn));
-                            m = mn;
-                            dv = dn;
-                        } else {
-                            const float mn = fmaxf(m, best - kLift);
-                            al = av = fast_exp2(m - mn);
-                            m = mn;
-                        }
+                    const bool move = best - m > kHeadroom + kLift;
+                    if (first) {
+                        m = fmaxf(m, best - kLift);
+                    } else if (__any_sync(0xffffffffu, move)) {
+                        const float mn = move ? fmaxf(m, best - kLift) : m, by = fast_exp2(m - mn);
+                        l *= by;
+                        m = mn;
+                        if (!rescale(c, p, to, c.pv_done + 8 * w, count, by)) return;
                     }
-                    if (!first) {
-                        l *= al;
-                        // the accumulator: its last product is done, the next one waits for this tile's weights
-                        if (!wait(p, c.pv_done + 8 * w, (count - 1) & 1)) return;
-                        tmem_fence_after_sync();
-#pragma unroll 1
-                        for (int d = 0; d < D; d += 32) {
-                            float o[32];
-                            tmem_ld32_start(to + d, o);
-                            tmem_ld_wait();
-                            hold32(o);
-                            uint32_t x0[16], x1[16];
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                x0[j] = __float_as_uint(o[j] * av);
-                                x1[j] = __float_as_uint(o[j + 16] * av);
-                            }
-                            tmem_st16_start(to + d, x0);
-                            tmem_st16_start(to + d + 16, x1);
-                        }
-                    }
-                }
-                if constexpr (!KV8) {
                     if (w == 0 && !plain) {
                         const uint32_t v = 2 * count + 1;
                         if (!wait(p, c.kv_full + 8 * (v % Sh::kRing), (v / Sh::kRing) & 1)) return;
@@ -928,10 +950,13 @@ struct ChunkKernel {
                         o[j / 2] = pack2<MT>(a, b);
                     }
                     tmem_st16_start(ts + 16 * i, o);
+                    if (i == 1) {
+                        tmem_st_wait();
+                        tmem_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(c.p_half + 8 * w);
+                    }
                 }
-                float a, b;
-                unpair(add2(sum0, sum1), a, b);
-                l += a + b;
                 tmem_st_wait();
                 tmem_fence_before_sync();
                 __syncwarp();
@@ -939,39 +964,44 @@ struct ChunkKernel {
                     mbar_arrive(c.p_full + 8 * w);
                     if constexpr (KV8) mbar_arrive(c.sc_empty + 8 * (count % kScaleRing));
                 }
+                float a, b;
+                unpair(add2(sum0, sum1), a, b);
+                l += a + b;
             }
             // ---- the piece's end
             if (!wait(p, c.pv_done + 8 * w, (count - 1) & 1)) return;
             tmem_fence_after_sync();
-            const bool whole = t0 == 0 && t1 == x.tiles.nt, dirty = *static_cast<volatile int*>(&x.dirty) != 0;
-            if (dirty) add_non_finite(p, x, pos, to);
+            const bool whole = t0 == 0 && t1 == x.tiles.nt;
+            if (*static_cast<volatile int*>(&x.dirty) != 0) add_non_finite(p, x, pos, to);
             const bool none = m == kNoKey && l == 0.f;
-            const float by = whole ? (none ? 0.f : 1.f / l) : 1.f;
+            const float by = none ? 0.f : 1.f / l;
             const int64_t row = x.s.r0 + token, head = static_cast<int64_t>(x.kvh) * p.G + (f - token * p.G);
             const int slot = 2 * static_cast<int>(blockIdx.x) + (t0 == 0 ? 1 : 0);
-            const float half = KV8 ? fast_exp2(0.5f * dv) : 1.f;   // 2^dv in two steps, which stay normal floats for every scale
-#pragma unroll 1
-            for (int d = 0; d < D; d += 32) {
-                float o[32];
-                tmem_ld32_start(to + d, o);
+            const float root = KV8 ? fast_exp2(0.5f * dv) : 1.f;   // 2^dv in two steps, which stay normal floats for every scale
+#pragma unroll
+            for (int d0 = 0; d0 < D; d0 += 64) {
+                float o[64];
+                tmem_ld32_start(to + d0, o);
+                tmem_ld32_start(to + d0 + 32, o + 32);
                 tmem_ld_wait();
                 hold32(o);
+                hold32(o + 32);
                 if constexpr (KV8) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) o[j] = o[j] * half * half;
+                    for (int j = 0; j < 64; ++j) o[j] = o[j] * root * root;
                 }
                 if (whole) {
                     if (live) {
-                        uint4* out = reinterpret_cast<uint4*>(p.out + row * p.out_stride + head * D + d);
+                        uint4* out = reinterpret_cast<uint4*>(p.out + row * p.out_stride + head * D + d0);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
+                        for (int j = 0; j < 8; ++j)
                             out[j] = make_uint4(pack2<DT>(o[8 * j] * by, o[8 * j + 1] * by), pack2<DT>(o[8 * j + 2] * by, o[8 * j + 3] * by),
                                                 pack2<DT>(o[8 * j + 4] * by, o[8 * j + 5] * by), pack2<DT>(o[8 * j + 6] * by, o[8 * j + 7] * by));
                     }
                 } else {
-                    float4* out = p.part + (static_cast<int64_t>(slot) * (D / 4) + d / 4) * kItemRows + w * kTileRows + r;
+                    float4* out = p.part + (static_cast<int64_t>(slot) * (D / 4) + d0 / 4) * kItemRows + w * kTileRows + r;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
+                    for (int j = 0; j < 16; ++j)
                         out[j * kItemRows] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
                 }
             }
@@ -989,13 +1019,15 @@ __global__ void __launch_bounds__(ChunkShape<D, KV8>::kThreads, 1)
 chunk_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const ChunkParams p) {
     using K = ChunkKernel<D, DT, KV8>;
     using Sh = typename K::Sh;
-    extern __shared__ uint8_t smem_raw[];
-    __shared__ ChunkPlan plan;
-    __shared__ uint32_t tmem_slot;
-    __shared__ ChunkPiece pieces[kPieceRing];
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
     typename K::Ctx c;
-    c.smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    c.smem = smem_raw;
     c.base = smem_addr(c.smem);
+    if (c.base & 1023) {   // (it begins the block's shared memory, there is no room to move it)
+        if (threadIdx.x == 0) flag_error(p.err, DA_DEVERR_TIMEOUT);
+        return;
+    }
+    ChunkPlan& plan = *reinterpret_cast<ChunkPlan*>(c.smem + Sh::kPlanOff);
     uint32_t bar = c.base + Sh::kBarOff;
     auto bars = [&](int n) {
         const uint32_t at = bar;
@@ -1012,11 +1044,12 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CU
     c.x_empty = bars(kPieceRing);
     c.q_full = bars(2);
     c.s_full = bars(2);
+    c.p_half = bars(2);
     c.p_full = bars(2);
     c.pv_done = bars(2);
     c.fin = bars(1);
     c.cuts = plan.cuts;
-    c.pieces = pieces;
+    c.pieces = reinterpret_cast<ChunkPiece*>(c.smem + Sh::kPieceOff);
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         for (int i = 0; i < Sh::kRing; ++i) {
@@ -1029,11 +1062,12 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CU
         }
         for (int i = 0; i < kScaleRing; ++i) {
             mbar_init(c.sc_full + 8 * i, 1);
-            mbar_init(c.sc_empty + 8 * i, 8);
+            mbar_init(c.sc_empty + 8 * i, Sh::kRowWarps);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(c.q_full + 8 * i, 4);
             mbar_init(c.s_full + 8 * i, 1);
+            mbar_init(c.p_half + 8 * i, 4);
             mbar_init(c.p_full + 8 * i, 4);
             mbar_init(c.pv_done + 8 * i, 1);
         }
@@ -1046,8 +1080,8 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CU
         prefetch_tensormap(&tmK);
         prefetch_tensormap(&tmV);
     }
-    if (warp == 9) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_slot)), "r"(Sh::kCols) : "memory");
+    if (warp == Sh::kRowWarps + 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(c.base + Sh::kTmemOff), "r"(Sh::kCols) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     // From here on this grid touches global memory: wait for the previous kernel.
@@ -1058,21 +1092,21 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CU
     tmem_fence_before_sync();
     __syncthreads();
     tmem_fence_after_sync();
-    c.tmem = tmem_slot;
-    if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Sh::kRowRegs));
+    c.tmem = *reinterpret_cast<const volatile uint32_t*>(c.smem + Sh::kTmemOff);
+    if (warp < Sh::kRowWarps) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Sh::kRowRegs));
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Sh::kOtherRegs));
-    if (warp < 8) K::rows(c, p, warp >> 2);
-    else if (warp == 8) K::producer(c, p, &tmK, &tmV);
-    else if (warp == 9) {
+    if (warp < Sh::kRowWarps) K::rows(c, p);
+    else if (warp == Sh::kRowWarps) K::producer(c, p, &tmK, &tmV);
+    else if (warp == Sh::kRowWarps + 1) {
         if ((threadIdx.x & 31) == 0) K::multiplier(c, p);
         __syncwarp();
     }
     if constexpr (KV8) {
-        if (warp >= 12) K::converter(c, p);
+        if (warp >= Sh::kRowWarps + 4) K::converter(c, p);
     }
     tmem_fence_before_sync();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == Sh::kRowWarps + 1) {
         tmem_fence_after_sync();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(c.tmem), "r"(Sh::kCols));
     }
