@@ -9,7 +9,7 @@
 //
 // S, P and O live in tensor memory (S and P in the same columns), Q, K and V in shared memory.
 // One thread per row holds the row's scores in registers. One warp copies K and V by TMA, a box
-// per page, or per 16 to 128 keys of it; one thread issues the products:
+// per page, or per 16 to 128 keys of it; one warp issues the products:
 //
 //     ... P0(j) V(j), Q0 K(j+1), P1(j) V(j), Q1 K(j+1), P0(j+1) V(j+1) ...
 //
@@ -618,73 +618,88 @@ struct ChunkKernel {
         }
     }
 
-    // ------------------------------------------------------------ products (one thread)
+    // ------------------------------------------------------------ products (one warp, all lanes alike)
     static __device__ void multiplier(const Ctx& c, const ChunkParams& p) {
         multiply(c, p);
         // nothing is in flight when the tensor memory is freed, after a wait that timed out neither
-        umma_commit(c.fin);
-        wait_lane(c.fin, 0, p.wait_limit_ns);
+        umma_commit_elect(c.fin);
+        wait_warp(c.fin, 0, p.wait_limit_ns);
     }
 
+    static __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
     static __device__ __forceinline__ void multiply(const Ctx& c, const ChunkParams& p) {
-        const uint64_t q0 = umma_desc_sw128(c.base + Sh::kQOff, 16, 1024);
-        uint32_t slot = 0, tiles = 0;
+        const uint32_t tmem = uniform(c.tmem), base = uniform(c.base);
+        const uint64_t q0 = umma_desc_sw128(base + Sh::kQOff, 16, 1024);
+        const uint64_t k0 = umma_desc_sw128(base + Sh::kRingOff, 16, 1024), v0 = umma_desc_sw128(base + Sh::kRingOff, Sh::kSliceBytes, 1024);
+        uint32_t at = 0, phase = 0;            // the next tile's place in the ring, and its parity
+        uint32_t tiles = 0;
         auto ready = [&](uint32_t bar, uint32_t parity) {
-            const bool ok = wait_lane(bar, parity, p.wait_limit_ns);
-            if (!ok) flag_error(p.err, DA_DEVERR_TIMEOUT);
+            const bool ok = wait(p, bar, parity);
             tmem_fence_after_sync();
             return ok;
         };
-        auto landed = [&](uint32_t i) { return ready(c.kv_full + 8 * (i % Sh::kRing), (i / Sh::kRing) & 1); };
-        auto scores = [&](int w, uint32_t i) {
-            const uint64_t kd = umma_desc_sw128(ring(c, i % Sh::kRing), 16, 1024), qd = q0 + ((w * Sh::kTileBytes) >> 4);
+        auto advance = [&]() {
+            if (++at == Sh::kRing) {
+                at = 0;
+                phase ^= 1;
+            }
+        };
+        auto scores = [&](int w, uint32_t place) {
+            const uint64_t kd = k0 + ((place * Sh::kTileBytes) >> 4), qd = q0 + ((w * Sh::kTileBytes) >> 4);
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
                 const uint32_t off = ((k >> 2) * Sh::kSliceBytes + (k & 3) * 32) >> 4;
-                umma_ss(c.tmem + w * kTileKeys, qd + off, kd + off, kIdS, k > 0);
+                umma_ss_elect(tmem + w * kTileKeys, qd + off, kd + off, kIdS, k > 0);
             }
-            umma_commit(c.s_full + 8 * w);
+            umma_commit_elect(c.s_full + 8 * w);
         };
         // (a half of the tile's keys at a time: the second half's weights are computed beside the first product)
-        auto weigh = [&](int w, uint32_t i, int half, bool first) {
-            const uint64_t vd = umma_desc_sw128(ring(c, i % Sh::kRing), Sh::kSliceBytes, 1024);
+        auto weigh = [&](int w, uint32_t place, int half, bool first) {
+            const uint64_t vd = v0 + ((place * Sh::kTileBytes) >> 4);
 #pragma unroll
             for (int j = 0; j < kTileKeys / 32; ++j) {
                 const int k = half * (kTileKeys / 32) + j;
-                umma_ts(c.tmem + Sh::kO + w * D, c.tmem + w * kTileKeys + k * 8, vd + ((k * 16 * 128) >> 4), kIdPV, !(first && k == 0));
+                umma_ts_elect(tmem + Sh::kO + w * D, tmem + w * kTileKeys + k * 8, vd + ((k * 16 * 128) >> 4), kIdPV, !(first && k == 0));
             }
-            if (half == 1) umma_commit(c.pv_done + 8 * w);
+            if (half == 1) umma_commit_elect(c.pv_done + 8 * w);
         };
         for (uint32_t piece = 0;; ++piece) {
             const ChunkPiece* x = take_piece(c, p, piece);
-            if (!x) return;
-            const int t0 = x->t0, t1 = x->t1;
-            drop_piece(c, piece);
-            // slots: K, V, K, V ...
-            if (!landed(slot)) return;
+            if (__any_sync(0xffffffffu, x == nullptr)) return;
+            const int nt = uniform(x->t1 - x->t0);
+            __syncwarp();
+            if ((threadIdx.x & 31) == 0) drop_piece(c, piece);
+            // the ring: K, V, K, V ...
+            if (!ready(c.kv_full + 8 * at, phase)) return;
+#pragma unroll
             for (int w = 0; w < 2; ++w) {
                 if (!ready(c.q_full + 8 * w, piece & 1)) return;
-                scores(w, slot);
+                scores(w, at);
             }
-            umma_commit(c.kv_empty + 8 * (slot % Sh::kRing));
-            ++slot;
-            for (int t = t0; t < t1; ++t, ++tiles) {
-                const uint32_t v = slot++, k = v + 1;
-                const bool more = t + 1 < t1;
-                if (!landed(v)) return;
+            umma_commit_elect(c.kv_empty + 8 * at);
+            advance();
+            for (int t = 0; t < nt; ++t, ++tiles) {
+                const uint32_t v = at;
+                const bool more = t + 1 < nt;
+                if (!ready(c.kv_full + 8 * v, phase)) return;
+                advance();
+#pragma unroll
                 for (int w = 0; w < 2; ++w) {
                     if (!ready(c.p_half + 8 * w, tiles & 1)) return;
-                    weigh(w, v, 0, t == t0);
+                    weigh(w, v, 0, t == 0);
                     if (!ready(c.p_full + 8 * w, tiles & 1)) return;
                     weigh(w, v, 1, false);
-                    if (w == 1) umma_commit(c.kv_empty + 8 * (v % Sh::kRing));
+                    if (w == 1) umma_commit_elect(c.kv_empty + 8 * v);
                     if (more) {
-                        if (w == 0 && !landed(k)) return;
-                        scores(w, k);
-                        if (w == 1) umma_commit(c.kv_empty + 8 * (k % Sh::kRing));
+                        if (w == 0 && !ready(c.kv_full + 8 * at, phase)) return;
+                        scores(w, at);
+                        if (w == 1) {
+                            umma_commit_elect(c.kv_empty + 8 * at);
+                            advance();
+                        }
                     }
                 }
-                if (more) ++slot;
             }
         }
     }
@@ -1050,7 +1065,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CU
     c.fin = bars(1);
     c.cuts = plan.cuts;
     c.pieces = reinterpret_cast<ChunkPiece*>(c.smem + Sh::kPieceOff);
-    const int warp = threadIdx.x >> 5;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
     if (threadIdx.x == 0) {
         for (int i = 0; i < Sh::kRing; ++i) {
             mbar_init(c.kv_full + 8 * i, KV8 ? 4 : 1);
@@ -1098,8 +1113,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CU
     if (warp < Sh::kRowWarps) K::rows(c, p);
     else if (warp == Sh::kRowWarps) K::producer(c, p, &tmK, &tmV);
     else if (warp == Sh::kRowWarps + 1) {
-        if ((threadIdx.x & 31) == 0) K::multiplier(c, p);
-        __syncwarp();
+        K::multiplier(c, p);
     }
     if constexpr (KV8) {
         if (warp >= Sh::kRowWarps + 4) K::converter(c, p);
