@@ -67,9 +67,17 @@ struct ChunkParams {
     int64_t q_stride, out_stride;
     int B, T, Hq, Hkv, G, P, max_pages, table_stride, num_pages, layout, window, sinks;
     int box_keys;            // keys of a TMA box: gcd(page size, 128)
+    uint32_t group_mul;      // f / G by multiplication (token())
+    int group_shift;
     uint32_t q_and, q_xor;   // on two query elements: zeroes them if the scale is 0, and takes its sign
     float scale_log2;        // |scale| log2e (1 if it is 0)
+    int out_wide;            // every row of out begins on a 32-byte border
     unsigned long long wait_limit_ns;
+
+    // Token of row f of a sequence (f < 2^31).
+    __device__ __forceinline__ int token(int f) const {
+        return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(f)) * group_mul) >> group_shift);
+    }
 };
 
 struct ChunkSeq {
@@ -103,8 +111,8 @@ struct ChunkTiles {
 
     __device__ __forceinline__ ChunkTiles(const ChunkParams& p, const ChunkSeq& s, int rt) {
         const int f = rt * kItemRows;
-        first = s.L - s.n + f / p.G;
-        last = s.L - s.n + min(s.n - 1, (f + kItemRows - 1) / p.G);
+        first = s.L - s.n + p.token(f);
+        last = s.L - s.n + min(s.n - 1, p.token(f + kItemRows - 1));
         low = p.window ? max(0, max(first, 0) - p.window + 1) : 0;
         ns = (min(p.sinks, low) + kTileKeys - 1) / kTileKeys;
         lo = max(ns, low / kTileKeys);
@@ -140,12 +148,17 @@ struct ChunkPiece {
     int dirty;               // special tiles had values that are not finite
 };
 
+// A CTA's range: its cuts, and the split item that begins in it.
+struct ChunkPlan {
+    ChunkCut cuts[2];
+    ChunkSeq seqs[2];        // of the sequences that they lie in
+    ChunkJoin join;
+};
+
 struct ChunkWalk {
     ChunkCut at, end;
     ChunkSeq s;
-    __device__ __forceinline__ ChunkWalk(const ChunkParams& p, const ChunkCut* cuts) : at(cuts[0]), end(cuts[1]) {
-        if (at.b < p.B) s = chunk_seq(p, at.b, false);
-    }
+    __device__ __forceinline__ explicit ChunkWalk(const ChunkPlan& plan) : at(plan.cuts[0]), end(plan.cuts[1]), s(plan.seqs[0]) {}
     __device__ __forceinline__ bool next(const ChunkParams& p, ChunkPiece& x) {
         if (at.b >= p.B || (at.b == end.b && at.kvh == end.kvh && at.rt == end.rt && at.tile >= end.tile)) return false;
         x.tiles = ChunkTiles(p, s, at.rt);
@@ -178,17 +191,9 @@ struct ChunkWalk {
 };
 
 // ------------------------------------------------------------ the plan
-// This CTA's range: its cuts, and the split item that begins in it (by all threads; `space` is shared memory that
-// the pipeline uses later).
-struct ChunkPlan {
-    ChunkCut cuts[2];
-    int ranges;
-    ChunkJoin join;
-};
-
 template <int D, bool KV8>
 struct ChunkShape {
-    // warps: 0 - 7 rows, 8 copies, 9 products, 12 - 15 conversion. The rows' threads take most of the launch's registers.
+    // warps: 0 - 7 rows, 8 copies, 9 products, 10 and 11 queries, 12 - 15 conversion. The rows' threads take most of the launch's registers.
     static constexpr int kRowWarps = 8, kThreads = KV8 ? 512 : 384;
     static constexpr int kRowRegs = KV8 ? 192 : 208, kOtherRegs = KV8 ? 64 : 88;
     static_assert(256 * kRowRegs + (kThreads - 256) * kOtherRegs <= kThreads * (65536 / kThreads / 8 * 8), "registers of the launch");
@@ -207,8 +212,8 @@ struct ChunkShape {
     static constexpr int kPieceOff = kFactorOff + (KV8 ? kItemRows * 4 : 0);
     static constexpr int kPlanOff = kPieceOff + (kPieceRing * static_cast<int>(sizeof(ChunkPiece)) + 7) / 8 * 8;
     static constexpr int kBarOff = kPlanOff + (static_cast<int>(sizeof(ChunkPlan)) + 7) / 8 * 8;
-    static constexpr int kNumBars = 2 * kRing + 2 * kRaw + 2 * kScaleRing + 2 * kPieceRing + 11;
-    static constexpr int kPieceReaders = kRowWarps + 1 + (KV8 ? 4 : 0);               // warps
+    static constexpr int kNumBars = 2 * kRing + 2 * kRaw + 2 * kScaleRing + 2 * kPieceRing + 13;
+    static constexpr int kPieceReaders = kRowWarps + 3 + (KV8 ? 4 : 0);               // warps
     static constexpr int kTmemOff = kBarOff + kNumBars * 8;               // where the tensor memory begins
     static constexpr int kSmemBytes = kTmemOff + 8;
     static constexpr int kPlanBytes = (DA_MAX_PAGED_BATCH + 1) * 8 + DA_MAX_PAGED_BATCH * 12;
@@ -217,133 +222,181 @@ struct ChunkShape {
     static constexpr int kCols = 512, kO = 2 * kTileKeys;      // S0, S1, O0, O1
 };
 
-template <int THREADS>
-__device__ void chunk_plan(const ChunkParams& p, uint8_t* space, ChunkPlan& plan) {
-    int64_t* pre = reinterpret_cast<int64_t*>(space);                    // [B + 1] cost before a sequence
-    ChunkSeq* seqs = reinterpret_cast<ChunkSeq*>(pre + p.B + 1);         // [B]
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    constexpr int kFew = 4;                                              // items that a thread counts by itself
-    for (int b = threadIdx.x; b < p.B; b += THREADS) {
-        const ChunkSeq s = chunk_seq(p, b, blockIdx.x == 0);
-        seqs[b] = s;
-        const int items = chunk_items(p, s.n);
-        int64_t cost = 0;
-        for (int rt = 0; rt < min(items, kFew); ++rt) cost += ChunkTiles(p, s, rt).nt + kItemCost;
-        pre[b + 1] = items > kFew ? -1 : cost * p.Hkv;
-    }
-    __syncthreads();
-    for (int b = warp; b < p.B; b += THREADS / 32) {
-        if (pre[b + 1] >= 0) continue;
-        const ChunkSeq s = seqs[b];
-        int64_t cost = 0;
-        for (int rt = lane; rt < chunk_items(p, s.n); rt += 32) cost += ChunkTiles(p, s, rt).nt + kItemCost;
+__device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Cost of an item per tile and once, summed over a sequence's items of one KV head (by a warp).
+__device__ __forceinline__ int64_t chunk_cost(const ChunkParams& p, const ChunkSeq& s) {
+    int64_t cost = 0;
+    for (int rt = threadIdx.x & 31; rt < chunk_items(p, s.n); rt += 32) cost += ChunkTiles(p, s, rt).nt + kItemCost;
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) cost += __shfl_xor_sync(0xffffffffu, cost, off);
-        if (lane == 0) pre[b + 1] = cost * p.Hkv;
-    }
-    __syncthreads();
-    if (warp == 0) {
-        int64_t before = 0;
-        for (int b0 = 0; b0 < p.B; b0 += 32) {
-            int64_t run = b0 + lane < p.B ? pre[b0 + lane + 1] : 0;
+    for (int off = 16; off > 0; off >>= 1) cost += __shfl_xor_sync(0xffffffffu, cost, off);
+    return cost;
+}
+__device__ __forceinline__ int64_t scan_add(int64_t x) {
 #pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const int64_t y = __shfl_up_sync(0xffffffffu, run, off);
-                if (lane >= off) run += y;
-            }
-            if (b0 + lane < p.B) pre[b0 + lane + 1] = before + run;
-            before += __shfl_sync(0xffffffffu, run, 31);
-        }
-        if (lane == 0) pre[0] = 0;
+    for (int off = 1; off < 32; off <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, off);
+        if ((threadIdx.x & 31) >= off) x += y;
     }
-    __syncthreads();
-    const int64_t all = pre[p.B];
+    return x;
+}
+
+// Cut number r (by a warp, in all lanes alike), the sequence it lies in, and for a cut within an item what is known of
+// the cuts after it. pre(b): cost of the sequences before b; seq(b): the sequence.
+template <class Pre, class Seq>
+__device__ __forceinline__ void chunk_cut(const ChunkParams& p, int r, Pre pre, Seq seq, ChunkCut& cut, ChunkSeq& s, ChunkJoin* join) {
+    const int lane = threadIdx.x & 31;
+    const int64_t all = pre(p.B);
     const int ranges = static_cast<int>(max(int64_t(1), min(static_cast<int64_t>(gridDim.x), all / kLeastCost)));
     const int64_t q = all / ranges;
     const int rem = static_cast<int>(all - q * ranges);
-    auto raw = [&](int r) { return r * q + min(r, rem); };
-    if (warp < 2) {
-        // warp 0 the range's begin, warp 1 its end and what follows from it
-        const int r = static_cast<int>(blockIdx.x) + warp;
-        ChunkCut cut = {p.B, 0, 0, 0};
-        ChunkJoin join = {};
-        if (r < ranges && all > 0) {         // (no rows at all: no work, and nothing to divide by)
-            const int64_t at = raw(r);
-            int lo = 0, hi = p.B - 1;       // last b with pre[b] <= at
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (pre[mid] <= at) lo = mid;
-                else hi = mid - 1;
-            }
-            const ChunkSeq s = seqs[lo];
-            const int64_t head = (pre[lo + 1] - pre[lo]) / p.Hkv;
-            const int items = chunk_items(p, s.n);
-            cut.b = lo;
-            cut.kvh = static_cast<int>((at - pre[lo]) / head);
-            int64_t begin = pre[lo] + cut.kvh * head;
-            int nt = 0;
-            for (int rt0 = 0; rt0 < items; rt0 += 32) {
-                const int mine = rt0 + lane < items ? ChunkTiles(p, s, rt0 + lane).nt : 0;
-                int64_t run = mine + (rt0 + lane < items ? kItemCost : 0);
-#pragma unroll
-                for (int off = 1; off < 32; off <<= 1) {
-                    const int64_t y = __shfl_up_sync(0xffffffffu, run, off);
-                    if (lane >= off) run += y;
-                }
-                const uint32_t past = __ballot_sync(0xffffffffu, begin + run > at);
-                if (past != 0) {
-                    const int i = __ffs(past) - 1;
-                    cut.rt = rt0 + i;
-                    nt = __shfl_sync(0xffffffffu, mine, i);
-                    begin += __shfl_sync(0xffffffffu, run, i) - nt - kItemCost;
-                    break;
-                }
-                begin += __shfl_sync(0xffffffffu, run, 31);
-            }
-            cut.tile = cut_tile(static_cast<int>(at - begin), nt);
-            if (warp == 1 && cut.tile > 0 && cut.tile < nt) {
-                // the cuts of other ranges in the same item
-                int inside = 0;
-                bool more = true;
-                for (int r0 = r + 1; more; r0 += 32) {
-                    const int64_t x = r0 + lane < ranges ? raw(r0 + lane) - begin : int64_t(1) << 40;
-                    int tile = nt;
-                    if (x < nt + kItemCost) tile = cut_tile(static_cast<int>(x), nt);
-                    const uint32_t in = __ballot_sync(0xffffffffu, tile < nt);
-                    inside += __popc(in);
-                    more = in == 0xffffffffu;
-                }
-                join.parts = 2 + inside;
-                join.n = s.n;
-                join.r0 = s.r0;
-                join.kvh = cut.kvh;
-                join.rt = cut.rt;
-            }
-            if (cut.tile == nt) {            // the next item's begin
-                cut.tile = 0;
-                if (++cut.rt == items) {
-                    cut.rt = 0;
-                    if (++cut.kvh == p.Hkv) {
-                        cut.kvh = 0;
-                        do ++cut.b;
-                        while (cut.b < p.B && pre[cut.b + 1] == pre[cut.b]);
-                    }
-                }
+    auto raw = [&](int i) { return i * q + min(i, rem); };
+    cut = {p.B, 0, 0, 0};
+    s = {0, 0, 0};
+    if (r >= ranges || all == 0) return;     // (no rows at all: no work, and nothing to divide by)
+    const int64_t at = raw(r);
+    int lo = 0, hi = p.B - 1;       // last b with pre(b) <= at
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (pre(mid) <= at) lo = mid;
+        else hi = mid - 1;
+    }
+    s = seq(lo);
+    int64_t begin = pre(lo);
+    const int64_t head = (pre(lo + 1) - begin) / p.Hkv;
+    const int items = chunk_items(p, s.n);
+    cut.b = lo;
+    cut.kvh = static_cast<int>((at - begin) / head);
+    begin += cut.kvh * head;
+    int nt = 0;
+    for (int rt0 = 0; rt0 < items; rt0 += 32) {
+        const int mine = rt0 + lane < items ? ChunkTiles(p, s, rt0 + lane).nt : 0;
+        const int64_t run = scan_add(rt0 + lane < items ? mine + kItemCost : 0);
+        const uint32_t past = __ballot_sync(0xffffffffu, begin + run > at);
+        if (past != 0) {
+            const int i = __ffs(past) - 1;
+            cut.rt = rt0 + i;
+            nt = __shfl_sync(0xffffffffu, mine, i);
+            begin += __shfl_sync(0xffffffffu, run, i) - nt - kItemCost;
+            break;
+        }
+        begin += __shfl_sync(0xffffffffu, run, 31);
+    }
+    cut.tile = cut_tile(static_cast<int>(at - begin), nt);
+    if (join && cut.tile > 0 && cut.tile < nt) {
+        // the cuts of other ranges in the same item
+        int inside = 0;
+        bool more = true;
+        for (int r0 = r + 1; more; r0 += 32) {
+            const int64_t x = r0 + lane < ranges ? raw(r0 + lane) - begin : int64_t(1) << 40;
+            int tile = nt;
+            if (x < nt + kItemCost) tile = cut_tile(static_cast<int>(x), nt);
+            const uint32_t in = __ballot_sync(0xffffffffu, tile < nt);
+            inside += __popc(in);
+            more = in == 0xffffffffu;
+        }
+        join->parts = 2 + inside;
+        join->n = s.n;
+        join->r0 = s.r0;
+        join->kvh = cut.kvh;
+        join->rt = cut.rt;
+    }
+    if (cut.tile == nt) {            // the next item's begin
+        cut.tile = 0;
+        if (++cut.rt == items) {
+            cut.rt = 0;
+            if (++cut.kvh == p.Hkv) {
+                cut.kvh = 0;
+                do ++cut.b;
+                while (cut.b < p.B && pre(cut.b + 1) == pre(cut.b));
+                if (cut.b < p.B) s = seq(cut.b);
             }
         }
-        if (lane == 0) {
-            plan.cuts[warp] = cut;
-            if (warp == 1) plan.join = join;
+    }
+}
+
+// This CTA's range, by all threads; `space` is shared memory that the pipeline uses later.
+template <int THREADS>
+__device__ void chunk_plan(const ChunkParams& p, uint8_t* space, ChunkPlan& plan) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int r = static_cast<int>(blockIdx.x) + warp;       // warp 0: the range's begin, warp 1: its end
+    ChunkCut cut;
+    ChunkSeq s;
+    ChunkJoin join = {};
+    if (p.B <= 32) {
+        // a lane per sequence, in either of the two warps: nothing to wait for
+        if (warp < 2) {
+            ChunkSeq mine = {0, 0, 0};
+            if (lane < p.B) mine = chunk_seq(p, lane, blockIdx.x == 0 && warp == 0);
+            const int items = chunk_items(p, mine.n);
+            int64_t cost = 0;
+            if (items == 1) cost = ChunkTiles(p, mine, 0).nt + kItemCost;
+            uint32_t many = __ballot_sync(0xffffffffu, items > 1);
+            while (many != 0) {
+                const int b = __ffs(many) - 1;
+                many &= many - 1;
+                const ChunkSeq x = {__shfl_sync(0xffffffffu, mine.n, b), __shfl_sync(0xffffffffu, mine.L, b), 0};
+                const int64_t sum = chunk_cost(p, x);
+                if (lane == b) cost = sum;
+            }
+            const int64_t run = scan_add(cost * p.Hkv);      // (0 beyond the last sequence)
+            auto pre = [&](int b) {
+                const int64_t x = __shfl_sync(0xffffffffu, run, max(b - 1, 0));
+                return b == 0 ? int64_t(0) : x;
+            };
+            auto seq = [&](int b) {
+                return ChunkSeq{__shfl_sync(0xffffffffu, mine.n, b), __shfl_sync(0xffffffffu, mine.L, b),
+                                __shfl_sync(0xffffffffu, mine.r0, b)};
+            };
+            chunk_cut(p, r, pre, seq, cut, s, warp == 1 ? &join : nullptr);
         }
+    } else {
+        int64_t* before = reinterpret_cast<int64_t*>(space);                   // [B + 1] cost before a sequence
+        ChunkSeq* seqs = reinterpret_cast<ChunkSeq*>(before + p.B + 1);        // [B]
+        constexpr int kFew = 4;                                                // items that a thread counts by itself
+        for (int b = threadIdx.x; b < p.B; b += THREADS) {
+            const ChunkSeq x = chunk_seq(p, b, blockIdx.x == 0);
+            seqs[b] = x;
+            const int items = chunk_items(p, x.n);
+            int64_t cost = 0;
+            for (int rt = 0; rt < min(items, kFew); ++rt) cost += ChunkTiles(p, x, rt).nt + kItemCost;
+            before[b + 1] = items > kFew ? -1 : cost * p.Hkv;
+        }
+        __syncthreads();
+        for (int b = warp; b < p.B; b += THREADS / 32) {
+            if (before[b + 1] >= 0) continue;
+            const int64_t cost = chunk_cost(p, seqs[b]);
+            __syncwarp();
+            if (lane == 0) before[b + 1] = cost * p.Hkv;
+        }
+        __syncthreads();
+        if (warp == 0) {
+            int64_t sum = 0;
+            for (int b0 = 0; b0 < p.B; b0 += 32) {
+                const int64_t run = scan_add(b0 + lane < p.B ? before[b0 + lane + 1] : 0);
+                if (b0 + lane < p.B) before[b0 + lane + 1] = sum + run;
+                sum += __shfl_sync(0xffffffffu, run, 31);
+            }
+            if (lane == 0) before[0] = 0;
+        }
+        __syncthreads();
+        if (warp < 2)
+            chunk_cut(p, r, [&](int b) { return before[b]; }, [&](int b) { return seqs[b]; }, cut, s, warp == 1 ? &join : nullptr);
+        proxy_fence();                 // this memory is the ring from here on
     }
-    __syncthreads();
-    // the first part begins in this range, unless the item did in an earlier one
-    if (threadIdx.x == 0) {
-        const ChunkCut &a = plan.cuts[0], &e = plan.cuts[1];
-        const bool earlier = a.b == e.b && a.kvh == e.kvh && a.rt == e.rt && a.tile > 0;
-        if (earlier) plan.join.parts = 0;
-        p.join[blockIdx.x] = plan.join;
+    if (warp < 2 && lane == 0) {
+        plan.cuts[warp] = cut;
+        plan.seqs[warp] = s;
+        if (warp == 1) plan.join = join;
     }
+}
+
+// The split item that begins in this range, for the kernel that joins its parts (none if it began in an earlier one).
+__device__ __forceinline__ void leave_join(const ChunkParams& p, const ChunkPlan& plan) {
+    const ChunkCut &a = plan.cuts[0], &e = plan.cuts[1];
+    ChunkJoin join = plan.join;
+    if (a.b == e.b && a.kvh == e.kvh && a.rt == e.rt && a.tile > 0) join.parts = 0;
+    p.join[blockIdx.x] = join;
 }
 
 // ------------------------------------------------------------ arithmetic on pairs
@@ -386,7 +439,6 @@ __device__ __forceinline__ void tmem_st16_start(uint32_t taddr, const uint32_t (
                  : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
     uint4 x;
@@ -410,6 +462,7 @@ template <int D, int DT, bool KV8>
 struct ChunkKernel {
     using Sh = ChunkShape<D, KV8>;
     static constexpr int MT = KV8 ? DA_F16 : DT;                 // type of the products
+    static constexpr bool kRowFactors = KV8 && DT == DA_BF16;    // queries scaled to fp16, row by row
     // A weight enters its product as 2^kLift times itself and is at most 2^kHeadroom times the largest one at the
     // time that its row's reference was set; fp16 then holds all bits of a weight down to 2^-25 of the largest (bf16 any).
     static constexpr float kHeadroom = MT == DA_F16 ? 4.f : 8.f;
@@ -420,8 +473,8 @@ struct ChunkKernel {
     struct Ctx {
         uint8_t* smem;
         uint32_t base, tmem;
-        uint32_t kv_full, kv_empty, raw_full, raw_empty, sc_full, sc_empty, x_full, x_empty, q_full, s_full, p_half, p_full, pv_done, fin;
-        const ChunkCut* cuts;
+        uint32_t kv_full, kv_empty, raw_full, raw_empty, sc_full, sc_empty, x_full, x_empty, q_full, q_empty, s_full, p_half, p_full, pv_done, fin;
+        const ChunkPlan* plan;
         ChunkPiece* pieces;
     };
 
@@ -467,7 +520,7 @@ struct ChunkKernel {
         const int lane = threadIdx.x & 31;
         const int boxes = kTileKeys / p.box_keys, batch = 32 / boxes;       // tiles whose boxes the lanes look up at once
         const int my_tile = lane / boxes, my_box = lane - my_tile * boxes;
-        ChunkWalk walk(p, c.cuts);
+        ChunkWalk walk(*c.plan);
         uint32_t count = 0;                // key tiles so far
         for (uint32_t piece = 0;; ++piece) {
             ChunkPiece x;
@@ -676,6 +729,7 @@ struct ChunkKernel {
             for (int w = 0; w < 2; ++w) {
                 if (!ready(c.q_full + 8 * w, piece & 1)) return;
                 scores(w, at);
+                if (nt == 1) umma_commit_elect(c.q_empty + 8 * w);
             }
             umma_commit_elect(c.kv_empty + 8 * at);
             advance();
@@ -694,6 +748,7 @@ struct ChunkKernel {
                     if (more) {
                         if (w == 0 && !ready(c.kv_full + 8 * at, phase)) return;
                         scores(w, at);
+                        if (t + 2 == nt) umma_commit_elect(c.q_empty + 8 * w);
                         if (w == 1) {
                             umma_commit_elect(c.kv_empty + 8 * at);
                             advance();
@@ -705,50 +760,84 @@ struct ChunkKernel {
     }
 
     // ------------------------------------------------------------ rows
-    // 32 rows of tile w into shared memory, this warp's quarter of it.
-    static __device__ __forceinline__ void load_queries(const Ctx& c, const ChunkParams& p, const ChunkPiece& x, int w, int quarter) {
-        const int lane = threadIdx.x & 31;
-        constexpr int kChunks = D / 8, kPerPass = 32 / kChunks, kPasses = 32 / kPerPass;
+    // The rows' queries into shared memory, a warp per row tile, as soon as the piece before is done with its own.
+    static __device__ void queries(const Ctx& c, const ChunkParams& p, int w) {
+        constexpr int kChunks = D / 8, kPerPass = 32 / kChunks, kPasses = kTileRows / kPerPass, kBatch = 8;
+        const int lane = threadIdx.x & 31, ch = lane % kChunks, sub = lane / kChunks;
         const uint32_t tile = c.base + Sh::kQOff + w * Sh::kTileBytes;
-        const int ch = lane % kChunks, sub = lane / kChunks;
-        const int rows = x.s.n * p.G, row0 = x.rt * kItemRows + w * kTileRows + quarter * 32;
-        const uint16_t* q = p.q + static_cast<int64_t>(x.kvh) * p.G * D + ch * 8;
-        uint4 v[kPasses];
-#pragma unroll
-        for (int i = 0; i < kPasses; ++i) {
-            const int f = row0 + i * kPerPass + sub;
-            v[i] = make_uint4(0, 0, 0, 0);
-            if (f < rows) {
-                const int t = f / p.G, g = f - t * p.G;
-                v[i] = __ldg(reinterpret_cast<const uint4*>(q + (x.s.r0 + t) * p.q_stride + g * D));
+        const bool asis = !kRowFactors && p.q_and == 0xffffffffu && p.q_xor == 0;
+        for (uint32_t piece = 0;; ++piece) {
+            const ChunkPiece* x = take_piece(c, p, piece);
+            if (!x) return;
+            const int rows = x->s.n * p.G, row0 = x->rt * kItemRows + w * kTileRows;
+            const uint16_t* q = p.q + x->s.r0 * p.q_stride + static_cast<int64_t>(x->kvh) * p.G * D + ch * 8;
+            auto address = [&](int f) {
+                const int t = p.token(f);
+                return q + t * p.q_stride + (f - t * p.G) * D;
+            };
+            // (into the L2 while the tensor cores still read the tile)
+            for (int r = lane; r < kTileRows; r += 32) {
+                const int f = row0 + r;
+                if (f >= rows) break;
+                const int t = p.token(f);
+                const uint16_t* line = p.q + (x->s.r0 + t) * p.q_stride + (static_cast<int64_t>(x->kvh) * p.G + f - t * p.G) * D;
+                for (int d = 0; d < D; d += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(line + d));
             }
-        }
-#pragma unroll
-        for (int i = 0; i < kPasses; ++i) {
-            const int r = quarter * 32 + i * kPerPass + sub;
-            uint32_t e[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) e[j] = (e[j] & p.q_and) ^ p.q_xor;
-            if constexpr (KV8) {
-                float down = 1.f;
-                if constexpr (DT == DA_BF16) {
-                    uint32_t top = 0;   // largest exponent field of the row
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) top = max(top, max((e[j] >> 7) & 0xffu, (e[j] >> 23) & 0xffu));
-#pragma unroll
-                    for (int off = 1; off < kChunks; off <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
-                    // 2^e takes the largest element to [2^14, 2^15); an infinity or a NaN stays one
-                    const int field = top == 255 ? 127 : min(max(268 - static_cast<int>(top), 14), 240);
-                    const float up = __uint_as_float(static_cast<uint32_t>(field) << 23);
-                    down = __uint_as_float(static_cast<uint32_t>(254 - field) << 23);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        e[j] = pack2<DA_F16>(__uint_as_float(e[j] << 16) * up, __uint_as_float(e[j] & 0xffff0000u) * up);
+            if (!wait(p, c.q_empty + 8 * w, (piece & 1) ^ 1)) return;
+            if (asis) {
+#pragma unroll 4
+                for (int i = 0; i < kPasses; ++i) {
+                    const int r = i * kPerPass + sub, f = row0 + r;
+                    const uint16_t* from = f < rows ? address(f) : p.q;
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tile_addr(tile, r, ch)), "l"(from),
+                                 "r"(f < rows ? 16 : 0)
+                                 : "memory");
                 }
-                if (ch == 0) reinterpret_cast<float*>(c.smem + Sh::kFactorOff)[w * kTileRows + r] = down * p.scale_log2;
+                asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+            } else {
+#pragma unroll 1
+                for (int i0 = 0; i0 < kPasses; i0 += kBatch) {
+                    uint4 v[kBatch];
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) {
+                        const int f = row0 + (i0 + i) * kPerPass + sub;
+                        v[i] = f < rows ? __ldg(reinterpret_cast<const uint4*>(address(f))) : make_uint4(0, 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) put_query(c, p, v[i], w, (i0 + i) * kPerPass + sub, ch);
+                }
             }
-            sts128(tile_addr(tile, r, ch), make_uint4(e[0], e[1], e[2], e[3]));
+            proxy_fence();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(c.q_full + 8 * w);
+                drop_piece(c, piece);
+            }
         }
+    }
+
+    // 16 bytes of a query: the sign of the scale, and for 8-bit pages fp16, with a factor per row.
+    static __device__ __forceinline__ void put_query(const Ctx& c, const ChunkParams& p, const uint4& v, int w, int r, int ch) {
+        uint32_t e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) e[j] = (e[j] & p.q_and) ^ p.q_xor;
+        if constexpr (kRowFactors) {
+            uint32_t top = 0;   // largest exponent field of the row
+#pragma unroll
+            for (int j = 0; j < 4; ++j) top = max(top, max((e[j] >> 7) & 0xffu, (e[j] >> 23) & 0xffu));
+#pragma unroll
+            for (int off = 1; off < D / 8; off <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
+            // 2^e takes the largest element to [2^14, 2^15); an infinity or a NaN stays one
+            const int field = top == 255 ? 127 : min(max(268 - static_cast<int>(top), 14), 240);
+            const float up = __uint_as_float(static_cast<uint32_t>(field) << 23);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                e[j] = pack2<DA_F16>(__uint_as_float(e[j] << 16) * up, __uint_as_float(e[j] & 0xffff0000u) * up);
+            if (ch == 0)
+                reinterpret_cast<float*>(c.smem + Sh::kFactorOff)[w * kTileRows + r] =
+                    __uint_as_float(static_cast<uint32_t>(254 - field) << 23) * p.scale_log2;
+        }
+        sts128(tile_addr(c.base + Sh::kQOff + w * Sh::kTileBytes, r, ch), make_uint4(e[0], e[1], e[2], e[3]));
     }
 
     // A special tile's values, 16-bit pages (by the 128 threads of row tile 0): zeros for what no row sees and for what
@@ -857,13 +946,8 @@ struct ChunkKernel {
             ChunkPiece* const taken = take_piece(c, p, piece);
             if (!taken) return;
             ChunkPiece& x = *taken;
-            load_queries(c, p, x, w, quarter);
-            proxy_fence();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(c.q_full + 8 * w);
             float factor = p.scale_log2;
-            if constexpr (KV8) factor = reinterpret_cast<const float*>(c.smem + Sh::kFactorOff)[w * kTileRows + r];
-            const int f = x.rt * kItemRows + w * kTileRows + r, token = f / p.G;
+            const int f = x.rt * kItemRows + w * kTileRows + r, token = p.token(f);
             const bool live = f < x.s.n * p.G;
             const int pos = live ? x.s.L - x.s.n + token : -1;
             // references: scores' maximum m (16-bit pages: less kLift), and (8-bit pages) dv, how far the weights' is above it
@@ -882,6 +966,13 @@ struct ChunkKernel {
                 const float2* sc = reinterpret_cast<const float2*>(c.smem + Sh::kScaleOff) + (count % kScaleRing) * 8;
                 if constexpr (KV8) {
                     if (!wait(p, c.sc_full + 8 * (count % kScaleRing), (count / kScaleRing) & 1)) return;
+                    if (kRowFactors && first) {
+                        // (in place since before the scores; the next queries wait until it is read)
+                        if (!wait(p, c.q_full + 8 * w, piece & 1)) return;
+                        factor = reinterpret_cast<const volatile float*>(c.smem + Sh::kFactorOff)[w * kTileRows + r];
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(c.q_empty + 8 * w);
+                    }
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const float by = factor * sc[i].x;
@@ -1007,11 +1098,21 @@ struct ChunkKernel {
                 }
                 if (whole) {
                     if (live) {
-                        uint4* out = reinterpret_cast<uint4*>(p.out + row * p.out_stride + head * D + d0);
+                        uint16_t* out = p.out + row * p.out_stride + head * D + d0;
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            out[j] = make_uint4(pack2<DT>(o[8 * j] * by, o[8 * j + 1] * by), pack2<DT>(o[8 * j + 2] * by, o[8 * j + 3] * by),
-                                                pack2<DT>(o[8 * j + 4] * by, o[8 * j + 5] * by), pack2<DT>(o[8 * j + 6] * by, o[8 * j + 7] * by));
+                        for (int j = 0; j < 64; j += 16) {
+                            uint32_t y[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) y[i] = pack2<DT>(o[j + 2 * i] * by, o[j + 2 * i + 1] * by);
+                            if (p.out_wide) {      // a sector each
+                                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + j), "r"(y[0]), "r"(y[1]),
+                                             "r"(y[2]), "r"(y[3]), "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7])
+                                             : "memory");
+                            } else {
+                                *reinterpret_cast<uint4*>(out + j) = make_uint4(y[0], y[1], y[2], y[3]);
+                                *reinterpret_cast<uint4*>(out + j + 8) = make_uint4(y[4], y[5], y[6], y[7]);
+                            }
+                        }
                     }
                 } else {
                     float4* out = p.part + (static_cast<int64_t>(slot) * (D / 4) + d0 / 4) * kItemRows + w * kTileRows + r;
@@ -1058,12 +1159,13 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CU
     c.x_full = bars(kPieceRing);
     c.x_empty = bars(kPieceRing);
     c.q_full = bars(2);
+    c.q_empty = bars(2);
     c.s_full = bars(2);
     c.p_half = bars(2);
     c.p_full = bars(2);
     c.pv_done = bars(2);
     c.fin = bars(1);
-    c.cuts = plan.cuts;
+    c.plan = &plan;
     c.pieces = reinterpret_cast<ChunkPiece*>(c.smem + Sh::kPieceOff);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
     if (threadIdx.x == 0) {
@@ -1080,7 +1182,8 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CU
             mbar_init(c.sc_empty + 8 * i, Sh::kRowWarps);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(c.q_full + 8 * i, 4);
+            mbar_init(c.q_full + 8 * i, 1);
+            mbar_init(c.q_empty + 8 * i, 1 + (K::kRowFactors ? 4 : 0));
             mbar_init(c.s_full + 8 * i, 1);
             mbar_init(c.p_half + 8 * i, 4);
             mbar_init(c.p_full + 8 * i, 4);
@@ -1103,10 +1206,10 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CU
     grid_dependency_wait();
     if (threadIdx.x == 0) grid_dependents_launch();
     chunk_plan<Sh::kThreads>(p, c.smem + Sh::kRingOff, plan);
-    proxy_fence();                 // the plan's memory is the ring from here on
     tmem_fence_before_sync();
     __syncthreads();
     tmem_fence_after_sync();
+    if (threadIdx.x == 0) leave_join(p, plan);
     c.tmem = *reinterpret_cast<const volatile uint32_t*>(c.smem + Sh::kTmemOff);
     if (warp < Sh::kRowWarps) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Sh::kRowRegs));
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Sh::kOtherRegs));
@@ -1114,6 +1217,8 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CU
     else if (warp == Sh::kRowWarps) K::producer(c, p, &tmK, &tmV);
     else if (warp == Sh::kRowWarps + 1) {
         K::multiplier(c, p);
+    } else if (warp < Sh::kRowWarps + 4) {
+        K::queries(c, p, warp - Sh::kRowWarps - 2);
     }
     if constexpr (KV8) {
         if (warp >= Sh::kRowWarps + 4) K::converter(c, p);
@@ -1158,7 +1263,7 @@ __global__ void __launch_bounds__(32 * D / 16) chunk_join_kernel(const ChunkPara
     }
     const bool none = m == kNoKey && l == 0.f;
     const float by = none ? 0.f : 1.f / l;
-    const int token = f / p.G;
+    const int token = p.token(f);
     const int64_t row = join.r0 + token, head = static_cast<int64_t>(join.kvh) * p.G + (f - token * p.G);
     uint4* out = reinterpret_cast<uint4*>(p.out + row * p.out_stride + head * D + d);
 #pragma unroll
@@ -1247,11 +1352,17 @@ da_status decode_attn_paged_chunk(const da_paged_chunk* args, void* stream) {
     p.part_sum = reinterpret_cast<float2*>(p.part + static_cast<size_t>(2 * kMaxRanges) * kItemRows * (c.D / 4));
     p.q_stride = a.q_stride;
     p.out_stride = a.out_stride;
+    p.out_wide = aligned(a.out, 32) && a.out_stride % 16 == 0;
     p.B = a.B;
     p.T = a.T_new;
     p.Hq = a.Hq;
     p.Hkv = c.Hkv;
     p.G = a.Hq / c.Hkv;
+    // floor(f / G) = f * ceil(2^(31 + l) / G) >> (31 + l) for every f < 2^31, with 2^l >= G > 2^(l - 1)
+    int l = 0;
+    while ((1ll << l) < p.G) ++l;
+    p.group_shift = 31 + l;
+    p.group_mul = static_cast<uint32_t>(((1ull << p.group_shift) + p.G - 1) / p.G);
     p.P = c.page_size;
     p.max_pages = a.max_pages;
     p.table_stride = a.table_stride;
