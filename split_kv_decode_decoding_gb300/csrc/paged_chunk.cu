@@ -13,7 +13,8 @@
 //
 //     ... P0(j) V(j), Q0 K(j+1), P1(j) V(j), Q1 K(j+1), P0(j+1) V(j+1) ...
 //
-// so that the softmax of one row tile runs beside the products of the other.
+// so that the softmax of one row tile runs beside the products of the other. (At head size 64 tensor memory
+// has room for P beside S, and the next scores are computed while the softmax of these runs.)
 //
 // The work of the whole call, in units of a key tile of an item, is cut into as many equal ranges
 // as there are CTAs, one per SM, whatever the lengths, the causal triangle and the window leave of it. An item that lies in
@@ -200,9 +201,9 @@ struct ChunkShape {
     static constexpr int kSlices = D / 64;                     // 128-byte columns of a tile in 16 bits
     static constexpr int kSliceBytes = 128 * 128;
     static constexpr int kTileBytes = kSlices * kSliceBytes;
-    static constexpr int kRing = KV8 ? 3 : (D == 128 ? 5 : 8); // K and V tiles in 16 bits
+    static constexpr int kRing = D == 64 ? 8 : KV8 ? 4 : 5;    // K and V tiles in 16 bits
     static constexpr int kRawBytes = KV8 ? kTileKeys * D : 0;  // and as they come, in 8
-    static constexpr int kRaw = KV8 ? (D == 128 ? 4 : 6) : 0;
+    static constexpr int kRaw = KV8 ? (D == 128 ? 2 : 4) : 0;
     static constexpr int kRawRow = D;
     static constexpr int kQOff = 0;
     static constexpr int kRingOff = 2 * kTileBytes;
@@ -212,14 +213,19 @@ struct ChunkShape {
     static constexpr int kPieceOff = kFactorOff + (KV8 ? kItemRows * 4 : 0);
     static constexpr int kPlanOff = kPieceOff + (kPieceRing * static_cast<int>(sizeof(ChunkPiece)) + 7) / 8 * 8;
     static constexpr int kBarOff = kPlanOff + (static_cast<int>(sizeof(ChunkPlan)) + 7) / 8 * 8;
-    static constexpr int kNumBars = 2 * kRing + 2 * kRaw + 2 * kScaleRing + 2 * kPieceRing + 13;
+    static constexpr int kNumBars = 2 * kRing + 2 * kRaw + 2 * kScaleRing + 2 * kPieceRing + 15;
     static constexpr int kPieceReaders = kRowWarps + 3 + (KV8 ? 4 : 0);               // warps
     static constexpr int kTmemOff = kBarOff + kNumBars * 8;               // where the tensor memory begins
     static constexpr int kSmemBytes = kTmemOff + 8;
     static constexpr int kPlanBytes = (DA_MAX_PAGED_BATCH + 1) * 8 + DA_MAX_PAGED_BATCH * 12;
     static_assert(kPlanBytes <= kRing * kTileBytes, "the plan is made where the ring is later");
     // tensor memory
-    static constexpr int kCols = 512, kO = 2 * kTileKeys;      // S0, S1, O0, O1
+    // S0, S1, O0, O1 and, where there is room (head size 64), P0 and P1: the next scores then need not wait for the
+    // products of these weights. Otherwise P lies where S was.
+    static constexpr int kCols = 512, kO = 2 * kTileKeys;
+    static constexpr bool kApart = D == 64;
+    static constexpr int kP = kApart ? kO + 2 * D : 0, kPStep = kApart ? kTileKeys / 2 : kTileKeys;
+    static_assert(!kApart || kP + 2 * kPStep <= kCols, "tensor memory");
 };
 
 __device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -473,7 +479,7 @@ struct ChunkKernel {
     struct Ctx {
         uint8_t* smem;
         uint32_t base, tmem;
-        uint32_t kv_full, kv_empty, raw_full, raw_empty, sc_full, sc_empty, x_full, x_empty, q_full, q_empty, s_full, p_half, p_full, pv_done, fin;
+        uint32_t kv_full, kv_empty, raw_full, raw_empty, sc_full, sc_empty, x_full, x_empty, q_full, q_empty, s_full, s_free, p_half, p_full, pv_done, fin;
         const ChunkPlan* plan;
         ChunkPiece* pieces;
     };
@@ -621,49 +627,50 @@ struct ChunkKernel {
                 for (int kv = 0; kv < 2; ++kv, ++slot) {
                     const int from = slot % Sh::kRaw, to = slot % Sh::kRing;
                     if (!wait(p, c.raw_full + 8 * from, (slot / Sh::kRaw) & 1)) return;
-                    if (!wait(p, c.kv_empty + 8 * to, ((slot / Sh::kRing) & 1) ^ 1)) return;
-                    const uint32_t src = c.base + Sh::kRawOff + from * Sh::kRawBytes, dst = ring(c, to);
-                    const bool clean = kv == 1 && !plain;
-                    uint32_t found = 0;
+                    const uint32_t src = c.base + Sh::kRawOff + from * Sh::kRawBytes;
                     constexpr int kPer = kTileKeys * kChunks / 128;    // chunks per thread
+                    uint4 in[kPer];
 #pragma unroll
-                    for (int i0 = 0; i0 < kPer; i0 += 4) {
-                        uint4 w[4];
+                    for (int i = 0; i < kPer; ++i) {
+                        const int u = i * 128 + tid, r = u / kChunks, ch = u % kChunks;
+                        const int sw = kChunks == 8 ? r & 7 : (r >> 1) & 3;    // the copy's swizzle
+                        in[i] = lds128(src + r * Sh::kRawRow + ((ch ^ sw) << 4));
+                    }
+                    uint32_t found = 0;
+                    if (kv == 1 && !plain) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int u = (i0 + i) * 128 + tid, r = u / kChunks, ch = u % kChunks;
-                            const int sw = kChunks == 8 ? r & 7 : (r >> 1) & 3;    // the copy's swizzle
-                            w[i] = lds128(src + r * Sh::kRawRow + ((ch ^ sw) << 4));
-                        }
+                        for (int i = 0; i < kPer; ++i) {
+                            const bool seen = tiles.wanted(p, k0 + (i * 128 + tid) / kChunks, 1);
+                            uint32_t* e = &in[i].x;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int u = (i0 + i) * 128 + tid, r = u / kChunks, ch = u % kChunks;
-                            uint32_t in[4] = {w[i].x, w[i].y, w[i].z, w[i].w}, o[8];
-                            if (clean) {
-                                const bool seen = tiles.wanted(p, k0 + r, 1);
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) {
-                                    const uint32_t bad = __vcmpeq4(in[j] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                                    if (seen) found |= bad;
-                                    in[j] = seen ? in[j] & ~bad : 0u;
-                                }
+                            for (int j = 0; j < 4; ++j) {
+                                const uint32_t bad = __vcmpeq4(e[j] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                                if (seen) found |= bad;
+                                e[j] = seen ? e[j] & ~bad : 0u;
                             }
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) e4m3x4_to_f16(in[j], o[2 * j], o[2 * j + 1]);
-                            const uint4 a = make_uint4(o[0], o[1], o[2], o[3]), b = make_uint4(o[4], o[5], o[6], o[7]);
-                            // lanes of the two slices write their halves in opposite order, which spreads the banks
-                            const bool second = kChunks == 8 && ch >= 4;
-                            sts128(tile_addr(dst, r, 2 * ch + (second ? 1 : 0)), second ? b : a);
-                            sts128(tile_addr(dst, r, 2 * ch + (second ? 0 : 1)), second ? a : b);
                         }
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(c.raw_empty + 8 * from);
+                    if (!wait(p, c.kv_empty + 8 * to, ((slot / Sh::kRing) & 1) ^ 1)) return;
+                    const uint32_t dst = ring(c, to);
+#pragma unroll
+                    for (int i = 0; i < kPer; ++i) {
+                        const int u = i * 128 + tid, r = u / kChunks, ch = u % kChunks;
+                        uint4 a, b;
+                        e4m3x4_to_f16(in[i].x, a.x, a.y);
+                        e4m3x4_to_f16(in[i].y, a.z, a.w);
+                        e4m3x4_to_f16(in[i].z, b.x, b.y);
+                        e4m3x4_to_f16(in[i].w, b.z, b.w);
+                        // lanes of the two slices write their halves in opposite order, which spreads the banks
+                        const bool second = kChunks == 8 && ch >= 4;
+                        sts128(tile_addr(dst, r, 2 * ch + (second ? 1 : 0)), second ? b : a);
+                        sts128(tile_addr(dst, r, 2 * ch + (second ? 0 : 1)), second ? a : b);
                     }
                     if (found) x->dirty = 1;
                     proxy_fence();
                     __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(c.raw_empty + 8 * from);
-                        mbar_arrive(c.kv_full + 8 * to);
-                    }
+                    if (lane == 0) mbar_arrive(c.kv_full + 8 * to);
                 }
             }
             __syncwarp();
@@ -713,7 +720,7 @@ struct ChunkKernel {
 #pragma unroll
             for (int j = 0; j < kTileKeys / 32; ++j) {
                 const int k = half * (kTileKeys / 32) + j;
-                umma_ts_elect(tmem + Sh::kO + w * D, tmem + w * kTileKeys + k * 8, vd + ((k * 16 * 128) >> 4), kIdPV, !(first && k == 0));
+                umma_ts_elect(tmem + Sh::kO + w * D, tmem + Sh::kP + w * Sh::kPStep + k * 8, vd + ((k * 16 * 128) >> 4), kIdPV, !(first && k == 0));
             }
             if (half == 1) umma_commit_elect(c.pv_done + 8 * w);
         };
@@ -734,10 +741,22 @@ struct ChunkKernel {
             umma_commit_elect(c.kv_empty + 8 * at);
             advance();
             for (int t = 0; t < nt; ++t, ++tiles) {
-                const uint32_t v = at;
+                const uint32_t v = at, v_phase = phase;
                 const bool more = t + 1 < nt;
-                if (!ready(c.kv_full + 8 * v, phase)) return;
                 advance();
+                const uint32_t k = at;
+                if (Sh::kApart && more) {
+                    // the next scores as soon as these are read
+                    if (!ready(c.kv_full + 8 * k, phase)) return;
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) {
+                        if (!ready(c.s_free + 8 * w, tiles & 1)) return;
+                        scores(w, k);
+                        if (t + 2 == nt) umma_commit_elect(c.q_empty + 8 * w);
+                    }
+                    umma_commit_elect(c.kv_empty + 8 * k);
+                }
+                if (!ready(c.kv_full + 8 * v, v_phase)) return;
 #pragma unroll
                 for (int w = 0; w < 2; ++w) {
                     if (!ready(c.p_half + 8 * w, tiles & 1)) return;
@@ -745,16 +764,14 @@ struct ChunkKernel {
                     if (!ready(c.p_full + 8 * w, tiles & 1)) return;
                     weigh(w, v, 1, false);
                     if (w == 1) umma_commit_elect(c.kv_empty + 8 * v);
-                    if (more) {
-                        if (w == 0 && !ready(c.kv_full + 8 * at, phase)) return;
-                        scores(w, at);
+                    if (!Sh::kApart && more) {
+                        if (w == 0 && !ready(c.kv_full + 8 * k, phase)) return;
+                        scores(w, k);
                         if (t + 2 == nt) umma_commit_elect(c.q_empty + 8 * w);
-                        if (w == 1) {
-                            umma_commit_elect(c.kv_empty + 8 * at);
-                            advance();
-                        }
+                        if (w == 1) umma_commit_elect(c.kv_empty + 8 * k);
                     }
                 }
+                if (more) advance();
             }
         }
     }
@@ -940,7 +957,7 @@ struct ChunkKernel {
     static __device__ void rows(const Ctx& c, const ChunkParams& p) {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-        const uint32_t ts = c.tmem + lanes + w * kTileKeys, to = c.tmem + lanes + Sh::kO + w * D;
+        const uint32_t ts = c.tmem + lanes + w * kTileKeys, tp = c.tmem + lanes + Sh::kP + w * Sh::kPStep, to = c.tmem + lanes + Sh::kO + w * D;
         uint32_t count = 0;            // key tiles so far
         for (uint32_t piece = 0;; ++piece) {
             ChunkPiece* const taken = take_piece(c, p, piece);
@@ -963,6 +980,11 @@ struct ChunkKernel {
                 tmem_ld_wait();
 #pragma unroll
                 for (int i = 0; i < 4; ++i) hold32(s + 32 * i);
+                if constexpr (Sh::kApart) {
+                    tmem_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(c.s_free + 8 * w);
+                }
                 const float2* sc = reinterpret_cast<const float2*>(c.smem + Sh::kScaleOff) + (count % kScaleRing) * 8;
                 if constexpr (KV8) {
                     if (!wait(p, c.sc_full + 8 * (count % kScaleRing), (count / kScaleRing) & 1)) return;
@@ -1031,6 +1053,13 @@ struct ChunkKernel {
                         if (clean_values(p, x.tiles, x.tiles.key(t), ring(c, v % Sh::kRing))) x.dirty = 1;
                     }
                 }
+                if constexpr (Sh::kApart) {
+                    // the weights before are no longer read
+                    if (!first) {
+                        if (!wait(p, c.pv_done + 8 * w, (count - 1) & 1)) return;
+                        tmem_fence_after_sync();
+                    }
+                }
                 uint64_t sum0 = 0, sum1 = 0;
                 float lift = 1.f;
                 const uint64_t by2 = pair(factor, factor), m2 = pair(-m, -m);
@@ -1055,7 +1084,7 @@ struct ChunkKernel {
                         }
                         o[j / 2] = pack2<MT>(a, b);
                     }
-                    tmem_st16_start(ts + 16 * i, o);
+                    tmem_st16_start(tp + 16 * i, o);
                     if (i == 1) {
                         tmem_st_wait();
                         tmem_fence_before_sync();
@@ -1161,6 +1190,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CU
     c.q_full = bars(2);
     c.q_empty = bars(2);
     c.s_full = bars(2);
+    c.s_free = bars(2);
     c.p_half = bars(2);
     c.p_full = bars(2);
     c.pv_done = bars(2);
@@ -1185,6 +1215,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CU
             mbar_init(c.q_full + 8 * i, 1);
             mbar_init(c.q_empty + 8 * i, 1 + (K::kRowFactors ? 4 : 0));
             mbar_init(c.s_full + 8 * i, 1);
+            mbar_init(c.s_free + 8 * i, 4);
             mbar_init(c.p_half + 8 * i, 4);
             mbar_init(c.p_full + 8 * i, 4);
             mbar_init(c.pv_done + 8 * i, 1);
