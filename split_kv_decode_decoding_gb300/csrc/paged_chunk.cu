@@ -455,6 +455,12 @@ __device__ __forceinline__ void sts128(uint32_t a, uint4 x) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // 0 times two 16-bit elements, added to y.
 template <int DT>
 __device__ __forceinline__ uint32_t zero_times(uint32_t x, uint32_t y) {
@@ -732,13 +738,17 @@ struct ChunkKernel {
             if ((threadIdx.x & 31) == 0) drop_piece(c, piece);
             // the ring: K, V, K, V ...
             if (!ready(c.kv_full + 8 * at, phase)) return;
+            const uint32_t begin = at;
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
+                // (Where the next scores do not wait for products, the second row tile begins half a softmax after the first
+                // and stays behind it: both at once would take turns at the same units, exponents here, maxima there.)
+                if (Sh::kApart && w == 1 && !ready(c.p_half, tiles & 1)) return;
                 if (!ready(c.q_full + 8 * w, piece & 1)) return;
-                scores(w, at);
+                scores(w, begin);
                 if (nt == 1) umma_commit_elect(c.q_empty + 8 * w);
             }
-            umma_commit_elect(c.kv_empty + 8 * at);
+            umma_commit_elect(c.kv_empty + 8 * begin);
             advance();
             for (int t = 0; t < nt; ++t, ++tiles) {
                 const uint32_t v = at, v_phase = phase;
@@ -945,13 +955,13 @@ struct ChunkKernel {
     }
 
     static __device__ __forceinline__ float max16(const float* s) {
-        float a = fmaxf(s[0], s[1]), b = fmaxf(s[2], s[3]);
+        float a = s[0], b = s[1];
 #pragma unroll
-        for (int j = 4; j < 16; j += 4) {
-            a = fmaxf(a, fmaxf(s[j], s[j + 1]));
-            b = fmaxf(b, fmaxf(s[j + 2], s[j + 3]));
+        for (int j = 2; j < 14; j += 4) {
+            a = max3(a, s[j], s[j + 1]);
+            b = max3(b, s[j + 2], s[j + 3]);
         }
-        return fmaxf(a, b);
+        return fmaxf(max3(a, s[14], s[15]), b);
     }
 
     static __device__ void rows(const Ctx& c, const ChunkParams& p) {
@@ -1018,7 +1028,7 @@ struct ChunkKernel {
                 float top[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) top[i] = max16(s + 16 * i);
-                float best = fmaxf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), fmaxf(fmaxf(top[4], top[5]), fmaxf(top[6], top[7])));
+                float best = max3(max3(top[0], top[1], top[2]), max3(top[3], top[4], top[5]), fmaxf(top[6], top[7]));
                 if constexpr (KV8) {
                     // a weight that is too large moves the references as a score does
                     bool move = best - m > kHeadroom;
