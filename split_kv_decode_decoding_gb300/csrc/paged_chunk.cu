@@ -501,6 +501,14 @@ struct ChunkKernel {
         return ok;
     }
 
+    // wait, for warps that are not in a hurry: each question reads shared memory, of which the 8-bit kernel has no time to
+    // spare (4096 of 32768 tokens 1992 us with the queries' warps asking all the time, 1827 so).
+    template <int NS>
+    static __device__ __forceinline__ bool wait_calmly(const ChunkParams& p, uint32_t bar, uint32_t parity) {
+        for (int i = 0; i < 10000 && !mbar_try_wait(bar, parity); ++i) __nanosleep(NS);
+        return wait(p, bar, parity);
+    }
+
     // Piece number i, or nullptr after the last one (or a wait that timed out); it is given back with drop_piece.
     static __device__ __forceinline__ ChunkPiece* take_piece(const Ctx& c, const ChunkParams& p, uint32_t i) {
         const bool ok = wait_lane(c.x_full + 8 * (i % kPieceRing), (i / kPieceRing) & 1, p.wait_limit_ns);
@@ -539,7 +547,7 @@ struct ChunkKernel {
             x.valid = 0;
             walk.next(p, x);
             const int place = piece % kPieceRing;
-            if (!wait(p, c.x_empty + 8 * place, ((piece / kPieceRing) & 1) ^ 1)) return false;
+            if (!wait_calmly<500>(p, c.x_empty + 8 * place, ((piece / kPieceRing) & 1) ^ 1)) return false;
             if (lane == 0) {
                 c.pieces[place] = x;
                 mbar_arrive(c.x_full + 8 * place);
@@ -578,7 +586,7 @@ struct ChunkKernel {
                     const int from = (t - t0) * boxes;      // this tile's lanes
                     if constexpr (KV8) {
                         const int at = count % kScaleRing;
-                        if (!wait(p, c.sc_empty + 8 * at, ((count / kScaleRing) & 1) ^ 1)) return false;
+                        if (!wait_calmly<100>(p, c.sc_empty + 8 * at, ((count / kScaleRing) & 1) ^ 1)) return false;
                         const int owner = (from + (lane * 16) / p.box_keys) & 31;
                         const float a = __shfl_sync(0xffffffffu, ks, owner), b = __shfl_sync(0xffffffffu, lv, owner);
                         if (lane < 8) reinterpret_cast<float2*>(c.smem + Sh::kScaleOff)[at * 8 + lane] = make_float2(a, b);
@@ -596,7 +604,7 @@ struct ChunkKernel {
 #pragma unroll
                     for (int kv = 0; kv < 2; ++kv, ++slot) {
                         const int at = slot % kSlots;
-                        if (!wait(p, empty + 8 * at, ((slot / kSlots) & 1) ^ 1)) return false;
+                        if (!wait_calmly<KV8 ? 20 : 100>(p, empty + 8 * at, ((slot / kSlots) & 1) ^ 1)) return false;
                         const uint32_t bar = full + 8 * at;
                         if (lane == 0) mbar_arrive_expect_tx(bar, kBytes);
                         __syncwarp();
@@ -810,7 +818,7 @@ struct ChunkKernel {
                 const uint16_t* line = p.q + (x->s.r0 + t) * p.q_stride + (static_cast<int64_t>(x->kvh) * p.G + f - t * p.G) * D;
                 for (int d = 0; d < D; d += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(line + d));
             }
-            if (!wait(p, c.q_empty + 8 * w, (piece & 1) ^ 1)) return;
+            if (!wait_calmly<500>(p, c.q_empty + 8 * w, (piece & 1) ^ 1)) return;
             if (asis) {
 #pragma unroll 4
                 for (int i = 0; i < kPasses; ++i) {
