@@ -795,59 +795,70 @@ struct ChunkKernel {
     }
 
     // ------------------------------------------------------------ rows
-    // The rows' queries into shared memory, a warp per row tile, as soon as the piece before is done with its own.
-    static __device__ void queries(const Ctx& c, const ChunkParams& p, int w) {
-        constexpr int kChunks = D / 8, kPerPass = 32 / kChunks, kPasses = kTileRows / kPerPass, kBatch = 8;
+    // Queries of rows first .. first + ROWS - 1 of tile w into shared memory, by a warp.
+    template <int ROWS>
+    static __device__ __forceinline__ void fetch_queries(const Ctx& c, const ChunkParams& p, const ChunkPiece& x, int w, int first) {
+        constexpr int kChunks = D / 8, kPerPass = 32 / kChunks, kPasses = ROWS / kPerPass, kBatch = 8;
         const int lane = threadIdx.x & 31, ch = lane % kChunks, sub = lane / kChunks;
         const uint32_t tile = c.base + Sh::kQOff + w * Sh::kTileBytes;
         const bool asis = !kRowFactors && p.q_and == 0xffffffffu && p.q_xor == 0;
+        const int rows = x.s.n * p.G;
+        int f = x.rt * kItemRows + w * kTileRows + first + sub, t = p.token(f), g = f - t * p.G;
+        const uint16_t* q = p.q + (x.s.r0 + t) * p.q_stride + static_cast<int64_t>(x.kvh) * p.G * D + ch * 8;   // of token t
+        auto next = [&]() {            // kPerPass rows on
+            f += kPerPass;
+            g += kPerPass;
+            while (g >= p.G) {
+                g -= p.G;
+                q += p.q_stride;
+            }
+        };
+        if (asis) {
+#pragma unroll 4
+            for (int i = 0; i < kPasses; ++i, next()) {
+                const bool live = f < rows;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tile_addr(tile, first + i * kPerPass + sub, ch)),
+                             "l"(live ? q + g * D : p.q), "r"(live ? 16 : 0)
+                             : "memory");
+            }
+            asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+        } else {
+#pragma unroll 1
+            for (int i0 = 0; i0 < kPasses; i0 += kBatch) {
+                uint4 v[kBatch];
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i, next())
+                    v[i] = f < rows ? __ldg(reinterpret_cast<const uint4*>(q + g * D)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) put_query(c, p, v[i], w, first + (i0 + i) * kPerPass + sub, ch);
+            }
+        }
+        proxy_fence();
+        __syncwarp();
+    }
+
+    // The queries of every piece but the first (which the rows' warps fetch, four of them a tile), a warp per row tile, as
+    // soon as the piece before is done with its own.
+    static __device__ void queries(const Ctx& c, const ChunkParams& p, int w) {
+        const int lane = threadIdx.x & 31;
         for (uint32_t piece = 0;; ++piece) {
             const ChunkPiece* x = take_piece(c, p, piece);
             if (!x) return;
-            const int rows = x->s.n * p.G, row0 = x->rt * kItemRows + w * kTileRows;
-            const uint16_t* q = p.q + x->s.r0 * p.q_stride + static_cast<int64_t>(x->kvh) * p.G * D + ch * 8;
-            auto address = [&](int f) {
-                const int t = p.token(f);
-                return q + t * p.q_stride + (f - t * p.G) * D;
-            };
-            // (into the L2 while the tensor cores still read the tile)
-            for (int r = lane; r < kTileRows; r += 32) {
-                const int f = row0 + r;
-                if (f >= rows) break;
-                const int t = p.token(f);
-                const uint16_t* line = p.q + (x->s.r0 + t) * p.q_stride + (static_cast<int64_t>(x->kvh) * p.G + f - t * p.G) * D;
-                for (int d = 0; d < D; d += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(line + d));
-            }
-            if (!wait_calmly<500>(p, c.q_empty + 8 * w, (piece & 1) ^ 1)) return;
-            if (asis) {
-#pragma unroll 4
-                for (int i = 0; i < kPasses; ++i) {
-                    const int r = i * kPerPass + sub, f = row0 + r;
-                    const uint16_t* from = f < rows ? address(f) : p.q;
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tile_addr(tile, r, ch)), "l"(from),
-                                 "r"(f < rows ? 16 : 0)
-                                 : "memory");
+            if (piece > 0) {
+                // (into the L2 while the tensor cores still read the tile)
+                for (int r = lane; r < kTileRows; r += 32) {
+                    const int f = x->rt * kItemRows + w * kTileRows + r;
+                    if (f >= x->s.n * p.G) break;
+                    const int t = p.token(f);
+                    const uint16_t* line = p.q + (x->s.r0 + t) * p.q_stride + (static_cast<int64_t>(x->kvh) * p.G + f - t * p.G) * D;
+                    for (int d = 0; d < D; d += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(line + d));
                 }
-                asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
-            } else {
-#pragma unroll 1
-                for (int i0 = 0; i0 < kPasses; i0 += kBatch) {
-                    uint4 v[kBatch];
-#pragma unroll
-                    for (int i = 0; i < kBatch; ++i) {
-                        const int f = row0 + (i0 + i) * kPerPass + sub;
-                        v[i] = f < rows ? __ldg(reinterpret_cast<const uint4*>(address(f))) : make_uint4(0, 0, 0, 0);
-                    }
-#pragma unroll
-                    for (int i = 0; i < kBatch; ++i) put_query(c, p, v[i], w, (i0 + i) * kPerPass + sub, ch);
-                }
+                if (!wait_calmly<500>(p, c.q_empty + 8 * w, (piece & 1) ^ 1)) return;
+                fetch_queries<kTileRows>(c, p, *x, w, 0);
+                if (lane < 4) mbar_arrive(c.q_full + 8 * w);
             }
-            proxy_fence();
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(c.q_full + 8 * w);
-                drop_piece(c, piece);
-            }
+            if (lane == 0) drop_piece(c, piece);
         }
     }
 
@@ -981,6 +992,10 @@ struct ChunkKernel {
             ChunkPiece* const taken = take_piece(c, p, piece);
             if (!taken) return;
             ChunkPiece& x = *taken;
+            if (piece == 0) {
+                fetch_queries<32>(c, p, x, w, quarter * 32);
+                if (lane == 0) mbar_arrive(c.q_full + 8 * w);
+            }
             float factor = p.scale_log2;
             const int f = x.rt * kItemRows + w * kTileRows + r, token = p.token(f);
             const bool live = f < x.s.n * p.G;
@@ -1161,15 +1176,15 @@ struct ChunkKernel {
                             }
                         }
                     }
-                } else {
+                } else if (live) {
                     float4* out = p.part + (static_cast<int64_t>(slot) * (D / 4) + d0 / 4) * kItemRows + w * kTileRows + r;
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
                         out[j * kItemRows] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
                 }
             }
-            if (!whole) p.part_sum[static_cast<int64_t>(slot) * kItemRows + w * kTileRows + r] = make_float2(m, l);
-            else if (p.lse != nullptr && live) p.lse[row * p.Hq + head] = none ? -INFINITY : (m + fast_log2(l)) * kLn2;
+            if (!whole && live) p.part_sum[static_cast<int64_t>(slot) * kItemRows + w * kTileRows + r] = make_float2(m, l);
+            if (whole && p.lse != nullptr && live) p.lse[row * p.Hq + head] = none ? -INFINITY : (m + fast_log2(l)) * kLn2;
             tmem_fence_before_sync();
             __syncwarp();
             if (lane == 0) drop_piece(c, piece);
@@ -1230,7 +1245,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CU
             mbar_init(c.sc_empty + 8 * i, Sh::kRowWarps);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(c.q_full + 8 * i, 1);
+            mbar_init(c.q_full + 8 * i, 4);
             mbar_init(c.q_empty + 8 * i, 1 + (K::kRowFactors ? 4 : 0));
             mbar_init(c.s_full + 8 * i, 1);
             mbar_init(c.s_free + 8 * i, 4);
