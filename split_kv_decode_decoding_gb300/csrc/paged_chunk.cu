@@ -38,9 +38,9 @@ constexpr int kTileRows = 128;
 constexpr int kItemRows = 2 * kTileRows;
 constexpr int kTileKeys = 128;
 constexpr int kMaxRanges = 160;       // CTAs at most (GB300 has 152 SMs)
-constexpr int kItemCost = 2;          // an item's begin and end, in key tiles
-constexpr int kLeastCost = 6;         // of a range
-constexpr int kLeastPart = 2;         // key tiles of a partial result at least
+constexpr int kItemCost = 4;          // an item's begin and end, in key tiles
+constexpr int kLeastCost = 7;         // of a range
+constexpr int kLeastPart = 1;         // key tiles of a partial result at least
 constexpr int kScaleRing = 4;         // tiles whose scales are in shared memory
 constexpr int kPieceRing = 4;         // pieces whose description is
 constexpr int kJoinSlices = 8;        // blocks that join one split item, 32 rows each
@@ -454,6 +454,9 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
 __device__ __forceinline__ void sts128(uint32_t a, uint4 x) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
 }
+
+// Bits 0 .. n - 1 (any n).
+__device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
@@ -1002,10 +1005,11 @@ struct ChunkKernel {
             const int pos = live ? x.s.L - x.s.n + token : -1;
             // references: scores' maximum m (16-bit pages: less kLift), and (8-bit pages) dv, how far the weights' is above it
             float m = kNoKey, dv = 0.f, l = 0.f;
+            bool asked = false;            // the scores of the coming tile are known to be there
             const int t0 = x.t0, t1 = x.t1, plain0 = x.tiles.from, plain1 = x.tiles.to;
             for (int t = t0; t < t1; ++t, ++count) {
                 const bool plain = t >= plain0 && t < plain1, first = t == t0;
-                if (!wait(p, c.s_full + 8 * w, count & 1)) return;
+                if (!(Sh::kApart && asked) && !wait(p, c.s_full + 8 * w, count & 1)) return;
                 tmem_fence_after_sync();
                 float s[kTileKeys];
 #pragma unroll
@@ -1013,7 +1017,9 @@ struct ChunkKernel {
                 tmem_ld_wait();
 #pragma unroll
                 for (int i = 0; i < 4; ++i) hold32(s + 32 * i);
+                bool done = first;       // the weights before are no longer read (asked here, needed after the maxima)
                 if constexpr (Sh::kApart) {
+                    if (!first) done = mbar_try_wait(c.pv_done + 8 * w, (count - 1) & 1);
                     tmem_fence_before_sync();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(c.s_free + 8 * w);
@@ -1044,7 +1050,11 @@ struct ChunkKernel {
                     } else {
                         const int low = max(pos, 0) - p.window + 1 - k0, sink = p.sinks - k0;
 #pragma unroll
-                        for (int i = 0; i < kTileKeys; ++i) s[i] = i <= hi && (i >= low || i < sink) ? s[i] : -INFINITY;
+                        for (int i = 0; i < kTileKeys; i += 32) {      // a bit per key: two instructions for each, not four
+                            const uint32_t seen = bits_below(hi + 1 - i) & (~bits_below(low - i) | bits_below(sink - i));
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) s[i + j] = seen & (1u << j) ? s[i + j] : -INFINITY;
+                        }
                     }
                 }
                 // maxima of 16 keys, the size of the smallest page
@@ -1087,11 +1097,8 @@ struct ChunkKernel {
                     }
                 }
                 if constexpr (Sh::kApart) {
-                    // the weights before are no longer read
-                    if (!first) {
-                        if (!wait(p, c.pv_done + 8 * w, (count - 1) & 1)) return;
-                        tmem_fence_after_sync();
-                    }
+                    if (!__all_sync(0xffffffffu, done) && !wait(p, c.pv_done + 8 * w, (count - 1) & 1)) return;
+                    tmem_fence_after_sync();
                 }
                 uint64_t sum0 = 0, sum1 = 0;
                 float lift = 1.f;
@@ -1125,9 +1132,11 @@ struct ChunkKernel {
                         if (lane == 0) mbar_arrive(c.p_half + 8 * w);
                     }
                 }
+                if constexpr (Sh::kApart) asked = mbar_try_wait(c.s_full + 8 * w, (count + 1) & 1) && t + 1 < t1;   // the next scores
                 tmem_st_wait();
                 tmem_fence_before_sync();
                 __syncwarp();
+                if constexpr (Sh::kApart) asked = __all_sync(0xffffffffu, asked);
                 if (lane == 0) {
                     mbar_arrive(c.p_full + 8 * w);
                     if constexpr (KV8) mbar_arrive(c.sc_empty + 8 * (count % kScaleRing));
