@@ -20,7 +20,7 @@ constexpr int kCopyUnits = 4;                                  // 16-byte units 
 constexpr int kCopyChunk = kPageThreads * kCopyUnits;          // units per chunk
 constexpr int kOneThreads = 1024;                              // of the block that plans alone
 constexpr int kOneWords = 8192;                                // words of its bitmap
-constexpr int kRowEntries = 1024;                              // block-table entries that a warp takes at a time
+constexpr int kRowEntries = 128;                               // block-table entries that a warp takes at a time
 
 struct RowsParams {
     const int32_t* lens;
@@ -66,7 +66,15 @@ __device__ __forceinline__ void mark_pages(const RowsParams& p, uint32_t* bits) 
     }
 }
 
+// (A kernel of its own, not a memset: each of the kernels here is launched before the one in front of it has ended.)
+__global__ void __launch_bounds__(kPageThreads) page_clear_kernel(uint32_t* bits, int words) {
+    grid_dependency_wait();
+    if (threadIdx.x == 0) grid_dependents_launch();
+    for (int w = blockIdx.x * kPageThreads + threadIdx.x; w < words; w += gridDim.x * kPageThreads) bits[w] = 0;
+}
+
 __global__ void __launch_bounds__(kPageThreads) page_mark_kernel(const RowsParams p, uint32_t* bits) {
+    grid_dependency_wait();
     if (threadIdx.x == 0) grid_dependents_launch();
     mark_pages<kPageThreads>(p, bits);
 }
@@ -232,65 +240,63 @@ struct ForkParams {
     int64_t page_units;
 };
 
-// One block per (child, piece of its work): the first pieces copy the row, the others the tokens of its last page.
-__global__ void __launch_bounds__(kPageThreads) page_fork_kernel(const ForkParams p) {
+// A block per (child, share of its work): what it has to know of the child is four loads that wait for one another, so it
+// then copies all its chunks, `split` of them apart.
+__global__ void __launch_bounds__(kPageThreads, 6) page_fork_kernel(const ForkParams p, int split) {
     grid_dependency_wait();
     if (threadIdx.x == 0) grid_dependents_launch();
     const RowsParams& r = p.rows;
-    const int row_pieces = (r.max_pages + kRowEntries - 1) / kRowEntries;
-    const int64_t chunks = (p.page_units + kCopyChunk - 1) / kCopyChunk;
-    const int64_t per = row_pieces + 2 * chunks, items = per * p.n_out;
+    const int64_t items = static_cast<int64_t>(p.n_out) * split;
     for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
-        const int child = static_cast<int>(i / per);
-        const int64_t piece = i - child * per;
+        const int child = static_cast<int>(i / split), share = static_cast<int>(i - static_cast<int64_t>(child) * split);
         const int parent = ld_cg_s32(p.parents + child), fresh = ld_cg_s32(p.new_pages + child);
         int len = 0;
         if (parent >= 0 && parent < r.B) len = r.length(parent);
-        else if (piece == 0 && threadIdx.x == 0) flag_error(r.err, DA_DEVERR_SEQLENS);
+        else if (share == 0 && threadIdx.x == 0) flag_error(r.err, DA_DEVERR_SEQLENS);
         const int pages = (len + r.P - 1) / r.P, used = len - (pages - 1) * r.P;   // tokens of the last page
-        const bool own = fresh >= 0 && len > 0 && used < r.P;
+        const bool own = fresh >= 0 && len > 0 && used < r.P, writable = own && fresh < r.num_pages;
         const int32_t* row = r.table + static_cast<int64_t>(parent) * r.table_stride;
-        if (piece < row_pieces) {
-            if (piece == 0 && threadIdx.x == 0) {
-                p.lens_out[child] = len;
-                if (own && fresh >= r.num_pages) flag_error(r.err, DA_DEVERR_PAGE);
-            }
-            int32_t* out = p.table_out + static_cast<int64_t>(child) * p.table_out_stride;
-            const int begin = static_cast<int>(piece) * kRowEntries, end = min(pages, begin + kRowEntries);
-            for (int e = begin + static_cast<int>(threadIdx.x); e < end; e += kPageThreads) {
-                const int page = ld_cg_s32(row + e);
-                if (page < 0 || page >= r.num_pages) flag_error(r.err, DA_DEVERR_PAGE);
-                out[e] = own && e == pages - 1 ? fresh : page;
-            }
-            continue;
+        const int64_t old = writable ? ld_cg_s32(row + pages - 1) : -1;
+        // the row
+        if (share == 0 && threadIdx.x == 0) {
+            p.lens_out[child] = len;
+            if (own && !writable) flag_error(r.err, DA_DEVERR_PAGE);
         }
-        if (!own || fresh >= r.num_pages) continue;
-        const int64_t c = (piece - row_pieces) >> 1;
-        const bool values = (piece - row_pieces) & 1;
-        // the page's used tokens: one run, or one per head
-        const bool thd = p.layout == DA_LAYOUT_VARLEN;
-        const int64_t run = static_cast<int64_t>(used) * p.row_units * (thd ? p.Hkv : 1), units = thd ? run : run * p.Hkv;
-        if (c * kCopyChunk >= units) continue;
-        const int64_t old = ld_cg_s32(row + pages - 1);
+        int32_t* out = p.table_out + static_cast<int64_t>(child) * p.table_out_stride;
+        for (int e = share * kPageThreads + static_cast<int>(threadIdx.x); e < pages; e += split * kPageThreads) {
+            const int page = ld_cg_s32(row + e);
+            if (page < 0 || page >= r.num_pages) flag_error(r.err, DA_DEVERR_PAGE);
+            out[e] = own && e == pages - 1 ? fresh : page;
+        }
         if (old < 0 || old >= r.num_pages) continue;
-        const uint4* from = (values ? p.v : p.k) + old * p.page_units;
-        uint4* to = (values ? p.v : p.k) + fresh * p.page_units;
-        const int64_t stride = static_cast<int64_t>(r.P) * p.row_units;   // of heads, where they lie outside the tokens
-        uint4 x[kCopyUnits];
-        int64_t at[kCopyUnits];
+        // the used tokens of its last page: one run, or one per head (a page has at most 2^27 units)
+        const bool thd = p.layout == DA_LAYOUT_VARLEN;
+        const uint32_t run = static_cast<uint32_t>(used) * p.row_units * (thd ? p.Hkv : 1), units = thd ? run : run * p.Hkv;
+        const uint32_t stride = static_cast<uint32_t>(r.P) * p.row_units;   // of heads, where they lie outside the tokens
+        const uint32_t chunks = (units + kCopyChunk - 1) / kCopyChunk;
+        for (uint32_t c = share; c < 2 * chunks; c += split) {
+            const bool values = c >= chunks;
+            const uint32_t u0 = (values ? c - chunks : c) * kCopyChunk + threadIdx.x;
+            const uint4* from = (values ? p.v : p.k) + old * p.page_units;
+            uint4* to = (values ? p.v : p.k) + fresh * p.page_units;
+            uint4 x[kCopyUnits];
+            uint32_t at[kCopyUnits];
 #pragma unroll
-        for (int j = 0; j < kCopyUnits; ++j) {
-            const int64_t u = c * kCopyChunk + j * kPageThreads + threadIdx.x;
-            at[j] = u >= units ? -1 : thd ? u : u / run * stride + u % run;
-            if (at[j] >= 0) x[j] = __ldcs(from + at[j]);
+            for (int j = 0; j < kCopyUnits; ++j) {
+                const uint32_t u = u0 + j * kPageThreads;
+                at[j] = thd ? u : u / run * stride + u % run;
+                if (u < units) x[j] = __ldcs(from + at[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < kCopyUnits; ++j)
+                if (u0 + j * kPageThreads < units) __stcs(to + at[j], x[j]);
         }
-#pragma unroll
-        for (int j = 0; j < kCopyUnits; ++j)
-            if (at[j] >= 0) __stcs(to + at[j], x[j]);
-        if (p.ks != nullptr && c == 0) {
-            float* scale = values ? p.vs : p.ks;
-            for (int h = threadIdx.x; h < p.Hkv; h += kPageThreads)
-                scale[static_cast<int64_t>(fresh) * p.Hkv + h] = scale[old * p.Hkv + h];
+        if (p.ks != nullptr && share == 0) {
+            for (int h = threadIdx.x; h < 2 * p.Hkv; h += kPageThreads) {
+                float* scale = h < p.Hkv ? p.ks : p.vs;
+                const int hh = h < p.Hkv ? h : h - p.Hkv;
+                scale[static_cast<int64_t>(fresh) * p.Hkv + hh] = scale[old * p.Hkv + hh];
+            }
         }
     }
 }
@@ -387,10 +393,12 @@ da_status launch_plan(const RowsParams& p, const PlanSpace& s, int32_t* free_pag
     const int64_t entries = static_cast<int64_t>(p.B) * p.max_pages;
     if (words <= kOneWords && entries <= kOneEntries)
         return launch_after(page_plan_kernel<COMPACT, true>, 1, kOneThreads, stream, p, s, free_pages, count) ? DA_OK : DA_ERR_CUDA;
-    if (cudaMemsetAsync(s.bits, 0, static_cast<size_t>(words) * 4, stream) != cudaSuccess) return DA_ERR_CUDA;
+    if (!launch_after(page_clear_kernel, std::max(1, std::min(152, words / kPageThreads)), kPageThreads, stream, s.bits, words))
+        return DA_ERR_CUDA;
     const int64_t items = p.B * ((p.max_pages + kRowEntries - 1ll) / kRowEntries), per = kPageThreads / 32;
-    page_mark_kernel<<<static_cast<int>(std::min<int64_t>(kPageBlocks, (items + per - 1) / per)), kPageThreads, 0, stream>>>(p, s.bits);
-    if (cudaGetLastError() != cudaSuccess) return DA_ERR_CUDA;
+    if (!launch_after(page_mark_kernel, static_cast<int>(std::min<int64_t>(kPageBlocks, (items + per - 1) / per)), kPageThreads, stream,
+                      p, s.bits))
+        return DA_ERR_CUDA;
     const int blocks = std::max(1, std::min(152, words / kPageThreads));
     return launch_after(page_plan_kernel<COMPACT, false>, blocks, kPageThreads, stream, p, s, free_pages, count) ? DA_OK : DA_ERR_CUDA;
 }
@@ -458,9 +466,11 @@ da_status decode_attn_paged_fork(const da_paged_rows* rows, const da_paged_cache
     p.layout = c.layout;
     p.row_units = c.D * (c.kv_dtype == DA_E4M3 ? 1 : 2) / 16;
     p.page_units = static_cast<int64_t>(c.page_size) * c.Hkv * p.row_units;
-    const int64_t per = (r.max_pages + kRowEntries - 1) / kRowEntries + 2 * ((p.page_units + kCopyChunk - 1) / kCopyChunk);
-    const int grid = static_cast<int>(std::min<int64_t>(kPageBlocks, per * n_out));
-    return launch_after(page_fork_kernel, grid, kPageThreads, static_cast<cudaStream_t>(stream), p) ? DA_OK : DA_ERR_CUDA;
+    // as many blocks for a child as there is work for, and as fill the device
+    const int64_t work = std::max<int64_t>(2 * ((p.page_units + kCopyChunk - 1) / kCopyChunk), (r.max_pages + kPageThreads - 1) / kPageThreads);
+    const int split = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(work, kPageBlocks / n_out)));
+    const int grid = static_cast<int>(std::min<int64_t>(kPageBlocks, static_cast<int64_t>(split) * n_out));
+    return launch_after(page_fork_kernel, grid, kPageThreads, static_cast<cudaStream_t>(stream), p, split) ? DA_OK : DA_ERR_CUDA;
 }
 
 da_status decode_attn_paged_compact(const da_paged_rows* rows, const da_paged_cache* cache, int32_t* block_table_out,
