@@ -39,7 +39,7 @@ constexpr int kItemRows = 2 * kTileRows;
 constexpr int kTileKeys = 128;
 constexpr int kMaxRanges = 160;       // CTAs at most (GB300 has 152 SMs)
 constexpr int kItemCost = 4;          // an item's begin and end, in key tiles
-constexpr int kLeastCost = 7;         // of a range
+constexpr int kLeastCost = 4;         // of a range
 constexpr int kLeastPart = 1;         // key tiles of a partial result at least
 constexpr int kScaleRing = 4;         // tiles whose scales are in shared memory
 constexpr int kPieceRing = 4;         // pieces whose description is

@@ -19,7 +19,8 @@ constexpr int kPageThreads = 256;
 constexpr int kCopyUnits = 4;                                  // 16-byte units per thread and chunk
 constexpr int kCopyChunk = kPageThreads * kCopyUnits;          // units per chunk
 constexpr int kOneThreads = 1024;                              // of the block that plans alone
-constexpr int kOneWords = 8192;                                // words of its bitmap
+constexpr int kOneWords = 7168;                                // words of its bitmap
+constexpr int kOneRows = 1024;                                 // rows that it takes
 constexpr int kRowEntries = 128;                               // block-table entries that a warp takes at a time
 
 struct RowsParams {
@@ -47,7 +48,7 @@ struct PlanSpace {
     int32_t* rank;       // [num_pages]: of a mover among the movers
 };
 
-// Marks the pages that the rows use.
+// Marks the pages that the rows use: a warp per run of entries, or (below) one block.
 template <int THREADS>
 __device__ __forceinline__ void mark_pages(const RowsParams& p, uint32_t* bits) {
     const int lane = threadIdx.x & 31;
@@ -61,6 +62,30 @@ __device__ __forceinline__ void mark_pages(const RowsParams& p, uint32_t* bits) 
         for (int e = from + lane; e < to; e += 32) {
             const int page = ld_cg_s32(row + e);
             if (page >= 0 && page < p.num_pages) atomicOr(bits + (page >> 5), 1u << (page & 31));
+            else flag_error(p.err, DA_DEVERR_PAGE);
+        }
+    }
+}
+
+// One block: the rows' pages first, then all entries alike, so that no load waits for another row's length.
+__device__ __forceinline__ void mark_pages_one(const RowsParams& p, int* pages, uint32_t* marked) {
+    for (int b = threadIdx.x; b < p.B; b += kOneThreads) pages[b] = p.pages(b);
+    __syncthreads();
+    const int all = p.B * p.max_pages;
+    constexpr int kAhead = 8;
+    for (int i0 = threadIdx.x; i0 < all; i0 += kAhead * kOneThreads) {
+        int page[kAhead];
+        bool live[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int i = i0 + j * kOneThreads, b = i / p.max_pages, e = i - b * p.max_pages;
+            live[j] = i < all && e < pages[b];
+            page[j] = live[j] ? ld_cg_s32(p.table + static_cast<int64_t>(b) * p.table_stride + e) : 0;
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            if (!live[j]) continue;
+            if (page[j] >= 0 && page[j] < p.num_pages) atomicOr(marked + (page[j] >> 5), 1u << (page[j] & 31));
             else flag_error(p.err, DA_DEVERR_PAGE);
         }
     }
@@ -100,13 +125,16 @@ page_plan_kernel(const RowsParams p, const PlanSpace s, int32_t* free_pages, int
     constexpr int kT = ONE ? kOneThreads : kPageThreads;
     __shared__ int scratch[kT / 32];
     __shared__ uint32_t marked[ONE ? kOneWords : 1];
+    __shared__ int row_pages[ONE ? kOneRows : 1];
+    __shared__ uint32_t run_word[kT];
+    __shared__ int run_used[kT];
     grid_dependency_wait();
     if (threadIdx.x == 0) grid_dependents_launch();
     const int num_pages = p.num_pages, words = (num_pages + 31) / 32;
     if (ONE) {
         for (int w = threadIdx.x; w < words; w += kT) marked[w] = 0;
         __syncthreads();
-        mark_pages<kT>(p, marked);
+        mark_pages_one(p, row_pages, marked);
         __syncthreads();
     }
     auto word_at = [&](int w) { return ONE ? marked[w] : __ldcg(s.bits + w); };
@@ -114,6 +142,7 @@ page_plan_kernel(const RowsParams p, const PlanSpace s, int32_t* free_pages, int
     auto used_before = [&](int pages) {
         int n = 0;
         const int whole = pages >> 5;
+#pragma unroll 8
         for (int w = threadIdx.x; w < whole; w += kT) n += __popc(word_at(w));
         if (threadIdx.x == 0 && (pages & 31)) n += __popc(word_at(whole) & ((1u << (pages & 31)) - 1));
         return block_sum<kT>(n, scratch);
@@ -149,12 +178,13 @@ page_plan_kernel(const RowsParams p, const PlanSpace s, int32_t* free_pages, int
             if (i < warp) at += scratch[i];
             before += scratch[i];
         }
+        run_word[threadIdx.x] = mine;
+        run_used[threadIdx.x] = at;
         __syncthreads();
-        const int first = base + warp * 32;
-        for (int i = 0; i < min(32, w1 - first); ++i) {   // (uniform in a warp)
-            const uint32_t word = __shfl_sync(0xffffffffu, mine, i);
-            const int used0 = __shfl_sync(0xffffffffu, at, i);
-            const int64_t page = static_cast<int64_t>(first + i) * 32 + lane;
+        for (int i = warp; i < min(kT, w1 - base); i += kT / 32) {   // a warp per word, a lane per page
+            const uint32_t word = run_word[i];
+            const int used0 = run_used[i];
+            const int64_t page = static_cast<int64_t>(base + i) * 32 + lane;
             if (page >= num_pages) continue;
             const bool used = (word >> lane) & 1;
             const int k = used0 + __popc(word & ((1u << lane) - 1));
@@ -167,6 +197,7 @@ page_plan_kernel(const RowsParams p, const PlanSpace s, int32_t* free_pages, int
                 s.rank[page] = k - before_n;
             }
         }
+        __syncthreads();
     }
     if (!COMPACT && blockIdx.x == gridDim.x - 1 && threadIdx.x == 0) *count = num_pages - before;
 }
@@ -303,7 +334,10 @@ __global__ void __launch_bounds__(kPageThreads, 6) page_fork_kernel(const ForkPa
 
 // ------------------------------------------------------------ host side
 constexpr int kPageBlocks = 152 * 8;                       // blocks of a kernel that loops over its work
-constexpr int64_t kOneEntries = 32768;                     // table entries up to which one block plans alone
+constexpr int kPlanWords = 64;                             // words of the bitmap that a block plans, at least
+constexpr int64_t kOneEntries = 4096;                      // table entries up to which one block plans alone: one launch, not three
+                                                           // (1024 entries 4.9 us against 4.4 in a graph, but 5.8 against 9.7
+                                                           // of host time; 6300: 5.5 against 5.2; 20000: 10.7 against 8.0)
 
 inline size_t pages_space(int num_pages, PlanSpace* s, uint8_t* ws) {
     const size_t words = (static_cast<size_t>(num_pages) + 31) / 32 * 4, list = static_cast<size_t>(num_pages) * 4;
@@ -391,7 +425,7 @@ template <bool COMPACT>
 da_status launch_plan(const RowsParams& p, const PlanSpace& s, int32_t* free_pages, int32_t* count, cudaStream_t stream) {
     const int words = (p.num_pages + 31) / 32;
     const int64_t entries = static_cast<int64_t>(p.B) * p.max_pages;
-    if (words <= kOneWords && entries <= kOneEntries)
+    if (words <= kOneWords && p.B <= kOneRows && entries <= kOneEntries)
         return launch_after(page_plan_kernel<COMPACT, true>, 1, kOneThreads, stream, p, s, free_pages, count) ? DA_OK : DA_ERR_CUDA;
     if (!launch_after(page_clear_kernel, std::max(1, std::min(152, words / kPageThreads)), kPageThreads, stream, s.bits, words))
         return DA_ERR_CUDA;
@@ -399,7 +433,7 @@ da_status launch_plan(const RowsParams& p, const PlanSpace& s, int32_t* free_pag
     if (!launch_after(page_mark_kernel, static_cast<int>(std::min<int64_t>(kPageBlocks, (items + per - 1) / per)), kPageThreads, stream,
                       p, s.bits))
         return DA_ERR_CUDA;
-    const int blocks = std::max(1, std::min(152, words / kPageThreads));
+    const int blocks = std::max(1, std::min(152, words / kPlanWords));
     return launch_after(page_plan_kernel<COMPACT, false>, blocks, kPageThreads, stream, p, s, free_pages, count) ? DA_OK : DA_ERR_CUDA;
 }
 
