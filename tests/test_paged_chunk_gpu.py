@@ -321,3 +321,34 @@ def test_prompt_in_parts_equals_the_prompt_at_once():
     once = torch.empty_like(out)
     da.decode_attn_paged_chunk(rotated, cache, ints([0, T]), ints([T]), table, once, ws, lse=lse)
     assert check(once, lse, want, torch.bfloat16) is None and check(out, lse, want, torch.bfloat16) is None
+
+
+@pytest.mark.parametrize("kv,dtype", TYPES)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (6000, 300)])
+def test_long_histories_are_cut_and_joined(window, sinks, D, kv, dtype):
+    """Few rows over many keys: parts of an item on many blocks, with values that are not finite in the first and the last."""
+    paged = Paged([20000, 700, 9000], 1, D, kv, 64, BHSD, seed=30, scale_spread=4)
+    new = [3, 1, 130]
+    q = queries(134, 4, D, dtype, 31)
+    want = chunk64(q, paged, new, None, window, sinks)
+    out, lse = run_chunk(q, paged, new, window=window, sinks=sinks)
+    assert check(out, lse, want, DTYPES[dtype]) is None
+    for b, p in ((0, 19999), (2, 8900), (2, 8999)):
+        token_view(paged.v, BHSD)[int(paged.table[b, p // 64]), p % 64, 0, 7] = math.nan
+    want = chunk64(q, paged, new, None, window, sinks)
+    out, lse = run_chunk(q, paged, new, window=window, sinks=sinks)
+    assert torch.isnan(want[0]).any() and check(out, lse, want, DTYPES[dtype]) is None
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_batches(seed):
+    import random
+    rng = random.Random(seed)
+    kv, dtype = TYPES[seed % 4]
+    D, page, layout = rng.choice([64, 128]), rng.choice([16, 32, 48, 64, 128, 272]), rng.choice([VARLEN, BHSD])
+    Hkv, G, B = rng.choice([1, 2, 3]), rng.choice([1, 2, 3, 4, 5, 7, 8, 16]), rng.randint(1, 40)
+    lens = [rng.choice([0, 1, rng.randint(1, 200), rng.randint(1, 1500)]) for _ in range(B)]
+    new = [rng.choice([0, 1, min(n, rng.randint(0, 60)), min(n, rng.randint(0, 400))]) for n in lens]
+    window, sinks = rng.choice([(0, 0), (0, 5), (rng.randint(1, 800), rng.choice([0, 4, rng.randint(1, 400)]))])
+    compare(lens, new, Hkv * G, Hkv, D, kv, dtype, page, layout, window, sinks, seed=seed, spread=seed % 5, mean=(seed % 3) * 0.3)
