@@ -1315,23 +1315,42 @@ __global__ void __launch_bounds__(32 * D / 16) chunk_join_kernel(const ChunkPara
     const int r = slice * 32 + (threadIdx.x & 31), f = join.rt * kItemRows + r, d = threadIdx.x / 32 * 16;
     if (join.parts == 0 || f >= join.n * p.G) return;
     auto slot = [&](int j) { return static_cast<int64_t>(j == 0 ? 2 * range + 1 : 2 * (range + j)); };
-    float m = kNoKey;
-    for (int j = 0; j < join.parts; ++j) m = fmaxf(m, __ldcg(p.part_sum + slot(j) * kItemRows + r).x);
-    float l = 0.f, o[16];
+    // a few parts at a time, all of their loads before any is needed
+    constexpr int kAhead = 4;
+    float m = kNoKey, l = 0.f, o[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[i] = 0.f;
-    for (int j = 0; j < join.parts; ++j) {
-        const float2 sum = __ldcg(p.part_sum + slot(j) * kItemRows + r);
-        const float w = fast_exp2(sum.x - m);
-        l = fmaf(w, sum.y, l);
-        const float4* part = p.part + (slot(j) * (D / 4) + d / 4) * kItemRows + r;
+    for (int j0 = 0; j0 < join.parts; j0 += kAhead) {
+        float2 sum[kAhead];
+        float4 x[kAhead][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float4 x = __ldcg(part + i * kItemRows);
-            o[4 * i] = fmaf(w, x.x, o[4 * i]);
-            o[4 * i + 1] = fmaf(w, x.y, o[4 * i + 1]);
-            o[4 * i + 2] = fmaf(w, x.z, o[4 * i + 2]);
-            o[4 * i + 3] = fmaf(w, x.w, o[4 * i + 3]);
+        for (int j = 0; j < kAhead; ++j) {
+            const bool some = j0 + j < join.parts;
+            const float4* part = p.part + (slot(some ? j0 + j : 0) * (D / 4) + d / 4) * kItemRows + r;
+            sum[j] = some ? __ldcg(p.part_sum + slot(j0 + j) * kItemRows + r) : make_float2(kNoKey, 0.f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[j][i] = some ? __ldcg(part + i * kItemRows) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        float top = m;
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) top = fmaxf(top, sum[j].x);
+        const float old = fast_exp2(m - top);
+        m = top;
+        l *= old;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] *= old;
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            if (j0 + j >= join.parts) break;
+            const float w = fast_exp2(sum[j].x - m);
+            l = fmaf(w, sum[j].y, l);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                o[4 * i] = fmaf(w, x[j][i].x, o[4 * i]);
+                o[4 * i + 1] = fmaf(w, x[j][i].y, o[4 * i + 1]);
+                o[4 * i + 2] = fmaf(w, x[j][i].z, o[4 * i + 2]);
+                o[4 * i + 3] = fmaf(w, x[j][i].w, o[4 * i + 3]);
+            }
         }
     }
     const bool none = m == kNoKey && l == 0.f;
