@@ -631,33 +631,44 @@ struct ChunkKernel {
     // ------------------------------------------------------------ e4m3 to fp16
     static __device__ void converter(const Ctx& c, const ChunkParams& p) {
         constexpr int kChunks = D / 16;                        // 16-byte chunks of a raw row
+        constexpr int kStep = 128 / kChunks, kPer = kTileKeys / kStep;    // rows that the threads take at a time; times
         const int tid = threadIdx.x & 127, lane = threadIdx.x & 31;
+        // A thread's chunk of its rows row0, row0 + kStep ... Eight lanes at a time read 8 x 16 bytes of raw rows and write as much of
+        // 16-bit rows, both swizzled: rows r and r ^ 5, four neighbouring chunks each, meet in no bank either way (head size
+        // 64: two neighbouring rows of four chunks).
+        const int four = tid & 3, other = (tid >> 2) & 1, pr = (tid >> 3) & 3;
+        const int row0 = kChunks == 8 ? ((tid >> 5) & 1) * 8 + (other ? pr ^ 5 : pr) : tid / 4;
+        const int ch = kChunks == 8 ? (tid >> 6) * 4 + four : four;
+        const int sw = kChunks == 8 ? row0 & 7 : (row0 >> 1) & 3;         // the copy's swizzle
+        const uint32_t from0 = row0 * Sh::kRawRow + ((ch ^ sw) << 4);
+        const uint32_t to0 = tile_addr(0, row0, 2 * ch), to1 = tile_addr(0, row0, 2 * ch + 1);
+        static_assert(kStep % 8 == 0, "a thread's rows have one swizzle");
         uint32_t slot = 0;
         for (uint32_t piece = 0;; ++piece) {
             ChunkPiece* x = take_piece(c, p, piece);
             if (!x) break;
-            const ChunkTiles& tiles = x->tiles;
+            const int plain0 = x->tiles.from, plain1 = x->tiles.to;
             for (int t = x->t0, t1 = x->t1; t < t1; ++t) {
-                const int k0 = tiles.key(t);
-                const bool plain = tiles.plain(t);
+                const bool plain = t >= plain0 && t < plain1;
 #pragma unroll 1
                 for (int kv = 0; kv < 2; ++kv, ++slot) {
-                    const int from = slot % Sh::kRaw, to = slot % Sh::kRing;
-                    if (!wait(p, c.raw_full + 8 * from, (slot / Sh::kRaw) & 1)) return;
-                    const uint32_t src = c.base + Sh::kRawOff + from * Sh::kRawBytes;
-                    constexpr int kPer = kTileKeys * kChunks / 128;    // chunks per thread
+                    const uint32_t from = slot % Sh::kRaw, to = slot % Sh::kRing;
+                    const uint32_t landed = c.raw_full + 8 * from, free = c.kv_empty + 8 * to;
+                    const uint32_t landed_phase = (slot / Sh::kRaw) & 1, free_phase = ((slot / Sh::kRing) & 1) ^ 1;
+                    // (both asked at once)
+                    const bool a = mbar_try_wait(landed, landed_phase), b = mbar_try_wait(free, free_phase);
+                    if (!__all_sync(0xffffffffu, a && b) && (!wait(p, landed, landed_phase) || !wait(p, free, free_phase))) return;
+                    const uint32_t src = c.base + Sh::kRawOff + from * Sh::kRawBytes + from0;
+                    const uint32_t dst = c.base + Sh::kRingOff + to * Sh::kTileBytes;
                     uint4 in[kPer];
 #pragma unroll
-                    for (int i = 0; i < kPer; ++i) {
-                        const int u = i * 128 + tid, r = u / kChunks, ch = u % kChunks;
-                        const int sw = kChunks == 8 ? r & 7 : (r >> 1) & 3;    // the copy's swizzle
-                        in[i] = lds128(src + r * Sh::kRawRow + ((ch ^ sw) << 4));
-                    }
+                    for (int i = 0; i < kPer; ++i) in[i] = lds128(src + i * kStep * Sh::kRawRow);
                     uint32_t found = 0;
                     if (kv == 1 && !plain) {
+                        const int k0 = x->tiles.key(t) + row0;
 #pragma unroll
                         for (int i = 0; i < kPer; ++i) {
-                            const bool seen = tiles.wanted(p, k0 + (i * 128 + tid) / kChunks, 1);
+                            const bool seen = x->tiles.wanted(p, k0 + i * kStep, 1);
                             uint32_t* e = &in[i].x;
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
@@ -667,27 +678,23 @@ struct ChunkKernel {
                             }
                         }
                     }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(c.raw_empty + 8 * from);
-                    if (!wait(p, c.kv_empty + 8 * to, ((slot / Sh::kRing) & 1) ^ 1)) return;
-                    const uint32_t dst = ring(c, to);
 #pragma unroll
                     for (int i = 0; i < kPer; ++i) {
-                        const int u = i * 128 + tid, r = u / kChunks, ch = u % kChunks;
-                        uint4 a, b;
-                        e4m3x4_to_f16(in[i].x, a.x, a.y);
-                        e4m3x4_to_f16(in[i].y, a.z, a.w);
-                        e4m3x4_to_f16(in[i].z, b.x, b.y);
-                        e4m3x4_to_f16(in[i].w, b.z, b.w);
-                        // lanes of the two slices write their halves in opposite order, which spreads the banks
-                        const bool second = kChunks == 8 && ch >= 4;
-                        sts128(tile_addr(dst, r, 2 * ch + (second ? 1 : 0)), second ? b : a);
-                        sts128(tile_addr(dst, r, 2 * ch + (second ? 0 : 1)), second ? a : b);
+                        uint4 lo, hi;
+                        e4m3x4_to_f16(in[i].x, lo.x, lo.y);
+                        e4m3x4_to_f16(in[i].y, lo.z, lo.w);
+                        e4m3x4_to_f16(in[i].z, hi.x, hi.y);
+                        e4m3x4_to_f16(in[i].w, hi.z, hi.w);
+                        sts128(dst + to0 + i * kStep * 128, lo);
+                        sts128(dst + to1 + i * kStep * 128, hi);
                     }
                     if (found) x->dirty = 1;
                     proxy_fence();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(c.kv_full + 8 * to);
+                    if (lane == 0) {
+                        mbar_arrive(c.raw_empty + 8 * from);
+                        mbar_arrive(c.kv_full + 8 * to);
+                    }
                 }
             }
             __syncwarp();
