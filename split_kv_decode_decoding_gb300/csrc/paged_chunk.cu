@@ -839,8 +839,23 @@ struct ChunkKernel {
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i, next())
                     v[i] = f < rows ? __ldg(reinterpret_cast<const uint4*>(q + g * D)) : make_uint4(0, 0, 0, 0);
+                // the largest exponent field of each row, all rows of the batch a step at a time
+                uint32_t top[kBatch];
+                if constexpr (kRowFactors) {
 #pragma unroll
-                for (int i = 0; i < kBatch; ++i) put_query(c, p, v[i], w, first + (i0 + i) * kPerPass + sub, ch);
+                    for (int i = 0; i < kBatch; ++i) {
+                        const uint32_t e[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                        top[i] = 0;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) top[i] = max(top[i], max(e[j] & 0x7f80u, (e[j] >> 16) & 0x7f80u));
+                    }
+#pragma unroll
+                    for (int off = 1; off < kChunks; off <<= 1)
+#pragma unroll
+                        for (int i = 0; i < kBatch; ++i) top[i] = max(top[i], __shfl_xor_sync(0xffffffffu, top[i], off));
+                }
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) put_query(c, p, v[i], kRowFactors ? top[i] >> 7 : 0u, w, first + (i0 + i) * kPerPass + sub, ch);
             }
         }
         proxy_fence();
@@ -848,7 +863,8 @@ struct ChunkKernel {
     }
 
     // The queries of every piece but the first (which the rows' warps fetch, four of them a tile), a warp per row tile, as
-    // soon as the piece before is done with its own.
+    // soon as the piece before is done with its own. Queries that have to be scaled to fp16 are too much work for one warp (9 us a
+    // tile): the rows' warps fetch those of every piece, and these only pull them into the L2.
     static __device__ void queries(const Ctx& c, const ChunkParams& p, int w) {
         const int lane = threadIdx.x & 31;
         for (uint32_t piece = 0;; ++piece) {
@@ -863,26 +879,24 @@ struct ChunkKernel {
                     const uint16_t* line = p.q + (x->s.r0 + t) * p.q_stride + (static_cast<int64_t>(x->kvh) * p.G + f - t * p.G) * D;
                     for (int d = 0; d < D; d += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(line + d));
                 }
-                if (!wait_calmly<500>(p, c.q_empty + 8 * w, (piece & 1) ^ 1)) return;
-                fetch_queries<kTileRows>(c, p, *x, w, 0);
-                if (lane < 4) mbar_arrive(c.q_full + 8 * w);
+                if constexpr (!kRowFactors) {
+                    if (!wait_calmly<500>(p, c.q_empty + 8 * w, (piece & 1) ^ 1)) return;
+                    fetch_queries<kTileRows>(c, p, *x, w, 0);
+                    if (lane < 4) mbar_arrive(c.q_full + 8 * w);
+                }
             }
             __syncwarp();
             if (lane == 0) drop_piece(c, piece);
         }
     }
 
-    // 16 bytes of a query: the sign of the scale, and for 8-bit pages fp16, with a factor per row.
-    static __device__ __forceinline__ void put_query(const Ctx& c, const ChunkParams& p, const uint4& v, int w, int r, int ch) {
+    // 16 bytes of a query: the sign of the scale, and for bf16 over 8-bit pages fp16, with a factor per row (`top`: the largest
+    // exponent field of the row).
+    static __device__ __forceinline__ void put_query(const Ctx& c, const ChunkParams& p, const uint4& v, uint32_t top, int w, int r, int ch) {
         uint32_t e[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) e[j] = (e[j] & p.q_and) ^ p.q_xor;
         if constexpr (kRowFactors) {
-            uint32_t top = 0;   // largest exponent field of the row
-#pragma unroll
-            for (int j = 0; j < 4; ++j) top = max(top, max((e[j] >> 7) & 0xffu, (e[j] >> 23) & 0xffu));
-#pragma unroll
-            for (int off = 1; off < D / 8; off <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
             // 2^e takes the largest element to [2^14, 2^15); an infinity or a NaN stays one
             const int field = top == 255 ? 127 : min(max(268 - static_cast<int>(top), 14), 240);
             const float up = __uint_as_float(static_cast<uint32_t>(field) << 23);
@@ -1002,11 +1016,13 @@ struct ChunkKernel {
             ChunkPiece* const taken = take_piece(c, p, piece);
             if (!taken) return;
             ChunkPiece& x = *taken;
-            if (piece == 0) {
+            // (the scores of the piece before are complete: the queries are no longer read)
+            if (kRowFactors || piece == 0) {
                 fetch_queries<32>(c, p, x, w, quarter * 32);
                 if (lane == 0) mbar_arrive(c.q_full + 8 * w);
             }
             float factor = p.scale_log2;
+            if constexpr (kRowFactors) factor = reinterpret_cast<const float*>(c.smem + Sh::kFactorOff)[w * kTileRows + r];
             const int f = x.rt * kItemRows + w * kTileRows + r, token = p.token(f);
             const bool live = f < x.s.n * p.G;
             const int pos = live ? x.s.L - x.s.n + token : -1;
@@ -1034,13 +1050,6 @@ struct ChunkKernel {
                 const float2* sc = reinterpret_cast<const float2*>(c.smem + Sh::kScaleOff) + (count % kScaleRing) * 8;
                 if constexpr (KV8) {
                     if (!wait(p, c.sc_full + 8 * (count % kScaleRing), (count / kScaleRing) & 1)) return;
-                    if (kRowFactors && first) {
-                        // (in place since before the scores; the next queries wait until it is read)
-                        if (!wait(p, c.q_full + 8 * w, piece & 1)) return;
-                        factor = reinterpret_cast<const volatile float*>(c.smem + Sh::kFactorOff)[w * kTileRows + r];
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(c.q_empty + 8 * w);
-                    }
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const float by = factor * sc[i].x;
@@ -1262,7 +1271,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CU
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(c.q_full + 8 * i, 4);
-            mbar_init(c.q_empty + 8 * i, 1 + (K::kRowFactors ? 4 : 0));
+            mbar_init(c.q_empty + 8 * i, 1);
             mbar_init(c.s_full + 8 * i, 1);
             mbar_init(c.s_free + 8 * i, 4);
             mbar_init(c.p_half + 8 * i, 4);
