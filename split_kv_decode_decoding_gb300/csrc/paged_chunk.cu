@@ -1047,15 +1047,22 @@ struct ChunkKernel {
                     __syncwarp();
                     if (lane == 0) mbar_arrive(c.s_free + 8 * w);
                 }
-                const float2* sc = reinterpret_cast<const float2*>(c.smem + Sh::kScaleOff) + (count % kScaleRing) * 8;
+                float lv[8];             // 8-bit pages: log2 of the value scale, of 16 keys each
                 if constexpr (KV8) {
                     if (!wait(p, c.sc_full + 8 * (count % kScaleRing), (count / kScaleRing) & 1)) return;
+                    const float4* sc = reinterpret_cast<const float4*>(c.smem + Sh::kScaleOff) + (count % kScaleRing) * 4;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float by = factor * sc[i].x;
-                        const uint64_t by2 = pair(by, by);
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 f = sc[i];
+                        lv[2 * i] = f.y;
+                        lv[2 * i + 1] = f.w;
 #pragma unroll
-                        for (int j = 16 * i; j < 16 * i + 16; j += 2) unpair(mul2(pair(s[j], s[j + 1]), by2), s[j], s[j + 1]);
+                        for (int g = 2 * i; g < 2 * i + 2; ++g) {
+                            const float by = factor * (g & 1 ? f.z : f.x);
+                            const uint64_t by2 = pair(by, by);
+#pragma unroll
+                            for (int j = 16 * g; j < 16 * g + 16; j += 2) unpair(mul2(pair(s[j], s[j + 1]), by2), s[j], s[j + 1]);
+                        }
                     }
                 }
                 if (!plain) {
@@ -1082,12 +1089,12 @@ struct ChunkKernel {
                     // a weight that is too large moves the references as a score does
                     bool move = best - m > kHeadroom;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) move = move || (top[i] - m) + (sc[i].y - dv) > kHeadroom + kLift;
+                    for (int i = 0; i < 8; ++i) move = move || (top[i] - m) + (lv[i] - dv) > kHeadroom + kLift;
                     if (first || __any_sync(0xffffffffu, move)) {
                         const float mn = fmaxf(m, best);
                         float dn = first ? kNoKey : (m - mn) + dv;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) dn = fmaxf(dn, (top[i] - mn) + (sc[i].y - kLift));
+                        for (int i = 0; i < 8; ++i) dn = fmaxf(dn, (top[i] - mn) + (lv[i] - kLift));
                         if (!first) {
                             l *= fast_exp2(m - mn);
                             if (!rescale(c, p, to, c.pv_done + 8 * w, count, fast_exp2((m - mn) + (dv - dn)))) return;
@@ -1134,7 +1141,7 @@ struct ChunkKernel {
                         if (j & 2) sum1 = add2(sum1, e);
                         else sum0 = add2(sum0, e);
                         if constexpr (KV8) {
-                            if (j % 16 == 0) lift = fast_exp2(fminf(sc[k / 16].y - dv, 127.f));
+                            if (j % 16 == 0) lift = fast_exp2(fminf(lv[k / 16] - dv, 127.f));
                             e = mul2(e, pair(lift, lift));
                             unpair(e, a, b);
                         }
