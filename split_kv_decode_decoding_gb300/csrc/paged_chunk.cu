@@ -203,7 +203,7 @@ struct ChunkShape {
     static constexpr int kTileBytes = kSlices * kSliceBytes;
     static constexpr int kRing = D == 64 ? 8 : KV8 ? 4 : 5;    // K and V tiles in 16 bits
     static constexpr int kRawBytes = KV8 ? kTileKeys * D : 0;  // and as they come, in 8
-    static constexpr int kRaw = KV8 ? (D == 128 ? 2 : 4) : 0;
+    static constexpr int kRaw = KV8 ? (D == 128 ? 2 : 8) : 0;
     static constexpr int kRawRow = D;
     static constexpr int kQOff = 0;
     static constexpr int kRingOff = 2 * kTileBytes;
@@ -607,7 +607,7 @@ struct ChunkKernel {
 #pragma unroll
                     for (int kv = 0; kv < 2; ++kv, ++slot) {
                         const int at = slot % kSlots;
-                        if (!wait_calmly<KV8 ? 20 : 100>(p, empty + 8 * at, ((slot / kSlots) & 1) ^ 1)) return false;
+                        if (!wait(p, empty + 8 * at, ((slot / kSlots) & 1) ^ 1)) return false;
                         const uint32_t bar = full + 8 * at;
                         if (lane == 0) mbar_arrive_expect_tx(bar, kBytes);
                         __syncwarp();
@@ -663,6 +663,9 @@ struct ChunkKernel {
                     uint4 in[kPer];
 #pragma unroll
                     for (int i = 0; i < kPer; ++i) in[i] = lds128(src + i * kStep * Sh::kRawRow);
+                    // (the raw tile is in registers: the next one may land)
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(c.raw_empty + 8 * from);
                     uint32_t found = 0;
                     if (kv == 1 && !plain) {
                         const int k0 = x->tiles.key(t) + row0;
@@ -691,10 +694,7 @@ struct ChunkKernel {
                     if (found) x->dirty = 1;
                     proxy_fence();
                     __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(c.raw_empty + 8 * from);
-                        mbar_arrive(c.kv_full + 8 * to);
-                    }
+                    if (lane == 0) mbar_arrive(c.kv_full + 8 * to);
                 }
             }
             __syncwarp();
