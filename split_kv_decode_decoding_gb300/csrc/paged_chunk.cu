@@ -25,9 +25,25 @@
 // out, values that no row sees are zeroed, and so are elements that are not finite (0 times NaN is no
 // zero), which the end of the piece then adds to the rows that see them.
 //
-// e4m3 pages: four warps convert each tile to fp16, exactly. Queries enter as fp16 (load_queries of the
-// decode kernel has the reasons); ks multiplies the scores and vs the weights, page by page, relative to
-// a reference per row (`dv`) that keeps the fp16 weights in range.
+// e4m3 pages: four warps convert each tile to fp16, exactly. Queries enter as fp16, bf16 ones scaled by a
+// power of two per row into the top of its range; ks multiplies the scores and vs the weights, page by page,
+// relative to a reference per row (`dv`, the distance of the weights' maximum from the scores' m) that keeps the
+// fp16 weights in range however unequal the scales are.
+//
+// Sums, maxima, accumulators and partial results are float32. Rounded to fewer bits are the outputs, once, and the
+// weights, once, to the 16-bit type of their product: the tensor cores have no wider one at this rate, and a second
+// term (as in the decode kernel, which waits for bytes) would add half of all products. The outputs' error is 1.3 times
+// that of float32 weights (16-bit pages; over e4m3 pages 1.0, where fp16 weights meet a bf16 output).
+//
+// What bounds it. Head size 128: the tensor cores, 74 % of the time active (2048 of 8192 tokens, 32 / 8 heads, bf16:
+// 145 us, 1.65 PFLOP/s, 86 % of cuBLAS's burst rate; 4096 of 32768: 1.33 ms, 1.55 PFLOP/s, 90 % of its sustained rate, where the
+// power limit lowers the clock). A pair of row tiles takes 2048 cycles of products and 2900 in all: a row tile's
+// softmax (1280 cycles from its scores to its weights) and the products after it hide behind the other's not quite.
+// e4m3 pages: shared memory, which a pair of tiles keeps busy for 2560 cycles (the products' operands 1536, the raw tile in and
+// out 512, the converted one in 512): 203 us for the first call above, 1.47 ms for the second. Head size 64: the rows'
+// threads: an exponent takes 4 cycles of a scheduler's unit, two warps 1024 cycles per pair of tiles that the products
+// need 1024 for; 2100 in all (16 heads, 16384 tokens: 383 us, 1.08 PFLOP/s). Short calls: latency, 2 us to the plan, 2 to the first scores,
+// 1.4 per key tile, 2.5 for a piece's end and 3 for the join (107 of 1131 tokens 17.3 us).
 
 #include "paged_common.cuh"
 #include "tcgen05.cuh"
@@ -38,9 +54,13 @@ constexpr int kTileRows = 128;
 constexpr int kItemRows = 2 * kTileRows;
 constexpr int kTileKeys = 128;
 constexpr int kMaxRanges = 160;       // CTAs at most (GB300 has 152 SMs)
-constexpr int kItemCost = 4;          // an item's begin and end, in key tiles
-constexpr int kLeastCost = 4;         // of a range
-constexpr int kLeastPart = 1;         // key tiles of a partial result at least
+// An item's begin and end, in key tiles: what its pipeline's filling and draining cost. (4 prompts of 4096 tokens 411 us with 2,
+// 375 with 3, 370 with 4, 376 with 5; the ragged batch of 24 667, 600, 611 and 625.)
+constexpr int kItemCost = 4;
+// Of a range: a short call takes more CTAs, and joins more parts (107 of 1131 tokens 23.7 us with 7, 21.5 with 5, 19.0 with 3; 64 of
+// 8192 29.3, 28.4 and 30.7).
+constexpr int kLeastCost = 4;
+constexpr int kLeastPart = 1;         // key tiles of a partial result at least (with 4 the ragged batch takes 677 us, with 2 611, with 1 579)
 constexpr int kScaleRing = 4;         // tiles whose scales are in shared memory
 constexpr int kPieceRing = 4;         // pieces whose description is
 constexpr int kJoinSlices = 8;        // blocks that join one split item, 32 rows each

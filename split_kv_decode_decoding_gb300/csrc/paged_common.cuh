@@ -1,5 +1,5 @@
-// Pieces shared by the paged-cache translation units (paged_attn.cu,
-// paged_append.cu): the checks of a cache description, and where a page's rows lie.
+// Pieces shared by the paged-cache translation units (paged_*.cu): what a workspace begins with, the checks of a
+// cache description, where a page's rows lie, waits and conversions of the kernels, the tensor maps of the pages.
 #ifndef DECODE_ATTN_PAGED_COMMON_CUH
 #define DECODE_ATTN_PAGED_COMMON_CUH
 
