@@ -90,7 +90,8 @@ struct ChunkParams {
     int box_keys;            // keys of a TMA box: gcd(page size, 128)
     uint32_t group_mul;      // f / G by multiplication (token())
     int group_shift;
-    uint32_t q_and, q_xor;   // on two query elements: zeroes them if the scale is 0, and takes its sign
+    int q_zero;              // the scale is 0: so are the queries (0 times what is not finite is NaN), and the factor is 1
+    uint32_t q_xor;          // the scale's sign, on two query elements
     float scale_log2;        // |scale| log2e (1 if it is 0)
     int out_wide;            // every row of out begins on a 32-byte border
     unsigned long long wait_limit_ns;
@@ -128,7 +129,7 @@ struct ChunkTiles {
     int first, last;         // positions of its first and last token (may be < 0)
     int low;                 // the first key that the first token sees through the window
     int ns, lo, nt;
-    int from, to;            // tiles of which every row sees every key (besides those of the first tokens)
+    int sure, from, to;      // every row sees every key of the tiles 0 .. sure - 1 and from .. to - 1
 
     __device__ __forceinline__ ChunkTiles(const ChunkParams& p, const ChunkSeq& s, int rt) {
         const int f = rt * kItemRows;
@@ -138,14 +139,15 @@ struct ChunkTiles {
         ns = (min(p.sinks, low) + kTileKeys - 1) / kTileKeys;
         lo = max(ns, low / kTileKeys);
         nt = ns + max(last, 0) / kTileKeys - lo + 1;
-        // tiles from lo on that end at or before the first token, and begin in the last token's window
+        // tiles of first tokens before the first token's window, and tiles from lo on that end at or before the first token and
+        // begin in the last token's window
+        sure = min(p.sinks, low) / kTileKeys;
         to = ns + max((first + 1) / kTileKeys - lo, 0);
         from = ns;
         if (p.window) from += max((max(0, last - p.window + 1) + kTileKeys - 1) / kTileKeys - lo, 0);
     }
     __device__ __forceinline__ int key(int tile) const { return (tile < ns ? tile : lo + tile - ns) * kTileKeys; }
-    // (k0 + 127 <= first, and last - k0 < window)
-    __device__ __forceinline__ bool plain(int tile) const { return tile >= from && tile < to; }
+    __device__ __forceinline__ bool plain(int tile) const { return tile < sure || (tile >= from && tile < to); }
     // whether some row sees a key in [k, k + keys), or the key k
     __device__ __forceinline__ bool wanted(const ChunkParams& p, int k, int keys) const {
         return k <= last && (k + keys > low || k < p.sinks);
@@ -524,17 +526,23 @@ struct ChunkKernel {
         return ok;
     }
 
+    // A wait for the end of a piece, which may be long: 20 us for each of its key tiles more than other waits.
+    static __device__ __forceinline__ unsigned long long piece_limit(const ChunkParams& p, int tiles) {
+        return p.wait_limit_ns + static_cast<unsigned long long>(tiles) * 20000ull;
+    }
+
     // wait, for warps that are not in a hurry: each question reads shared memory, of which the 8-bit kernel has no time to
     // spare (4096 of 32768 tokens 1992 us with the queries' warps asking all the time, 1827 so).
     template <int NS>
-    static __device__ __forceinline__ bool wait_calmly(const ChunkParams& p, uint32_t bar, uint32_t parity) {
-        for (int i = 0; i < 10000 && !mbar_try_wait(bar, parity); ++i) __nanosleep(NS);
+    static __device__ __forceinline__ bool wait_calmly(const ChunkParams& p, uint32_t bar, uint32_t parity, int tiles = 0) {
+        const unsigned long long limit = piece_limit(p, tiles), start = global_ns();
+        while (!mbar_try_wait(bar, parity) && global_ns() - start <= limit) __nanosleep(NS);
         return wait(p, bar, parity);
     }
 
     // Piece number i, or nullptr after the last one (or a wait that timed out); it is given back with drop_piece.
-    static __device__ __forceinline__ ChunkPiece* take_piece(const Ctx& c, const ChunkParams& p, uint32_t i) {
-        const bool ok = wait_lane(c.x_full + 8 * (i % kPieceRing), (i / kPieceRing) & 1, p.wait_limit_ns);
+    static __device__ __forceinline__ ChunkPiece* take_piece(const Ctx& c, const ChunkParams& p, uint32_t i, int tiles = 0) {
+        const bool ok = wait_lane(c.x_full + 8 * (i % kPieceRing), (i / kPieceRing) & 1, piece_limit(p, tiles));
         if (!ok) flag_error(p.err, DA_DEVERR_TIMEOUT);
         ChunkPiece* x = c.pieces + i % kPieceRing;
         return ok && x->valid ? x : nullptr;
@@ -667,9 +675,8 @@ struct ChunkKernel {
         for (uint32_t piece = 0;; ++piece) {
             ChunkPiece* x = take_piece(c, p, piece);
             if (!x) break;
-            const int plain0 = x->tiles.from, plain1 = x->tiles.to;
             for (int t = x->t0, t1 = x->t1; t < t1; ++t) {
-                const bool plain = t >= plain0 && t < plain1;
+                const bool plain = x->tiles.plain(t);
 #pragma unroll 1
                 for (int kv = 0; kv < 2; ++kv, ++slot) {
                     const uint32_t from = slot % Sh::kRaw, to = slot % Sh::kRing;
@@ -831,7 +838,7 @@ struct ChunkKernel {
         constexpr int kChunks = D / 8, kPerPass = 32 / kChunks, kPasses = ROWS / kPerPass, kBatch = 8;
         const int lane = threadIdx.x & 31, ch = lane % kChunks, sub = lane / kChunks;
         const uint32_t tile = c.base + Sh::kQOff + w * Sh::kTileBytes;
-        const bool asis = !kRowFactors && p.q_and == 0xffffffffu && p.q_xor == 0;
+        const bool asis = !kRowFactors && !p.q_zero && p.q_xor == 0;
         const int rows = x.s.n * p.G;
         int f = x.rt * kItemRows + w * kTileRows + first + sub, t = p.token(f), g = f - t * p.G;
         const uint16_t* q = p.q + (x.s.r0 + t) * p.q_stride + static_cast<int64_t>(x.kvh) * p.G * D + ch * 8;   // of token t
@@ -887,9 +894,12 @@ struct ChunkKernel {
     // tile): the rows' warps fetch those of every piece, and these only pull them into the L2.
     static __device__ void queries(const Ctx& c, const ChunkParams& p, int w) {
         const int lane = threadIdx.x & 31;
+        int before = 0, tiles = 0;         // key tiles of the piece before, and of this one
         for (uint32_t piece = 0;; ++piece) {
-            const ChunkPiece* x = take_piece(c, p, piece);
+            const ChunkPiece* x = take_piece(c, p, piece, tiles);
             if (!x) return;
+            before = tiles;
+            tiles = x->t1 - x->t0;
             if (piece > 0) {
                 // (into the L2 while the tensor cores still read the tile)
                 for (int r = lane; r < kTileRows; r += 32) {
@@ -900,7 +910,7 @@ struct ChunkKernel {
                     for (int d = 0; d < D; d += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(line + d));
                 }
                 if constexpr (!kRowFactors) {
-                    if (!wait_calmly<500>(p, c.q_empty + 8 * w, (piece & 1) ^ 1)) return;
+                    if (!wait_calmly<500>(p, c.q_empty + 8 * w, (piece & 1) ^ 1, before)) return;
                     fetch_queries<kTileRows>(c, p, *x, w, 0);
                     if (lane < 4) mbar_arrive(c.q_full + 8 * w);
                 }
@@ -915,7 +925,7 @@ struct ChunkKernel {
     static __device__ __forceinline__ void put_query(const Ctx& c, const ChunkParams& p, const uint4& v, uint32_t top, int w, int r, int ch) {
         uint32_t e[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) e[j] = (e[j] & p.q_and) ^ p.q_xor;
+        for (int j = 0; j < 4; ++j) e[j] = p.q_zero ? zero_times<DT>(e[j], 0u) : e[j] ^ p.q_xor;
         if constexpr (kRowFactors) {
             // 2^e takes the largest element to [2^14, 2^15); an infinity or a NaN stays one
             const int field = top == 255 ? 127 : min(max(268 - static_cast<int>(top), 14), 240);
@@ -1049,9 +1059,9 @@ struct ChunkKernel {
             // references: scores' maximum m (16-bit pages: less kLift), and (8-bit pages) dv, how far the weights' is above it
             float m = kNoKey, dv = 0.f, l = 0.f;
             bool asked = false;            // the scores of the coming tile are known to be there
-            const int t0 = x.t0, t1 = x.t1, plain0 = x.tiles.from, plain1 = x.tiles.to;
+            const int t0 = x.t0, t1 = x.t1, sure = x.tiles.sure, plain0 = x.tiles.from, plain1 = x.tiles.to;
             for (int t = t0; t < t1; ++t, ++count) {
-                const bool plain = t >= plain0 && t < plain1, first = t == t0;
+                const bool plain = t < sure || (t >= plain0 && t < plain1), first = t == t0;
                 if (!(Sh::kApart && asked) && !wait(p, c.s_full + 8 * w, count & 1)) return;
                 tmem_fence_after_sync();
                 float s[kTileKeys];
@@ -1508,7 +1518,7 @@ da_status decode_attn_paged_chunk(const da_paged_chunk* args, void* stream) {
     p.scale_log2 = std::fabs(a.scale) * kLog2e;
     const bool zero = p.scale_log2 == 0.f;       // (a factor of 0 would make NaN of the scores taken out)
     if (zero) p.scale_log2 = 1.f;
-    p.q_and = zero ? 0u : 0xffffffffu;
+    p.q_zero = zero;
     p.q_xor = !zero && a.scale < 0.f ? 0x80008000u : 0u;
     p.wait_limit_ns = kWaitLimitNs;
     cudaStream_t s = static_cast<cudaStream_t>(stream);

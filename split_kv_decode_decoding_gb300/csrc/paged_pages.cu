@@ -463,6 +463,7 @@ da_status decode_attn_paged_free_pages(const da_paged_rows* rows, int32_t* free_
         if (overlap(out, bytes, rows->block_table, table) || overlap(out, bytes, rows->kv_lens, 4 * static_cast<int64_t>(rows->B)))
             return DA_ERR_INVALID_ARG;
     }
+    if (overlap(free_pages, list, num_free, 4)) return DA_ERR_INVALID_ARG;
     PlanSpace s;
     pages_space(rows->num_pages, &s, static_cast<uint8_t*>(rows->workspace));
     return launch_plan<false>(rows_params(*rows), s, free_pages, num_free, static_cast<cudaStream_t>(stream));

@@ -94,6 +94,21 @@ def test_scales(scale, kv, dtype):
 
 
 @pytest.mark.parametrize("kv,dtype", TYPES)
+def test_scale_zero_keeps_what_is_not_finite(kv, dtype):
+    """0 times a score that is not a number is none."""
+    paged = Paged([200], 1, 64, kv, 16, VARLEN, seed=40)
+    q = queries(200, 2, 64, dtype, 41)
+    q[7, 1, 3], q[100, 0, 5] = math.nan, math.inf
+    want = chunk64(q, paged, [200], 0.0)
+    out, lse = run_chunk(q, paged, [200], scale=0.0)
+    bad = torch.zeros(200, 2, dtype=torch.bool)
+    bad[7, 1] = bad[100, 0] = True
+    assert torch.isnan(out.cpu()[bad]).all() and torch.isnan(lse.cpu()[bad]).all()
+    good = tuple(x[:, 0][~bad[:, 0]] for x in want)
+    assert check(out[:, 0].cpu()[~bad[:, 0]], lse[:, 0].cpu()[~bad[:, 0]], good, DTYPES[dtype]) is None
+
+
+@pytest.mark.parametrize("kv,dtype", TYPES)
 def test_growing_scores(kv, dtype):
     """Every key's score above the last one's by more than any headroom, and one far above the rest."""
     paged = Paged([700], 1, 64, kv, 16, VARLEN, seed=6)
@@ -144,6 +159,20 @@ def test_values_that_are_not_finite_reach_the_rows_that_see_them(bad, window, si
     want = chunk64(q, paged, new, None, window, sinks)
     assert torch.isfinite(want[0][:, :2]).all() and not torch.isfinite(want[0][:, 2:]).all()
     out, lse = run_chunk(q, paged, new, window=window, sinks=sinks)
+    assert check(out, lse, want, DTYPES[dtype]) is None
+
+
+@pytest.mark.parametrize("kv,dtype", TYPES)
+def test_values_that_are_not_finite_among_many_first_tokens(kv, dtype):
+    """Whole tiles of first tokens, seen by all rows, beside those that the window cuts."""
+    paged = Paged([4000], 1, 128, kv, 64, BHSD, seed=42)
+    new, window, sinks = [300], 500, 1500
+    q = queries(300, 2, 128, dtype, 43)
+    for p, d in ((100, 1), (1407, 2), (1408, 3), (1499, 4), (1500, 5), (3300, 6), (3999, 7)):
+        token_view(paged.v, BHSD)[int(paged.table[0, p // 64]), p % 64, 0, d] = math.nan
+    want = chunk64(q, paged, new, None, window, sinks)
+    out, lse = run_chunk(q, paged, new, window=window, sinks=sinks)
+    assert torch.isnan(want[0][:, :, 1:5]).all() and torch.isfinite(want[0][:, :, 5]).all()
     assert check(out, lse, want, DTYPES[dtype]) is None
 
 

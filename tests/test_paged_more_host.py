@@ -173,7 +173,7 @@ def test_rows_refusals(lib, change, status):
 
 @pytest.mark.parametrize("change,status", [
     (dict(out=0), ARG), (dict(count=0), ARG), (dict(out=2), ALIGN), (dict(count=6), ALIGN),
-    (dict(out=7 << 20), ARG), (dict(out=(7 << 20) - 36), ARG), (dict(out=6 << 20), ARG), (dict(count=(7 << 20) + 28), ARG), (dict(count=(6 << 20) + 4), ARG),
+    (dict(out=7 << 20), ARG), (dict(out=(7 << 20) - 36), ARG), (dict(out=6 << 20), ARG), (dict(count=(20 << 20) + 36), ARG), (dict(count=(7 << 20) + 28), ARG), (dict(count=(6 << 20) + 4), ARG),
 ], ids=str)
 def test_free_refusals(lib, change, status):
     assert free(lib, **change) == status
