@@ -37,12 +37,12 @@
 //
 // What bounds it. Head size 128: the tensor cores, 74 % of the time active (2048 of 8192 tokens, 32 / 8 heads, bf16:
 // 145 us, 1.65 PFLOP/s, 86 % of cuBLAS's burst rate; 4096 of 32768: 1.33 ms, 1.55 PFLOP/s, 90 % of its sustained rate, where the
-// power limit lowers the clock). A pair of row tiles takes 2048 cycles of products and 2900 in all: a row tile's
-// softmax (1280 cycles from its scores to its weights) and the products after it hide behind the other's not quite.
+// power limit lowers the clock). A pair of row tiles takes 2048 cycles of products and 2900 in all; their operands and the
+// copies keep shared memory busy for the 2048, too, and a shorter softmax (1280 cycles from scores to weights) changes nothing.
 // e4m3 pages: shared memory, which a pair of tiles keeps busy for 2560 cycles (the products' operands 1536, the raw tile in and
 // out 512, the converted one in 512): 203 us for the first call above, 1.47 ms for the second. Head size 64: the rows'
 // threads: an exponent takes 4 cycles of a scheduler's unit, two warps 1024 cycles per pair of tiles that the products
-// need 1024 for; 2100 in all (16 heads, 16384 tokens: 383 us, 1.08 PFLOP/s). Short calls: latency, 2 us to the plan, 2 to the first scores,
+// need 1024 for; 2000 in all (16 heads, 16384 tokens: 370 us, 1.11 PFLOP/s). Short calls: latency, 2 us to the plan, 2 to the first scores,
 // 1.4 per key tile, 2.5 for a piece's end and 3 for the join (107 of 1131 tokens 17.3 us).
 
 #include "paged_common.cuh"
@@ -1110,6 +1110,36 @@ struct ChunkKernel {
                         }
                     }
                 }
+                uint64_t sum0 = 0, sum1 = 0;
+                // weights of keys 32 i on, relative to m
+                const auto weights = [&](int i, uint32_t (&o)[16]) {
+                    const uint64_t by2 = pair(factor, factor), m2 = pair(-m, -m);
+                    float lift = 1.f;
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        const int k = 32 * i + j;
+                        float a, b;
+                        unpair(KV8 ? add2(pair(s[k], s[k + 1]), m2) : fma2(pair(s[k], s[k + 1]), by2, m2), a, b);
+                        a = fast_exp2(a);
+                        b = fast_exp2(b);
+                        uint64_t e = pair(a, b);
+                        if (j & 2) sum1 = add2(sum1, e);
+                        else sum0 = add2(sum0, e);
+                        if constexpr (KV8) {
+                            if (j % 16 == 0) lift = fast_exp2(fminf(lv[k / 16] - dv, 127.f));
+                            e = mul2(e, pair(lift, lift));
+                            unpair(e, a, b);
+                        }
+                        o[j / 2] = pack2<MT>(a, b);
+                    }
+                };
+                uint32_t o0[16], o1[16];
+                // 16-bit pages: the first half's weights by the reference as it is, beside the maxima, which seldom move it: the exponents'
+                // unit and the maxima's need not wait for each other (16 heads of size 64, 16384 tokens 383 -> 370 us)
+                if constexpr (!KV8) {
+                    weights(0, o0);
+                    weights(1, o1);
+                }
                 // maxima of 16 keys, the size of the smallest page
                 float top[8];
 #pragma unroll
@@ -1134,14 +1164,15 @@ struct ChunkKernel {
                     }
                 } else {
                     best *= factor;
-                    const bool move = best - m > kHeadroom + kLift;
-                    if (first) {
-                        m = fmaxf(m, best - kLift);
-                    } else if (__any_sync(0xffffffffu, move)) {
+                    const bool move = first || best - m > kHeadroom + kLift;
+                    if (__any_sync(0xffffffffu, move)) {
                         const float mn = move ? fmaxf(m, best - kLift) : m, by = fast_exp2(m - mn);
                         l *= by;
                         m = mn;
-                        if (!rescale(c, p, to, c.pv_done + 8 * w, count, by)) return;
+                        if (!first && !rescale(c, p, to, c.pv_done + 8 * w, count, by)) return;
+                        sum0 = sum1 = 0;
+                        weights(0, o0);
+                        weights(1, o1);
                     }
                     if (w == 0 && !plain) {
                         const uint32_t v = 2 * count + 1;
@@ -1153,38 +1184,18 @@ struct ChunkKernel {
                     if (!__all_sync(0xffffffffu, done) && !wait(p, c.pv_done + 8 * w, (count - 1) & 1)) return;
                     tmem_fence_after_sync();
                 }
-                uint64_t sum0 = 0, sum1 = 0;
-                float lift = 1.f;
-                const uint64_t by2 = pair(factor, factor), m2 = pair(-m, -m);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t o[16];
-#pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        const int k = 32 * i + j;
-                        const uint64_t y = KV8 ? add2(pair(s[k], s[k + 1]), m2) : fma2(pair(s[k], s[k + 1]), by2, m2);
-                        float a, b;
-                        unpair(y, a, b);
-                        a = fast_exp2(a);
-                        b = fast_exp2(b);
-                        uint64_t e = pair(a, b);
-                        if (j & 2) sum1 = add2(sum1, e);
-                        else sum0 = add2(sum0, e);
-                        if constexpr (KV8) {
-                            if (j % 16 == 0) lift = fast_exp2(fminf(lv[k / 16] - dv, 127.f));
-                            e = mul2(e, pair(lift, lift));
-                            unpair(e, a, b);
-                        }
-                        o[j / 2] = pack2<MT>(a, b);
-                    }
-                    tmem_st16_start(tp + 16 * i, o);
-                    if (i == 1) {
-                        tmem_st_wait();
-                        tmem_fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(c.p_half + 8 * w);
-                    }
-                }
+                if constexpr (KV8) weights(0, o0);
+                tmem_st16_start(tp, o0);
+                if constexpr (KV8) weights(1, o1);
+                tmem_st16_start(tp + 16, o1);
+                tmem_st_wait();
+                tmem_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(c.p_half + 8 * w);
+                weights(2, o0);
+                tmem_st16_start(tp + 32, o0);
+                weights(3, o1);
+                tmem_st16_start(tp + 48, o1);
                 if constexpr (Sh::kApart) asked = mbar_try_wait(c.s_full + 8 * w, (count + 1) & 1) && t + 1 < t1;   // the next scores
                 tmem_st_wait();
                 tmem_fence_before_sync();
