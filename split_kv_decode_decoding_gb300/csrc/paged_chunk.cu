@@ -690,9 +690,6 @@ struct ChunkKernel {
                     uint4 in[kPer];
 #pragma unroll
                     for (int i = 0; i < kPer; ++i) in[i] = lds128(src + i * kStep * Sh::kRawRow);
-                    // (the raw tile is in registers: the next one may land)
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(c.raw_empty + 8 * from);
                     uint32_t found = 0;
                     if (kv == 1 && !plain) {
                         const int k0 = x->tiles.key(t) + row0;
@@ -721,7 +718,11 @@ struct ChunkKernel {
                     if (found) x->dirty = 1;
                     proxy_fence();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(c.kv_full + 8 * to);
+                    // (the raw tile is given back here, where what was read of it has been used: an arrival overtakes reads in flight)
+                    if (lane == 0) {
+                        mbar_arrive(c.raw_empty + 8 * from);
+                        mbar_arrive(c.kv_full + 8 * to);
+                    }
                 }
             }
             __syncwarp();

@@ -381,3 +381,29 @@ def test_random_batches(seed):
     new = [rng.choice([0, 1, min(n, rng.randint(0, 60)), min(n, rng.randint(0, 400))]) for n in lens]
     window, sinks = rng.choice([(0, 0), (0, 5), (rng.randint(1, 800), rng.choice([0, 4, rng.randint(1, 400)]))])
     compare(lens, new, Hkv * G, Hkv, D, kv, dtype, page, layout, window, sinks, seed=seed, spread=seed % 5, mean=(seed % 3) * 0.3)
+
+
+@pytest.mark.parametrize("kv,dtype", TYPES)
+@pytest.mark.parametrize("D,window", [(128, 0), (64, 0), (128, 3000)])
+def test_long_calls_have_the_same_bits_every_time(D, window, kv, dtype):
+    """Every block busy for hundreds of key tiles, again and again: a hand-over that comes too early shows in some run."""
+    g = torch.Generator(device="cuda").manual_seed(50)
+    lens, new, pages = [16384, 5000], [2048, 700], 400
+    shape = (pages, 8, 64, D)
+    k, v = (torch.randn(shape, generator=g, device="cuda", dtype=torch.bfloat16).to(DTYPES[kv]) for _ in range(2))
+    scales = [torch.exp2(torch.randint(-3, 3, (pages, 8), generator=g, device="cuda").float()) for _ in range(2)] if kv == "e4m3" else [None, None]
+    cache = da.PagedCache(k, v, *scales, layout=BHSD)
+    table = torch.randperm(pages, generator=g, device="cuda").to(torch.int32)[:358]
+    table = torch.stack([table[:256], torch.cat([table[256:], table.new_zeros(154)])])
+    q = torch.randn(2748, 32, D, generator=g, device="cuda", dtype=DTYPES[dtype])
+    ws = da.alloc_paged_chunk_workspace(32, 8, D)
+    out, lse = torch.empty_like(q), torch.empty(2748, 32, device="cuda")
+    first = None
+    for _ in range(40):
+        out.fill_(7.0)
+        da.decode_attn_paged_chunk(q, cache, ints(starts(new)), ints(lens), table, out, ws, window=window, sinks=5, lse=lse)
+        if first is None:
+            first = (out.clone(), lse.clone())
+            assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    assert da.decode_attn_splitkv_get_error(ws) == 0
