@@ -407,3 +407,52 @@ def test_long_calls_have_the_same_bits_every_time(D, window, kv, dtype):
             assert torch.isfinite(out).all() and torch.isfinite(lse).all()
         assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
     assert da.decode_attn_splitkv_get_error(ws) == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_two_calls_at_once(D):
+    """Calls that overlap, on streams and with workspaces of their own, beside decode steps on a third."""
+    cases = []
+    for i, (kv, dtype) in enumerate([("bf16", "bf16"), ("e4m3", "f16")]):
+        paged = Paged([900 + 300 * i, 64, 0, 2000], 2, D, kv, 16, VARLEN, seed=60 + i)
+        new = [300, 64, 0, 1 + 200 * i]
+        q = queries(sum(new), 8, D, dtype, 62 + i)
+        qd = q.cuda()
+        cases.append(dict(want=chunk64(q, paged, new), dtype=DTYPES[dtype], stream=torch.cuda.Stream(), out=torch.empty_like(qd),
+                          lse=torch.empty(len(q), 8, device="cuda"),
+                          args=(qd, on_device(paged), ints(starts(new)), ints(paged.lens), paged.table.cuda()),
+                          ws=da.alloc_paged_chunk_workspace(8, 2, D)))
+    last = cases[0]
+    dec = da.alloc_paged_workspace(1, 8, 2, D)
+    dq = queries(4, 8, D, "bf16", 70).cuda()
+    dout, third = torch.empty_like(dq), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for c in cases:
+            da.decode_attn_paged_chunk(*c["args"], c["out"], c["ws"], lse=c["lse"], stream=c["stream"])
+        da.decode_attn_paged_window(dq, last["args"][1], last["args"][3], last["args"][4], dout, dec, window=100, sinks=4, stream=third)
+    torch.cuda.synchronize()
+    for c in cases:
+        assert da.decode_attn_splitkv_get_error(c["ws"]) == 0
+        assert check(c["out"], c["lse"], c["want"], c["dtype"]) is None
+    assert da.decode_attn_splitkv_get_error(dec) == 0
+
+
+@pytest.mark.parametrize("kv,dtype", TYPES)
+@pytest.mark.parametrize("D", [64, 128])
+def test_rows_on_16_byte_borders_only(D, kv, dtype):
+    """Strides that are odd multiples of 16 bytes, and bases between 32-byte borders; parts and whole items alike."""
+    paged = Paged([3000, 90], 1, D, kv, 16, VARLEN, seed=80)
+    new = [40, 90]
+    q = queries(130, 3, D, dtype, 81)
+    want = chunk64(q, paged, new)
+    flat_q = torch.full((130 * (3 * D + 8) + 8,), float("nan"), dtype=q.dtype, device="cuda")
+    flat_o = torch.full_like(flat_q, 3.0)
+    view = lambda x: x[8:].view(130, 3 * D + 8)[:, :3 * D].unflatten(1, (3, D))
+    view(flat_q).copy_(q)
+    out, lse = view(flat_o), torch.empty(130, 3, device="cuda")
+    assert out.data_ptr() % 32 == 16 and out.stride(0) % 16 == 8
+    ws = da.alloc_paged_chunk_workspace(3, 1, D)
+    da.decode_attn_paged_chunk(view(flat_q), on_device(paged), ints(starts(new)), ints(paged.lens), paged.table.cuda(), out, ws, lse=lse)
+    assert check(out, lse, want, DTYPES[dtype]) is None
+    assert (flat_o[:8] == 3.0).all() and (flat_o[8:].view(130, 3 * D + 8)[:, 3 * D:] == 3.0).all()
