@@ -1153,7 +1153,9 @@ struct ChunkKernel {
                     for (int i = 0; i < 8; ++i) move = move || (top[i] - m) + (lv[i] - dv) > kHeadroom + kLift;
                     if (first || __any_sync(0xffffffffu, move)) {
                         const float mn = fmaxf(m, best);
-                        float dn = first ? kNoKey : (m - mn) + dv;
+                        // (not below kNoKey: with no value that counts so far, as behind a first tile that the row does not see, the
+                        // sum is -inf, and a tile whose value scales are all 0 would leave lv - dv without a value)
+                        float dn = first ? kNoKey : fmaxf(kNoKey, (m - mn) + dv);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) dn = fmaxf(dn, (top[i] - mn) + (lv[i] - kLift));
                         if (!first) {
