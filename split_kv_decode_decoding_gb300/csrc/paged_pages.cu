@@ -40,7 +40,7 @@ struct RowsParams {
         flag_error(err, DA_DEVERR_SEQLENS);
         return 0;
     }
-    __device__ __forceinline__ int pages(int b) const { return (length(b) + P - 1) / P; }   // (lengths end below 2^31 - P)
+    __device__ __forceinline__ int pages(int b) const { return pages_of(length(b), P); }
 };
 
 // The workspace of a plan: bitmap, count of movers, lists.
@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kPageThreads, 6) page_fork_kernel(const ForkPa
         int len = 0;
         if (parent >= 0 && parent < r.B) len = r.length(parent);
         else if (share == 0 && threadIdx.x == 0) flag_error(r.err, DA_DEVERR_SEQLENS);
-        const int pages = (len + r.P - 1) / r.P, used = len - (pages - 1) * r.P;   // tokens of the last page
+        const int pages = pages_of(len, r.P), used = len - (pages - 1) * r.P;   // tokens of the last page
         const bool own = fresh >= 0 && len > 0 && used < r.P, writable = own && fresh < r.num_pages;
         const int32_t* row = r.table + static_cast<int64_t>(parent) * r.table_stride;
         const int64_t old = writable ? ld_cg_s32(row + pages - 1) : -1;

@@ -101,3 +101,19 @@ def test_entries_outside_the_cache_behind_a_window(window, sinks, D, G, kv, dtyp
     want = chunk64(q, zero, [4, 4], None, 70, sinks)
     out, lse = run_window(q, bad, 4, 70, sinks, expect=da.DA_DEVERR_PAGE)
     assert check(out, lse, want, DTYPES[dtype]) is None
+
+
+# ------------------------------------------------------------ sizes
+@pytest.mark.parametrize("page", [304, 976, 16])
+def test_free_pages_of_a_sequence_as_long_as_can_be(page):
+    """Length and page size add up to more than 32 bits hold."""
+    num_pages = 0x7FFFFF00 // page
+    table = torch.arange(num_pages, dtype=torch.int32, device="cuda").flip(0).view(1, -1)
+    ws = da.alloc_paged_pages_workspace(num_pages)
+    free, count = torch.full((num_pages,), -9, dtype=torch.int32, device="cuda"), ints([-1])
+    for length, left in ((num_pages * page, 0), (num_pages * page - page + 1, 0), (num_pages * page - 3 * page, 3)):
+        free.fill_(-9)
+        da.decode_attn_paged_free_pages(ints([length]), table, free, count, ws, page_size=page)
+        assert da.decode_attn_splitkv_get_error(ws) == 0
+        assert count.item() == left
+        assert free[:left].tolist() == list(range(left)) and (free[left:] == -9).all()

@@ -1,0 +1,34 @@
+"""Chunk and windowed attention and the page operators on the host: sizes at their limits, and what the sources promise of every call."""
+import os
+import subprocess
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "split_kv_decode_decoding_gb300", "csrc")
+
+
+def test_pages_of_the_longest_sequences(tmp_path):
+    """Every page size, at the longest sequence that the checks admit and around it: no sum passes what its type holds."""
+    src = tmp_path / "pages.cpp"
+    src.write_text(r"""
+#include <cstdio>
+#include "geometry.h"
+int main() {
+    for (int page = 16; page <= 1024; page += 16) {
+        const int64_t most = 0x7fffff00ll / page * page;      // max_pages * page_size
+        const int64_t lengths[] = {0, 1, page - 1, page, page + 1, most / 2, most - page, most - page + 1, most - 1, most};
+        for (int64_t n : lengths) {
+            const int64_t want = n / page + (n % page != 0), got = da_impl::pages_of(static_cast<int>(n), page);
+            if (got != want) return std::printf("%lld tokens in pages of %d: %lld, not %lld\n", (long long)n, page, (long long)got, (long long)want), 1;
+        }
+    }
+    return 0;
+}
+""")
+    exe = str(tmp_path / "pages")
+    subprocess.run(["g++", "-std=c++17", "-fsanitize=undefined", "-fno-sanitize-recover=all", "-I", CSRC, "-o", exe, str(src)], check=True)
+    got = subprocess.run([exe], capture_output=True, text=True)
+    assert got.returncode == 0, got.stdout + got.stderr
+
+
+def test_the_page_operators_count_pages_in_one_place():
+    text = open(os.path.join(CSRC, "paged_pages.cu")).read()
+    assert text.count("pages_of(") >= 2 and "P - 1) /" not in text
