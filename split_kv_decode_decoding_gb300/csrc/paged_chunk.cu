@@ -540,12 +540,13 @@ struct ChunkKernel {
         return wait(p, bar, parity);
     }
 
-    // Piece number i, or nullptr after the last one (or a wait that timed out); it is given back with drop_piece.
+    // Piece number i, or nullptr after the last one (or a wait that timed out), by a whole warp and with one answer for all of
+    // its lanes: a time-out that only some of them saw must not split them. It is given back with drop_piece.
     static __device__ __forceinline__ ChunkPiece* take_piece(const Ctx& c, const ChunkParams& p, uint32_t i, int tiles = 0) {
         const bool ok = wait_lane(c.x_full + 8 * (i % kPieceRing), (i / kPieceRing) & 1, piece_limit(p, tiles));
         if (!ok) flag_error(p.err, DA_DEVERR_TIMEOUT);
         ChunkPiece* x = c.pieces + i % kPieceRing;
-        return ok && x->valid ? x : nullptr;
+        return __any_sync(0xffffffffu, !ok || !x->valid) ? nullptr : x;
     }
     static __device__ __forceinline__ void drop_piece(const Ctx& c, uint32_t i) {   // (one lane of a warp)
         mbar_arrive(c.x_empty + 8 * (i % kPieceRing));
@@ -778,7 +779,7 @@ struct ChunkKernel {
         };
         for (uint32_t piece = 0;; ++piece) {
             const ChunkPiece* x = take_piece(c, p, piece);
-            if (__any_sync(0xffffffffu, x == nullptr)) return;
+            if (!x) return;
             const int nt = uniform(x->t1 - x->t0);
             __syncwarp();
             if ((threadIdx.x & 31) == 0) drop_piece(c, piece);

@@ -1,5 +1,6 @@
 """Chunk and windowed attention and the page operators on the host: sizes at their limits, and what the sources promise of every call."""
 import os
+import re
 import subprocess
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "split_kv_decode_decoding_gb300", "csrc")
@@ -32,3 +33,35 @@ int main() {
 def test_the_page_operators_count_pages_in_one_place():
     text = open(os.path.join(CSRC, "paged_pages.cu")).read()
     assert text.count("pages_of(") >= 2 and "P - 1) /" not in text
+
+
+def functions(text):
+    """Bodies of the device functions of a source file, with their heads."""
+    found = []
+    for head in re.finditer(r"^ *(?:template[^\n]*\n *)?(?:static )?__device__[^;{]*\{|^__global__[^;{]*\{", text, re.M):
+        depth, at = 1, head.end()
+        while depth:
+            depth += {"{": 1, "}": -1}.get(text[at], 0)
+            at += 1
+        found.append(text[head.start():at])
+    return found
+
+
+def test_a_wait_that_ends_some_lanes_ends_their_warp():
+    """The lanes of a warp look at their own clocks. Where the answer of a wait is used, the warp votes on it, so that a time-out
+    that some lanes saw cannot leave the others alone at the next instruction for a whole warp."""
+    used = 0
+    for name in sorted(os.listdir(CSRC)):
+        if not name.startswith("paged_"):
+            continue
+        text = re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, name)).read())
+        for body in functions(text):
+            if re.match(r"[^{]*\bwait_lane\(", body):
+                continue                                                   # its own definition
+            for call in re.finditer(r"\bwait_lane\(", body):
+                before = body[:call.start()].rstrip()
+                if before.endswith((";", "{", "}", ")")):
+                    continue                                               # a statement: nothing is done with the answer
+                used += 1
+                assert re.search(r"__(all|any)_sync\(0xffffffffu,", body[call.end():]), (name, body[:200])
+    assert used >= 2
