@@ -866,8 +866,8 @@ struct ChunkKernel {
             for (int i0 = 0; i0 < kPasses; i0 += kBatch) {
                 uint4 v[kBatch];
 #pragma unroll
-                for (int i = 0; i < kBatch; ++i, next())
-                    v[i] = f < rows ? __ldg(reinterpret_cast<const uint4*>(q + g * D)) : make_uint4(0, 0, 0, 0);
+                for (int i = 0; i < kBatch; ++i, next())   // (from the L2: the kernel before, which this one overlaps, may have written q)
+                    v[i] = f < rows ? __ldcg(reinterpret_cast<const uint4*>(q + g * D)) : make_uint4(0, 0, 0, 0);
                 // the largest exponent field of each row, all rows of the batch a step at a time
                 uint32_t top[kBatch];
                 if constexpr (kRowFactors) {

@@ -65,3 +65,11 @@ def test_a_wait_that_ends_some_lanes_ends_their_warp():
                 used += 1
                 assert re.search(r"__(all|any)_sync\(0xffffffffu,", body[call.end():]), (name, body[:200])
     assert used >= 2
+
+
+def test_no_kernel_reads_past_the_coherent_path():
+    """Every kernel may begin while the one before it in the stream still writes, so none of its inputs is read as constant."""
+    for name in sorted(os.listdir(CSRC)):
+        if name.endswith((".cu", ".cuh")):
+            text = re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, name)).read())
+            assert not re.search(r"\b__ldg\b|ld\.global(\.\w+)*\.nc\b|\b__restrict__\b", text), name
