@@ -1279,7 +1279,11 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CU
     c.smem = smem_raw;
     c.base = smem_addr(c.smem);
     if (c.base & 1023) {   // (it begins the block's shared memory, there is no room to move it)
-        if (threadIdx.x == 0) flag_error(p.err, DA_DEVERR_TIMEOUT);
+        grid_dependency_wait();
+        if (threadIdx.x == 0) {
+            p.join[blockIdx.x] = {};   // no parts that the second kernel could join
+            flag_error(p.err, DA_DEVERR_TIMEOUT);
+        }
         return;
     }
     ChunkPlan& plan = *reinterpret_cast<ChunkPlan*>(c.smem + Sh::kPlanOff);

@@ -73,3 +73,12 @@ def test_no_kernel_reads_past_the_coherent_path():
         if name.endswith((".cu", ".cuh")):
             text = re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, name)).read())
             assert not re.search(r"\b__ldg\b|ld\.global(\.\w+)*\.nc\b|\b__restrict__\b", text), name
+
+
+def test_every_block_of_a_chunk_leaves_the_second_kernel_its_list():
+    """Whichever way a block of the first kernel ends, it has written its entry of the list of parts to join."""
+    text = re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, "paged_chunk.cu")).read())
+    body = re.search(r"\nchunk_kernel\(.*?\n\}\n", text, re.S).group(0)
+    assert "leave_join(p, plan);" in body
+    for leave in re.finditer(r"\breturn;", body):
+        assert re.search(r"p\.join\[blockIdx\.x\] = |leave_join\(", body[:leave.start()])
