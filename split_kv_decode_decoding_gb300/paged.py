@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import operator
 import struct
 
 DA_E4M3 = 2
@@ -265,10 +266,14 @@ def decode_attn_paged(q, cache: PagedCache, kv_lens, block_table, out, workspace
 
 
 def _int32_of(x, name):
-    """x as a C int."""
-    if isinstance(x, bool) or not isinstance(x, int) or not -(1 << 31) <= x < 1 << 31:
+    """x, a whole number of Python's or of a type with __index__, as a C int."""
+    try:
+        n = operator.index(x)
+    except TypeError:
+        n = None
+    if n is None or isinstance(x, bool) or not -(1 << 31) <= n < 1 << 31:
         raise ValueError(f"{name} must be a whole number of 32 bits, not {x!r}")
-    return x
+    return n
 
 
 def decode_attn_paged_window(q, cache: PagedCache, kv_lens, block_table, out, workspace, *, window: int, sinks: int = 0,
@@ -388,10 +393,10 @@ def decode_attn_paged_chunk(q, cache: PagedCache, cu_new, kv_lens, block_table, 
     try:
         args = _pack_chunk(q.data_ptr(), q_stride, cache._ref, cu_new.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(),
                            max_pages, table_stride, B, T, Hq, code, 1.0 / math.sqrt(D) if scale is None else scale,
-                           0 if window is None else window, sinks, out.data_ptr(), out_stride, lse_ptr, workspace.data_ptr(),
-                           workspace.nbytes)
+                           0 if window is None else _int32_of(window, "window"), _int32_of(sinks, "sinks"), out.data_ptr(),
+                           out_stride, lse_ptr, workspace.data_ptr(), workspace.nbytes)
     except struct.error as e:
-        raise ValueError(f"scale, window, sinks, or a size, is no number of its C type: {e}") from None
+        raise ValueError(f"scale, or a size, is no number of its C type: {e}") from None
     st = _lib().decode_attn_paged_chunk(args, _raw_stream(stream, dev))
     if st:
         _fail(st, "decode_attn_paged_chunk")

@@ -1,4 +1,6 @@
 """Chunk and windowed attention and the page operators where their arithmetic, their sizes or what they share could go wrong."""
+import math
+
 import pytest
 import torch
 
@@ -117,3 +119,20 @@ def test_free_pages_of_a_sequence_as_long_as_can_be(page):
         assert da.decode_attn_splitkv_get_error(ws) == 0
         assert count.item() == left
         assert free[:left].tolist() == list(range(left)) and (free[left:] == -9).all()
+
+
+# ------------------------------------------------------------ refusals of the binding
+def test_windows_and_sinks_are_whole_numbers():
+    import numpy as np
+    paged = Paged([100], 1, 64, "f16", 16, VARLEN, seed=31)
+    q = queries(3, 2, 64, "f16", 32)
+    for bad in (True, 1.5, "4", 1 << 31, math.nan):
+        with pytest.raises(ValueError):
+            run_chunk(q, paged, [3], window=bad)
+        with pytest.raises(ValueError):
+            run_chunk(q, paged, [3], window=5, sinks=bad)
+        with pytest.raises(ValueError):
+            run_window(q, paged, 3, bad, 0)
+    want = chunk64(q, paged, [3], None, 5, 2)
+    for out, lse in (run_chunk(q, paged, [3], window=np.int64(5), sinks=np.int32(2)), run_window(q, paged, 3, np.int64(5), np.int32(2))):
+        assert check(out, lse, want, torch.float16) is None
