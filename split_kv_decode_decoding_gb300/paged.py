@@ -286,6 +286,13 @@ def decode_attn_paged_window(q, cache: PagedCache, kv_lens, block_table, out, wo
     return out
 
 
+def _length(x, name):
+    """The first dimension of a tensor that has one."""
+    if x.dim() == 0:
+        raise ValueError(f"{name} must have a dimension")
+    return x.shape[0]
+
+
 def _rows(x, name, T, heads, D, dtype, dev):
     """Check [T, heads, D] rows with contiguous heads; their row stride."""
     if x.shape != (T, heads, D):
@@ -320,7 +327,7 @@ def decode_attn_paged_append(q, k, v, cache: PagedCache, cu_new, kv_lens, block_
         raise TypeError(f"k must be float16 or bfloat16, not {dtype}")
     if cache.kv_dtype != DA_E4M3 and cache.kv_dtype != code:
         raise TypeError(f"k is {dtype}, the cache {cache.dtype}")
-    T, D = k.shape[0], cache.D
+    T, D = _length(k, "k"), cache.D
     k_stride = _rows(k, "k", T, cache.Hkv, D, dtype, dev)
     v_stride = _rows(v, "v", T, cache.Hkv, D, dtype, dev)
     q_ptr = out_ptr = q_stride = out_stride = Hq = 0
@@ -444,8 +451,9 @@ def decode_attn_paged_free_pages(kv_lens, block_table, free_pages, num_free, wor
     kv_lens: int32 [B]; block_table: int32 [B, max_pages]; free_pages: int32 [num_pages] of the cache;
     num_free: int32 [1]. Returned.
     """
-    args, _, _, dev = _rows_args(kv_lens, block_table, workspace, page_size, free_pages.shape[0])
-    st = _lib().decode_attn_paged_free_pages(args, _list(free_pages, "free_pages", free_pages.shape[0], dev),
+    n = _length(free_pages, "free_pages")
+    args, _, _, dev = _rows_args(kv_lens, block_table, workspace, page_size, n)
+    st = _lib().decode_attn_paged_free_pages(args, _list(free_pages, "free_pages", n, dev),
                                              _list(num_free, "num_free", 1, dev), _raw_stream(stream, dev))
     if st:
         _fail(st, "decode_attn_paged_free_pages")
@@ -462,7 +470,7 @@ def decode_attn_paged_fork(cache: PagedCache, kv_lens, block_table, parents, new
     args, _, max_pages, dev = _rows_args(kv_lens, block_table, workspace, cache.page_size, cache.num_pages)
     if cache.device != dev:
         raise ValueError("the cache must be on the tensors' device")
-    n = parents.shape[0]
+    n = _length(parents, "parents")
     stride = _table_out(block_table_out, n, max_pages, dev)
     st = _lib().decode_attn_paged_fork(args, cache._ref, _list(parents, "parents", n, dev), _list(new_pages, "new_pages", n, dev), n,
                                        _list(kv_lens_out, "kv_lens_out", n, dev), block_table_out.data_ptr(), stride,

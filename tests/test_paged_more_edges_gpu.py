@@ -136,3 +136,15 @@ def test_windows_and_sinks_are_whole_numbers():
     want = chunk64(q, paged, [3], None, 5, 2)
     for out, lse in (run_chunk(q, paged, [3], window=np.int64(5), sinks=np.int32(2)), run_window(q, paged, 3, np.int64(5), np.int32(2))):
         assert check(out, lse, want, torch.float16) is None
+
+
+def test_tensors_without_a_dimension_are_refused():
+    paged = Paged([100], 1, 64, "f16", 16, VARLEN, seed=33)
+    cache, ws = on_device(paged), da.alloc_paged_pages_workspace(len(paged.k))
+    lens, table, one = ints([100]), paged.table.cuda(), ints(1)
+    with pytest.raises(ValueError):
+        da.decode_attn_paged_fork(cache, lens, table, one, ints([-1]), ints([0]), table.clone(), ws)
+    with pytest.raises(ValueError):
+        da.decode_attn_paged_free_pages(lens, table, one, ints([0]), ws, page_size=16)
+    with pytest.raises(ValueError):
+        da.decode_attn_paged_append(None, cache.k.flatten()[0], cache.v.flatten()[0], cache, ints([0, 1]), lens, table, ws)
