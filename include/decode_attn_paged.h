@@ -290,7 +290,8 @@ da_status decode_attn_paged_free_pages(const da_paged_rows* rows, int32_t* free_
  * partly filled page, and that page's tokens (keys, values and 8-bit pages' scales) are copied to it, so that both
  * rows can be appended to; with new_pages[i] < 0 the last page is shared like the others (one row at most may
  * append to it). A parent outside [0, B) sets DA_DEVERR_SEQLENS and gives a row of length 0; a new page outside the
- * cache sets DA_DEVERR_PAGE and is not written. Entries behind a row's pages are left alone. The new pages must be
+ * cache sets DA_DEVERR_PAGE and is not written. A last entry outside the cache stays as it is like the others: there is
+ * nothing that the new page could hold. Entries behind a row's pages are left alone. The new pages must be
  * distinct, and none of them in use.
  *   parents, new_pages   device, int32 [n_out], n_out in [1, 65536]
  *   kv_lens_out          device, int32 [n_out]; block_table_out device, int32 [n_out][table_out_stride],

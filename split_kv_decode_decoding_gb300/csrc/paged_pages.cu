@@ -300,8 +300,9 @@ __global__ void __launch_bounds__(kPageThreads, 6) page_fork_kernel(const ForkPa
         int32_t* out = p.table_out + static_cast<int64_t>(child) * p.table_out_stride;
         for (int e = share * kPageThreads + static_cast<int>(threadIdx.x); e < pages; e += split * kPageThreads) {
             const int page = ld_cg_s32(row + e);
-            if (page < 0 || page >= r.num_pages) flag_error(r.err, DA_DEVERR_PAGE);
-            out[e] = own && e == pages - 1 ? fresh : page;
+            const bool there = page >= 0 && page < r.num_pages;
+            if (!there) flag_error(r.err, DA_DEVERR_PAGE);
+            out[e] = own && there && e == pages - 1 ? fresh : page;
         }
         if (old < 0 || old >= r.num_pages) continue;
         // the used tokens of its last page: one run, or one per head (a page has at most 2^27 units)

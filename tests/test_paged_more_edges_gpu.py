@@ -121,6 +121,27 @@ def test_free_pages_of_a_sequence_as_long_as_can_be(page):
         assert free[:left].tolist() == list(range(left)) and (free[left:] == -9).all()
 
 
+# ------------------------------------------------------------ pages
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_a_fork_of_a_row_whose_last_entry_is_outside_the_cache(kv):
+    """There is nothing to copy: the entry stays what it is, and the new page is not taken into use as it lies."""
+    paged = Paged([40, 37], 2, 64, kv, 16, VARLEN, seed=30, extra_pages=4)
+    cache = on_device(paged)
+    n = cache.num_pages
+    unused = [i for i in range(n) if i not in set(paged.table.flatten().tolist())][:2]
+    table = paged.table.clone()
+    table[0, 2], before = n + 5, [x.view(torch.uint8).clone() for x in (cache.k, cache.v)]
+    lens, out, ws = ints([0, 0]), torch.full((2, 3), -9, dtype=torch.int32, device="cuda"), da.alloc_paged_pages_workspace(n)
+    da.decode_attn_paged_fork(cache, ints(paged.lens), table.cuda(), ints([0, 1]), ints(unused), lens, out, ws)
+    assert da.decode_attn_splitkv_get_error(ws) == da.DA_DEVERR_PAGE
+    assert lens.tolist() == paged.lens
+    assert out.tolist() == [table[0].tolist(), [*table[1, :2].tolist(), unused[1]]]
+    after = [x.view(torch.uint8) for x in (cache.k, cache.v)]
+    for x, y in zip(before, after):
+        x[unused[1], :5] = x[int(table[1, 2]), :5]
+        assert torch.equal(x, y)
+
+
 # ------------------------------------------------------------ refusals of the binding
 def test_windows_and_sinks_are_whole_numbers():
     import numpy as np
