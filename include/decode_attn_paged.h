@@ -296,7 +296,7 @@ da_status decode_attn_paged_free_pages(const da_paged_rows* rows, int32_t* free_
  *   parents, new_pages   device, int32 [n_out], n_out in [1, 65536]
  *   kv_lens_out          device, int32 [n_out]; block_table_out device, int32 [n_out][table_out_stride],
  *                        table_out_stride >= max_pages; neither overlaps an input
- *   rows                 page_size and num_pages must be the cache's
+ *   rows                 page_size and num_pages must be the cache's, a page's keys less than 32 GB (else DA_ERR_UNSUPPORTED)
  */
 da_status decode_attn_paged_fork(const da_paged_rows* rows, const da_paged_cache* cache, const int32_t* parents,
                                  const int32_t* new_pages, int n_out, int32_t* kv_lens_out, int32_t* block_table_out,

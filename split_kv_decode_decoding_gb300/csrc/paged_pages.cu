@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kPageThreads, 6) page_fork_kernel(const ForkPa
             out[e] = own && there && e == pages - 1 ? fresh : page;
         }
         if (old < 0 || old >= r.num_pages) continue;
-        // the used tokens of its last page: one run, or one per head (a page has at most 2^27 units)
+        // the used tokens of its last page: one run, or one per head (a page has at most kMostUnits units)
         const bool thd = p.layout == DA_LAYOUT_VARLEN;
         const uint32_t run = static_cast<uint32_t>(used) * p.row_units * (thd ? p.Hkv : 1), units = thd ? run : run * p.Hkv;
         const uint32_t stride = static_cast<uint32_t>(r.P) * p.row_units;   // of heads, where they lie outside the tokens
@@ -339,6 +339,7 @@ __global__ void __launch_bounds__(kPageThreads, 6) page_fork_kernel(const ForkPa
 
 // ------------------------------------------------------------ host side
 constexpr int kPageBlocks = 152 * 8;                       // blocks of a kernel that loops over its work
+constexpr int64_t kMostUnits = 0x7fffffff;                 // of a page's keys in a fork, which counts them in 32 bits: 32 GB
 constexpr int kPlanWords = 64;                             // words of the bitmap that a block plans, at least
 constexpr int64_t kOneEntries = 4096;                      // table entries up to which one block plans alone: one launch, not three
                                                            // (1024 entries 4.9 us against 4.4 in a graph, but 5.8 against 9.7
@@ -506,6 +507,7 @@ da_status decode_attn_paged_fork(const da_paged_rows* rows, const da_paged_cache
     p.layout = c.layout;
     p.row_units = c.D * (c.kv_dtype == DA_E4M3 ? 1 : 2) / 16;
     p.page_units = static_cast<int64_t>(c.page_size) * c.Hkv * p.row_units;
+    if (p.page_units > kMostUnits) return DA_ERR_UNSUPPORTED;
     // as many blocks for a child as there is work for, and as fill the device
     const int64_t work = std::max<int64_t>(2 * ((p.page_units + kCopyChunk - 1) / kCopyChunk), (r.max_pages + kPageThreads - 1) / kPageThreads);
     const int split = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(work, kPageBlocks / n_out)));

@@ -3,6 +3,9 @@ import os
 import re
 import subprocess
 
+import split_kv_decode_decoding_gb300 as da
+from test_paged_more_host import fork
+
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "split_kv_decode_decoding_gb300", "csrc")
 
 
@@ -33,6 +36,14 @@ int main() {
 def test_the_page_operators_count_pages_in_one_place():
     text = open(os.path.join(CSRC, "paged_pages.cu")).read()
     assert text.count("pages_of(") >= 2 and "P - 1) /" not in text
+
+
+def test_a_fork_refuses_pages_whose_parts_pass_32_bits():
+    """Refused on the host, before any device work (the addresses are never followed)."""
+    da.build()
+    lib = da.load()
+    for heads, D, kv in ((1 << 17, 128, da.DA_F16), (1 << 18, 64, da.DA_BF16), (1 << 18, 128, da.DA_E4M3), (5 << 20, 64, da.DA_E4M3)):
+        assert fork(lib, cache=dict(page_size=1024, Hkv=heads, D=D, kv_dtype=kv), page_size=1024) == da.DA_ERR_UNSUPPORTED
 
 
 def functions(text):
