@@ -144,7 +144,7 @@ struct ChunkTiles {
         sure = min(p.sinks, low) / kTileKeys;
         to = ns + max((first + 1) / kTileKeys - lo, 0);
         from = ns;
-        if (p.window) from += max((max(0, last - p.window + 1) + kTileKeys - 1) / kTileKeys - lo, 0);
+        if (p.window) from += max((max(0, max(last, 0) - p.window + 1) + kTileKeys - 1) / kTileKeys - lo, 0);
     }
     __device__ __forceinline__ int key(int tile) const { return (tile < ns ? tile : lo + tile - ns) * kTileKeys; }
     __device__ __forceinline__ bool plain(int tile) const { return tile < sure || (tile >= from && tile < to); }

@@ -106,6 +106,18 @@ def test_entries_outside_the_cache_behind_a_window(window, sinks, D, G, kv, dtyp
 
 
 # ------------------------------------------------------------ sizes
+def test_a_length_that_cannot_be_and_the_widest_window():
+    """Many rows of a sequence that counts as empty lie far below position 0."""
+    paged = Paged([2000, 3], 1, 64, "f16", 16, VARLEN, seed=98)
+    new = [1500, 3]
+    q = queries(1503, 2, 64, "f16", 99)
+    for sinks in (0, 0x7FFFFFFF):
+        out, lse = run_chunk(q, paged, new, window=0x7FFFFFFF, sinks=sinks, lens=[1 << 30, 3], expect=da.DA_DEVERR_SEQLENS)
+        assert (out[:1500] == 0).all() and torch.isneginf(lse[:1500]).all()
+        want = chunk64(q, paged, new)
+        assert check(out[1500:], lse[1500:], tuple(x[1500:] for x in want), torch.float16) is None
+
+
 @pytest.mark.parametrize("page", [304, 976, 16])
 def test_free_pages_of_a_sequence_as_long_as_can_be(page):
     """Length and page size add up to more than 32 bits hold."""
