@@ -6,8 +6,8 @@ import torch
 
 import split_kv_decode_decoding_gb300 as da
 from paged_more_ref import check, chunk64
-from paged_more_util import ints, on_device, queries, run_chunk
-from paged_ref import DTYPES, VARLEN, Paged
+from paged_more_util import ints, on_device, queries, run_chunk, starts
+from paged_ref import BHSD, DTYPES, VARLEN, Paged
 
 pytestmark = pytest.mark.gpu
 TYPES = [("f16", "f16"), ("bf16", "bf16"), ("e4m3", "f16"), ("e4m3", "bf16")]
@@ -131,6 +131,125 @@ def test_free_pages_of_a_sequence_as_long_as_can_be(page):
         assert da.decode_attn_splitkv_get_error(ws) == 0
         assert count.item() == left
         assert free[:left].tolist() == list(range(left)) and (free[left:] == -9).all()
+
+
+# ------------------------------------------------------------ long calls
+@pytest.mark.parametrize("kv,dtype", TYPES)
+@pytest.mark.parametrize("D,window", [(128, 0), (64, 0), (128, 3000), (64, 3000)])
+def test_long_calls_against_the_definition(D, window, kv, dtype):
+    """Every block walks through many key tiles: rows at the edges of items, each over its whole history."""
+    g = torch.Generator().manual_seed(51)
+    lens, new, pages = [16384, 5000], [2048, 700], 400
+    shape = (pages, 8, 64, D)
+    k, v = (torch.randn(shape, generator=g).to(DTYPES[kv]) for _ in range(2))
+    scales = [torch.exp2(torch.randint(-3, 3, (pages, 8), generator=g).float()) for _ in range(2)] if kv == "e4m3" else [None, None]
+    order = torch.randperm(pages, generator=g).to(torch.int32)[:358]
+    table = torch.stack([order[:256], torch.cat([order[256:], order.new_zeros(154)])])
+    q = torch.randn(2748, 32, D, generator=g).to(DTYPES[dtype])
+    cache = da.PagedCache(k.cuda(), v.cuda(), *(s if s is None else s.cuda() for s in scales), layout=BHSD)
+    ws = da.alloc_paged_chunk_workspace(32, 8, D)
+    out, lse = torch.empty(q.shape, dtype=q.dtype, device="cuda"), torch.empty(2748, 32, device="cuda")
+    da.decode_attn_paged_chunk(q.cuda(), cache, ints(starts(new)), ints(lens), table.cuda(), out, ws, window=window, sinks=5, lse=lse)
+    assert da.decode_attn_splitkv_get_error(ws) == 0
+    # (sequence, new token): of items of 64 tokens
+    picked = [(0, 0), (0, 63), (0, 64), (0, 1055), (0, 2047), (1, 0), (1, 351), (1, 699)]
+    rows = [t + (2048 if b else 0) for b, t in picked]
+    heads = [0, 1, 2, 3, 28, 29, 30, 31]
+    some = object.__new__(Paged)       # two of the KV heads
+    some.Hkv, some.D, some.kv, some.page, some.layout = 2, D, kv, 64, BHSD
+    raw = lambda x: x.view(torch.uint8 if kv == "e4m3" else torch.int16)[:, [0, 7]].contiguous().view(x.dtype)
+    some.k, some.v = raw(k), raw(v)
+    some.k_scale, some.v_scale = (s if s is None else s[:, [0, 7]] for s in scales)
+    some.table = table[[b for b, _ in picked]]
+    some.lens = [lens[b] - new[b] + t + 1 for b, t in picked]
+    want = chunk64(q[rows][:, heads], some, [1] * len(picked), None, window, 5)
+    assert check(out[rows][:, heads], lse[rows][:, heads], want, DTYPES[dtype]) is None
+
+
+# ------------------------------------------------------------ together
+def test_a_window_of_single_tokens_by_either_call():
+    paged = Paged([3000, 70, 1], 2, 128, "bf16", 64, BHSD, seed=12)
+    q = queries(3, 8, 128, "bf16", 13)
+    want = chunk64(q, paged, [1, 1, 1], None, 500, 4)
+    for out, lse in (run_chunk(q, paged, [1, 1, 1], window=500, sinks=4), run_window(q, paged, 1, 500, 4)):
+        assert check(out, lse, want, torch.bfloat16) is None
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_decode_steps_beside_chunks(D):
+    """A chunk call and windowed decode steps over the same pages, on two streams."""
+    paged = Paged([900, 64, 10, 2000], 2, D, "bf16", 16, VARLEN, seed=60)
+    new = [300, 64, 0, 1]
+    q, dq = queries(sum(new), 8, D, "bf16", 62), queries(4, 8, D, "bf16", 70)
+    want, dwant = chunk64(q, paged, new), chunk64(dq, paged, [1] * 4, None, 100, 4)
+    cache, table, lens, cu = on_device(paged), paged.table.cuda(), ints(paged.lens), ints(starts(new))
+    ws, dec = da.alloc_paged_chunk_workspace(8, 2, D), da.alloc_paged_workspace(1, 8, 2, D)
+    qd, dqd = q.cuda(), dq.cuda()
+    out, lse, dout, dlse = torch.empty_like(qd), torch.empty(len(q), 8, device="cuda"), torch.empty_like(dqd), torch.empty(4, 8, device="cuda")
+    one, other = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(30):
+        da.decode_attn_paged_chunk(qd, cache, cu, lens, table, out, ws, lse=lse, stream=one)
+        da.decode_attn_paged_window(dqd, cache, lens, table, dout, dec, window=100, sinks=4, lse=dlse, stream=other)
+    torch.cuda.synchronize()
+    assert da.decode_attn_splitkv_get_error(ws) == 0 and da.decode_attn_splitkv_get_error(dec) == 0
+    assert check(out, lse, want, torch.bfloat16) is None and check(dout, dlse, dwant, torch.bfloat16) is None
+
+
+@pytest.mark.parametrize("kv", ["f16", "e4m3"])
+def test_one_workspace_for_attention_append_and_pages(kv):
+    """Every call of the paged cache in turn on one workspace, nothing waited for in between."""
+    Hq, Hkv, D, P, Tq = 8, 2, 128, 16, 4
+    paged = Paged([6005, 900, 33], Hkv, D, kv, P, VARLEN, seed=21, extra_pages=60)
+    cache, B = on_device(paged), 3
+    n = cache.num_pages
+    size = max(da.paged_workspace_size(Tq, Hq, Hkv, D), da.paged_chunk_workspace_size(Hq, Hkv, D), da.paged_pages_workspace_size(n))
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda").fill_(0xA5)
+    assert da.load().decode_attn_paged_workspace_init(ws.data_ptr(), size, torch.cuda.current_stream().cuda_stream) == 0
+    q = queries(B * Tq, Hq, D, "f16", 22).cuda()
+    want, windowed = chunk64(q.cpu(), paged, [Tq] * B), chunk64(q.cpu(), paged, [Tq] * B, None, 700, 20)
+    lens, cu = ints(paged.lens), ints(starts([Tq] * B))
+    width = paged.table.shape[1] + 2
+    table = torch.zeros(B, width, dtype=torch.int32, device="cuda")
+    table[:, :width - 2] = paged.table.cuda()
+    used = sum(-(-m // P) for m in paged.lens)
+    # the last token's own key and value, appended again (16-bit pages; into 8-bit ones a page that no row uses)
+    rows = [paged.sequence(b) for b in range(B)]
+    newest = [torch.stack([r[i][-1] for r in rows]).half().cuda() for i in range(2)]
+    free, count, moved = torch.empty(n, dtype=torch.int32, device="cuda"), ints([0]), ints([0])
+    parents, fresh = ints([0, 1, 2]), ints([0] * B)
+    got, results = {}, []
+    for turn in range(4):
+        table2, table3, lens2 = torch.zeros_like(table), torch.zeros_like(table), torch.zeros_like(lens)
+        for name in ("chunk", "window", "decode"):
+            got[name] = (torch.full_like(q, 7.0), torch.full((B * Tq, Hq), 7.0, device="cuda"))
+        o, l = got["chunk"]
+        da.decode_attn_paged_chunk(q, cache, cu, lens, table, o, ws, lse=l)
+        da.decode_attn_paged_free_pages(lens, table, free, count, ws, page_size=P)
+        o, l = got["decode"]
+        da.decode_attn_paged(q.view(B, Tq, Hq, D), cache, lens, table, o.view(B, Tq, Hq, D), ws, lse=l.view(B, Tq, Hq))
+        fresh.copy_(free[:B])
+        da.decode_attn_paged_fork(cache, lens, table, parents, fresh, lens2, table2, ws)
+        if kv == "f16":
+            da.decode_attn_paged_append(None, *newest, cache, ints(list(range(B + 1))), lens2, table2, ws)
+        else:
+            da.decode_attn_paged_append(None, *newest, cache, ints(list(range(B + 1))), ints([1] * B), free[B:2 * B].view(B, 1), ws)
+        o, l = got["window"]
+        da.decode_attn_paged_window(q.view(B, Tq, Hq, D), cache, lens2, table2, o.view(B, Tq, Hq, D), ws, window=700, sinks=20,
+                                    lse=l.view(B, Tq, Hq))
+        da.decode_attn_paged_compact(cache, lens2, table2, table3, moved, ws)
+        results.append({k: (a.clone(), b.clone()) for k, (a, b) in got.items()} | dict(
+            free=free[:n - used].clone(), count=count.clone(), moved=moved.clone(), before=table, after=table3, lens=lens2))
+        table, lens = table3, lens2
+    assert da.decode_attn_splitkv_get_error(ws) == 0
+    need = [-(-m // P) for m in paged.lens]
+    for r in results:
+        for name, ref in (("chunk", want), ("decode", want), ("window", windowed)):
+            assert check(*r[name], ref, torch.float16) is None, name
+        in_use = {x for row, m in zip(r["before"].tolist(), need) for x in row[:m]}
+        assert r["free"].tolist() == [x for x in range(n) if x not in in_use] and r["count"].item() == n - used
+        assert r["moved"].item() == used and r["lens"].tolist() == paged.lens
+        assert sorted(x for row, m in zip(r["after"].tolist(), need) for x in row[:m]) == list(range(used))
 
 
 # ------------------------------------------------------------ pages
