@@ -57,8 +57,9 @@
 // Measured (one GB300, mean of a graph of calls): 16 sequences of 131072 keys, 32 / 8 heads, bf16
 // 1156 us, 7.4 TB/s; 64 sequences of 512 to 8192 keys, 28 / 4 heads 86.2 us, 6.4 TB/s, over e4m3
 // pages 51.3 us, 5.4 TB/s; one sequence of 1024 keys 9.0 us, of 8192 keys over e4m3 pages 11.1 us.
-// With a window: 32 sequences of 4096 to 65536 keys that see 2000 and the first four, 32 / 8 heads, bf16 46.5 us, 5.7 TB/s
-// (as many keys without a window 44.6 us); four tokens over 8192 + 128 keys in e4m3 pages, 28 / 4 heads 21.7 us (20.0).
+// With a window: 32 sequences of 4096 to 65536 keys that see 2000 and the first four, 32 / 8 heads, bf16 46.8 us, 5.6 TB/s
+// (as many keys without a window 44.6 us), over e4m3 pages 30.0 us, 4.4 TB/s; 64 sequences that see 1004 keys, 16 / 2 heads of size
+// 64, fp16 14.7 us, 2.3 TB/s; four tokens over 8192 + 128 keys in e4m3 pages, 28 / 4 heads 22.6 us (20.0).
 
 #ifndef DECODE_ATTN_PAGED_ATTN_CUH
 #define DECODE_ATTN_PAGED_ATTN_CUH

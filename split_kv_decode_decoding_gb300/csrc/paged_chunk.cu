@@ -32,18 +32,21 @@
 //
 // Sums, maxima, accumulators and partial results are float32. Rounded to fewer bits are the outputs, once, and the
 // weights, once, to the 16-bit type of their product: the tensor cores have no wider one at this rate, and a second
-// term (as in the decode kernel, which waits for bytes) would add half of all products. The outputs' error is 1.3 times
-// that of float32 weights (16-bit pages; over e4m3 pages 1.0, where fp16 weights meet a bf16 output).
+// term (as in the decode kernel, which waits for bytes) would add half of all products. The outputs' error is 1.3 (fp16)
+// to 1.4 times (bf16) that of float32 weights (16-bit pages; over e4m3 pages 1.0, where fp16 weights meet a bf16 output).
 //
-// What bounds it. Head size 128: the tensor cores, 74 % of the time active (2048 of 8192 tokens, 32 / 8 heads, bf16:
-// 145 us, 1.65 PFLOP/s, 86 % of cuBLAS's burst rate; 4096 of 32768: 1.33 ms, 1.55 PFLOP/s, 90 % of its sustained rate, where the
-// power limit lowers the clock). A pair of row tiles takes 2048 cycles of products and 2900 in all; their operands and the
-// copies keep shared memory busy for the 2048, too, and a shorter softmax (1280 cycles from scores to weights) changes nothing.
-// e4m3 pages: shared memory, which a pair of tiles keeps busy for 2560 cycles (the products' operands 1536, the raw tile in and
-// out 512, the converted one in 512): 203 us for the first call above, 1.47 ms for the second. Head size 64: the rows'
-// threads: an exponent takes 4 cycles of a scheduler's unit, two warps 1024 cycles per pair of tiles that the products
-// need 1024 for; 2000 in all (16 heads, 16384 tokens: 370 us, 1.11 PFLOP/s). Short calls: latency, 2 us to the plan, 2 to the first scores,
-// 1.4 per key tile, 2.5 for a piece's end and 3 for the join (107 of 1131 tokens 17.3 us).
+// What bounds it (times in a graph of 20 calls, and of calls in a row, where the power limit lowers the clock). Head size 128:
+// the tensor cores, 75 % of the time active (2048 of 8192 tokens, 32 / 8 heads, bf16: 145 and 157 us, 1.66 and 1.53 PFLOP/s, 86 %
+// of cuBLAS's burst and 90 % of its sustained rate; 4096 of 32768: 1.18 to 1.32 and 1.34 ms, 1.54 PFLOP/s in a row). A pair of row
+// tiles takes 2048 cycles of products and 2900 in all; their operands and the copies keep shared memory busy for the 2048, too, and
+// a shorter softmax (1280 cycles from scores to weights) changes nothing. e4m3 pages: shared memory, which a pair of tiles keeps busy
+// for 2560 cycles (the products' operands 1536, the raw tile in and out 512, the converted one in 512): 206 us for the first call
+// above, 1.46 and 1.48 ms for the second. Head size 64: the rows' threads: an exponent takes 4 cycles of a scheduler's unit, two
+// warps 1024 cycles per pair of tiles that the products need 1024 for; 2000 in all (16 / 2 heads, 8192 of 16384 tokens: 371 us,
+// 1.11 PFLOP/s; over e4m3 pages 528 us with fp16 queries, 543 with bf16 ones). Short calls: latency, 2 us to the plan, 2 to the first
+// scores, 1.4 per key tile, 2.5 for a piece's end and 3 for the join (107 of 1131 tokens 17.5 us). Row tiles without a row are
+// computed like the others: 64 sequences with one token each over 8192 keys take 326 us in 16-bit pages, bound by the bytes, and
+// 404 in e4m3 ones, whose bytes would take 158.
 
 #include "paged_common.cuh"
 #include "tcgen05.cuh"

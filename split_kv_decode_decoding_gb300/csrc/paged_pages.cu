@@ -11,9 +11,9 @@
 //                       mover i >= n, used,    movers[used_before(i) - used_before(n)] = i
 //     (as many holes as movers), and the k-th mover goes to the k-th hole.
 //
-// What bounds them: the copies the bytes (512 beams with half a page of 512 KB each 35.0 us, 6.5 TB/s read and written;
-// 1.5 thousand pages of 128 KB moved 69 us, of which 60 the copy, 6.5 TB/s), the lists latency: three launches that wait for one
-// another, each with one or two loads that do (357000 pages, 257000 entries 12.5 us; a small pool by one block 4.5 us).
+// What bounds them: the copies the bytes (512 beams with half a page of 512 KB each 35.8 us, 6.3 TB/s read and written;
+// 1.5 thousand pages of 128 KB moved 70 us, of which 60 the copy, 6.5 TB/s), the lists latency: three launches that wait for one
+// another, each with one or two loads that do (357000 pages, 257000 entries 12.9 us; a small pool by one block 4.8 us).
 
 #include "paged_common.cuh"
 
